@@ -428,6 +428,188 @@ moe_status_t moe_layer_bwd_mx(const moe_config_t *cfg, const void *ctx, const fl
                               void *dW2s, float *dlogits, void *ws, void *stream);
 
 /*
+ * ---- Group-limited routing.  For token t with logits l (NaN counts as -inf and sets
+ * MOE_DEVERR_NAN_LOGIT, +inf as the largest finite value):
+ *   score s_e = sigma(l_e), or exp(l_e) / sum_i exp(l_i) over all E experts
+ *   key   c_e = s_e + bias_e with a bias (the choice alone sees it), else l_e
+ *   The E experts form `groups` runs of E / groups consecutive ones.  A group is worth its
+ *   largest c (group_top = 1) or the sum of its two largest (2; of the scores s when there is
+ *   no bias; of one alone if only one is in service); the top_groups worthiest stay.
+ *   The k largest keys of the groups that stay are chosen, in descending order.  Every tie
+ *   goes to the lower index; keys and worths that include scores are compared in 64 bits.
+ *   weight w_j = route_scale * s_j (renorm = 0), or route_scale * s_j / sum of the chosen s
+ *   (renorm = 1; the quotient's limit where all of them underflow).
+ * An expert whose logit is -inf is out of service for that token and never chosen.  A slot
+ * for which nothing is left (a padding token: all its logits -inf) gets expert -1, weight 0
+ * and dest_row -1, and takes no row.
+ */
+typedef enum {
+    MOE_SCORE_SOFTMAX = 0,
+    MOE_SCORE_SIGMOID = 1
+} moe_score_t;
+
+typedef struct {
+    int32_t score;        /* moe_score_t                                                  */
+    int32_t groups;       /* 1 <= groups <= 32, divides E; 1 = no groups                  */
+    int32_t top_groups;   /* 1 <= top_groups <= groups, top_groups * (E / groups) >= k    */
+    int32_t group_top;    /* 1 or 2 (2 needs groups of at least two experts)              */
+    int32_t renorm;       /* 0 or 1                                                       */
+    const float *bias;    /* [E] device fp32, finite, or NULL                             */
+} moe_router_t;
+
+/*
+ * Route with `router`.  cfg gives T, E, k, route_scale and capacity (dropping by token order);
+ * its gate is not used, and select_bias, drop_negative and drop_by_score must be unset
+ * (MOE_ERR_INVALID_ARG).  Outputs, workspace and determinism as moe_route, except for slots
+ * without an expert as described above; those are marked in drop_mask too.
+ */
+moe_status_t moe_route_groups(const moe_config_t *cfg, const moe_router_t *router,
+                              const float *logits, int32_t *topk_idx, float *topk_w,
+                              int32_t *counts, int32_t *kept, int32_t *offsets,
+                              int32_t *dest_row, int32_t *src_tok, int32_t *src_slot,
+                              uint8_t *drop_mask, void *ws, void *stream);
+
+/*
+ * Gradient of moe_route_groups' weights: dlogits [T,E] fp32 from dw [T,k] fp32, the gradient of
+ * topk_w.  The choice is piecewise constant: with renorm, or sigmoid scores, only the chosen
+ * experts' logits have a gradient; softmax scores without renorm reach every expert.  Slots
+ * with topk_idx -1 are ignored; another index outside [0, E) sets MOE_DEVERR_BAD_INDEX and is
+ * ignored too.
+ */
+moe_status_t moe_route_groups_bwd(const moe_config_t *cfg, const moe_router_t *router,
+                                  const float *logits, const int32_t *topk_idx, const float *dw,
+                                  float *dlogits, void *ws, void *stream);
+
+/*
+ * The combine's backward for a gate whose own backward is a separate call:
+ *   dyp[p] = bf16(topk_w[t,j] * dy[t]), dw[t,j] = <dy[t], yp[p]> with p = dest_row[t,j]; dw is 0
+ *   where dest_row is -1.  dw [T,k] fp32.
+ */
+moe_status_t moe_combine_bwd_dw(const moe_config_t *cfg, const void *dy, const void *yp,
+                                const float *topk_w, const int32_t *dest_row, void *dyp,
+                                float *dw, void *ws, void *stream);
+
+/*
+ * ---- 8-bit operands with one scale for each block of 128.
+ * A block is 128 consecutive elements along the product's contraction axis (the last one of a
+ * row may be shorter), or 128 x 128 elements of a weight.  With amax the block's largest
+ * magnitude, held at or above 2^-110:
+ *   scale  s = amax / 448, or (pow2) the smallest power of two >= amax / 448;   fp32
+ *   code   E4M3(v * (448 / amax)), or E4M3(v / s) with pow2; nearest, ties to even,
+ *          saturated at 448; quotients and products are single fp32 roundings
+ * so that v is close to code * s.  A NaN makes its block NaN; an infinity has an infinite scale
+ * (pow2 or not), its own code is NaN and the others' are 0.
+ *
+ * Along the row:    codes [rows][ld] bytes, scales [rows][ceil(C/128)].
+ * Along the tokens: for a weight gradient, whose contraction runs over an expert's rows.  Each
+ *   segment's rows form blocks of 128 from its first row; the segments' blocks follow one
+ *   another, B = moe_fp8_token_blocks(rows, G) bounds their number.  codes_t [C][128 B]: column
+ *   c of block i at codes_t[c][128 i ..], zero codes past the segment's end; scales_t [B][C].
+ *   Blocks past the last segment's are not written.
+ * ld is a multiple of 16 and at least the row's length; what lies past it may be written with
+ * zeros and is never read.  offsets [G+1] (device) delimit the segments as in moe_route;
+ * NULL with G = 1: one segment of `rows` rows.  G <= 256, C, N, K < 2^24, rows < 2^31 - 2^15.
+ * `ws` is any workspace initialised by moe_ws_init (MOE_FP8_WS_BYTES suffice): it holds the
+ * error word.
+ */
+#define MOE_FP8_WS_BYTES 256
+
+/* ceil(rows / 128) + G: the number of token blocks to provide for.  -1 for invalid arguments.
+ * Host-only. */
+int64_t moe_fp8_token_blocks(int64_t rows, int32_t G);
+
+typedef struct {
+    int64_t rows;         /* rows of the outputs (offsets[G] <= rows of them live); >= 0  */
+    int64_t src_rows;     /* rows of x when src_tok is given                              */
+    int32_t G;            /* segments                                                     */
+    int32_t C;            /* columns                                                      */
+    int64_t ldx;          /* elements between rows of x, >= C                             */
+    int64_t ld;           /* bytes between rows of codes                                  */
+    int32_t pow2;         /* 0 or 1                                                       */
+} moe_fp8_quant_t;
+
+/*
+ * Quantise bf16 rows: row p is x[p], or x[src_tok[p]] (entries outside [0, src_rows) set
+ * MOE_DEVERR_BAD_INDEX; such a row is not written by the row form and read as row 0 by the
+ * token form).  codes and scales, codes_t and scales_t, or all four are given; either pair may
+ * be NULL.
+ */
+moe_status_t moe_fp8_quantize(const moe_fp8_quant_t *q, const void *x,
+                              const int32_t *src_tok_or_null, const int32_t *offsets_or_null,
+                              void *codes, float *scales, void *codes_t, float *scales_t, void *ws,
+                              void *stream);
+
+/*
+ * Quantise weights W [G][N][K] bf16 in 128 x 128 blocks: codes [G][N][ld], scales
+ * [G][ceil(N/128)][ceil(K/128)]; with codes_t also the transposes codes_t [G][K][ld_t] (the
+ * same codes) and scales_t [G][ceil(K/128)][ceil(N/128)], the operand of the data gradient.
+ */
+moe_status_t moe_fp8_quantize_weights(const void *W, int32_t G, int32_t N, int32_t K, void *codes,
+                                      int64_t ld, float *scales, void *codes_t_or_null,
+                                      int64_t ld_t, float *scales_t_or_null, int32_t pow2,
+                                      void *stream);
+
+typedef struct {
+    int64_t rows;
+    int32_t G;
+    int32_t f;            /* SwiGLU width; ab is [rows][2f] bf16, dense                   */
+    int64_t ld;           /* bytes between rows of codes                                  */
+    int32_t pow2;
+} moe_fp8_act_t;
+
+/* SwiGLU with quantised output: h = silu(a) * b of ab = [a | b], rounded to bf16 once from its
+ * exact value, quantised as moe_fp8_quantize does with C = f (codes, scales and, or, codes_t,
+ * scales_t). */
+moe_status_t moe_fp8_swiglu(const moe_fp8_act_t *p, const void *ab, const int32_t *offsets_or_null,
+                            void *codes, float *scales, void *codes_t, float *scales_t, void *ws,
+                            void *stream);
+
+/* Its backward from dh [rows][f] bf16: da = dh b silu'(a), db = dh silu(a), each rounded to bf16
+ * once, [da | db] quantised with C = 2f; with h_codes_t, h_scales_t also h along the tokens
+ * (C = f), recomputed from ab.  codes and scales are required; codes_t, scales_t and h_codes_t,
+ * h_scales_t are optional pairs (the latter only with the former). */
+moe_status_t moe_fp8_swiglu_bwd(const moe_fp8_act_t *p, const void *dh, const void *ab,
+                                const int32_t *offsets_or_null, void *codes, float *scales,
+                                void *codes_t, float *scales_t, void *h_codes_t,
+                                float *h_scales_t, void *ws, void *stream);
+
+typedef enum { MOE_OUT_BF16 = 0, MOE_OUT_FP32 = 1 } moe_out_t;
+
+typedef struct {
+    int64_t rows;         /* rows of a and out                                            */
+    int32_t G, N, K;
+    int64_t lda, ldb;     /* bytes between rows of a and b, multiples of 16, >= K         */
+    int64_t ldo;          /* elements between rows of out, >= N                           */
+    int32_t out_type;     /* moe_out_t                                                    */
+} moe_fp8_gemm_t;
+
+/*
+ * Grouped product: for the rows p of segment g, out[p][n] = sum_k A[p][k] B[g][n][k] over the
+ * values (codes times scales); a [rows][lda] with scales along the row, b [G][N][ldb] with
+ * weight block scales.  Products over a block accumulate in the tensor core's fp32, blocks are
+ * scaled and summed in fp32, one rounding to the output type.  Rows past offsets[G] are not
+ * written.  The data gradient is the same call on the transposed weights.
+ */
+moe_status_t moe_fp8_gemm(const moe_fp8_gemm_t *g, const void *a, const float *a_scales,
+                          const void *b, const float *b_scales, const int32_t *offsets_or_null,
+                          void *out, void *ws, void *stream);
+
+typedef struct {
+    int64_t rows;
+    int32_t G, M, N;
+    int32_t out_type;
+} moe_fp8_wgrad_t;
+
+/*
+ * Weight gradient: dW[g][m][n] = sum over the rows p of segment g of A[p][m] B[p][n], from
+ * along-token operands a [M][128 B] and b [N][128 B] with their scales (the same segments in
+ * both); zeros for an empty segment.  dW [G][M][N] dense, every element written.
+ */
+moe_status_t moe_fp8_wgrad(const moe_fp8_wgrad_t *g, const void *a, const float *a_scales,
+                           const void *b, const float *b_scales, const int32_t *offsets_or_null,
+                           void *dW, void *ws, void *stream);
+
+/*
  * Whole forward: route -> permute -> grouped FFN -> (shared expert) -> combine.
  *   logits [T,E] fp32, x [T,d], W1, W2 (W1s, W2s if ffn_shared > 0, else may be NULL)
  *   y [T,d] out.  ctx (moe_workspace_size bytes) receives the saved tensors listed in

@@ -25,6 +25,9 @@ __all__ = [
     "moe_mx_weights_size", "moe_mx_quantize_weights", "moe_mx_act_scales_size",
     "moe_mx_permute_quant", "moe_grouped_ffn_mx", "moe_grouped_ffn_bwd_mx", "moe_layer_fwd_mx",
     "moe_layer_bwd_mx",
+    "MoERouterC", "make_router", "moe_route_groups", "moe_route_groups_bwd", "moe_combine_bwd_dw",
+    "FP8_WS_BYTES", "moe_fp8_token_blocks", "moe_fp8_quantize", "moe_fp8_quantize_weights",
+    "moe_fp8_swiglu", "moe_fp8_swiglu_bwd", "moe_fp8_gemm", "moe_fp8_wgrad", "Fp8MoELayer",
     "moe_status", "moe_status_string", "moe_selftest_wait_timeout", "moe_gemm_clock_trace",
     "moe_gemm_clock_read", "ctx_views", "MoELayer", "CTX_FIELDS",
 ]
@@ -44,6 +47,34 @@ class MoEConfigC(ctypes.Structure):
                 ("capacity", ctypes.c_int32), ("select_bias", ctypes.c_void_p),
                 ("drop_negative", ctypes.c_int32), ("recompute", ctypes.c_int32),
                 ("drop_by_score", ctypes.c_int32), ("mxfp8", ctypes.c_int32)]
+
+
+class MoERouterC(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("bias", ctypes.c_void_p)]
+
+
+class _QuantC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("src_rows", ctypes.c_int64), ("G", ctypes.c_int32),
+                ("C", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("pow2", ctypes.c_int32)]
+
+
+class _ActC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("G", ctypes.c_int32), ("f", ctypes.c_int32),
+                ("ld", ctypes.c_int64), ("pow2", ctypes.c_int32)]
+
+
+class _Fp8GemmC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("G", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldo", ctypes.c_int64), ("out_type", ctypes.c_int32)]
+
+
+class _Fp8WgradC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("G", ctypes.c_int32), ("M", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("out_type", ctypes.c_int32)]
 
 
 class MoEError(RuntimeError):
@@ -93,6 +124,16 @@ def lib() -> ctypes.CDLL:
             "moe_grouped_ffn_bwd_mx": ([cfgp] + [P] * 12, I32),
             "moe_layer_bwd_mx": ([cfgp] + [P] * 15, I32),
             "moe_layer_bwd": ([cfgp] + [P] * 16, I32),
+            "moe_route_groups": ([cfgp, ctypes.POINTER(MoERouterC)] + [P] * 12, I32),
+            "moe_route_groups_bwd": ([cfgp, ctypes.POINTER(MoERouterC)] + [P] * 6, I32),
+            "moe_combine_bwd_dw": ([cfgp] + [P] * 8, I32),
+            "moe_fp8_token_blocks": ([I64, I32], I64),
+            "moe_fp8_quantize": ([ctypes.POINTER(_QuantC)] + [P] * 9, I32),
+            "moe_fp8_quantize_weights": ([P, I32, I32, I32, P, I64, P, P, I64, P, I32, P], I32),
+            "moe_fp8_swiglu": ([ctypes.POINTER(_ActC)] + [P] * 8, I32),
+            "moe_fp8_swiglu_bwd": ([ctypes.POINTER(_ActC)] + [P] * 11, I32),
+            "moe_fp8_gemm": ([ctypes.POINTER(_Fp8GemmC)] + [P] * 8, I32),
+            "moe_fp8_wgrad": ([ctypes.POINTER(_Fp8WgradC)] + [P] * 8, I32),
             "moe_status": ([P, P, ctypes.POINTER(ctypes.c_int32)], I32),
             "moe_gemm_clock_trace": ([I32], I32),
             "moe_gemm_clock_read": ([ctypes.POINTER(ctypes.c_uint64)] * 3, I32),
@@ -340,6 +381,209 @@ def moe_gemm_clock_read():
     return c.value, n.value, k.value
 
 
+# ------------------------------------------------------------------- group-limited routing
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def make_router(score="softmax", groups=1, top_groups=None, group_top=1, renorm=True, bias=None):
+    """A router for moe_route_groups (see include/moe.h): score "softmax" or "sigmoid";
+    top_groups of `groups` groups stay (None: all); bias: a float32 device tensor [E] (kept
+    alive by the returned struct) or None."""
+    r = MoERouterC(SCORES[score] if isinstance(score, str) else int(score), int(groups),
+                   int(groups if top_groups is None else top_groups), int(group_top),
+                   int(renorm), _typed(bias, "float32", "bias"))
+    r._keep = bias
+    return r
+
+
+def _typed(t, dtype, name):
+    """_p for a buffer of one element type (a torch dtype's name)."""
+    if t is not None and not isinstance(t, int) and str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    return _p(t)
+
+
+def moe_route_groups(cfg, router, logits, topk_idx, topk_w, counts, kept, offsets, dest_row,
+                     src_tok, src_slot, drop_mask, ws, stream=None):
+    _check(lib().moe_route_groups(_cfg(cfg), _cfg(router), _typed(logits, "float32", "logits"),
+                                  _p(topk_idx), _p(topk_w), _p(counts), _p(kept), _p(offsets),
+                                  _p(dest_row), _p(src_tok), _p(src_slot), _p(drop_mask), _p(ws),
+                                  _s(stream)), "moe_route_groups")
+
+
+def moe_route_groups_bwd(cfg, router, logits, topk_idx, dw, dlogits, ws, stream=None):
+    _check(lib().moe_route_groups_bwd(_cfg(cfg), _cfg(router), _typed(logits, "float32", "logits"),
+                                      _p(topk_idx), _typed(dw, "float32", "dw"), _p(dlogits),
+                                      _p(ws), _s(stream)), "moe_route_groups_bwd")
+
+
+def moe_combine_bwd_dw(cfg, dy, yp, topk_w, dest_row, dyp, dw, ws, stream=None):
+    _check(lib().moe_combine_bwd_dw(_cfg(cfg), _p(dy), _p(yp), _p(topk_w), _p(dest_row), _p(dyp),
+                                    _typed(dw, "float32", "dw"), _p(ws), _s(stream)),
+           "moe_combine_bwd_dw")
+
+
+# ------------------------------------------------- 8-bit operands, a scale per block of 128
+FP8_WS_BYTES = 256
+
+
+def moe_fp8_token_blocks(rows, G) -> int:
+    """The number of 128-row blocks that `rows` rows in G segments can need."""
+    return lib().moe_fp8_token_blocks(int(rows), int(G))
+
+
+def _shape(name, t, shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+
+
+def _bytes(t, name):
+    if t is not None and t.element_size() != 1:
+        raise ValueError(f"{name}: expected 8-bit codes, got {t.dtype}")
+    return _p(t)
+
+
+def _groups(offsets):
+    return 1 if offsets is None else offsets.numel() - 1
+
+
+def _quant_outputs(rows, G, cols, codes, scales, codes_t, scales_t):
+    """Check what a quantiser writes; the distance of the codes' rows."""
+    ld = 0
+    if codes is not None:
+        ld = codes.shape[-1]
+        _shape("codes", codes, (rows, ld))
+        _shape("scales", scales, (rows, (cols + 127) // 128))
+    if codes_t is not None:
+        blocks = moe_fp8_token_blocks(rows, G)
+        _shape("codes_t", codes_t, (cols, 128 * blocks))
+        _shape("scales_t", scales_t, (blocks, cols))
+    return ld
+
+
+def moe_fp8_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, *, offsets=None,
+                     src_tok=None, pow2=False, ws, stream=None):
+    """Quantise rows of x (bf16, rows may be strided) along the row (codes, scales) and, or, along
+    the tokens of the segments (codes_t, scales_t); row p is x[src_tok[p]] when src_tok is
+    given."""
+    if x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda or str(x.dtype) != "torch.bfloat16":
+        raise ValueError("x: expected a CUDA bf16 matrix with adjacent columns")
+    G = _groups(offsets)
+    rows = x.shape[0] if src_tok is None else src_tok.numel()
+    ld = _quant_outputs(rows, G, x.shape[1], codes, scales, codes_t, scales_t)
+    ldx = x.stride(0) if x.shape[0] > 1 else x.shape[1]
+    q = _QuantC(rows, x.shape[0], G, x.shape[1], ldx, ld, int(pow2))
+    _check(lib().moe_fp8_quantize(ctypes.byref(q), x.data_ptr(), _typed(src_tok, "int32", "src_tok"),
+                                  _typed(offsets, "int32", "offsets"), _bytes(codes, "codes"),
+                                  _typed(scales, "float32", "scales"), _bytes(codes_t, "codes_t"),
+                                  _typed(scales_t, "float32", "scales_t"), _p(ws), _s(stream)),
+           "moe_fp8_quantize")
+
+
+def moe_fp8_quantize_weights(w, codes, scales, codes_t=None, scales_t=None, *, pow2=False,
+                             stream=None):
+    """Quantise weights w [G, N, K] (bf16) in 128 x 128 blocks, optionally transposed too."""
+    G, N, K = w.shape
+    _shape("codes", codes, (G, N, codes.shape[-1]))
+    _shape("scales", scales, (G, (N + 127) // 128, (K + 127) // 128))
+    if codes_t is not None:
+        _shape("codes_t", codes_t, (G, K, codes_t.shape[-1]))
+        _shape("scales_t", scales_t, (G, (K + 127) // 128, (N + 127) // 128))
+    _check(lib().moe_fp8_quantize_weights(_typed(w, "bfloat16", "w"), G, N, K,
+                                          _bytes(codes, "codes"), codes.shape[-1],
+                                          _typed(scales, "float32", "scales"),
+                                          _bytes(codes_t, "codes_t"),
+                                          0 if codes_t is None else codes_t.shape[-1],
+                                          _typed(scales_t, "float32", "scales_t"), int(pow2),
+                                          _s(stream)), "moe_fp8_quantize_weights")
+
+
+def moe_fp8_swiglu(ab, codes=None, scales=None, codes_t=None, scales_t=None, *, offsets=None,
+                   pow2=False, ws, stream=None):
+    """silu(a) * b of ab = [a | b] (bf16), quantised."""
+    rows, G, f = ab.shape[0], _groups(offsets), ab.shape[1] // 2
+    _shape("ab", ab, (rows, 2 * f))
+    ld = _quant_outputs(rows, G, f, codes, scales, codes_t, scales_t)
+    _check(lib().moe_fp8_swiglu(ctypes.byref(_ActC(rows, G, f, ld, int(pow2))),
+                                _typed(ab, "bfloat16", "ab"), _typed(offsets, "int32", "offsets"),
+                                _bytes(codes, "codes"), _typed(scales, "float32", "scales"),
+                                _bytes(codes_t, "codes_t"),
+                                _typed(scales_t, "float32", "scales_t"), _p(ws), _s(stream)),
+           "moe_fp8_swiglu")
+
+
+def moe_fp8_swiglu_bwd(dh, ab, codes, scales, codes_t=None, scales_t=None, h_codes_t=None,
+                       h_scales_t=None, *, offsets=None, pow2=False, ws, stream=None):
+    """[da | db] of the SwiGLU from dh (bf16), quantised; h_codes_t: also h along the tokens."""
+    rows, f = dh.shape
+    G = _groups(offsets)
+    _shape("ab", ab, (rows, 2 * f))
+    ld = _quant_outputs(rows, G, 2 * f, codes, scales, codes_t, scales_t)
+    if h_codes_t is not None:
+        _quant_outputs(rows, G, f, None, None, h_codes_t, h_scales_t)
+    _check(lib().moe_fp8_swiglu_bwd(ctypes.byref(_ActC(rows, G, f, ld, int(pow2))),
+                                    _typed(dh, "bfloat16", "dh"), _typed(ab, "bfloat16", "ab"),
+                                    _typed(offsets, "int32", "offsets"), _bytes(codes, "codes"),
+                                    _typed(scales, "float32", "scales"),
+                                    _bytes(codes_t, "codes_t"),
+                                    _typed(scales_t, "float32", "scales_t"),
+                                    _bytes(h_codes_t, "h_codes_t"),
+                                    _typed(h_scales_t, "float32", "h_scales_t"), _p(ws),
+                                    _s(stream)), "moe_fp8_swiglu_bwd")
+
+
+OUT_TYPES = {"torch.bfloat16": 0, "torch.float32": 1}
+
+
+def _out_type(t, name):
+    if str(t.dtype) not in OUT_TYPES:
+        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return OUT_TYPES[str(t.dtype)]
+
+
+def moe_fp8_gemm(a, a_scales, b, b_scales, out, K, *, offsets=None, ws, stream=None):
+    """out[p] = A[p] B[g]^T for the rows p of each segment g, over K columns of the codes a
+    [rows, lda] and b [G, N, ldb]; out (bf16 or fp32) may have strided rows."""
+    rows, G, N = a.shape[0], _groups(offsets), b.shape[1]
+    _shape("a_scales", a_scales, (rows, (K + 127) // 128))
+    _shape("b", b, (G, N, b.shape[2]))
+    _shape("b_scales", b_scales, (G, (N + 127) // 128, (K + 127) // 128))
+    _shape("out", out, (rows, N))
+    if out.stride(1) != 1 and N > 1 or not out.is_cuda:
+        raise ValueError("out: expected a CUDA matrix with adjacent columns")
+    ldo = out.stride(0) if rows > 1 else N
+    g = _Fp8GemmC(rows, G, N, int(K), a.shape[1], b.shape[2], ldo, _out_type(out, "out"))
+    _check(lib().moe_fp8_gemm(ctypes.byref(g), _bytes(a, "a"),
+                              _typed(a_scales, "float32", "a_scales"), _bytes(b, "b"),
+                              _typed(b_scales, "float32", "b_scales"),
+                              _typed(offsets, "int32", "offsets"), out.data_ptr(), _p(ws),
+                              _s(stream)), "moe_fp8_gemm")
+
+
+def moe_fp8_wgrad(a, a_scales, b, b_scales, dw, *, offsets=None, rows=None, ws, stream=None):
+    """dw[g] = A_g^T B_g over the rows of each segment, from along-token operands a [M, 128 B] and
+    b [N, 128 B] with scales [B, M] and [B, N].  `rows`: the row capacity the operands were made
+    for (default: the largest that gives the same B)."""
+    G, M, N = dw.shape
+    blocks = a_scales.shape[0]
+    if G != _groups(offsets):
+        raise ValueError(f"dw: expected {_groups(offsets)} gradients, got {G}")
+    if rows is None:
+        rows = 128 * (blocks - G)
+    if moe_fp8_token_blocks(rows, G) != blocks:
+        raise ValueError(f"a_scales: {blocks} token blocks do not fit {rows} rows in {G} segments")
+    _shape("a", a, (M, 128 * blocks))
+    _shape("a_scales", a_scales, (blocks, M))
+    _shape("b", b, (N, 128 * blocks))
+    _shape("b_scales", b_scales, (blocks, N))
+    g = _Fp8WgradC(rows, G, M, N, _out_type(dw, "dw"))
+    _check(lib().moe_fp8_wgrad(ctypes.byref(g), _bytes(a, "a"),
+                               _typed(a_scales, "float32", "a_scales"), _bytes(b, "b"),
+                               _typed(b_scales, "float32", "b_scales"),
+                               _typed(offsets, "int32", "offsets"), _p(dw), _p(ws), _s(stream)),
+           "moe_fp8_wgrad")
+
+
 def moe_status(ws, stream=None):
     """Synchronise the stream and read + clear the device error word: (status, flags)."""
     flags = ctypes.c_int32(0)
@@ -449,6 +693,103 @@ class MoELayer:
         moe_layer_bwd(self.cfg, self.ctx, logits, x, dy, W1, W2, W1s, W2s, out["dx"], out["dW1"],
                       out["dW2"], out.get("dW1s"), out.get("dW2s"), out["dlogits"], self.ws,
                       stream)
+        return out
+
+    def status(self, stream=None):
+        return moe_status(self.ws, stream)
+
+
+class Fp8MoELayer:
+    """A layer whose router limits the choice to groups of experts and whose routed experts run
+    on 8-bit operands with a scale per block of 128, forward and backward.  Owns its buffers;
+    the weights are quantised once per update (quantize_weights) and passed to every call.
+
+        layer = Fp8MoELayer(cfg, make_router("sigmoid", groups=8, top_groups=4, group_top=2))
+        w = layer.quantize_weights(W1, W2)
+        y = layer.forward(logits, x, w)
+        g = layer.backward(logits, x, dy, w)      # dx, dW1, dW2, dlogits
+    """
+
+    def __init__(self, cfg: MoEConfigC, router: MoERouterC, device="cuda", grad_dtype=None):
+        import torch
+        if cfg.ffn_shared:
+            raise ValueError("Fp8MoELayer has no shared expert")
+        self.cfg, self.router, self.device = cfg, router, device
+        self.grad_dtype = torch.bfloat16 if grad_dtype is None else grad_dtype
+        T, k, E, d, f = cfg.T, cfg.k, cfg.E, cfg.d, cfg.ffn
+        R = T * k
+        B = moe_fp8_token_blocks(R, E)
+        self.ws = torch.empty(moe_workspace_size(cfg)[0], dtype=torch.uint8, device=device)
+        moe_ws_init(self.ws)
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+        i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
+        e4 = torch.float8_e4m3fn
+        blk = lambda n: (n + 127) // 128  # noqa: E731
+        self.r = {"topk_idx": new((T, k), i32), "topk_w": new((T, k), f32),
+                  "counts": new((E,), i32), "kept": new((E,), i32), "offsets": new((E + 1,), i32),
+                  "dest_row": new((T, k), i32), "src_tok": new((R,), i32),
+                  "src_slot": new((R,), i32), "drop_mask": new((T, k), torch.uint8)}
+        self.ab, self.yp = new((R, 2 * f), bf), new((R, d), bf)
+        # along the row: the operands of the products; along the tokens: of the weight gradients
+        self.q = {n: (new((R, c), e4), new((R, blk(c)), f32))
+                  for n, c in (("x", d), ("h", f), ("dy", d), ("dab", 2 * f))}
+        self.qt = {n: (new((c, 128 * B), e4), new((B, c), f32))
+                   for n, c in (("x", d), ("h", f), ("dy", d), ("dab", 2 * f))}
+        self.dyp, self.dh, self.dxp = new((R, d), bf), new((R, f), bf), new((R, d), bf)
+        self.dw = new((T, k), f32)
+
+    def quantize_weights(self, W1, W2, stream=None):
+        """W1 [E, 2f, d], W2 [E, d, f] (bf16) -> what forward and backward read."""
+        import torch
+        out = {}
+        for name, w in (("W1", W1), ("W2", W2)):
+            G, N, K = w.shape
+            new = lambda shape, dt: torch.empty(shape, dtype=dt, device=w.device)  # noqa: E731
+            blk = lambda n: (n + 127) // 128  # noqa: E731
+            t = (new((G, N, K), torch.float8_e4m3fn), new((G, blk(N), blk(K)), torch.float32),
+                 new((G, K, N), torch.float8_e4m3fn), new((G, blk(K), blk(N)), torch.float32))
+            moe_fp8_quantize_weights(w, *t, stream=stream)
+            out[name], out[name + "_t"] = t[:2], t[2:]
+        return out
+
+    def forward(self, logits, x, w, y=None, stream=None):
+        import torch
+        c, r, ws = self.cfg, self.r, self.ws
+        if y is None:
+            y = torch.empty_like(x)
+        moe_route_groups(c, self.router, logits, *r.values(), ws, stream)
+        seg = dict(offsets=r["offsets"], ws=ws, stream=stream)
+        moe_fp8_quantize(x, *self.q["x"], src_tok=r["src_tok"], **seg)
+        moe_fp8_gemm(*self.q["x"], *w["W1"], self.ab, c.d, **seg)
+        moe_fp8_swiglu(self.ab, *self.q["h"], **seg)
+        moe_fp8_gemm(*self.q["h"], *w["W2"], self.yp, c.ffn, **seg)
+        moe_combine(c, self.yp, r["dest_row"], r["topk_w"], None, y, ws, stream)
+        return y
+
+    def backward(self, logits, x, dy, w, out=None, stream=None):
+        """After forward() on the same logits, x and w."""
+        import torch
+        c, r, ws = self.cfg, self.r, self.ws
+        R = c.T * c.k
+        if out is None:
+            out = {"dx": torch.empty_like(x), "dlogits": torch.empty_like(logits),
+                   "dW1": torch.empty((c.E, 2 * c.ffn, c.d), dtype=self.grad_dtype,
+                                      device=x.device),
+                   "dW2": torch.empty((c.E, c.d, c.ffn), dtype=self.grad_dtype, device=x.device)}
+        seg = dict(offsets=r["offsets"], ws=ws, stream=stream)
+        moe_combine_bwd_dw(c, dy, self.yp, r["topk_w"], r["dest_row"], self.dyp, self.dw, ws,
+                           stream)
+        moe_route_groups_bwd(c, self.router, logits, r["topk_idx"], self.dw, out["dlogits"], ws,
+                             stream)
+        moe_fp8_quantize(self.dyp, *self.q["dy"], *self.qt["dy"], **seg)
+        moe_fp8_gemm(*self.q["dy"], *w["W2_t"], self.dh, c.d, **seg)
+        moe_fp8_swiglu_bwd(self.dh, self.ab, *self.q["dab"], *self.qt["dab"], *self.qt["h"], **seg)
+        moe_fp8_wgrad(*self.qt["dy"], *self.qt["h"], out["dW2"], rows=R, **seg)
+        moe_fp8_gemm(*self.q["dab"], *w["W1_t"], self.dxp, 2 * c.ffn, **seg)
+        moe_unpermute_reduce(c, self.dxp, r["dest_row"], None, out["dx"], ws, stream)
+        moe_fp8_quantize(x, codes_t=self.qt["x"][0], scales_t=self.qt["x"][1],
+                         src_tok=r["src_tok"], **seg)
+        moe_fp8_wgrad(*self.qt["dab"], *self.qt["x"], out["dW1"], rows=R, **seg)
         return out
 
     def status(self, stream=None):

@@ -160,14 +160,17 @@ combine_kernel(const uint4* __restrict__ rows, const int32_t* __restrict__ dest_
 
 // One warp per token: dyp[p_j] = w_j dy[t]; dw_j = <dy[t], yp[p_j]> (warp reduction);
 // dlogits from dw for the softmax or the sigmoid gate.  Batches of B vectors per lane with
-// all (1 + KMAX) * B loads issued first.
-template <int KMAX>
+// all (1 + KMAX) * B loads issued first.  DW: the weights' gradients dw [T,k] are the output
+// (0 for a dropped slot) and the gate is left to its own kernel; logits, topk_idx and E are
+// not read.
+template <int KMAX, bool DW>
 __global__ void __launch_bounds__(THREADS)
 combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ yp,
                    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
                    const float* __restrict__ topk_w, const int32_t* __restrict__ dest_row,
                    int64_t T, int E, int k, int nvec, int gate, float scale, int64_t rows_cap,
-                   uint4* __restrict__ dyp, float* __restrict__ dlogits, int* err) {
+                   uint4* __restrict__ dyp, float* __restrict__ dlogits, int* err,
+                   float* __restrict__ dw) {
   griddep_wait();   // see common.cuh: dependent launches
   constexpr int B = KMAX >= 6 ? 2 : 16 / (KMAX + 2);
   const int lane = threadIdx.x & 31;
@@ -178,7 +181,7 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ yp,
     float wt[KMAX];
     load_slots<KMAX>(dest_row, topk_w, t, k, rows_cap, err, p, wt);
     int my_e = -1;
-    if (lane < k) {
+    if (!DW && lane < k) {
       my_e = __ldg(topk_idx + t * k + lane);
       if (my_e < 0 || my_e >= E) {
         flag_error(err, MOE_DEVERR_BAD_INDEX);
@@ -226,6 +229,14 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint4* __restrict__ yp,
     }
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) dot[j] = warp_sum(dot[j]);
+    if (DW) {
+      float mine = 0.0f;
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j)
+        if (j == lane) mine = dot[j];
+      if (lane < k) dw[t * k + lane] = mine;
+      continue;
+    }
     // Both gates normalise over the k selected experts, so the gradient of slot j is
     // proportional to dot_j - sum_i u_i dot_i with sum_i u_i = 1 (u: the normalised
     // scores).  It is summed pairwise, sum_i u_i (dot_j - dot_i): when one score carries
@@ -311,15 +322,33 @@ cudaError_t launch_combine_bwd(const void* dy, const void* yp, const float* logi
                                float* dlogits, int* err, cudaStream_t st) {
   const int grid = grid_warps(T);
 #define MOE_COMBINE_BWD(KM)                                                                   \
-  launch_pdl(combine_bwd_kernel<KM>, dim3(grid), dim3(THREADS), 0, st, 1,                     \
+  launch_pdl(combine_bwd_kernel<KM, false>, dim3(grid), dim3(THREADS), 0, st, 1,                     \
              static_cast<const uint4*>(dy), static_cast<const uint4*>(yp), logits, topk_idx,   \
              topk_w, dest_row, T, E, k, d / 8, gate, scale, rows_cap,                          \
-             static_cast<uint4*>(dyp), dlogits, err)
+             static_cast<uint4*>(dyp), dlogits, err, static_cast<float*>(nullptr))
   if (k <= 2) return MOE_COMBINE_BWD(2);
   if (k <= 4) return MOE_COMBINE_BWD(4);
   if (k <= 6) return MOE_COMBINE_BWD(6);
   return MOE_COMBINE_BWD(8);
 #undef MOE_COMBINE_BWD
+}
+
+cudaError_t launch_combine_bwd_dw(const void* dy, const void* yp, const float* topk_w,
+                                  const int32_t* dest_row, int64_t T, int k, int d,
+                                  int64_t rows_cap, void* dyp, float* dw, int* err,
+                                  cudaStream_t st) {
+  const int grid = grid_warps(T);
+#define MOE_COMBINE_DW(KM)                                                                    \
+  launch_pdl(combine_bwd_kernel<KM, true>, dim3(grid), dim3(THREADS), 0, st, 1,               \
+             static_cast<const uint4*>(dy), static_cast<const uint4*>(yp),                     \
+             static_cast<const float*>(nullptr), static_cast<const int32_t*>(nullptr), topk_w, \
+             dest_row, T, 0, k, d / 8, 0, 1.0f, rows_cap, static_cast<uint4*>(dyp),            \
+             static_cast<float*>(nullptr), err, dw)
+  if (k <= 2) return MOE_COMBINE_DW(2);
+  if (k <= 4) return MOE_COMBINE_DW(4);
+  if (k <= 6) return MOE_COMBINE_DW(6);
+  return MOE_COMBINE_DW(8);
+#undef MOE_COMBINE_DW
 }
 
 }  // namespace moe

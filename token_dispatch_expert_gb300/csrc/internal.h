@@ -46,6 +46,23 @@ cudaError_t launch_route(const moe_config_t* c, const float* logits, int32_t* to
                          int32_t* dest_row, int32_t* src_tok, int32_t* src_slot,
                          uint8_t* drop_mask, void* scratch, int* err, cudaStream_t st);
 
+// F2 from the chosen experts: chunk_cnt [E][route_chunks(T)] holds each chunk's count of every
+// expert, dest_row each slot's rank inside its chunk (-1: not routed); token-order capacity.
+cudaError_t launch_route_order(int64_t T, int E, int k, int cap, const int32_t* topk_idx,
+                               int32_t* chunk_cnt, int32_t* counts, int32_t* kept,
+                               int32_t* offsets, int32_t* dest_row, int32_t* src_tok,
+                               int32_t* src_slot, uint8_t* drop_mask, cudaStream_t st);
+
+// Group-limited routing (router.cu) and the gradient of its weights; scratch as launch_route.
+cudaError_t launch_route_groups(const moe_config_t* c, const moe_router_t* r, const float* logits,
+                                int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* kept,
+                                int32_t* offsets, int32_t* dest_row, int32_t* src_tok,
+                                int32_t* src_slot, uint8_t* drop_mask, void* scratch, int* err,
+                                cudaStream_t st);
+cudaError_t launch_route_groups_bwd(const moe_config_t* c, const moe_router_t* r,
+                                    const float* logits, const int32_t* topk_idx, const float* dw,
+                                    float* dlogits, int* err, cudaStream_t st);
+
 cudaError_t launch_permute(const void* x, const int32_t* src_tok, const int32_t* offsets,
                            int E, int64_t T, int64_t rows_cap, int d, void* xp, int* err,
                            cudaStream_t st);
@@ -60,6 +77,12 @@ cudaError_t launch_combine_bwd(const void* dy, const void* yp, const float* logi
                                const int32_t* dest_row, int64_t T, int E, int k, int d,
                                int gate, float scale, int64_t rows_cap, void* dyp,
                                float* dlogits, int* err, cudaStream_t st);
+
+// dyp[p] = w dy[t] and dw[t,j] = <dy[t], yp[p]> (0 for a dropped slot)
+cudaError_t launch_combine_bwd_dw(const void* dy, const void* yp, const float* topk_w,
+                                  const int32_t* dest_row, int64_t T, int k, int d,
+                                  int64_t rows_cap, void* dyp, float* dw, int* err,
+                                  cudaStream_t st);
 
 // ----------------------------------------------------------------- grouped GEMM
 enum GemmMode : int {
@@ -212,5 +235,58 @@ cudaError_t gemm_clock_trace_set(bool on);
 cudaError_t gemm_clock_trace_add(unsigned long long out[3]);
 cudaError_t mx_clock_trace_set(bool on);
 cudaError_t mx_clock_trace_add(unsigned long long out[3]);
+
+// ----------------------------------------------------------------- blocks of 128 (fp8.cu)
+// 128-row blocks that the segments of `rows` rows in G groups can need: the extent of the
+// along-token operands.
+inline int64_t fp8_token_blocks(int64_t rows, int G) { return (rows + 127) / 128 + G; }
+
+enum { FP8_SRC_ROWS, FP8_SRC_SWIGLU, FP8_SRC_SWIGLU_BWD };
+
+struct Fp8QuantArgs {
+  int src;
+  const void* x;            // FP8_SRC_ROWS: [src_rows][ldx] bf16; SwiGLU: ab [rows][2f]
+  const void* dh;           // SwiGLU backward: [rows][f]
+  int64_t ldx, src_rows;
+  const int32_t* src_tok;   // FP8_SRC_ROWS: row p is x[src_tok[p]], or null
+  int C, f;
+  int64_t rows;
+  const int32_t* offsets;   // [G + 1], or null with G = 1
+  int G;
+  void* codes;              // [rows][ld] and scales [rows][ceil(cols / 128)], or null
+  float* scales;
+  int64_t ld;
+  void* codes_t;            // [cols][128 blocks] and scales_t [blocks][cols], or null
+  float* scales_t;
+  void* h_codes_t;          // SwiGLU backward: those of h, or null
+  float* h_scales_t;
+  int pow2;
+  int* err;
+};
+cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, cudaStream_t st);
+
+cudaError_t launch_fp8_weights(const void* W, int G, int N, int K, void* codes, int64_t ld,
+                               float* scales, void* codes_t, int64_t ld_t, float* scales_t,
+                               int pow2, cudaStream_t st);
+
+// out[p][n] = sum_k a[p][k] b[g][n][k] over the codes' values (fp8_gemm.cu).  wgrad: dW[g] = sum
+// over group g's token blocks, a [M][128 blocks], b [N][128 blocks].
+struct Fp8GemmArgs {
+  bool wgrad;
+  int64_t rows;
+  int G, N, K;              // wgrad: K is M, the rows of dW
+  const void* a;
+  const float* a_scales;
+  int64_t lda;
+  const void* b;
+  const float* b_scales;
+  int64_t ldb;
+  const int32_t* offsets;   // or null with G = 1
+  void* out;
+  int64_t ldo;
+  bool out_fp32;
+  int* err;
+};
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
 
 }  // namespace moe

@@ -261,6 +261,56 @@ __global__ void selftest_wait_kernel(int* err, long long budget) {
   if (threadIdx.x == 0) mbar_wait_bounded(smem_u32(&bar), 0, &abort_flag, err, budget);
 }
 
+// ----------------------------------------------------------------- routers and 8-bit operands
+moe_status_t validate_router(const moe_config_t* c, const moe_router_t* r) {
+  const moe_status_t s = validate(c);
+  if (s != MOE_OK) return s;
+  if (!r || c->select_bias || c->drop_negative || c->drop_by_score) return MOE_ERR_INVALID_ARG;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (r->groups < 1 || c->E % r->groups || r->top_groups < 1 || r->top_groups > r->groups ||
+      (r->group_top != 1 && r->group_top != 2) || (r->renorm != 0 && r->renorm != 1))
+    return MOE_ERR_INVALID_ARG;
+  const int per = c->E / r->groups;
+  if (r->top_groups * per < c->k || (r->groups > 1 && r->group_top > per))
+    return MOE_ERR_INVALID_ARG;
+  if (r->bias && (reinterpret_cast<uintptr_t>(r->bias) & 3u)) return MOE_ERR_INVALID_ARG;
+  return r->groups > 32 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+constexpr int32_t FP8_MAX_DIM = 1 << 24;
+constexpr int64_t FP8_MAX_ROWS = (int64_t(1) << 31) - (1 << 15);
+
+moe_status_t validate_segments(int64_t rows, int32_t G, const int32_t* offsets) {
+  if (rows < 0 || G < 1 || (!offsets && G != 1)) return MOE_ERR_INVALID_ARG;
+  if (offsets && !aligned16(offsets)) return MOE_ERR_INVALID_ARG;
+  return (rows >= FP8_MAX_ROWS || G > 256) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+moe_status_t validate_dim(int64_t n) {
+  if (n < 1) return MOE_ERR_INVALID_ARG;
+  return n >= FP8_MAX_DIM ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+bool ld_ok(int64_t ld, int64_t n) { return ld >= n && ld % 16 == 0; }
+// codes and their scales: both given, or (optional) neither
+bool pair_ok(const void* codes, const void* scales, bool optional) {
+  return (optional && !codes && !scales) || ptrs_ok(codes, scales);
+}
+
+// What every quantiser checks of its outputs; `cols` columns.
+moe_status_t validate_quant_out(int64_t rows, int32_t G, const int32_t* offsets, int64_t cols,
+                                int64_t ld, int32_t pow2, const void* codes, const void* scales,
+                                const void* codes_t, const void* scales_t, const void* ws) {
+  moe_status_t s = validate_segments(rows, G, offsets);
+  if (s == MOE_OK) s = validate_dim(cols);
+  if (s != MOE_OK) return s;
+  if (pow2 != 0 && pow2 != 1) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;   // empty buffers may have no address
+  if (!pair_ok(codes, scales, true) ||
+      !pair_ok(codes_t, scales_t, true) || (!codes && !codes_t) || !ptrs_ok(ws) ||
+      (codes && !ld_ok(ld, cols)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -854,6 +904,224 @@ const char* moe_status_string(moe_status_t s) {
     case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT";
   }
   return "MOE_ERR_UNKNOWN";
+}
+
+moe_status_t moe_route_groups(const moe_config_t* cfg, const moe_router_t* router,
+                              const float* logits, int32_t* topk_idx, float* topk_w,
+                              int32_t* counts, int32_t* kept, int32_t* offsets, int32_t* dest_row,
+                              int32_t* src_tok, int32_t* src_slot, uint8_t* drop_mask, void* ws,
+                              void* stream) {
+  moe_status_t s = validate_router(cfg, router);
+  if (s != MOE_OK) return s;
+  if (!ptrs_ok(logits, topk_idx, topk_w, counts, kept, offsets, dest_row, src_tok, src_slot,
+               drop_mask, ws))
+    return MOE_ERR_INVALID_ARG;
+  const WsLayout W = ws_layout(cfg);
+  return cuda_status(launch_route_groups(cfg, router, logits, topk_idx, topk_w, counts, kept,
+                                         offsets, dest_row, src_tok, src_slot, drop_mask,
+                                         at<uint8_t>(ws, W.route), static_cast<int*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_route_groups_bwd(const moe_config_t* cfg, const moe_router_t* router,
+                                  const float* logits, const int32_t* topk_idx, const float* dw,
+                                  float* dlogits, void* ws, void* stream) {
+  moe_status_t s = validate_router(cfg, router);
+  if (s != MOE_OK) return s;
+  if (!ptrs_ok(logits, topk_idx, dw, dlogits, ws)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_route_groups_bwd(cfg, router, logits, topk_idx, dw, dlogits,
+                                             static_cast<int*>(ws),
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_combine_bwd_dw(const moe_config_t* cfg, const void* dy, const void* yp,
+                                const float* topk_w, const int32_t* dest_row, void* dyp, float* dw,
+                                void* ws, void* stream) {
+  moe_status_t s = validate(cfg);
+  if (s != MOE_OK) return s;
+  if (!ptrs_ok(dy, yp, topk_w, dest_row, dyp, dw, ws)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_combine_bwd_dw(dy, yp, topk_w, dest_row, cfg->T, cfg->k, cfg->d,
+                                           cfg->T * cfg->k, dyp, dw, static_cast<int*>(ws),
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_fp8_token_blocks(int64_t rows, int32_t G) {
+  return rows < 0 || G < 1 ? -1 : fp8_token_blocks(rows, G);
+}
+
+moe_status_t moe_fp8_quantize(const moe_fp8_quant_t* q, const void* x, const int32_t* src_tok,
+                              const int32_t* offsets, void* codes, float* scales, void* codes_t,
+                              float* scales_t, void* ws, void* stream) {
+  if (!q) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = validate_quant_out(q->rows, q->G, offsets, q->C, q->ld, q->pow2, codes, scales,
+                                      codes_t, scales_t, ws);
+  if (s != MOE_OK) return s;
+  if (q->rows == 0) return MOE_OK;
+  // x: any bf16 address and row distance (rows that start off 16 bytes are read by the element)
+  if (!x || (reinterpret_cast<uintptr_t>(x) & 1u) || q->ldx < q->C ||
+      (src_tok && (!aligned16(src_tok) || q->src_rows < 1)))
+    return MOE_ERR_INVALID_ARG;
+  Fp8QuantArgs a{};
+  a.src = FP8_SRC_ROWS;
+  a.x = x;
+  a.ldx = q->ldx;
+  a.src_rows = q->src_rows;
+  a.src_tok = src_tok;
+  a.C = q->C;
+  a.rows = q->rows;
+  a.offsets = offsets;
+  a.G = q->G;
+  a.codes = codes;
+  a.scales = scales;
+  a.ld = q->ld;
+  a.codes_t = codes_t;
+  a.scales_t = scales_t;
+  a.pow2 = q->pow2;
+  a.err = static_cast<int*>(ws);
+  return cuda_status(launch_fp8_quant(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_fp8_quantize_weights(const void* W, int32_t G, int32_t N, int32_t K, void* codes,
+                                      int64_t ld, float* scales, void* codes_t, int64_t ld_t,
+                                      float* scales_t, int32_t pow2, void* stream) {
+  if (G < 1 || (pow2 != 0 && pow2 != 1)) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = validate_dim(N);
+  if (s == MOE_OK) s = validate_dim(K);
+  if (s != MOE_OK) return s;
+  if (!W || (reinterpret_cast<uintptr_t>(W) & 1u) || !ptrs_ok(codes, scales) || !ld_ok(ld, K) ||
+      !pair_ok(codes_t, scales_t, true) || (codes_t && !ld_ok(ld_t, N)))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t blocks = ((N + 127) / 128) * static_cast<int64_t>((K + 127) / 128);
+  if (G > 256 || G * blocks >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return cuda_status(launch_fp8_weights(W, G, N, K, codes, ld, scales, codes_t, ld_t, scales_t,
+                                        pow2, static_cast<cudaStream_t>(stream)));
+}
+
+static Fp8QuantArgs act_args(int src, const moe_fp8_act_t* p, const void* dh, const void* ab,
+                             const int32_t* offsets, void* codes, float* scales, void* codes_t,
+                             float* scales_t, void* ws) {
+  Fp8QuantArgs a{};
+  a.src = src;
+  a.x = ab;
+  a.dh = dh;
+  a.f = p->f;
+  a.rows = p->rows;
+  a.offsets = offsets;
+  a.G = p->G;
+  a.codes = codes;
+  a.scales = scales;
+  a.ld = p->ld;
+  a.codes_t = codes_t;
+  a.scales_t = scales_t;
+  a.pow2 = p->pow2;
+  a.err = static_cast<int*>(ws);
+  return a;
+}
+
+moe_status_t moe_fp8_swiglu(const moe_fp8_act_t* p, const void* ab, const int32_t* offsets,
+                            void* codes, float* scales, void* codes_t, float* scales_t, void* ws,
+                            void* stream) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = validate_quant_out(p->rows, p->G, offsets, p->f, p->ld, p->pow2, codes, scales,
+                                      codes_t, scales_t, ws);
+  if (s != MOE_OK) return s;
+  if (p->rows == 0) return MOE_OK;
+  if (!ptrs_ok(ab)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_fp8_quant(act_args(FP8_SRC_SWIGLU, p, nullptr, ab, offsets, codes,
+                                               scales, codes_t, scales_t, ws),
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_fp8_swiglu_bwd(const moe_fp8_act_t* p, const void* dh, const void* ab,
+                                const int32_t* offsets, void* codes, float* scales, void* codes_t,
+                                float* scales_t, void* h_codes_t, float* h_scales_t, void* ws,
+                                void* stream) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = validate_dim(p->f);
+  if (s == MOE_OK)
+    s = validate_quant_out(p->rows, p->G, offsets, 2 * static_cast<int64_t>(p->f), p->ld, p->pow2,
+                           codes, scales, codes_t, scales_t, ws);
+  if (s != MOE_OK) return s;
+  if (p->rows == 0) return MOE_OK;
+  if (!ptrs_ok(dh, ab, codes) || !pair_ok(h_codes_t, h_scales_t, true) || (h_codes_t && !codes_t))
+    return MOE_ERR_INVALID_ARG;
+  Fp8QuantArgs a = act_args(FP8_SRC_SWIGLU_BWD, p, dh, ab, offsets, codes, scales, codes_t,
+                            scales_t, ws);
+  a.h_codes_t = h_codes_t;
+  a.h_scales_t = h_scales_t;
+  return cuda_status(launch_fp8_quant(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_fp8_gemm(const moe_fp8_gemm_t* g, const void* a, const float* a_scales,
+                          const void* b, const float* b_scales, const int32_t* offsets, void* out,
+                          void* ws, void* stream) {
+  if (!g) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = validate_segments(g->rows, g->G, offsets);
+  if (s == MOE_OK) s = validate_dim(g->N);
+  if (s == MOE_OK) s = validate_dim(g->K);
+  if (s != MOE_OK) return s;
+  const bool fp32 = g->out_type == MOE_OUT_FP32;
+  if ((!fp32 && g->out_type != MOE_OUT_BF16) || !ld_ok(g->lda, g->K) || !ld_ok(g->ldb, g->K) ||
+      g->ldo < g->N)
+    return MOE_ERR_INVALID_ARG;
+  if (g->rows == 0) return MOE_OK;
+  if (!ptrs_ok(a, a_scales, b, b_scales, ws) || !out ||
+      (reinterpret_cast<uintptr_t>(out) & (fp32 ? 3u : 1u)))
+    return MOE_ERR_INVALID_ARG;
+  // tile coordinates are 32-bit: every tile's first weight row
+  if (static_cast<int64_t>(g->G) * g->N >= FP8_MAX_ROWS) return MOE_ERR_UNSUPPORTED;
+  const int64_t tiles = (g->rows / 128 + g->G) * ((g->N + 127) / 128);
+  if (tiles >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  Fp8GemmArgs x{};
+  x.rows = g->rows;
+  x.G = g->G;
+  x.N = g->N;
+  x.K = g->K;
+  x.a = a;
+  x.a_scales = a_scales;
+  x.lda = g->lda;
+  x.b = b;
+  x.b_scales = b_scales;
+  x.ldb = g->ldb;
+  x.offsets = offsets;
+  x.out = out;
+  x.ldo = g->ldo;
+  x.out_fp32 = fp32;
+  x.err = static_cast<int*>(ws);
+  return cuda_status(launch_fp8_gemm(x, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_fp8_wgrad(const moe_fp8_wgrad_t* g, const void* a, const float* a_scales,
+                           const void* b, const float* b_scales, const int32_t* offsets, void* dW,
+                           void* ws, void* stream) {
+  if (!g) return MOE_ERR_INVALID_ARG;
+  moe_status_t s = validate_segments(g->rows, g->G, offsets);
+  if (s == MOE_OK) s = validate_dim(g->M);
+  if (s == MOE_OK) s = validate_dim(g->N);
+  if (s != MOE_OK) return s;
+  const bool fp32 = g->out_type == MOE_OUT_FP32;
+  if ((!fp32 && g->out_type != MOE_OUT_BF16) || !ptrs_ok(a, a_scales, b, b_scales, dW, ws))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t tiles = static_cast<int64_t>(g->G) * ((g->M + 127) / 128) * ((g->N + 127) / 128);
+  // 32-bit tile counts and positions along the tokens
+  if (tiles >= (int64_t(1) << 31) || 128 * fp8_token_blocks(g->rows, g->G) >= (int64_t(1) << 31))
+    return MOE_ERR_UNSUPPORTED;
+  Fp8GemmArgs x{};
+  x.wgrad = true;
+  x.rows = g->rows;
+  x.G = g->G;
+  x.N = g->N;
+  x.K = g->M;
+  x.a = a;
+  x.a_scales = a_scales;
+  x.b = b;
+  x.b_scales = b_scales;
+  x.offsets = offsets;
+  x.out = dW;
+  x.ldo = g->N;
+  x.out_fp32 = fp32;
+  x.err = static_cast<int*>(ws);
+  return cuda_status(launch_fp8_gemm(x, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
