@@ -8,17 +8,22 @@
 // K 32), accumulated in fp32 in TMEM; the outer sum runs in fp32 registers of the epilogue
 // warps, because a scale is any fp32 number and changes with every block.  So the accumulator
 // leaves TMEM once per block: two 256-column accumulators alternate, the MMA fills one while
-// eight epilogue warps read the other and add it, scaled, to 128 sums per thread (packed
-// fma.rn.f32x2).
+// sixteen epilogue warps read the other and add it, scaled, to 64 sums per thread (packed
+// fma.rn.f32x2).  Per 128 x 256 tile and block the MMA takes 512 cycles (8192 multiply-adds per
+// cycle and SM); each scheduler's four epilogue warps issue 4 x (32 multiply-adds, 2 TMEM loads,
+// about 15 others).  The scales of the next block are loaded while this one is added.
 //
-// Per 128 x 256 tile and block the MMA takes 512 cycles (8192 multiply-adds per cycle and SM);
-// the epilogue's 128 columns per warp are 64 packed multiply-adds (128 with per-column scales)
-// and 4 TMEM loads, two warps per scheduler.
+// Tiles are 256 x 256 on a CTA pair (cta_group::2, each CTA holding 128 rows of A and of B, which
+// halves the operand bytes per multiply-add) or 128 x 256 on one CTA, where a pair's second half
+// would mostly be padding.  A finished tile leaves through shared memory, one 32 x 128-byte box
+// per warp, by TMA stores that overlap the next tile; boxes that a segment's end cuts, and
+// outputs whose rows TMA cannot address, are copied row by row from the same box.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <cstddef>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -27,37 +32,49 @@ namespace moe {
 namespace {
 
 constexpr int FG_BK = 128;
-constexpr int FG_TILE_M = 128;
 constexpr int FG_TILE_N = 256;
-// Warps 0 - 3: producer, MMA issuer, two idle; warps 4 - 11: epilogue.  Launched with 168
-// registers a thread (64,512 in all); the first four warps hand theirs to the other eight,
-// whose 128 sums and 32 loaded columns need more: 128 * 40 + 256 * 232 = 64,512.
-constexpr int FG_THREADS = 384;
+// Warps 0 - 3: producer, MMA issuer, two idle; warps 4 - 19: epilogue.  Launched with 96
+// registers a thread (61,440 in all); the first four warps hand theirs to the others:
+// 128 * 32 + 512 * 112 = 61,440.
+constexpr int FG_THREADS = 640;
 constexpr int FG_EPI_WARP0 = 4;
-constexpr int FG_EPI_WARPS = 8;
+constexpr int FG_EPI_WARPS = 16;
 constexpr int FG_MAX_G = 256;
-constexpr int FG_STAGES = 4;
-constexpr int FG_A_BYTES = FG_TILE_M * FG_BK;
-constexpr int FG_B_BYTES = FG_TILE_N * FG_BK;
-constexpr int FG_STAGE_BYTES = FG_A_BYTES + FG_B_BYTES;
 constexpr uint32_t FG_TMEM_COLS = 512;
+constexpr int FG_BOX_BYTES = 32 * 128;    // a warp's piece of a finished tile: 32 rows x 128 bytes
 constexpr long long FG_WAIT_BUDGET = 4000000000LL;
 
+template <int PAIR>
+struct FgGeo {
+  static constexpr int TILE_M = 128 * PAIR;
+  static constexpr int A_BYTES = 128 * FG_BK;
+  static constexpr int B_ROWS = FG_TILE_N / PAIR;       // this CTA's rows of b
+  static constexpr int B_BYTES = B_ROWS * FG_BK;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = PAIR == 2 ? 4 : 3;
+};
+
 struct FgCtl {
-  uint64_t full[FG_STAGES], empty[FG_STAGES], tfull[2], tempty[2], drain;
+  uint64_t full[4], empty[4], tfull[2], tempty[2], drain;
   uint32_t tmem_base;
   int abort, bad;
-  long long gstart[FG_MAX_G + 1];
+  int gstart[FG_MAX_G + 1];
   int tprefix[FG_MAX_G + 1];    // tiles before each group
   int kbpre[FG_MAX_G + 1];      // wgrad: token blocks before each group
-  alignas(16) float bscale[FG_EPI_WARPS][2][128];   // read as float4
+  alignas(16) float bscale[FG_EPI_WARPS][2][64];   // wgrad: column scales, read as float4
 };
 static_assert(offsetof(FgCtl, bscale) % 16 == 0, "read as float4");
-constexpr size_t FG_SMEM = FG_STAGES * FG_STAGE_BYTES + sizeof(FgCtl) + 1024;
+
+template <int PAIR>
+constexpr size_t fg_smem() {
+  return FgGeo<PAIR>::STAGES * FgGeo<PAIR>::STAGE_BYTES + FG_EPI_WARPS * FG_BOX_BYTES +
+         sizeof(FgCtl) + 1024;
+}
+static_assert(fg_smem<1>() <= 232448 && fg_smem<2>() <= 232448, "227 KB per CTA");
 
 struct FgParams {
   int G, N, K;                  // K: of the product; wgrad: M
-  long long rows;
+  int rows;
   int n_tiles, m_tiles;         // m_tiles: wgrad
   int kb;                       // product: blocks along K; wgrad: token block capacity
   int nb;                       // product: 128-row blocks of b per group
@@ -66,6 +83,7 @@ struct FgParams {
   const float* sb;
   void* out;
   long long ldo;
+  int tma_out;                  // the output map is usable
   int* err;
 };
 
@@ -84,6 +102,15 @@ __device__ __forceinline__ void fg_mma(uint32_t d_tmem, uint64_t a_desc, uint64_
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void fg_mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -126,76 +153,70 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-__device__ __forceinline__ int ceil_div(long long a, int b) {
-  return static_cast<int>((a + b - 1) / b);
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
 }
 
-// One row's 128 sums to its place; n0 is the first column, cols the row's width.
+// The first `nr` rows of a warp's box (32 rows x 128 bytes, 16-byte pieces XOR-swizzled by row) to
+// rows of `out` starting at element `off`, `nc` columns of them: 4 bytes per lane and row.
 template <bool F32>
-__device__ __forceinline__ void store_row(void* out, long long off, const uint64_t* acc, int n0,
-                                          int cols) {
-  if (n0 >= cols) return;
+__device__ __forceinline__ void copy_box(const uint8_t* box, void* out, long long off,
+                                         long long ldo, int nr, int nc, int lane) {
+  const uint8_t* src = box + (lane & 3) * 4;
+  const int piece = lane >> 2;
   if (F32) {
-    float* dst = static_cast<float*>(out) + off + n0;
-    if (n0 + 128 <= cols && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 a = unpack2(acc[2 * i]), b = unpack2(acc[2 * i + 1]);
-        reinterpret_cast<float4*>(dst)[i] = make_float4(a.x, a.y, b.x, b.y);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float2 a = unpack2(acc[i]);
-        if (n0 + 2 * i < cols) dst[2 * i] = a.x;
-        if (n0 + 2 * i + 1 < cols) dst[2 * i + 1] = a.y;
-      }
-    }
+    float* dst = static_cast<float*>(out) + off + lane;
+    for (int i = 0; i < nr; ++i)
+      if (lane < nc)
+        dst[i * ldo] = *reinterpret_cast<const float*>(src + i * 128 + ((piece ^ (i & 7)) << 4));
   } else {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + off + n0;
-    if (n0 + 128 <= cols && (reinterpret_cast<uintptr_t>(dst) & 15u) == 0) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 a = unpack2(acc[4 * i + j]);
-          w[j] = pack_bf16x2(a.x, a.y);
-        }
-        reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        const float2 a = unpack2(acc[i]);
-        if (n0 + 2 * i < cols) dst[2 * i] = __float2bfloat16_rn(a.x);
-        if (n0 + 2 * i + 1 < cols) dst[2 * i + 1] = __float2bfloat16_rn(a.y);
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + off + 2 * lane;
+    const bool two = 2 * lane + 1 < nc, one = 2 * lane < nc;
+    for (int i = 0; i < nr; ++i) {
+      const uint32_t w =
+          *reinterpret_cast<const uint32_t*>(src + i * 128 + ((piece ^ (i & 7)) << 4));
+      __nv_bfloat16* d = dst + i * ldo;
+      if (two && (reinterpret_cast<uintptr_t>(d) & 3u) == 0) {
+        *reinterpret_cast<uint32_t*>(d) = w;
+      } else {
+        if (one) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(w);
+        if (two) *reinterpret_cast<uint16_t*>(d + 1) = static_cast<uint16_t>(w >> 16);
       }
     }
   }
 }
 
-template <bool WG, bool F32>
+// tmC: the output as [groups][rows][columns] (product: one group), box 128 bytes x 32 x 1.
+template <bool WG, bool F32, int PAIR>
 __global__ void __launch_bounds__(FG_THREADS, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const FgParams p) {
+                const __grid_constant__ CUtensorMap tmC, const FgParams p) {
   griddep_wait();   // see common.cuh: dependent launches
+  using GE = FgGeo<PAIR>;
+  constexpr int STAGES = GE::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  FgCtl* ctl = reinterpret_cast<FgCtl*>(smem + FG_STAGES * FG_STAGE_BYTES);
+  uint8_t* boxes = smem + STAGES * GE::STAGE_BYTES;
+  FgCtl* ctl = reinterpret_cast<FgCtl*>(boxes + FG_EPI_WARPS * FG_BOX_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem);
   volatile int* abort_flag = &ctl->abort;
+  const int rank = PAIR == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / PAIR, num_units = gridDim.x / PAIR;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < FG_STAGES; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&ctl->tfull[b]), 1);
-      mbar_init(smem_u32(&ctl->tempty[b]), FG_EPI_WARPS);
+      mbar_init(smem_u32(&ctl->tempty[b]), FG_EPI_WARPS * PAIR);
     }
     mbar_init(smem_u32(&ctl->drain), 1);
     fence_mbar_init();
@@ -205,53 +226,66 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   if (threadIdx.x == 32) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmC);
   }
   for (int g = threadIdx.x; g <= p.G; g += FG_THREADS)
-    ctl->gstart[g] = p.offsets ? p.offsets[g] : (g ? p.rows : 0LL);
+    ctl->gstart[g] = p.offsets ? p.offsets[g] : (g ? p.rows : 0);
   __syncthreads();
   if (warp == 0) {
-    auto blocks_of = [&](long long a, long long b) { return b > a ? ceil_div(b - a, 128) : 0; };
     const int per = (p.G + 31) / 32;
+    auto tiles_of = [&](int a, int b) {
+      return WG ? p.m_tiles * p.n_tiles : b > a ? ceil_div(b - a, GE::TILE_M) * p.n_tiles : 0;
+    };
+    auto blocks_of = [&](int a, int b) { return b > a ? ceil_div(b - a, 128) : 0; };
     int local = 0, local_kb = 0, bad = 0;
     for (int i = 0; i < per; ++i) {
       const int g = lane * per + i;
       if (g < p.G) {
-        const long long a = ctl->gstart[g], b = ctl->gstart[g + 1];
+        const int a = ctl->gstart[g], b = ctl->gstart[g + 1];
         if (b < a || a < 0 || b > p.rows) bad = 1;
-        const int n = blocks_of(a, b);
-        local += WG ? p.m_tiles * p.n_tiles : n * p.n_tiles;
-        local_kb += n;
+        else {
+          local += tiles_of(a, b);
+          local_kb += blocks_of(a, b);
+        }
       }
     }
     const int incl = warp_incl_scan(local), incl_kb = warp_incl_scan(local_kb);
     int run = incl - local, run_kb = incl_kb - local_kb;
-    for (int i = 0; i < per; ++i) {
-      const int g = lane * per + i;
-      if (g < p.G) {
-        const int n = blocks_of(ctl->gstart[g], ctl->gstart[g + 1]);
-        ctl->tprefix[g] = run;
-        ctl->kbpre[g] = run_kb;
-        run += WG ? p.m_tiles * p.n_tiles : n * p.n_tiles;
-        run_kb += n;
+    if (ctl->gstart[0] != 0) bad = 1;
+    bad = __any_sync(FULL_MASK, bad);
+    if (!bad) {
+      for (int i = 0; i < per; ++i) {
+        const int g = lane * per + i;
+        if (g < p.G) {
+          const int a = ctl->gstart[g], b = ctl->gstart[g + 1];
+          ctl->tprefix[g] = run;
+          ctl->kbpre[g] = run_kb;
+          run += tiles_of(a, b);
+          run_kb += blocks_of(a, b);
+        }
       }
     }
     if (lane == 31) {
       ctl->tprefix[p.G] = incl;
       ctl->kbpre[p.G] = incl_kb;
     }
-    if (ctl->gstart[0] != 0) bad = 1;
-    bad = __any_sync(FULL_MASK, bad);
     if (lane == 0 && bad) {
       ctl->bad = 1;
       if (blockIdx.x == 0) flag_error(p.err, MOE_DEVERR_BAD_OFFSETS);
     }
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&ctl->tmem_base), FG_TMEM_COLS);
-    tmem_relinquish();
+    if (PAIR == 2) {
+      tmem_alloc_pair(smem_u32(&ctl->tmem_base), FG_TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(&ctl->tmem_base), FG_TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR == 2) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
   const int total = ctl->bad ? 0 : ctl->tprefix[p.G];
   const uint32_t tmem_base = ctl->tmem_base;
@@ -267,60 +301,68 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     }
     g = lo;
     const int local = tile - ctl->tprefix[g];
-    const int mtg = WG ? p.m_tiles : ceil_div(ctl->gstart[g + 1] - ctl->gstart[g], FG_TILE_M);
+    const int mtg =
+        WG ? p.m_tiles : ceil_div(ctl->gstart[g + 1] - ctl->gstart[g], GE::TILE_M);
     nt = local / mtg;
     mt = local - nt * mtg;
   };
   auto blocks = [&](int g) { return WG ? ctl->kbpre[g + 1] - ctl->kbpre[g] : p.kb; };
 
   if (warp < FG_EPI_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
     if (warp == 0) {
-      // ---------------------------------------------------------------- producer
+      // -------------------------------------------------------------- producer
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int tile = unit; tile < total && ok; tile += num_units) {
         int g, mt, nt;
         map_tile(tile, g, mt, nt);
         const int nkb = blocks(g);
-        const int x0 = WG ? ctl->kbpre[g] * FG_BK : 0;
-        const int arow = WG ? mt * FG_TILE_M : static_cast<int>(ctl->gstart[g]) + mt * FG_TILE_M;
-        const int brow = WG ? nt * FG_TILE_N : g * p.N + nt * FG_TILE_N;
-        for (int kb = 0; kb < nkb; ++kb) {
+        int x = WG ? ctl->kbpre[g] * FG_BK : 0;
+        const int arow = (WG ? 0 : ctl->gstart[g]) + mt * GE::TILE_M + 128 * rank;
+        const int brow = (WG ? 0 : g * p.N) + nt * FG_TILE_N + GE::B_ROWS * rank;
+        for (int kb = 0; kb < nkb; ++kb, x += FG_BK) {
           if (!fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
           if (lane == 0) {
-            const uint32_t sa = smem_base + s * FG_STAGE_BYTES;
+            const uint32_t sa = smem_base + s * GE::STAGE_BYTES;
             const uint32_t full = smem_u32(&ctl->full[s]);
-            mbar_arrive_expect_tx(full, FG_STAGE_BYTES);
-            tma_load_2d(sa, &tmA, full, x0 + kb * FG_BK, arow);
-            tma_load_2d(sa + FG_A_BYTES, &tmB, full, x0 + kb * FG_BK, brow);
+            // the leader's single arrive announces both CTAs' bytes
+            if (rank == 0) mbar_arrive_expect_tx(full, PAIR * GE::STAGE_BYTES);
+            if (PAIR == 2) {
+              const uint32_t lead = mapa_shared(full, 0);
+              tma_load_2d_pair(sa, &tmA, lead, x, arow);
+              tma_load_2d_pair(sa + GE::A_BYTES, &tmB, lead, x, brow);
+            } else {
+              tma_load_2d(sa, &tmA, full, x, arow);
+              tma_load_2d(sa + GE::A_BYTES, &tmB, full, x, brow);
+            }
           }
           __syncwarp();
-          if (++s == FG_STAGES) {
+          if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
       griddep_launch();
-      for (int i = 0; i < FG_STAGES && ok; ++i) {   // every copy of this CTA has been consumed
+      for (int i = 0; i < STAGES && ok; ++i) {   // every copy of this CTA has been consumed
         if (!fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err)) break;
-        if (++s == FG_STAGES) {
+        if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
         }
       }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------------- MMA issuer
+    } else if (warp == 1 && rank == 0) {
+      // -------------------------------------------------------------- MMA issuer (leader)
       int s = 0;
       uint32_t ph = 0;
       uint32_t it = 0;   // blocks issued: accumulator it & 1
       bool ok = true;
-      for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+      for (int tile = unit; tile < total && ok; tile += num_units) {
         int g, mt, nt;
         map_tile(tile, g, mt, nt);
         const int nkb = blocks(g);
@@ -333,25 +375,37 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           }
           tc_fence_after();
           if (lane == 0) {
-            const uint32_t sa = smem_base + s * FG_STAGE_BYTES;
-            const uint32_t sb = sa + FG_A_BYTES;
+            const uint32_t sa = smem_base + s * GE::STAGE_BYTES;
+            const uint32_t sb = sa + GE::A_BYTES;
 #pragma unroll
-            for (int kk = 0; kk < FG_BK / 32; ++kk)
-              fg_mma(tmem_base + buf * FG_TILE_N, make_smem_desc(sa + kk * 32, 16, 1024),
-                     make_smem_desc(sb + kk * 32, 16, 1024), fg_idesc(FG_TILE_M, FG_TILE_N),
-                     kk != 0 ? 1u : 0u);
-            tc_commit(smem_u32(&ctl->empty[s]));
-            tc_commit(smem_u32(&ctl->tfull[buf]));
+            for (int kk = 0; kk < FG_BK / 32; ++kk) {
+              const uint64_t da = make_smem_desc(sa + kk * 32, 16, 1024);
+              const uint64_t db = make_smem_desc(sb + kk * 32, 16, 1024);
+              if (PAIR == 2)
+                fg_mma_pair(tmem_base + buf * FG_TILE_N, da, db, fg_idesc(256, FG_TILE_N),
+                            kk != 0 ? 1u : 0u);
+              else
+                fg_mma(tmem_base + buf * FG_TILE_N, da, db, fg_idesc(128, FG_TILE_N),
+                       kk != 0 ? 1u : 0u);
+            }
+            if (PAIR == 2) {
+              tc_commit_pair_mc(smem_u32(&ctl->empty[s]), 0x3);
+              tc_commit_pair_mc(smem_u32(&ctl->tfull[buf]), 0x3);
+            } else {
+              tc_commit(smem_u32(&ctl->empty[s]));
+              tc_commit(smem_u32(&ctl->tfull[buf]));
+            }
           }
           __syncwarp();
-          if (++s == FG_STAGES) {
+          if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
       if (!ok && it > 0 && lane == 0) {   // gave up: wait (bounded) for the MMAs in flight
-        tc_commit(smem_u32(&ctl->drain));
+        if (PAIR == 2) tc_commit_pair(smem_u32(&ctl->drain));
+        else tc_commit(smem_u32(&ctl->drain));
         const long long t0 = clock64();
         while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < FG_WAIT_BUDGET / 4) {
         }
@@ -359,96 +413,156 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;" ::: "memory");
-    // ---------------------------------------------------------------- epilogue (8 warps)
-    const int q = warp & 3;               // the lane quarter this warp may read
-    const int hh = (warp - FG_EPI_WARP0) >> 2;       // which 128 of the 256 columns
-    const int r_in_tile = q * 32 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;" ::: "memory");
+    // ---------------------------------------------------------------- epilogue (16 warps)
+    const int q = warp & 3;                          // the lane quarter this warp may read
+    const int cg = (warp - FG_EPI_WARP0) >> 2;       // which 64 of the 256 columns
     float* bs = ctl->bscale[warp - FG_EPI_WARP0][0];
+    uint8_t* box = boxes + (warp - FG_EPI_WARP0) * FG_BOX_BYTES;
+    const uint32_t box_row = smem_u32(box) + lane * 128;
     uint32_t it = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < total && ok; tile += gridDim.x) {
+    for (int tile = unit; tile < total && ok; tile += num_units) {
       int g, mt, nt;
       map_tile(tile, g, mt, nt);
       const int nkb = blocks(g);
-      const int lrow = mt * FG_TILE_M + r_in_tile;
-      const long long row = WG ? lrow : ctl->gstart[g] + lrow;
-      const bool valid = WG ? lrow < p.K : row < ctl->gstart[g + 1];
-      const int n0 = nt * FG_TILE_N + 128 * hh;
-      // a row or a column block past the end takes the scales of the last one; its sums are
-      // not stored
+      const int lrow0 = mt * GE::TILE_M + 128 * rank + 32 * q;   // this warp's first row
+      const int rows_g = WG ? p.K : ctl->gstart[g + 1] - ctl->gstart[g];
+      const int nr = min(max(rows_g - lrow0, 0), 32);            // rows of it in the output
+      const int n0 = nt * FG_TILE_N + 64 * cg;
+      // a row or a column block past the end takes scales of one inside; its sums are not
+      // stored
       const float* sa;
       const float* sb;
       if (WG) {
-        sa = p.sa + static_cast<long long>(ctl->kbpre[g]) * p.K + (valid ? lrow : 0);
-        sb = p.sb + static_cast<long long>(ctl->kbpre[g]) * p.N + n0;
+        sa = p.sa + static_cast<long long>(ctl->kbpre[g]) * p.K + (lane < nr ? lrow0 + lane : 0);
+        sb = p.sb + static_cast<long long>(ctl->kbpre[g]) * p.N + n0 + lane;
       } else {
-        sa = p.sa + (valid ? row : 0) * p.kb;
-        const int blk = 2 * nt + hh < p.nb ? 2 * nt + hh : p.nb - 1;
-        sb = p.sb + (static_cast<long long>(g) * p.nb + blk) * p.kb;
+        sa = p.sa + static_cast<long long>(lane < nr ? ctl->gstart[g] + lrow0 + lane : 0) * p.kb;
+        sb = p.sb + (static_cast<long long>(g) * p.nb + min(n0 >> 7, p.nb - 1)) * p.kb;
       }
-      uint64_t acc[64];
+      const bool c0 = n0 + lane < p.N, c1 = n0 + 32 + lane < p.N;
+      auto load_scales = [&](float& s, float& f0, float& f1) {
+        if (WG) {
+          s = __ldg(sa);
+          f0 = c0 ? __ldg(sb) : 0.0f;
+          f1 = c1 ? __ldg(sb + 32) : 0.0f;
+          sa += p.K;
+          sb += p.N;
+        } else {
+          s = __ldg(sa++);
+          f0 = __ldg(sb++);
+        }
+      };
+      uint64_t acc[32];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      for (int i = 0; i < 32; ++i) acc[i] = 0ull;
+      float s_next = 0.0f, f0_next = 0.0f, f1_next = 0.0f;
+      if (nkb > 0) load_scales(s_next, f0_next, f1_next);
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t buf = it & 1u, use = it >> 1;
-        float s;
+        float s = s_next;
         if (WG) {
-          s = valid ? __ldg(sa + static_cast<long long>(kb) * p.K) : 0.0f;
-          float* mine = bs + buf * 128;   // alternates with the accumulator
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = lane + 32 * i;
-            mine[c] = n0 + c < p.N ? __ldg(sb + static_cast<long long>(kb) * p.N + c) : 0.0f;
-          }
+          float* mine = bs + buf * 64;   // alternates with the accumulator
+          mine[lane] = f0_next;
+          mine[lane + 32] = f1_next;
           __syncwarp();
         } else {
-          s = __ldg(sa + kb) * __ldg(sb + kb);
+          s *= f0_next;
         }
+        if (kb + 1 < nkb) load_scales(s_next, f0_next, f1_next);
         if (!fg_wait(smem_u32(&ctl->tfull[buf]), use & 1u, abort_flag, p.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t taddr =
-            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * FG_TILE_N + 128 * hh;
+            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * FG_TILE_N + 64 * cg;
         const uint64_t s2 = pack2(s, s);
+        // 32 columns at a time; 16 where the column scales take registers too
+        constexpr int W = WG ? 16 : 32;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t d[16];
-          tmem_ld16(taddr + 16 * c, d);
+        for (int c = 0; c < 64 / W; ++c) {
+          uint32_t d[W];
+          if (WG) tmem_ld16(taddr + W * c, d);
+          else tmem_ld32(taddr + W * c, d);
           tmem_ld_wait();
-          if (c == 7) {
+          if (c == 64 / W - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[buf]));
+            if (lane == 0) {   // the accumulator is free (the leader counts both CTAs' warps)
+              if (PAIR == 2) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->tempty[buf]), 0));
+              else mbar_arrive(smem_u32(&ctl->tempty[buf]));
+            }
           }
           if (WG) {
-            const float4* cs = reinterpret_cast<const float4*>(bs + buf * 128 + 16 * c);
+            const float4* cs = reinterpret_cast<const float4*>(bs + buf * 64 + W * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < W / 4; ++i) {
               const float4 f = cs[i];
-              acc[8 * c + 2 * i] = fma2(pack2(d[4 * i], d[4 * i + 1]), mul2(pack2(f.x, f.y), s2),
-                                        acc[8 * c + 2 * i]);
-              acc[8 * c + 2 * i + 1] = fma2(pack2(d[4 * i + 2], d[4 * i + 3]),
-                                            mul2(pack2(f.z, f.w), s2), acc[8 * c + 2 * i + 1]);
+              uint64_t* a = acc + W / 2 * c + 2 * i;
+              a[0] = fma2(pack2(d[4 * i], d[4 * i + 1]), mul2(pack2(f.x, f.y), s2), a[0]);
+              a[1] = fma2(pack2(d[4 * i + 2], d[4 * i + 3]), mul2(pack2(f.z, f.w), s2), a[1]);
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              acc[8 * c + i] = fma2(pack2(d[2 * i], d[2 * i + 1]), s2, acc[8 * c + i]);
+            for (int i = 0; i < W / 2; ++i)
+              acc[W / 2 * c + i] = fma2(pack2(d[2 * i], d[2 * i + 1]), s2, acc[W / 2 * c + i]);
           }
         }
       }
-      if (ok && valid)
-        store_row<F32>(p.out, (WG ? static_cast<long long>(g) * p.K + lrow : row) * p.ldo, acc, n0,
-                       p.N);
+      if (!ok || nr == 0 || n0 >= p.N) continue;
+      // through the box: bf16 in one go, fp32 in two halves of 32 columns
+      const bool by_tma = p.tma_out && (WG || nr == 32);
+#pragma unroll
+      for (int half = 0; half < (F32 ? 2 : 1); ++half) {
+        if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4 v;
+          if (F32) {
+            const float2 x = unpack2(acc[16 * half + 2 * j]), y = unpack2(acc[16 * half + 2 * j + 1]);
+            v = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
+                           __float_as_uint(y.y));
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = unpack2(acc[4 * j + i]);
+              w[i] = pack_bf16x2(x.x, x.y);
+            }
+            v = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          st_shared_v4(box_row + ((j ^ (lane & 7)) << 4), v);
+        }
+        const int n = n0 + 32 * half;
+        if (by_tma) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && n < p.N) {
+            tma_store_3d(&tmC, smem_u32(box), n, WG ? lrow0 : ctl->gstart[g] + lrow0, WG ? g : 0);
+            bulk_commit_group();
+          }
+        } else if (n < p.N) {
+          __syncwarp();
+          const long long row = WG ? static_cast<long long>(g) * p.K + lrow0 : ctl->gstart[g] + lrow0;
+          copy_box<F32>(box, p.out, row * p.ldo + n, p.ldo, nr, p.N - n, lane);
+          __syncwarp();
+        }
+      }
     }
+    if (lane == 0) bulk_wait_group_all();   // stores done before exit
+    __syncwarp();
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR == 2) cluster_sync_all();
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, FG_TMEM_COLS);
+  if (warp == 1) {
+    if (PAIR == 2) tmem_dealloc_pair(tmem_base, FG_TMEM_COLS);
+    else tmem_dealloc(tmem_base, FG_TMEM_COLS);
+  }
 }
 
 // ------------------------------------------------------------------ host side
@@ -481,18 +595,36 @@ bool fg_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint64
          CUDA_SUCCESS;
 }
 
-template <bool WG, bool F32>
-cudaError_t fg_launch(const CUtensorMap& ta, const CUtensorMap& tb, const FgParams& p,
-                      cudaStream_t st) {
-  auto kern = fp8_gemm_kernel<WG, F32>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(FG_SMEM));
+// The output [groups][rows][cols] with rows `ld` elements apart, 128-byte swizzle, box 128 bytes
+// x 32 rows x 1 group: a store never crosses into the next group's rows.  False where TMA
+// cannot address it (a base or a row off 16 bytes).
+bool fg_out_map(CUtensorMap* m, const void* base, bool fp32, uint64_t cols, uint64_t ld,
+                uint64_t rows, uint64_t groups) {
+  auto enc = fg_encode_fn();
+  const uint64_t size = fp32 ? 4 : 2;
+  if (!enc || (reinterpret_cast<uintptr_t>(base) & 15u) || ld * size % 16) return false;
+  cuuint64_t dims[3] = {cols, rows, groups};
+  cuuint64_t strides[2] = {ld * size, ld * rows * size};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / size), 32, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool WG, bool F32, int PAIR>
+cudaError_t fg_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
+                      const FgParams& p, cudaStream_t st) {
+  auto kern = fp8_gemm_kernel<WG, F32, PAIR>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(fg_smem<PAIR>()));
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(sms)), dim3(FG_THREADS), FG_SMEM, st, 1, ta,
-                    tb, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(sms / PAIR * PAIR)), dim3(FG_THREADS),
+                    fg_smem<PAIR>(), st, PAIR, ta, tb, tc, p);
 }
 
 }  // namespace
@@ -502,7 +634,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.G = a.G;
   p.N = a.N;
   p.K = a.K;
-  p.rows = a.rows;
+  p.rows = static_cast<int>(a.rows);
   p.n_tiles = (a.N + FG_TILE_N - 1) / FG_TILE_N;
   p.nb = (a.N + 127) / 128;
   p.offsets = a.offsets;
@@ -511,25 +643,41 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.out = a.out;
   p.ldo = a.ldo;
   p.err = a.err;
-  CUtensorMap ta, tb;
+  // pairs: weight gradients of more than 128 rows; products whose average segment fills more
+  // than three quarters of a pair's 256 rows
+  const bool pair = a.wgrad ? a.K > 128 : a.rows >= 192 * static_cast<int64_t>(a.G);
+  const uint32_t b_rows = pair ? 128 : 256;
+  CUtensorMap ta, tb, tc;
   bool ok;
   if (a.wgrad) {
-    p.m_tiles = (a.K + FG_TILE_M - 1) / FG_TILE_M;
+    const int tile_m = pair ? 256 : 128;
+    p.m_tiles = (a.K + tile_m - 1) / tile_m;
     p.kb = static_cast<int>(fp8_token_blocks(a.rows, a.G));
     const uint64_t len = 128ull * static_cast<uint64_t>(p.kb);
-    ok = fg_map(&ta, a.a, len, len, static_cast<uint64_t>(a.K), FG_TILE_M) &&
-         fg_map(&tb, a.b, len, len, static_cast<uint64_t>(a.N), FG_TILE_N);
+    ok = fg_map(&ta, a.a, len, len, static_cast<uint64_t>(a.K), 128) &&
+         fg_map(&tb, a.b, len, len, static_cast<uint64_t>(a.N), b_rows);
+    p.tma_out = fg_out_map(&tc, a.out, a.out_fp32, static_cast<uint64_t>(a.N),
+                           static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.K),
+                           static_cast<uint64_t>(a.G));
   } else {
     p.kb = (a.K + 127) / 128;
     ok = fg_map(&ta, a.a, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.lda),
-                static_cast<uint64_t>(a.rows), FG_TILE_M) &&
+                static_cast<uint64_t>(a.rows), 128) &&
          fg_map(&tb, a.b, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.ldb),
-                static_cast<uint64_t>(a.G) * static_cast<uint64_t>(a.N), FG_TILE_N);
+                static_cast<uint64_t>(a.G) * static_cast<uint64_t>(a.N), b_rows);
+    p.tma_out = fg_out_map(&tc, a.out, a.out_fp32, static_cast<uint64_t>(a.N),
+                           static_cast<uint64_t>(a.ldo), static_cast<uint64_t>(a.rows), 1);
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (a.wgrad)
-    return a.out_fp32 ? fg_launch<true, true>(ta, tb, p, st) : fg_launch<true, false>(ta, tb, p, st);
-  return a.out_fp32 ? fg_launch<false, true>(ta, tb, p, st) : fg_launch<false, false>(ta, tb, p, st);
+  if (!p.tma_out) tc = ta;   // a valid map that no store uses
+  auto go = [&](auto wg, auto f32) {
+    return pair ? fg_launch<decltype(wg)::value, decltype(f32)::value, 2>(ta, tb, tc, p, st)
+                : fg_launch<decltype(wg)::value, decltype(f32)::value, 1>(ta, tb, tc, p, st);
+  };
+  if (a.wgrad) return a.out_fp32 ? go(std::true_type{}, std::true_type{})
+                                 : go(std::true_type{}, std::false_type{});
+  return a.out_fp32 ? go(std::false_type{}, std::true_type{})
+                    : go(std::false_type{}, std::false_type{});
 }
 
 }  // namespace moe
