@@ -4,14 +4,16 @@
 //   product       out[p][n]   = sum_kb sa[p][kb] sb[g][n/128][kb] sum_{k in kb} a[p][k] b[g][n][k]
 //   weight grad   dW[g][m][n] = sum_kb sa[kb][m] sb[kb][n] sum_{t in kb} a[m][t] b[n][t]
 //
-// The inner sums are tensor-core products over one block (tcgen05.mma kind::f8f6f4, four of
-// K 32), accumulated in fp32 in TMEM; the outer sum runs in fp32 registers of the epilogue
-// warps, because a scale is any fp32 number and changes with every block.  So the accumulator
-// leaves TMEM once per block: two 256-column accumulators alternate, the MMA fills one while
-// sixteen epilogue warps read the other and add it, scaled, to 64 sums per thread (packed
-// fma.rn.f32x2).  Per 128 x 256 tile and block the MMA takes 512 cycles (8192 multiply-adds per
-// cycle and SM); each scheduler's four epilogue warps issue 4 x (32 multiply-adds, 2 TMEM loads,
-// about 15 others).  The scales of the next block are loaded while this one is added.
+// The inner sums are tensor-core products over one block (tcgen05.mma kind::f8f6f4, K 32 each),
+// accumulated in fp32 in TMEM; the outer sum runs in fp32 registers of the epilogue warps,
+// because a scale is any fp32 number and changes with every block.  So an accumulator leaves
+// TMEM once per block, which is what bounds these kernels: 128 x 256 sums take 256 cycles of the
+// SM's fp32 lanes (512 with per-column scales), next to 512 cycles of MMA, and every hand-over
+// between the two costs a round trip of barriers.  Four accumulators of 128 columns rotate (two
+// halves of a tile, two blocks), so that one's round trip lies behind the MMAs of the others;
+// eight epilogue warps, four per half, own 128 sums a thread, and load the next 32 columns while
+// they add the last.  Another warp brings the scales into a ring in shared memory, up to eight
+// blocks ahead.
 //
 // Tiles are 256 x 256 on a CTA pair (cta_group::2, each CTA holding 128 rows of A and of B, which
 // halves the operand bytes per multiply-add) or 128 x 256 on one CTA, where a pair's second half
@@ -33,12 +35,13 @@ namespace {
 
 constexpr int FG_BK = 128;
 constexpr int FG_TILE_N = 256;
-// Warps 0 - 3: producer, MMA issuer, two idle; warps 4 - 19: epilogue.  Launched with 96
-// registers a thread (61,440 in all); the first four warps hand theirs to the others:
-// 128 * 32 + 512 * 112 = 61,440.
-constexpr int FG_THREADS = 640;
+// Warps 0 - 3: producer, MMA issuer, scale loader, MMA issuer; warps 4 - 11: epilogue.  Launched with 168
+// registers a thread (64,512 in all); the first four warps hand most of theirs to the others:
+// 128 * 56 + 256 * 224 = 64,512.
+constexpr int FG_THREADS = 384;
 constexpr int FG_EPI_WARP0 = 4;
-constexpr int FG_EPI_WARPS = 16;
+constexpr int FG_EPI_WARPS = 8;
+constexpr int FG_BUFS = 4;                // accumulators: (block & 1) * 2 + half
 constexpr int FG_MAX_G = 256;
 constexpr uint32_t FG_TMEM_COLS = 512;
 constexpr int FG_BOX_BYTES = 32 * 128;    // a warp's piece of a finished tile: 32 rows x 128 bytes
@@ -51,19 +54,27 @@ struct FgGeo {
   static constexpr int B_ROWS = FG_TILE_N / PAIR;       // this CTA's rows of b
   static constexpr int B_BYTES = B_ROWS * FG_BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = PAIR == 2 ? 4 : 3;
+  static constexpr int STAGES = PAIR == 2 ? 5 : 3;
 };
 
+// Scales of one block: a row's in row[], and in col[] the columns' (weight gradient) or the two
+// 128-column blocks' (product).
+struct alignas(16) FgScales {
+  float row[128];
+  float col[FG_TILE_N];
+};
+constexpr int FG_CHUNK = 4;    // blocks that are loaded, handed over and freed together
+
 struct FgCtl {
-  uint64_t full[4], empty[4], tfull[2], tempty[2], drain;
+  uint64_t full[5], empty[5], tfull[FG_BUFS], tempty[FG_BUFS], sfull[2], sempty[2], drain[2];
   uint32_t tmem_base;
   int abort, bad;
   int gstart[FG_MAX_G + 1];
   int tprefix[FG_MAX_G + 1];    // tiles before each group
   int kbpre[FG_MAX_G + 1];      // wgrad: token blocks before each group
-  alignas(16) float bscale[FG_EPI_WARPS][2][64];   // wgrad: column scales, read as float4
+  FgScales scales[2][FG_CHUNK];
 };
-static_assert(offsetof(FgCtl, bscale) % 16 == 0, "read as float4");
+static_assert(offsetof(FgCtl, scales) % 16 == 0, "read as float4");
 
 template <int PAIR>
 constexpr size_t fg_smem() {
@@ -87,10 +98,26 @@ struct FgParams {
   int* err;
 };
 
+// A whole warp's wait.
 __device__ __forceinline__ bool fg_wait(uint32_t bar, uint32_t parity, volatile int* abort,
                                         int* err) {
+  if (__all_sync(FULL_MASK, mbar_try_wait(bar, parity))) return true;
   return __all_sync(FULL_MASK, mbar_wait_bounded(bar, parity, abort, err, FG_WAIT_BUDGET));
 }
+// One thread of the warp, in a form that leaves the code around it warp-uniform: the operands of
+// tcgen05.mma and of the TMA copies are uniform registers, and in a branch on the lane's number
+// each of them was moved there first, about 100 cycles per MMA.
+__device__ __forceinline__ bool fg_elect() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0;
+}
+// a value that is the same in every lane, as a uniform one
+__device__ __forceinline__ int fg_uniform(int v) { return __reduce_max_sync(FULL_MASK, v); }
 
 // kind::f8f6f4 instruction descriptor: E4M3 x E4M3 -> fp32, both K-major
 __host__ __device__ constexpr uint32_t fg_idesc(int M, int N) {
@@ -115,45 +142,41 @@ __device__ __forceinline__ void fg_mma_pair(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// 32 lanes x 16 consecutive fp32 columns
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+// 32 lanes x 64 consecutive fp32 columns
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+        "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+        "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+        "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]),
+        "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]),
+        "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
 }
 
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// 4 bytes global -> shared, asynchronously; zero where !ok (nothing is read)
+__device__ __forceinline__ void cp_async4(float* dst, const float* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(ok ? 4 : 0)
+               : "memory");
+}
+// one arrival on `bar` when this thread's copies so far have landed
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
@@ -212,13 +235,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
-      mbar_init(smem_u32(&ctl->empty[s]), 1);
+      mbar_init(smem_u32(&ctl->empty[s]), 2);   // both halves' MMAs
+    }
+    for (int b = 0; b < FG_BUFS; ++b) {
+      mbar_init(smem_u32(&ctl->tfull[b]), 1);
+      mbar_init(smem_u32(&ctl->tempty[b]), FG_EPI_WARPS / 2 * PAIR);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_u32(&ctl->tfull[b]), 1);
-      mbar_init(smem_u32(&ctl->tempty[b]), FG_EPI_WARPS * PAIR);
+      mbar_init(smem_u32(&ctl->sfull[b]), 32);
+      mbar_init(smem_u32(&ctl->sempty[b]), FG_EPI_WARPS);
+      mbar_init(smem_u32(&ctl->drain[b]), 1);
     }
-    mbar_init(smem_u32(&ctl->drain), 1);
     fence_mbar_init();
     ctl->abort = 0;
     ctl->bad = 0;
@@ -287,7 +314,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   if (PAIR == 2) cluster_sync_all();
   else __syncthreads();
   tc_fence_after();
-  const int total = ctl->bad ? 0 : ctl->tprefix[p.G];
+  const int total = fg_uniform(ctl->bad ? 0 : ctl->tprefix[p.G]);
   const uint32_t tmem_base = ctl->tmem_base;
 
   // tile -> group, row tile, column tile; row tiles run fastest, so the CTAs at work share the
@@ -309,7 +336,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   auto blocks = [&](int g) { return WG ? ctl->kbpre[g + 1] - ctl->kbpre[g] : p.kb; };
 
   if (warp < FG_EPI_WARP0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;" ::: "memory");
     if (warp == 0) {
       // -------------------------------------------------------------- producer
       int s = 0;
@@ -318,16 +345,18 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       for (int tile = unit; tile < total && ok; tile += num_units) {
         int g, mt, nt;
         map_tile(tile, g, mt, nt);
-        const int nkb = blocks(g);
-        int x = WG ? ctl->kbpre[g] * FG_BK : 0;
-        const int arow = (WG ? 0 : ctl->gstart[g]) + mt * GE::TILE_M + 128 * rank;
-        const int brow = (WG ? 0 : g * p.N) + nt * FG_TILE_N + GE::B_ROWS * rank;
+        const int nkb = fg_uniform(blocks(g));
+        int x = fg_uniform(WG ? ctl->kbpre[g] * FG_BK : 0);
+        const int arow =
+            fg_uniform((WG ? 0 : ctl->gstart[g]) + mt * GE::TILE_M + 128 * rank);
+        // this CTA's rows of b: one CTA all 256; of a pair, 64 of each 128-column half
+        const int brow = fg_uniform((WG ? 0 : g * p.N) + nt * FG_TILE_N + 64 * rank);
         for (int kb = 0; kb < nkb; ++kb, x += FG_BK) {
           if (!fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
-          if (lane == 0) {
+          if (fg_elect()) {
             const uint32_t sa = smem_base + s * GE::STAGE_BYTES;
             const uint32_t full = smem_u32(&ctl->full[s]);
             // the leader's single arrive announces both CTAs' bytes
@@ -336,6 +365,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
               const uint32_t lead = mapa_shared(full, 0);
               tma_load_2d_pair(sa, &tmA, lead, x, arow);
               tma_load_2d_pair(sa + GE::A_BYTES, &tmB, lead, x, brow);
+              tma_load_2d_pair(sa + GE::A_BYTES + 64 * FG_BK, &tmB, lead, x, brow + 128);
             } else {
               tma_load_2d(sa, &tmA, full, x, arow);
               tma_load_2d(sa + GE::A_BYTES, &tmB, full, x, brow);
@@ -356,187 +386,222 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           ph ^= 1u;
         }
       }
-    } else if (warp == 1 && rank == 0) {
-      // -------------------------------------------------------------- MMA issuer (leader)
-      int s = 0;
-      uint32_t ph = 0;
-      uint32_t it = 0;   // blocks issued: accumulator it & 1
+    } else if (warp & 1) {
+      // -------------------------------------------------------------- MMA issuers (the leader's)
+      // warp 1 the tile's left half, warp 3 the right one, so that neither waits for the other's
+      // accumulator
+      if (rank == 0) {
+        const uint32_t h = static_cast<uint32_t>(warp >> 1);
+        int s = 0;
+        uint32_t ph = 0;
+        uint32_t it = 0;   // blocks issued
+        bool ok = true;
+        const uint32_t tmem = static_cast<uint32_t>(fg_uniform(static_cast<int>(tmem_base)));
+        const uint64_t da0 = make_smem_desc(smem_base, 16, 1024);
+        const uint64_t db0 =
+            make_smem_desc(smem_base + GE::A_BYTES + h * (GE::B_BYTES / 2), 16, 1024);
+        for (int tile = unit; tile < total && ok; tile += num_units) {
+          int nkb = p.kb;
+          if (WG) {
+            int g, mt, nt;
+            map_tile(tile, g, mt, nt);
+            nkb = fg_uniform(blocks(g));
+          }
+          for (int kb = 0; kb < nkb; ++kb, ++it) {
+            const uint32_t buf = (it & 1u) * 2u + h;
+            if (!fg_wait(smem_u32(&ctl->tempty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag, p.err) ||
+                !fg_wait(smem_u32(&ctl->full[s]), ph, abort_flag, p.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (fg_elect()) {
+              const uint64_t da = da0 + static_cast<uint32_t>(s * (GE::STAGE_BYTES >> 4));
+              const uint64_t db = db0 + static_cast<uint32_t>(s * (GE::STAGE_BYTES >> 4));
+#pragma unroll
+              for (uint32_t kk = 0; kk < FG_BK / 32; ++kk) {   // 32 bytes on, in 16-byte units
+                if (PAIR == 2)
+                  fg_mma_pair(tmem + buf * 128, da + 2 * kk, db + 2 * kk, fg_idesc(256, 128),
+                              kk != 0);
+                else
+                  fg_mma(tmem + buf * 128, da + 2 * kk, db + 2 * kk, fg_idesc(128, 128), kk != 0);
+              }
+              if (PAIR == 2) {
+                tc_commit_pair_mc(smem_u32(&ctl->tfull[buf]), 0x3);
+                tc_commit_pair_mc(smem_u32(&ctl->empty[s]), 0x3);
+              } else {
+                tc_commit(smem_u32(&ctl->tfull[buf]));
+                tc_commit(smem_u32(&ctl->empty[s]));
+              }
+            }
+            __syncwarp();
+            if (++s == STAGES) {
+              s = 0;
+              ph ^= 1u;
+            }
+          }
+        }
+        if (!ok && lane == 0) {   // gave up: wait (bounded) for the MMAs in flight
+          const uint32_t drain = smem_u32(&ctl->drain[h]);
+          if (PAIR == 2) tc_commit_pair(drain);
+          else tc_commit(drain);
+          const long long t0 = clock64();
+          while (!mbar_try_wait(drain, 0) && clock64() - t0 < FG_WAIT_BUDGET / 4) {
+          }
+        }
+        __syncwarp();
+      }
+    } else {
+      // -------------------------------------------------------------- scale loader (warp 2)
+      uint32_t ci = 0;   // chunks loaded
       bool ok = true;
       for (int tile = unit; tile < total && ok; tile += num_units) {
         int g, mt, nt;
         map_tile(tile, g, mt, nt);
         const int nkb = blocks(g);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const uint32_t buf = it & 1u, use = it >> 1;
-          if (!fg_wait(smem_u32(&ctl->tempty[buf]), (use & 1u) ^ 1u, abort_flag, p.err) ||
-              !fg_wait(smem_u32(&ctl->full[s]), ph, abort_flag, p.err)) {
+        const int m0 = mt * GE::TILE_M + 128 * rank;
+        const int rows_g = WG ? p.K : ctl->gstart[g + 1] - ctl->gstart[g];
+        for (int k0 = 0; k0 < nkb; k0 += FG_CHUNK, ++ci) {
+          const uint32_t buf = ci & 1u;
+          if (!fg_wait(smem_u32(&ctl->sempty[buf]), ((ci >> 1) & 1u) ^ 1u, abort_flag, p.err)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t sa = smem_base + s * GE::STAGE_BYTES;
-            const uint32_t sb = sa + GE::A_BYTES;
+          const int n = min(FG_CHUNK, nkb - k0);
+          FgScales* dst = ctl->scales[buf];
+          // rows and columns past the end get 0; their sums are not stored
+          if (WG) {
+            for (int j = 0; j < n; ++j) {
+              const long long blk = ctl->kbpre[g] + k0 + j;
+              const float* a = p.sa + blk * p.K + m0;
+              const float* b = p.sb + blk * p.N + nt * FG_TILE_N;
 #pragma unroll
-            for (int kk = 0; kk < FG_BK / 32; ++kk) {
-              const uint64_t da = make_smem_desc(sa + kk * 32, 16, 1024);
-              const uint64_t db = make_smem_desc(sb + kk * 32, 16, 1024);
-              if (PAIR == 2)
-                fg_mma_pair(tmem_base + buf * FG_TILE_N, da, db, fg_idesc(256, FG_TILE_N),
-                            kk != 0 ? 1u : 0u);
-              else
-                fg_mma(tmem_base + buf * FG_TILE_N, da, db, fg_idesc(128, FG_TILE_N),
-                       kk != 0 ? 1u : 0u);
+              for (int r = lane; r < 128; r += 32)
+                cp_async4(&dst[j].row[r], a + r, m0 + r < rows_g);
+#pragma unroll
+              for (int c = lane; c < FG_TILE_N; c += 32)
+                cp_async4(&dst[j].col[c], b + c, nt * FG_TILE_N + c < p.N);
             }
-            if (PAIR == 2) {
-              tc_commit_pair_mc(smem_u32(&ctl->empty[s]), 0x3);
-              tc_commit_pair_mc(smem_u32(&ctl->tfull[buf]), 0x3);
-            } else {
-              tc_commit(smem_u32(&ctl->empty[s]));
-              tc_commit(smem_u32(&ctl->tfull[buf]));
+          } else {
+            const int j = lane & (FG_CHUNK - 1);
+            const float* a = p.sa + static_cast<long long>(ctl->gstart[g] + m0) * p.kb + k0 + j;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = (lane >> 2) + 8 * i;
+              cp_async4(&dst[j].row[r], a + static_cast<long long>(r) * p.kb,
+                        j < n && m0 + r < rows_g);
+            }
+            if (lane < 2 * FG_CHUNK) {
+              const int blk = min(2 * nt + (lane >> 2), p.nb - 1);
+              cp_async4(&dst[j].col[lane >> 2],
+                        p.sb + (static_cast<long long>(g) * p.nb + blk) * p.kb + k0 + j, j < n);
             }
           }
-          __syncwarp();
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
+          cp_async_arrive(smem_u32(&ctl->sfull[buf]));
         }
       }
-      if (!ok && it > 0 && lane == 0) {   // gave up: wait (bounded) for the MMAs in flight
-        if (PAIR == 2) tc_commit_pair(smem_u32(&ctl->drain));
-        else tc_commit(smem_u32(&ctl->drain));
-        const long long t0 = clock64();
-        while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < FG_WAIT_BUDGET / 4) {
-        }
-      }
-      __syncwarp();
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;" ::: "memory");
-    // ---------------------------------------------------------------- epilogue (16 warps)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;" ::: "memory");
+    // ---------------------------------------------------------------- epilogue (8 warps)
     const int q = warp & 3;                          // the lane quarter this warp may read
-    const int cg = (warp - FG_EPI_WARP0) >> 2;       // which 64 of the 256 columns
-    float* bs = ctl->bscale[warp - FG_EPI_WARP0][0];
+    const int hh = (warp - FG_EPI_WARP0) >> 2;       // which 128 of the 256 columns
     uint8_t* box = boxes + (warp - FG_EPI_WARP0) * FG_BOX_BYTES;
     const uint32_t box_row = smem_u32(box) + lane * 128;
-    uint32_t it = 0;
+    // this half's two accumulators: TMEM address, barriers (the leader counts both CTAs' warps)
+    const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + 128 * hh;
+    const uint32_t tfull0 = smem_u32(&ctl->tfull[hh]);
+    const uint32_t tempty0 =
+        PAIR == 2 ? mapa_shared(smem_u32(&ctl->tempty[hh]), 0) : smem_u32(&ctl->tempty[hh]);
+    uint32_t it = 0;   // blocks added
+    uint32_t ci = 0;   // scale chunks used up
     bool ok = true;
     for (int tile = unit; tile < total && ok; tile += num_units) {
       int g, mt, nt;
       map_tile(tile, g, mt, nt);
       const int nkb = blocks(g);
-      const int lrow0 = mt * GE::TILE_M + 128 * rank + 32 * q;   // this warp's first row
-      const int rows_g = WG ? p.K : ctl->gstart[g + 1] - ctl->gstart[g];
-      const int nr = min(max(rows_g - lrow0, 0), 32);            // rows of it in the output
-      const int n0 = nt * FG_TILE_N + 64 * cg;
-      // a row or a column block past the end takes scales of one inside; its sums are not
-      // stored
-      const float* sa;
-      const float* sb;
-      if (WG) {
-        sa = p.sa + static_cast<long long>(ctl->kbpre[g]) * p.K + (lane < nr ? lrow0 + lane : 0);
-        sb = p.sb + static_cast<long long>(ctl->kbpre[g]) * p.N + n0 + lane;
-      } else {
-        sa = p.sa + static_cast<long long>(lane < nr ? ctl->gstart[g] + lrow0 + lane : 0) * p.kb;
-        sb = p.sb + (static_cast<long long>(g) * p.nb + min(n0 >> 7, p.nb - 1)) * p.kb;
-      }
-      const bool c0 = n0 + lane < p.N, c1 = n0 + 32 + lane < p.N;
-      auto load_scales = [&](float& s, float& f0, float& f1) {
-        if (WG) {
-          s = __ldg(sa);
-          f0 = c0 ? __ldg(sb) : 0.0f;
-          f1 = c1 ? __ldg(sb + 32) : 0.0f;
-          sa += p.K;
-          sb += p.N;
-        } else {
-          s = __ldg(sa++);
-          f0 = __ldg(sb++);
-        }
-      };
-      uint64_t acc[32];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) acc[i] = 0ull;
-      float s_next = 0.0f, f0_next = 0.0f, f1_next = 0.0f;
-      if (nkb > 0) load_scales(s_next, f0_next, f1_next);
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const uint32_t buf = it & 1u, use = it >> 1;
-        float s = s_next;
-        if (WG) {
-          float* mine = bs + buf * 64;   // alternates with the accumulator
-          mine[lane] = f0_next;
-          mine[lane + 32] = f1_next;
-          __syncwarp();
-        } else {
-          s *= f0_next;
-        }
-        if (kb + 1 < nkb) load_scales(s_next, f0_next, f1_next);
-        if (!fg_wait(smem_u32(&ctl->tfull[buf]), use & 1u, abort_flag, p.err)) {
+      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      for (int left = nkb; left > 0 && ok; left -= FG_CHUNK, ++ci) {
+        if (!fg_wait(smem_u32(&ctl->sfull[ci & 1u]), (ci >> 1) & 1u, abort_flag, p.err)) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        const uint32_t taddr =
-            tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * FG_TILE_N + 64 * cg;
-        const uint64_t s2 = pack2(s, s);
-        // 32 columns at a time; 16 where the column scales take registers too
-        constexpr int W = WG ? 16 : 32;
-#pragma unroll
-        for (int c = 0; c < 64 / W; ++c) {
-          uint32_t d[W];
-          if (WG) tmem_ld16(taddr + W * c, d);
-          else tmem_ld32(taddr + W * c, d);
-          tmem_ld_wait();
-          if (c == 64 / W - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {   // the accumulator is free (the leader counts both CTAs' warps)
-              if (PAIR == 2) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->tempty[buf]), 0));
-              else mbar_arrive(smem_u32(&ctl->tempty[buf]));
-            }
+        const FgScales* sc = ctl->scales[ci & 1u];
+        const int n = min(left, FG_CHUNK);
+        for (int j = 0; j < n; ++j, ++sc, ++it) {
+          const uint32_t par = it & 1u;
+          float s = sc->row[32 * q + lane];
+          if (!WG) s *= sc->col[hh];
+          if (!fg_wait(tfull0 + par * 16, (it >> 1) & 1u, abort_flag, p.err)) {
+            ok = false;
+            break;
           }
-          if (WG) {
-            const float4* cs = reinterpret_cast<const float4*>(bs + buf * 64 + W * c);
+          tc_fence_after();
+          // 64 columns at a time; 32 where the column scales take registers too
+          constexpr int W = WG ? 32 : 64;
 #pragma unroll
-            for (int i = 0; i < W / 4; ++i) {
-              const float4 f = cs[i];
-              uint64_t* a = acc + W / 2 * c + 2 * i;
-              a[0] = fma2(pack2(d[4 * i], d[4 * i + 1]), mul2(pack2(f.x, f.y), s2), a[0]);
-              a[1] = fma2(pack2(d[4 * i + 2], d[4 * i + 3]), mul2(pack2(f.z, f.w), s2), a[1]);
+          for (int c = 0; c < 128 / W; ++c) {
+            uint32_t d[W];
+            if constexpr (WG) tmem_ld32(taddr0 + par * 256 + W * c, d);
+            else tmem_ld64(taddr0 + par * 256 + W * c, d);
+            tmem_ld_wait();
+            if (c == 128 / W - 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {   // the accumulator is free
+                if (PAIR == 2) mbar_arrive_remote(tempty0 + par * 16);
+                else mbar_arrive(tempty0 + par * 16);
+              }
             }
-          } else {
+            if constexpr (WG) {
+              const float4* cs = reinterpret_cast<const float4*>(sc->col + 128 * hh + W * c);
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i)
-              acc[W / 2 * c + i] = fma2(pack2(d[2 * i], d[2 * i + 1]), s2, acc[W / 2 * c + i]);
+              for (int i = 0; i < W / 4; ++i) {
+                const float4 f = cs[i];
+                float* a = acc + W * c + 4 * i;
+                a[0] = fmaf(__uint_as_float(d[4 * i]), f.x * s, a[0]);
+                a[1] = fmaf(__uint_as_float(d[4 * i + 1]), f.y * s, a[1]);
+                a[2] = fmaf(__uint_as_float(d[4 * i + 2]), f.z * s, a[2]);
+                a[3] = fmaf(__uint_as_float(d[4 * i + 3]), f.w * s, a[3]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < W; ++i)
+                acc[W * c + i] = fmaf(__uint_as_float(d[i]), s, acc[W * c + i]);
+            }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->sempty[ci & 1u]));   // the scales are used up
       }
+      const int lrow0 = mt * GE::TILE_M + 128 * rank + 32 * q;   // this warp's first row
+      const int rows_g = WG ? p.K : ctl->gstart[g + 1] - ctl->gstart[g];
+      const int nr = min(max(rows_g - lrow0, 0), 32);            // rows of it in the output
+      const int n0 = nt * FG_TILE_N + 128 * hh;
       if (!ok || nr == 0 || n0 >= p.N) continue;
-      // through the box: bf16 in one go, fp32 in two halves of 32 columns
+      // through the box, 128 bytes of a row at a time
+      constexpr int BOX_COLS = F32 ? 32 : 64;
       const bool by_tma = p.tma_out && (WG || nr == 32);
 #pragma unroll
-      for (int half = 0; half < (F32 ? 2 : 1); ++half) {
+      for (int part = 0; part < 128 / BOX_COLS; ++part) {
+        const int n = n0 + BOX_COLS * part;
         if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           uint4 v;
           if (F32) {
-            const float2 x = unpack2(acc[16 * half + 2 * j]), y = unpack2(acc[16 * half + 2 * j + 1]);
-            v = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x),
-                           __float_as_uint(y.y));
+            const float* x = acc + BOX_COLS * part + 4 * j;
+            v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                           __float_as_uint(x[3]));
           } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 x = unpack2(acc[4 * j + i]);
-              w[i] = pack_bf16x2(x.x, x.y);
-            }
-            v = make_uint4(w[0], w[1], w[2], w[3]);
+            v = pack8(acc + BOX_COLS * part + 8 * j);
           }
           st_shared_v4(box_row + ((j ^ (lane & 7)) << 4), v);
         }
-        const int n = n0 + 32 * half;
         if (by_tma) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -546,7 +611,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
           }
         } else if (n < p.N) {
           __syncwarp();
-          const long long row = WG ? static_cast<long long>(g) * p.K + lrow0 : ctl->gstart[g] + lrow0;
+          const long long row =
+              WG ? static_cast<long long>(g) * p.K + lrow0 : ctl->gstart[g] + lrow0;
           copy_box<F32>(box, p.out, row * p.ldo + n, p.ldo, nr, p.N - n, lane);
           __syncwarp();
         }
@@ -646,7 +712,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   // pairs: weight gradients of more than 128 rows; products whose average segment fills more
   // than three quarters of a pair's 256 rows
   const bool pair = a.wgrad ? a.K > 128 : a.rows >= 192 * static_cast<int64_t>(a.G);
-  const uint32_t b_rows = pair ? 128 : 256;
+  const uint32_t b_rows = pair ? 64 : 256;   // a box of b
   CUtensorMap ta, tb, tc;
   bool ok;
   if (a.wgrad) {
