@@ -30,21 +30,18 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {   // a in the low
                                                         __NV_E4M3));
 }
 
-// Scale and factor of a block from the bits of its largest magnitude (bf16, so that NaN > inf
-// > every number in the bits' order).
-__device__ __forceinline__ void block_scale(uint32_t amax_bf16, int pow2, float& s, float& r) {
+// A block's factor (which = 0) or scale (1), from the bits of its largest magnitude (bf16, so
+// that NaN > inf > every number in the bits' order).
+__device__ __forceinline__ float block_quotient(uint32_t amax_bf16, int pow2, int which) {
   float a = __uint_as_float(amax_bf16 << 16);
   if (a < AMAX_FLOOR) a = AMAX_FLOOR;
-  if (!pow2 || !(a < INFINITY)) {
-    s = __fdiv_rn(a, E4M3_TOP);
-    r = __fdiv_rn(E4M3_TOP, a);
-  } else {
+  if (pow2 && a < INFINITY) {
     // 448 = 1.75 * 2^8: the exponent of a less 8, and one more where a's fraction is above
     const uint32_t u = __float_as_uint(a);
-    const int n = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    s = __uint_as_float(static_cast<uint32_t>(n) << 23);
-    r = __uint_as_float(static_cast<uint32_t>(254 - n) << 23);
+    const uint32_t n = (u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1u : 0u);
+    return __uint_as_float((which ? n : 254 - n) << 23);
   }
+  return __fdiv_rn(which ? a : E4M3_TOP, which ? E4M3_TOP : a);
 }
 
 __device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t w) {
@@ -68,85 +65,175 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, float r) {
 
 // ------------------------------------------------------------------ SwiGLU values
 // h = silu(a) b and its derivatives are rounded to bf16 once from their exact value, so that
-// codes and scales do not depend on how a kernel groups the arithmetic: the fp32 value is
-// computed with a known error bound, and where both ends of the bound do not round to the same
-// bf16 number (1 value in about 6000) it is computed again in 64 bits.
-__device__ __noinline__ float silu_mul_exact(float a, float b) {
+// codes and scales do not depend on how a kernel groups the arithmetic.  A value is computed in
+// fp32 with a known error bound; where the bound reaches a border between two bf16 numbers (one
+// h in about 3000, one da in about 1000) it is computed again in pairs of fp32 numbers, and where
+// even those do not settle it (practically never) or its magnitude is out of their range, in
+// 64 bits.  64 bits in the first place would cost three times the kernel: the card has two
+// 64-bit multiply-adds per SM and cycle.
+// Unevaluated sums of two fp32 numbers (about 48 bits).
+struct Pair {
+  float h, l;
+};
+__device__ __forceinline__ Pair quick_sum(float a, float b) {   // |a| >= |b|
+  const float s = a + b;
+  return {s, b - (s - a)};
+}
+__device__ __forceinline__ Pair exact_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Pair pair_mul(Pair x, Pair y) {
+  const float p = x.h * y.h;
+  return quick_sum(p, fmaf(x.h, y.h, -p) + fmaf(x.h, y.l, x.l * y.h));
+}
+// 2^(j/8), each as the nearest fp32 number and the nearest to what it leaves
+__constant__ float kRootHi[8] = {1.0f, 0x1.172b84p+0f, 0x1.306fe0p+0f, 0x1.4bfdaep+0f,
+                                  0x1.6a09e6p+0f, 0x1.8ace54p+0f, 0x1.ae89fap+0f, 0x1.d5818ep+0f};
+__constant__ float kRootLo[8] = {0.0f, -0x1.c15742p-27f, 0x1.4636e2p-25f, -0x1.593abcp-25f,
+                                  0x1.9fcef4p-26f, 0x1.15506ep-27f, -0x1.a94b14p-26f, -0x1.822dbcp-27f};
+// t = e^-a and s = 1 / (1 + t) for |a| <= 16, off by less than 2^-33 of themselves: with
+// -a = n ln2 / 8 + r, e^-a = 2^(n/8) e^r, |r| < 0.0434, and e^r = 1 + r + r^2/2 in pairs plus a
+// tail r^3 (1/6 + ...) below 2^-16, for which fp32 is enough.
+__device__ __forceinline__ void sigmoid_pair(float a, Pair& t, Pair& s) {
+  const float x = -a;
+  const float n = rintf(x * 0x1.715476p+3f);        // 8 / ln 2
+  const float d = fmaf(-n, 0x1.62e0p-4f, x);        // ln 2 / 8 to 13 bits: exact
+  const float rh = fmaf(-n, 0x1.0bfbe8p-18f, d);    // and 24 more
+  const float rl = fmaf(-n, 0x1.0bfbe8p-18f, d - rh);
+  const float r2 = rh * rh;
+  const float tail =
+      r2 * rh * fmaf(rh, fmaf(rh, fmaf(rh, 1.0f / 720, 1.0f / 120), 1.0f / 24), 1.0f / 6);
+  const Pair s1 = quick_sum(1.0f, rh);
+  const Pair s2 = quick_sum(s1.h, 0.5f * r2);
+  const float low = (s1.l + s2.l) + (fmaf(0.5f, fmaf(rh, rh, -r2), fmaf(rh, rl, rl)) + tail);
+  const int ni = static_cast<int>(n), j = ni & 7;
+  const Pair e = pair_mul(quick_sum(s2.h, low), Pair{kRootHi[j], kRootLo[j]});
+  const float scale = __uint_as_float(static_cast<uint32_t>(127 + (ni - j) / 8) << 23);
+  t = {e.h * scale, e.l * scale};
+  const Pair den0 = exact_sum(1.0f, t.h);
+  const Pair den = quick_sum(den0.h, den0.l + t.l);
+  const float q = 1.0f / den.h;
+  s = quick_sum(q, q * (fmaf(-q, den.h, 1.0f) - q * den.l));
+}
+
+__device__ __noinline__ float silu_mul_64(float a, float b) {
   const double x = static_cast<double>(a);
   return __double2float_rn(x * (1.0 / (1.0 + exp(-x))) * static_cast<double>(b));
 }
-__device__ __noinline__ float dsilu_mul_exact(float a, float b, float dh) {
+__device__ __noinline__ float dsilu_mul_64(float a, float b, float dh) {
   const double x = static_cast<double>(a);
   const double sg = 1.0 / (1.0 + exp(-x));
   return __double2float_rn(static_cast<double>(dh) * static_cast<double>(b) * sg *
                            (1.0 + x * (1.0 / (1.0 + exp(x)))));
 }
 
-// Two values and the bounds of their errors -> packed bf16; bit i of `open` set where value i
-// is not settled (its bound crosses a rounding border, it is tiny, infinite or NaN).
-__device__ __forceinline__ uint32_t settle2(float v0, float e0, float v1, float e1, int& open) {
-  const uint32_t hi = pack_bf16x2(v0 + e0, v1 + e1), lo = pack_bf16x2(v0 - e0, v1 - e1);
-  const uint32_t d = (hi ^ lo) & 0x7fff7fffu;   // an exact zero may change its sign in v + 0
-  auto fits = [](float v, float e) { return (e >= 0x1p-120f && e < INFINITY) || v == 0.0f; };
-  open = ((d & 0xffffu) || !fits(v0, e0) ? 1 : 0) | ((d >> 16) || !fits(v1, e1) ? 2 : 0);
-  return lo;
+__device__ __forceinline__ uint32_t bf16_bits(float v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+// v within e of the exact value: its fp32 neighbour(s) there, if both round to one bf16 number
+__device__ __forceinline__ bool settled(Pair v, float e, float& out) {
+  out = v.h + (v.l - e);
+  return bf16_bits(out) == bf16_bits(v.h + (v.l + e));
+}
+// the pairs' range: |gate| <= 16, and results far from fp32's smallest and largest numbers
+__device__ __forceinline__ bool in_range(float v) {
+  return fabsf(v) >= 0x1p-100f && fabsf(v) < 0x1p126f;
 }
 
-// silu(a) b = a b / (1 + e^-a): a b is exact (two 8-bit significands), expf is off by at most
-// one ulp (2^-23), the sum by 2^-24, the fast quotient by two ulp (2^-22): 1.75 * 2^-22.
-constexpr float SILU_ERR = 0x1p-21f;
-// silu'(a) = s (1 + a (1 - s)), s = 1 / (1 + t), 1 - s = t s: with u = a t s and g = 1 + u the
-// error is below |s| (|u| + |g|) 2.75 * 2^-22 (t 2^-23; s 1.75 * 2^-22; four roundings).
-constexpr float DSILU_ERR = 0x1.8p-21f;
+__device__ __noinline__ float silu_mul_exact(float a, float b) {
+  const float p = a * b;   // exact: two 8-bit significands
+  if (p == 0.0f) return p;
+  if (fabsf(a) <= 16.0f && in_range(p)) {
+    Pair t, s;
+    sigmoid_pair(a, t, s);
+    const float v = p * s.h;
+    float out;
+    if (in_range(v) &&
+        settled(quick_sum(v, fmaf(p, s.h, -v) + p * s.l), fabsf(v) * 0x1p-33f, out))
+      return out;
+  }
+  return silu_mul_64(a, b);
+}
+__device__ __noinline__ float dsilu_mul_exact(float a, float b, float dh) {
+  const float p = dh * b;
+  if (fabsf(a) <= 16.0f && (p == 0.0f || in_range(p))) {
+    if (p == 0.0f) return p;
+    Pair t, s;
+    sigmoid_pair(a, t, s);
+    Pair u = pair_mul(t, s);                   // 1 - sigma
+    u = {a * u.h, fmaf(a, u.h, -(a * u.h)) + a * u.l};
+    Pair g = exact_sum(1.0f, u.h);
+    g = quick_sum(g.h, g.l + u.l);
+    const Pair m = pair_mul(s, g);
+    const float v = p * m.h;
+    float out;
+    if (in_range(v) && settled(quick_sum(v, fmaf(p, m.h, -v) + p * m.l),
+                               fabsf(p * s.h) * (fabsf(u.h) + fabsf(g.h)) * 0x1p-32f, out))
+      return out;
+  }
+  return dsilu_mul_64(a, b, dh);
+}
 
+// Whether an fp32 value may not round as the exact one does: its fraction is within `ulps` fp32
+// steps of a border between bf16 numbers, or it is below 2^-100 (zeros too), infinite or NaN.
+__device__ __forceinline__ bool unsettled(float v, uint32_t ulps) {
+  const uint32_t u = __float_as_uint(v);
+  return ((u + ulps - 0x8000u) & 0xffffu) <= 2 * ulps ||
+         (u & 0x7fffffffu) - 0x0d800000u >= 0x7f800000u - 0x0d800000u;
+}
+
+// silu(a) b = a b / (1 + e^-a): a b is exact, expf is off by at most one ulp (2^-23), the sum by
+// 2^-24, the fast quotient by two ulp (2^-22): 1.75 * 2^-22 of the value, at most 7 of its fp32
+// steps.  Where e^-a or the quotient leaves its range the result is 0, which is unsettled.
 __device__ __forceinline__ uint32_t silu_mul2(uint32_t a, uint32_t b) {
   const float a0 = bf16_lo(a), a1 = bf16_hi(a), b0 = bf16_lo(b), b1 = bf16_hi(b);
-  const float v0 = __fdividef(a0 * b0, 1.0f + expf(-a0));
-  const float v1 = __fdividef(a1 * b1, 1.0f + expf(-a1));
-  int open;
-  uint32_t w = settle2(v0, fabsf(v0) * SILU_ERR, v1, fabsf(v1) * SILU_ERR, open);
-  if (a0 < -80.0f) open |= 1;   // the exponential's and the quotient's range
-  if (a1 < -80.0f) open |= 2;
-  if (open) {
-    const float x0 = (open & 1) ? silu_mul_exact(a0, b0) : bf16_lo(w);
-    const float x1 = (open & 2) ? silu_mul_exact(a1, b1) : bf16_hi(w);
-    w = pack_bf16x2(x0, x1);
+  float v0 = __fdividef(a0 * b0, 1.0f + expf(-a0));
+  float v1 = __fdividef(a1 * b1, 1.0f + expf(-a1));
+  const bool o0 = unsettled(v0, 8), o1 = unsettled(v1, 8);
+  if (o0 || o1) {
+    if (o0) v0 = silu_mul_exact(a0, b0);
+    if (o1) v1 = silu_mul_exact(a1, b1);
   }
-  return w;
+  return pack_bf16x2(v0, v1);
 }
 __device__ __forceinline__ uint4 silu_mul8(const uint4& a, const uint4& b) {
   return make_uint4(silu_mul2(a.x, b.x), silu_mul2(a.y, b.y), silu_mul2(a.z, b.z),
                     silu_mul2(a.w, b.w));
 }
-__device__ __forceinline__ uint32_t dsilu_mul2(uint32_t a, uint32_t b, uint32_t dh) {
-  float v[2], e[2], fa[2], fb[2], fd[2];
+
+// All three of a pair of columns from one exponential: h = a b s, db = dh a s, da = dh b s g with
+// s = 1 / (1 + t), t = e^-a, u = a t s = a (1 - s), g = 1 + u.  s is off by 1.75 * 2^-22 (as
+// above); h and db add one rounding: below 2^-21, 8 steps, again.  da: |dh b s| (|u| + |g|)
+// 2.75 * 2^-22 (t 2^-23; s 1.75 * 2^-22; four roundings).
+struct Swiglu2 {
+  uint32_t da, db, h;
+};
+__device__ __forceinline__ Swiglu2 swiglu_bwd2(uint32_t a, uint32_t b, uint32_t dh) {
+  float da[2], db[2], h[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    fa[i] = i ? bf16_hi(a) : bf16_lo(a);
-    fb[i] = i ? bf16_hi(b) : bf16_lo(b);
-    fd[i] = i ? bf16_hi(dh) : bf16_lo(dh);
-    const float t = expf(-fa[i]);
+    const float fa = i ? bf16_hi(a) : bf16_lo(a), fb = i ? bf16_hi(b) : bf16_lo(b),
+                fd = i ? bf16_hi(dh) : bf16_lo(dh);
+    const float t = expf(-fa);
     const float s = __fdividef(1.0f, 1.0f + t);
-    const float u = fa[i] * t * s;
+    const float u = fa * t * s;
     const float g = 1.0f + u;
-    const float qs = fd[i] * fb[i] * s;
-    v[i] = qs * g;
-    e[i] = fabsf(qs) * (fabsf(u) + fabsf(g)) * DSILU_ERR;
+    const float qs = fd * fb * s;
+    h[i] = fa * fb * s;
+    db[i] = fd * fa * s;
+    da[i] = qs * g;
+    const float e = fabsf(qs) * (fabsf(u) + fabsf(g)) * 0x1.8p-21f;
+    const bool oh = unsettled(h[i], 8), ob = unsettled(db[i], 8);
+    const uint32_t ends = pack_bf16x2(da[i] - e, da[i] + e);
+    const bool oa = (ends >> 16) != (ends & 0xffffu) || !(e >= 0x1p-120f && e < INFINITY);
+    if (oh || ob || oa) {
+      if (oh) h[i] = silu_mul_exact(fa, fb);
+      if (ob) db[i] = silu_mul_exact(fa, fd);
+      if (oa) da[i] = dsilu_mul_exact(fa, fb, fd);
+    }
   }
-  int open;
-  uint32_t w = settle2(v[0], e[0], v[1], e[1], open);
-  if (fa[0] < -80.0f) open |= 1;
-  if (fa[1] < -80.0f) open |= 2;
-  if (open) {
-    const float x0 = (open & 1) ? dsilu_mul_exact(fa[0], fb[0], fd[0]) : bf16_lo(w);
-    const float x1 = (open & 2) ? dsilu_mul_exact(fa[1], fb[1], fd[1]) : bf16_hi(w);
-    w = pack_bf16x2(x0, x1);
-  }
-  return w;
-}
-__device__ __forceinline__ uint4 dsilu_mul8(const uint4& a, const uint4& b, const uint4& d) {
-  return make_uint4(dsilu_mul2(a.x, b.x, d.x), dsilu_mul2(a.y, b.y, d.y),
-                    dsilu_mul2(a.z, b.z, d.z), dsilu_mul2(a.w, b.w, d.w));
+  return {pack_bf16x2(da[0], da[1]), pack_bf16x2(db[0], db[1]), pack_bf16x2(h[0], h[1])};
 }
 
 // ------------------------------------------------------------------ sources
@@ -160,7 +247,6 @@ struct Source {
   long long ld;
   int f;
   int cols;                  // columns quantised: C, f, or 2f
-  bool h_only;               // backward: the columns are those of h
 };
 
 template <bool VEC>
@@ -188,35 +274,28 @@ __device__ __forceinline__ uint4 value8(const Source& s, long long row, int c) {
     return load8<VEC>(s.x + row * s.ld + c, n);
   } else {
     const __nv_bfloat16* ab = s.x + row * 2 * s.f;
-    if (SRC == SRC_SWIGLU || s.h_only)
+    if constexpr (SRC == SRC_SWIGLU)
       return silu_mul8(load8<VEC>(ab + c, n), load8<VEC>(ab + s.f + c, n));
+    // one column at a time, wherever the halves meet; full blocks of 128 columns have kernels of
+    // their own
     const __nv_bfloat16* dh = s.dh + row * s.f;
-    if constexpr (VEC) {
-      const bool up = c >= s.f;
-      const int k = up ? c - s.f : c;
-      const uint4 a = load8<VEC>(ab + k, 8), d = load8<VEC>(dh + k, 8);
-      return up ? silu_mul8(a, d) : dsilu_mul8(a, load8<VEC>(ab + s.f + k, 8), d);
-    } else {
-      // odd widths: the gate's and the up projection's columns may meet inside a chunk
-      uint32_t w[4];
+    auto bits = [](const __nv_bfloat16* p) {
+      return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p)));
+    };
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = 0u;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int cc = c + 2 * i + j;
-          if (cc >= s.cols) continue;
-          const int k = cc < s.f ? cc : cc - s.f;
-          auto bits = [](const __nv_bfloat16* p) {
-            return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p)));
-          };
-          const uint32_t a = bits(ab + k), d = bits(dh + k);
-          const uint32_t r = cc < s.f ? dsilu_mul2(a, bits(ab + s.f + k), d) : silu_mul2(a, d);
-          w[i] |= (r & 0xffffu) << (16 * j);
-        }
+    for (int i = 0; i < 8; ++i) {
+      const int cc = c + i;
+      uint32_t r = 0u;
+      if (cc < s.cols) {
+        const int k = cc < s.f ? cc : cc - s.f;
+        const Swiglu2 x = swiglu_bwd2(bits(ab + k), bits(ab + s.f + k), bits(dh + k));
+        r = (cc < s.f ? x.da : x.db) & 0xffffu;
       }
-      return make_uint4(w[0], w[1], w[2], w[3]);
+      if (i & 1) w[i / 2] |= r << 16;
+      else w[i / 2] = r;
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -242,11 +321,32 @@ __device__ __forceinline__ long long live_rows(const int32_t* offsets, int G, lo
   return n;
 }
 
-// ------------------------------------------------------------------ along the rows
-// One warp per row; a lane takes eight values (16 bytes), half a warp a block.  ROW_BATCH
-// chunks' loads are issued before any is used.
-constexpr int ROW_BATCH = 4;
+// Four blocks of a row (or of four rows), a chunk of eight values per lane in each, sixteen lanes
+// to a block: their scales and factors, by one pass of shuffles (two blocks' maxima to a
+// word) and one division, lane 2 b of the sixteen dividing for block b's factor and lane 2 b + 1
+// for its scale.  `quot` gets this lane's quotient.
+__device__ __forceinline__ void four_scales(const uint4* v, int pow2, int lane, float* r,
+                                            float& quot) {
+  uint32_t m[4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) m[b] = max_mag8(v[b]);
+  uint32_t x = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+  uint32_t y = __vmaxu2(__byte_perm(m[2], m[3], 0x5410), __byte_perm(m[2], m[3], 0x7632));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    x = __vmaxu2(x, __shfl_xor_sync(FULL_MASK, x, o));
+    y = __vmaxu2(y, __shfl_xor_sync(FULL_MASK, y, o));
+  }
+  const uint32_t w = (lane & 4) ? y : x;
+  const uint32_t amax = (lane & 2) ? w >> 16 : w & 0xffffu;
+  quot = block_quotient(amax, pow2, lane & 1);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) r[b] = __shfl_sync(FULL_MASK, quot, (lane & 16) | (2 * b));
+}
 
+// ------------------------------------------------------------------ along the rows
+// One warp per row; a lane takes eight values (16 bytes), half a warp a block, four chunks'
+// loads before any is used.
 template <int SRC, bool VEC>
 __global__ void __launch_bounds__(FQ_THREADS)
 fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
@@ -257,41 +357,97 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
   const long long gw = (static_cast<long long>(blockIdx.x) * FQ_THREADS + threadIdx.x) >> 5;
   const long long nw = (static_cast<long long>(gridDim.x) * FQ_THREADS) >> 5;
   const long long n_rows = live_rows(offsets, G, rows, err, gw == 0 && lane == 0);
+  // the next row's source is looked up while this row is quantised
+  long long t_next = gw;
+  if (src_tok && gw < n_rows) t_next = __ldg(src_tok + gw);
   for (long long p = gw; p < n_rows; p += nw) {
-    long long t = p;
+    const long long t = t_next;
+    t_next = p + nw;
     if (src_tok) {
-      t = __ldg(src_tok + p);
+      if (p + nw < n_rows) t_next = __ldg(src_tok + p + nw);
       if (t < 0 || t >= src_rows) {
         if (lane == 0) flag_error(err, MOE_DEVERR_BAD_INDEX);
         continue;
       }
     }
-    for (int c0 = 8 * lane; c0 - 8 * lane < src.cols; c0 += 256 * ROW_BATCH) {
-      uint4 v[ROW_BATCH];
+    constexpr bool BOTH = SRC == SRC_SWIGLU_BWD && VEC;   // two chunks of da, two of db
+    const int span = BOTH ? src.f : src.cols;
+    for (int c0 = 0; c0 < span; c0 += BOTH ? 512 : 1024) {
+      uint4 v[4];
+      int col[4];
+      if constexpr (BOTH) {
+        uint4 a[2], b[2], d[2];
 #pragma unroll
-      for (int b = 0; b < ROW_BATCH; ++b) v[b] = value8<SRC, VEC>(src, t, c0 + 256 * b);
+        for (int i = 0; i < 2; ++i) {
+          const int c = c0 + 256 * i + 8 * lane;
+          col[i] = c;
+          col[2 + i] = src.f + c;
+          a[i] = b[i] = d[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (c < src.f) {
+            a[i] = load8<true>(src.x + t * 2 * src.f + c, 8);
+            b[i] = load8<true>(src.x + t * 2 * src.f + src.f + c, 8);
+            d[i] = load8<true>(src.dh + t * src.f + c, 8);
+          } else {
+            col[i] = col[2 + i] = 1 << 28;   // past every column
+          }
+        }
 #pragma unroll
-      for (int b = 0; b < ROW_BATCH; ++b) {
-        const int c = c0 + 256 * b;
-        uint32_t m = max_mag8(v[b]);
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t *pa = &a[i].x, *pb = &b[i].x, *pd = &d[i].x;
+          uint32_t x[4], y[4];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(FULL_MASK, m, o));
-        float s, r;
-        block_scale(fold2(m), out.pow2, s, r);
-        if (c >= src.cols) continue;
-        *reinterpret_cast<uint2*>(out.codes + p * out.ld + c) = codes8(v[b], r);
-        if ((lane & 15) == 0) out.scales[p * out.kb + (c >> 7)] = s;
+          for (int k = 0; k < 4; ++k) {
+            const Swiglu2 w = swiglu_bwd2(pa[k], pb[k], pd[k]);
+            x[k] = w.da;
+            y[k] = w.db;
+          }
+          v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+          v[2 + i] = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      } else if constexpr (SRC == SRC_SWIGLU && VEC) {
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          col[i] = c0 + 256 * i + 8 * lane;
+          a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (col[i] < src.cols) {
+            a[i] = load8<true>(src.x + t * 2 * src.f + col[i], 8);
+            b[i] = load8<true>(src.x + t * 2 * src.f + src.f + col[i], 8);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = col[i] < src.cols ? silu_mul8(a[i], b[i]) : a[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          col[i] = c0 + 256 * i + 8 * lane;
+          v[i] = value8<SRC, VEC>(src, t, col[i]);
+        }
       }
+      float r[4], quot;
+      four_scales(v, out.pow2, lane, r, quot);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col[i] < src.cols)
+          *reinterpret_cast<uint2*>(out.codes + p * out.ld + col[i]) = codes8(v[i], r[i]);
+      // lane 2 b + 1 of the first eight of each half stores block b's scale
+      const int b = (lane >> 1) & 3;
+      const int c = (b == 0 ? col[0] : b == 1 ? col[1] : b == 2 ? col[2] : col[3]) - 8 * (lane & 15);
+      if ((lane & 9) == 1 && c < src.cols && c >= 0) out.scales[p * out.kb + (c >> 7)] = quot;
     }
   }
   griddep_launch();
 }
 
 // ------------------------------------------------------------------ along the tokens (and rows)
-// One CTA per 128 columns and 128-row block of a segment (blocks are counted from the
-// segment's first row).  The tile goes through shared memory once: its rows are quantised from
-// the registers that loaded them, its columns from shared memory, two columns and a quarter of
-// the rows per thread, which then owns 32 consecutive codes of each column.
+// One CTA at a time per 128 columns and 128-row block of a segment (blocks are counted from the
+// segment's first row).  A tile goes through shared memory: its rows are quantised from
+// the registers that loaded them, its columns from shared memory, two columns and sixteen rows
+// per thread.  With BOTH the tile is 128 columns of f: da, db and h from one read of a, b and dh.
+constexpr int FT_THREADS = 512;
+constexpr int FT_TILE = 128 * 16;   // 16-byte pieces
+
 __device__ __forceinline__ uint32_t col_code(const uint32_t* w, int i, bool hi, float r) {
   float f[4];
 #pragma unroll
@@ -299,25 +455,74 @@ __device__ __forceinline__ uint32_t col_code(const uint32_t* w, int i, bool hi, 
   return e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
 }
 
-template <int SRC, bool VEC>
-__global__ void __launch_bounds__(FQ_THREADS)
+// The tile's columns (c0 ..) along the tokens into block kb.
+__device__ __forceinline__ void tile_columns(const uint4* tile, uint32_t (*s_max)[64], int c0,
+                                             int cols, int kb, uint8_t* codes_t, float* scales_t,
+                                             int kb_cap, int pow2) {
+  // columns c0 + 2 cp, + 1; rows 16 q .. 16 q + 15
+  const int cp = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
+  uint32_t w[16];
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    w[i] = words[(16 * q + i) * 64 + cp];
+    m = max_mag2(m, w[i]);
+  }
+  s_max[q][cp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, s_max[i][cp]);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = c0 + 2 * cp + j;
+    if (c >= cols) continue;
+    const uint32_t amax = j ? m >> 16 : m & 0xffffu;
+    const float r = block_quotient(amax, pow2, 0);
+    uint32_t code[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) code[i] = col_code(w, i, j != 0, r);
+    *reinterpret_cast<uint4*>(codes_t + (static_cast<long long>(c) * kb_cap + kb) * 128 + 16 * q) =
+        make_uint4(code[0], code[1], code[2], code[3]);
+    if (q == 0) scales_t[static_cast<long long>(kb) * cols + c] = block_quotient(amax, pow2, 1);
+  }
+}
+
+// Four rows of a tile (r + 32 u) along the row, a half-warp each.
+__device__ __forceinline__ void tile_rows(const uint4* v, long long r0, int nr, int c, int cols,
+                                          const QuantOut& out) {
+  const int lane = threadIdx.x & 31, r = threadIdx.x >> 4;
+  float f[4], quot;
+  four_scales(v, out.pow2, lane, f, quot);
+  if (c < cols) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (r + 32 * u < nr)
+        *reinterpret_cast<uint2*>(out.codes + (r0 + r + 32 * u) * out.ld + c) = codes8(v[u], f[u]);
+  }
+  const int row = r + 32 * ((lane >> 1) & 3), c_first = c - 8 * (lane & 15);
+  if ((lane & 9) == 1 && row < nr && c_first < cols)
+    out.scales[(r0 + row) * out.kb + (c_first >> 7)] = quot;
+}
+
+template <int SRC, bool VEC, bool BOTH>
+__global__ void __launch_bounds__(FT_THREADS, 2)
 fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
                   const int32_t* __restrict__ offsets, int G, long long rows, const QuantOut out,
-                  int* err) {
+                  const QuantOut out_h, int* err) {
   griddep_wait();   // see common.cuh: dependent launches
-  __shared__ uint4 tile[128][16];
-  __shared__ uint32_t s_max[4][64];
+  extern __shared__ uint4 tile[];   // BOTH: three tiles
+  __shared__ uint32_t s_max[BOTH ? 3 : 1][8][64];
   __shared__ int s_first[FQ_MAX_G + 1];
   __shared__ int s_sum[8];
   __shared__ int s_bad;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const bool first = blockIdx.x == 0 && blockIdx.y == 0;
   if (tid == 0) s_bad = 0;
   __syncthreads();
   auto start_of = [&](int g) {
-    return offsets ? static_cast<long long>(offsets[g]) : (g ? rows : 0LL);
+    return offsets ? static_cast<long long>(__ldg(offsets + g)) : (g ? rows : 0LL);
   };
-  // first block of every segment (G <= 256: one per thread)
+  // first block of every segment (G <= 256: one per thread of the first eight warps)
   int nb = 0;
   if (tid < G) {
     const long long a = start_of(tid), b = start_of(tid + 1);
@@ -325,20 +530,24 @@ fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long lo
     else nb = static_cast<int>((b - a + 127) / 128);
   }
   const int incl = warp_incl_scan(nb);
-  if (lane == 31) s_sum[warp] = incl;
+  if (lane == 31 && warp < 8) s_sum[warp] = incl;
   __syncthreads();
-  int before = 0;
-  for (int w = 0; w < warp; ++w) before += s_sum[w];
-  if (tid < G) s_first[tid] = before + incl - nb;
-  if (tid == G - 1) s_first[G] = before + incl;
+  if (tid < G) {
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s_sum[w];
+    s_first[tid] = before + incl - nb;
+    if (tid == G - 1) s_first[G] = before + incl;
+  }
   __syncthreads();
   if (s_bad) {
-    if (first && tid == 0) flag_error(err, MOE_DEVERR_BAD_OFFSETS);
+    if (blockIdx.x == 0 && tid == 0) flag_error(err, MOE_DEVERR_BAD_OFFSETS);
     return;
   }
-  const int total = s_first[G];
-  const int c0 = blockIdx.x * 128;
-  for (int kb = blockIdx.y; kb < total; kb += gridDim.y) {
+  const int gx = ((BOTH ? src.f : src.cols) + 127) / 128;   // column tiles, fastest
+  const long long total = static_cast<long long>(s_first[G]) * gx;
+  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
+    const int kb = static_cast<int>(item / gx);
+    const int c0 = static_cast<int>(item - static_cast<long long>(kb) * gx) * 128;
     int lo = 0, hi = G;   // s_first[lo] <= kb < s_first[lo + 1]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -348,70 +557,79 @@ fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long lo
     const long long r0 = start_of(lo) + 128LL * (kb - s_first[lo]);
     const long long left = start_of(lo + 1) - r0;
     const int nr = left < 128 ? static_cast<int>(left) : 128;
-    uint4 v[8];
+    const int r = tid >> 4, c = c0 + 8 * (tid & 15);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    uint4 v[4];
+    if constexpr (BOTH) {
+      uint4 a[4], b[4], d[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int r = (tid >> 4) + 16 * u, c = c0 + 8 * (tid & 15);
-      v[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < nr) {
-        long long t = r0 + r;
-        if (src_tok) {
-          t = __ldg(src_tok + t);
-          if (t < 0 || t >= src_rows) {
-            flag_error(err, MOE_DEVERR_BAD_INDEX);
-            t = 0;
+      for (int u = 0; u < 4; ++u) {
+        a[u] = b[u] = d[u] = zero;
+        if (r + 32 * u < nr) {
+          const long long t = r0 + r + 32 * u;
+          a[u] = load8<true>(src.x + t * 2 * src.f + c, 8);
+          b[u] = load8<true>(src.x + t * 2 * src.f + src.f + c, 8);
+          d[u] = load8<true>(src.dh + t * src.f + c, 8);
+        }
+      }
+      __syncthreads();   // the previous tiles are consumed
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = (r + 32 * u) * 16 + (tid & 15);
+        uint32_t x[4] = {0u, 0u, 0u, 0u}, y[4] = {0u, 0u, 0u, 0u}, z[4] = {0u, 0u, 0u, 0u};
+        if (r + 32 * u < nr) {
+          const uint32_t *pa = &a[u].x, *pb = &b[u].x, *pd = &d[u].x;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const Swiglu2 w = swiglu_bwd2(pa[k], pb[k], pd[k]);
+            x[k] = w.da;
+            y[k] = w.db;
+            z[k] = w.h;
           }
         }
-        v[u] = value8<SRC, VEC>(src, t, c);
+        tile[at] = make_uint4(x[0], x[1], x[2], x[3]);
+        tile[FT_TILE + at] = make_uint4(y[0], y[1], y[2], y[3]);
+        tile[2 * FT_TILE + at] = make_uint4(z[0], z[1], z[2], z[3]);
       }
-    }
-    __syncthreads();   // the previous block's tile is consumed
+      // this thread's own pieces back, for the rows of da and db
 #pragma unroll
-    for (int u = 0; u < 8; ++u) tile[(tid >> 4) + 16 * u][tid & 15] = v[u];
-    if (out.codes && !src.h_only) {
+      for (int part = 0; part < 2; ++part) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int r = (tid >> 4) + 16 * u, c = c0 + 8 * (tid & 15);
-        uint32_t m = max_mag8(v[u]);
+        for (int u = 0; u < 4; ++u)
+          v[u] = tile[part * FT_TILE + (r + 32 * u) * 16 + (tid & 15)];
+        tile_rows(v, r0, nr, part * src.f + c, src.cols, out);
+      }
+      __syncthreads();
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(FULL_MASK, m, o));
-        float s, f;
-        block_scale(fold2(m), out.pow2, s, f);
-        if (r < nr && c < src.cols) {
-          *reinterpret_cast<uint2*>(out.codes + (r0 + r) * out.ld + c) = codes8(v[u], f);
-          if ((tid & 15) == 0) out.scales[(r0 + r) * out.kb + (c >> 7)] = s;
+      for (int part = 0; part < 3; ++part) {
+        if (part == 2 && !out_h.codes_t) continue;
+        const QuantOut& o = part == 2 ? out_h : out;
+        tile_columns(tile + part * FT_TILE, s_max[part], (part == 1 ? src.f : 0) + c0,
+                     part == 2 ? src.f : src.cols, kb, o.codes_t, o.scales_t, o.kb_cap, o.pow2);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[u] = zero;
+        if (r + 32 * u < nr) {
+          long long t = r0 + r + 32 * u;
+          if (src_tok) {
+            t = __ldg(src_tok + t);
+            if (t < 0 || t >= src_rows) {
+              flag_error(err, MOE_DEVERR_BAD_INDEX);
+              t = 0;
+            }
+          }
+          v[u] = value8<SRC, VEC>(src, t, c);
         }
       }
-    }
-    __syncthreads();
-    // columns c0 + 2 cp, + 1; rows 32 q .. 32 q + 31
-    const int cp = tid & 63, q = tid >> 6;
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
-    uint32_t w[32];
-    uint32_t m = 0u;
+      __syncthreads();   // the previous tile is consumed
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      w[i] = words[(32 * q + i) * 64 + cp];
-      m = max_mag2(m, w[i]);
-    }
-    s_max[q][cp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, s_max[i][cp]);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int c = c0 + 2 * cp + j;
-      if (c >= src.cols) continue;
-      float s, r;
-      block_scale(j ? m >> 16 : m & 0xffffu, out.pow2, s, r);
-      uint32_t code[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) code[i] = col_code(w, i, j != 0, r);
-      uint4* dst = reinterpret_cast<uint4*>(
-          out.codes_t + (static_cast<long long>(c) * out.kb_cap + kb) * 128 + 32 * q);
-      dst[0] = make_uint4(code[0], code[1], code[2], code[3]);
-      dst[1] = make_uint4(code[4], code[5], code[6], code[7]);
-      if (q == 0) out.scales_t[static_cast<long long>(kb) * src.cols + c] = s;
+      for (int u = 0; u < 4; ++u) tile[(r + 32 * u) * 16 + (tid & 15)] = v[u];
+      if (out.codes) tile_rows(v, r0, nr, c, src.cols, out);
+      __syncthreads();
+      tile_columns(tile, s_max[0], c0, src.cols, kb, out.codes_t, out.scales_t, out.kb_cap,
+                   out.pow2);
     }
   }
   griddep_launch();
@@ -451,9 +669,9 @@ fp8_weights_kernel(const __nv_bfloat16* __restrict__ W, int N, int K, int nb, in
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, s_max[i]);
-  float s, r;
-  block_scale(m, pow2, s, r);
+  const float r = block_quotient(m, pow2, 0);
   if (tid == 0) {
+    const float s = block_quotient(m, pow2, 1);
     scales[gb * kb + kbi] = s;
     if (codes_t) scales_t[(g * kb + kbi) * nb + n0 / 128] = s;
   }
@@ -505,23 +723,27 @@ int fq_sms() {
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int SRC, bool VEC>
-cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut& o, bool tokens,
-                         cudaStream_t st) {
-  if (!tokens) {
+template <int SRC, bool VEC, bool BOTH = false>
+cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut& o,
+                         const QuantOut& oh, cudaStream_t st) {
+  if (!o.codes_t) {
     const long long want = (a.rows + FQ_THREADS / 32 - 1) / (FQ_THREADS / 32);
     const long long most = static_cast<long long>(fq_sms()) * 8;
-    return launch_pdl(fp8_rows_kernel<SRC, VEC>, dim3(static_cast<unsigned>(want < most ? want : most)),
-                      dim3(FQ_THREADS), 0, st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G, a.rows,
-                      o, a.err);
+    return launch_pdl(fp8_rows_kernel<SRC, VEC>,
+                      dim3(static_cast<unsigned>(want < most ? want : most)), dim3(FQ_THREADS), 0,
+                      st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, a.err);
   }
-  const unsigned gx = static_cast<unsigned>((s.cols + 127) / 128);
-  const long long most = (static_cast<long long>(fq_sms()) * 8 + gx - 1) / gx;
-  const long long blocks = fp8_token_blocks(a.rows, a.G);
-  return launch_pdl(fp8_tokens_kernel<SRC, VEC>,
-                    dim3(gx, static_cast<unsigned>(blocks < most ? blocks : most)),
-                    dim3(FQ_THREADS), 0, st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o,
-                    a.err);
+  auto kern = fp8_tokens_kernel<SRC, VEC, BOTH>;
+  constexpr int smem = (BOTH ? 3 : 1) * FT_TILE * 16;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const long long items =
+      fp8_token_blocks(a.rows, a.G) * (((BOTH ? s.f : s.cols) + 127) / 128);
+  const long long most = static_cast<long long>(fq_sms()) * 2;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(items < most ? items : most)),
+                    dim3(FT_THREADS), smem, st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G,
+                    a.rows, o, oh, a.err);
 }
 
 }  // namespace
@@ -542,26 +764,26 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, cudaStream_t st) {
   o.scales_t = a.scales_t;
   o.kb_cap = static_cast<int>(fp8_token_blocks(a.rows, a.G));
   o.pow2 = a.pow2;
-  const bool tokens = a.codes_t != nullptr;
+  QuantOut oh = o;
+  oh.codes = nullptr;
+  oh.codes_t = static_cast<uint8_t*>(a.h_codes_t);
+  oh.scales_t = a.h_scales_t;
   if (a.src == FP8_SRC_ROWS) {
     const bool vec = on16(a.x) && a.ldx % 8 == 0 && a.C % 8 == 0;
-    return vec ? launch_quant<SRC_ROWS, true>(s, a, o, tokens, st)
-               : launch_quant<SRC_ROWS, false>(s, a, o, tokens, st);
+    return vec ? launch_quant<SRC_ROWS, true>(s, a, o, oh, st)
+               : launch_quant<SRC_ROWS, false>(s, a, o, oh, st);
   }
-  const bool vec = a.f % 8 == 0;
   if (a.src == FP8_SRC_SWIGLU)
-    return vec ? launch_quant<SRC_SWIGLU, true>(s, a, o, tokens, st)
-               : launch_quant<SRC_SWIGLU, false>(s, a, o, tokens, st);
-  const cudaError_t e = vec ? launch_quant<SRC_SWIGLU_BWD, true>(s, a, o, tokens, st)
-                            : launch_quant<SRC_SWIGLU_BWD, false>(s, a, o, tokens, st);
+    return a.f % 8 == 0 ? launch_quant<SRC_SWIGLU, true>(s, a, o, oh, st)
+                        : launch_quant<SRC_SWIGLU, false>(s, a, o, oh, st);
+  // the backward reads a, b and dh once for da, db and h where the blocks of da and db do not
+  // share one (f a multiple of 128); other widths are computed by the column, and h apart
+  if (a.f % 128 == 0) return launch_quant<SRC_SWIGLU_BWD, true, true>(s, a, o, oh, st);
+  const cudaError_t e = launch_quant<SRC_SWIGLU_BWD, false>(s, a, o, oh, st);
   if (e != cudaSuccess || !a.h_codes_t) return e;
-  s.h_only = true;
   s.cols = a.f;
-  o.codes = nullptr;
-  o.codes_t = static_cast<uint8_t*>(a.h_codes_t);
-  o.scales_t = a.h_scales_t;
-  return vec ? launch_quant<SRC_SWIGLU_BWD, true>(s, a, o, true, st)
-             : launch_quant<SRC_SWIGLU_BWD, false>(s, a, o, true, st);
+  return a.f % 8 == 0 ? launch_quant<SRC_SWIGLU, true>(s, a, oh, oh, st)
+                      : launch_quant<SRC_SWIGLU, false>(s, a, oh, oh, st);
 }
 
 cudaError_t launch_fp8_weights(const void* W, int G, int N, int K, void* codes, int64_t ld,
