@@ -30,10 +30,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {   // a in the low
                                                         __NV_E4M3));
 }
 
-// A block's factor (which = 0) or scale (1), from the bits of its largest magnitude (bf16, so
-// that NaN > inf > every number in the bits' order).
-__device__ __forceinline__ float block_quotient(uint32_t amax_bf16, int pow2, int which) {
-  float a = __uint_as_float(amax_bf16 << 16);
+// A block's factor (which = 0) or scale (1), from the doubled bits of its largest magnitude.
+__device__ __forceinline__ float block_quotient(uint32_t amax2, int pow2, int which) {
+  float a = __uint_as_float(amax2 << 15);
   if (a < AMAX_FLOOR) a = AMAX_FLOOR;
   if (pow2 && a < INFINITY) {
     // 448 = 1.75 * 2^8: the exponent of a less 8, and one more where a's fraction is above
@@ -44,23 +43,28 @@ __device__ __forceinline__ float block_quotient(uint32_t amax_bf16, int pow2, in
   return __fdiv_rn(which ? a : E4M3_TOP, which ? E4M3_TOP : a);
 }
 
-__device__ __forceinline__ uint32_t max_mag2(uint32_t m, uint32_t w) {
-  return __vmaxu2(m, w & 0x7fff7fffu);
+// Magnitudes of two bf16 values as 16-bit numbers, doubled (x + x drops the sign): the larger of
+// them and m's, in one instruction.  In the bits' order NaN > inf > every number.
+__device__ __forceinline__ uint32_t max_mag(uint32_t m, uint32_t x) {
+  return __viaddmax_u16x2(x, x, m);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 __device__ __forceinline__ uint32_t max_mag8(const uint4& v) {
-  uint32_t m = max_mag2(v.x & 0x7fff7fffu, v.y);
-  m = max_mag2(m, v.z);
-  return max_mag2(m, v.w);
+  return max_mag(max_mag(max_mag(max_mag(0u, v.x), v.y), v.z), v.w);
 }
-__device__ __forceinline__ uint32_t fold2(uint32_t m) {   // the larger of the two halves
-  const uint32_t hi = m >> 16, lo = m & 0xffffu;
-  return hi > lo ? hi : lo;
+// four values (two packed words) times r
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, float r) {
+  const float2 r2 = make_float2(r, r);
+  const float2 x = __fmul2_rn(make_float2(bf16_lo(a), bf16_hi(a)), r2);
+  const float2 y = __fmul2_rn(make_float2(bf16_lo(b), bf16_hi(b)), r2);
+  return e4m3x2(x.x, x.y) | (e4m3x2(y.x, y.y) << 16);
 }
 __device__ __forceinline__ uint2 codes8(const uint4& v, float r) {
-  float f[8];
-  unpack8(v, f);
-  return make_uint2(e4m3x2(f[0] * r, f[1] * r) | (e4m3x2(f[2] * r, f[3] * r) << 16),
-                    e4m3x2(f[4] * r, f[5] * r) | (e4m3x2(f[6] * r, f[7] * r) << 16));
+  return make_uint2(codes4(v.x, v.y, r), codes4(v.z, v.w, r));
 }
 
 // ------------------------------------------------------------------ SwiGLU values
@@ -183,14 +187,22 @@ __device__ __forceinline__ bool unsettled(float v, uint32_t ulps) {
          (u & 0x7fffffffu) - 0x0d800000u >= 0x7f800000u - 0x0d800000u;
 }
 
+// 1 / d for d >= 1, off by at most one ulp (0 from 2^126 on)
+__device__ __forceinline__ float fast_rcp(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
+}
+
 // silu(a) b = a b / (1 + e^-a): a b is exact, expf is off by at most one ulp (2^-23), the sum by
-// 2^-24, the fast quotient by two ulp (2^-22): 1.75 * 2^-22 of the value, at most 7 of its fp32
-// steps.  Where e^-a or the quotient leaves its range the result is 0, which is unsettled.
+// 2^-24, the reciprocal by one ulp (2^-23), the product by 2^-24: 1.5 * 2^-22 of the value, at most
+// 6 of its fp32 steps.  Where e^-a or the reciprocal leaves its range the result is 0, which is
+// unsettled.
 __device__ __forceinline__ uint32_t silu_mul2(uint32_t a, uint32_t b) {
   const float a0 = bf16_lo(a), a1 = bf16_hi(a), b0 = bf16_lo(b), b1 = bf16_hi(b);
-  float v0 = __fdividef(a0 * b0, 1.0f + expf(-a0));
-  float v1 = __fdividef(a1 * b1, 1.0f + expf(-a1));
-  const bool o0 = unsettled(v0, 8), o1 = unsettled(v1, 8);
+  float v0 = a0 * b0 * fast_rcp(1.0f + expf(-a0));
+  float v1 = a1 * b1 * fast_rcp(1.0f + expf(-a1));
+  const bool o0 = unsettled(v0, 6), o1 = unsettled(v1, 6);
   if (o0 || o1) {
     if (o0) v0 = silu_mul_exact(a0, b0);
     if (o1) v1 = silu_mul_exact(a1, b1);
@@ -203,9 +215,9 @@ __device__ __forceinline__ uint4 silu_mul8(const uint4& a, const uint4& b) {
 }
 
 // All three of a pair of columns from one exponential: h = a b s, db = dh a s, da = dh b s g with
-// s = 1 / (1 + t), t = e^-a, u = a t s = a (1 - s), g = 1 + u.  s is off by 1.75 * 2^-22 (as
-// above); h and db add one rounding: below 2^-21, 8 steps, again.  da: |dh b s| (|u| + |g|)
-// 2.75 * 2^-22 (t 2^-23; s 1.75 * 2^-22; four roundings).
+// s = 1 / (1 + t), t = e^-a, u = a t s = a (1 - s), g = 1 + u.  s is off by 1.25 * 2^-22 (as
+// above); h and db add one rounding: 6 steps, again.  da: |dh b s| (|u| + |g|) 2.25 * 2^-22
+// (t 2^-23; s 1.25 * 2^-22; two roundings of u; one of g and two of the products).
 struct Swiglu2 {
   uint32_t da, db, h;
 };
@@ -216,15 +228,15 @@ __device__ __forceinline__ Swiglu2 swiglu_bwd2(uint32_t a, uint32_t b, uint32_t 
     const float fa = i ? bf16_hi(a) : bf16_lo(a), fb = i ? bf16_hi(b) : bf16_lo(b),
                 fd = i ? bf16_hi(dh) : bf16_lo(dh);
     const float t = expf(-fa);
-    const float s = __fdividef(1.0f, 1.0f + t);
+    const float s = fast_rcp(1.0f + t);
     const float u = fa * t * s;
     const float g = 1.0f + u;
     const float qs = fd * fb * s;
     h[i] = fa * fb * s;
     db[i] = fd * fa * s;
     da[i] = qs * g;
-    const float e = fabsf(qs) * (fabsf(u) + fabsf(g)) * 0x1.8p-21f;
-    const bool oh = unsettled(h[i], 8), ob = unsettled(db[i], 8);
+    const float e = fabsf(qs) * (fabsf(u) + fabsf(g)) * 0x1.4p-21f;
+    const bool oh = unsettled(h[i], 6), ob = unsettled(db[i], 6);
     const uint32_t ends = pack_bf16x2(da[i] - e, da[i] + e);
     const bool oa = (ends >> 16) != (ends & 0xffffu) || !(e >= 0x1p-120f && e < INFINITY);
     if (oh || ob || oa) {
@@ -323,25 +335,28 @@ __device__ __forceinline__ long long live_rows(const int32_t* offsets, int G, lo
 
 // Four blocks of a row (or of four rows), a chunk of eight values per lane in each, sixteen lanes
 // to a block: their scales and factors, by one pass of shuffles (two blocks' maxima to a
-// word) and one division, lane 2 b of the sixteen dividing for block b's factor and lane 2 b + 1
-// for its scale.  `quot` gets this lane's quotient.
+// word) and one division, of whose lanes one divides for each block's factor and its neighbour
+// for the scale.  `quot` gets this lane's quotient.
 __device__ __forceinline__ void four_scales(const uint4* v, int pow2, int lane, float* r,
                                             float& quot) {
   uint32_t m[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) m[b] = max_mag8(v[b]);
-  uint32_t x = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
-  uint32_t y = __vmaxu2(__byte_perm(m[2], m[3], 0x5410), __byte_perm(m[2], m[3], 0x7632));
+  const uint32_t x = max2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+  const uint32_t y = max2(__byte_perm(m[2], m[3], 0x5410), __byte_perm(m[2], m[3], 0x7632));
+  // eight lanes go on with blocks 0 and 1, the other eight with 2 and 3
+  const bool upper = lane & 8;
+  uint32_t w = max2(upper ? y : x, __shfl_xor_sync(FULL_MASK, upper ? x : y, 8));
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    x = __vmaxu2(x, __shfl_xor_sync(FULL_MASK, x, o));
-    y = __vmaxu2(y, __shfl_xor_sync(FULL_MASK, y, o));
-  }
-  const uint32_t w = (lane & 4) ? y : x;
-  const uint32_t amax = (lane & 2) ? w >> 16 : w & 0xffffu;
-  quot = block_quotient(amax, pow2, lane & 1);
+  for (int o = 4; o > 0; o >>= 1) w = max2(w, __shfl_xor_sync(FULL_MASK, w, o));
+  quot = block_quotient((lane & 2) ? w >> 16 : w & 0xffffu, pow2, lane & 1);
 #pragma unroll
-  for (int b = 0; b < 4; ++b) r[b] = __shfl_sync(FULL_MASK, quot, (lane & 16) | (2 * b));
+  for (int b = 0; b < 4; ++b)
+    r[b] = __shfl_sync(FULL_MASK, quot, (lane & 16) | ((b & 2) << 2) | ((b & 1) << 1));
+}
+// the block whose scale this lane's quotient is, or -1
+__device__ __forceinline__ int scale_of_lane(int lane) {
+  return (lane & 5) == 1 ? ((lane >> 2) & 2) | ((lane >> 1) & 1) : -1;
 }
 
 // ------------------------------------------------------------------ along the rows
@@ -430,11 +445,10 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (col[i] < src.cols)
-          *reinterpret_cast<uint2*>(out.codes + p * out.ld + col[i]) = codes8(v[i], r[i]);
-      // lane 2 b + 1 of the first eight of each half stores block b's scale
-      const int b = (lane >> 1) & 3;
-      const int c = (b == 0 ? col[0] : b == 1 ? col[1] : b == 2 ? col[2] : col[3]) - 8 * (lane & 15);
-      if ((lane & 9) == 1 && c < src.cols && c >= 0) out.scales[p * out.kb + (c >> 7)] = quot;
+          __stcs(reinterpret_cast<uint2*>(out.codes + p * out.ld + col[i]), codes8(v[i], r[i]));
+      const int sb = scale_of_lane(lane);
+      const int c = (sb == 1 ? col[1] : sb == 2 ? col[2] : sb == 3 ? col[3] : col[0]) - 8 * (lane & 15);
+      if (sb >= 0 && c < src.cols) out.scales[p * out.kb + (c >> 7)] = quot;
     }
   }
   griddep_launch();
@@ -448,13 +462,6 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
 constexpr int FT_THREADS = 512;
 constexpr int FT_TILE = 128 * 16;   // 16-byte pieces
 
-__device__ __forceinline__ uint32_t col_code(const uint32_t* w, int i, bool hi, float r) {
-  float f[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) f[j] = (hi ? bf16_hi(w[4 * i + j]) : bf16_lo(w[4 * i + j])) * r;
-  return e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
-}
-
 // The tile's columns (c0 ..) along the tokens into block kb.
 __device__ __forceinline__ void tile_columns(const uint4* tile, uint32_t (*s_max)[64], int c0,
                                              int cols, int kb, uint8_t* codes_t, float* scales_t,
@@ -467,12 +474,12 @@ __device__ __forceinline__ void tile_columns(const uint4* tile, uint32_t (*s_max
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     w[i] = words[(16 * q + i) * 64 + cp];
-    m = max_mag2(m, w[i]);
+    m = max_mag(m, w[i]);
   }
   s_max[q][cp] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, s_max[i][cp]);
+  for (int i = 0; i < 8; ++i) m = max2(m, s_max[i][cp]);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int c = c0 + 2 * cp + j;
@@ -481,7 +488,11 @@ __device__ __forceinline__ void tile_columns(const uint4* tile, uint32_t (*s_max
     const float r = block_quotient(amax, pow2, 0);
     uint32_t code[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) code[i] = col_code(w, i, j != 0, r);
+    for (int i = 0; i < 4; ++i) {   // the column's halves of two rows' words to one
+      const uint32_t sel = j ? 0x7632 : 0x5410;
+      code[i] = codes4(__byte_perm(w[4 * i], w[4 * i + 1], sel),
+                       __byte_perm(w[4 * i + 2], w[4 * i + 3], sel), r);
+    }
     *reinterpret_cast<uint4*>(codes_t + (static_cast<long long>(c) * kb_cap + kb) * 128 + 16 * q) =
         make_uint4(code[0], code[1], code[2], code[3]);
     if (q == 0) scales_t[static_cast<long long>(kb) * cols + c] = block_quotient(amax, pow2, 1);
@@ -500,8 +511,8 @@ __device__ __forceinline__ void tile_rows(const uint4* v, long long r0, int nr, 
       if (r + 32 * u < nr)
         *reinterpret_cast<uint2*>(out.codes + (r0 + r + 32 * u) * out.ld + c) = codes8(v[u], f[u]);
   }
-  const int row = r + 32 * ((lane >> 1) & 3), c_first = c - 8 * (lane & 15);
-  if ((lane & 9) == 1 && row < nr && c_first < cols)
+  const int sb = scale_of_lane(lane), row = r + 32 * sb, c_first = c - 8 * (lane & 15);
+  if (sb >= 0 && row < nr && c_first < cols)
     out.scales[(r0 + row) * out.kb + (c_first >> 7)] = quot;
 }
 
@@ -661,9 +672,9 @@ fp8_weights_kernel(const __nv_bfloat16* __restrict__ W, int N, int K, int nb, in
     const int n = n0 + (tid >> 4) + 16 * u;
     v[u] = make_uint4(0u, 0u, 0u, 0u);
     if (n < N && c < K) v[u] = load8<VEC>(W + (g * N + n) * K + c, K - c);
-    m = __vmaxu2(m, max_mag8(v[u]));
+    m = max2(m, max_mag8(v[u]));
   }
-  m = fold2(m);
+  m = max(m & 0xffffu, m >> 16);
   m = __reduce_max_sync(FULL_MASK, m);
   if ((tid & 31) == 0) s_max[tid >> 5] = m;
   __syncthreads();
