@@ -30,9 +30,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {   // a in the low
                                                         __NV_E4M3));
 }
 
-// A block's factor (which = 0) or scale (1), from the doubled bits of its largest magnitude.
-__device__ __forceinline__ float block_quotient(uint32_t amax2, int pow2, int which) {
-  float a = __uint_as_float(amax2 << 15);
+// A block's factor (which = 0) or scale (1), from the bits of its largest magnitude.
+__device__ __forceinline__ float block_quotient(uint32_t amax, int pow2, int which) {
+  float a = __uint_as_float(amax << 16);
   if (a < AMAX_FLOOR) a = AMAX_FLOOR;
   if (pow2 && a < INFINITY) {
     // 448 = 1.75 * 2^8: the exponent of a less 8, and one more where a's fraction is above
@@ -43,18 +43,18 @@ __device__ __forceinline__ float block_quotient(uint32_t amax2, int pow2, int wh
   return __fdiv_rn(which ? a : E4M3_TOP, which ? E4M3_TOP : a);
 }
 
-// Magnitudes of two bf16 values as 16-bit numbers, doubled (x + x drops the sign): the larger of
-// them and m's, in one instruction.  In the bits' order NaN > inf > every number.
-__device__ __forceinline__ uint32_t max_mag(uint32_t m, uint32_t x) {
-  return __viaddmax_u16x2(x, x, m);
-}
+// two 16-bit maxima at once
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// the larger magnitudes of two pairs of bf16 values, in whose bits' order NaN > inf > every number
+__device__ __forceinline__ uint32_t max_mag(uint32_t m, uint32_t x) {
+  return max2(m, x & 0x7fff7fffu);
+}
 __device__ __forceinline__ uint32_t max_mag8(const uint4& v) {
-  return max_mag(max_mag(max_mag(max_mag(0u, v.x), v.y), v.z), v.w);
+  return max_mag(max_mag(max_mag(v.x & 0x7fff7fffu, v.y), v.z), v.w);
 }
 // four values (two packed words) times r
 __device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b, float r) {
@@ -96,7 +96,7 @@ __constant__ float kRootHi[8] = {1.0f, 0x1.172b84p+0f, 0x1.306fe0p+0f, 0x1.4bfda
                                   0x1.6a09e6p+0f, 0x1.8ace54p+0f, 0x1.ae89fap+0f, 0x1.d5818ep+0f};
 __constant__ float kRootLo[8] = {0.0f, -0x1.c15742p-27f, 0x1.4636e2p-25f, -0x1.593abcp-25f,
                                   0x1.9fcef4p-26f, 0x1.15506ep-27f, -0x1.a94b14p-26f, -0x1.822dbcp-27f};
-// t = e^-a and s = 1 / (1 + t) for |a| <= 16, off by less than 2^-33 of themselves: with
+// t = e^-a and s = 1 / (1 + t) for |a| <= 80, off by less than 2^-31.5 of themselves: with
 // -a = n ln2 / 8 + r, e^-a = 2^(n/8) e^r, |r| < 0.0434, and e^r = 1 + r + r^2/2 in pairs plus a
 // tail r^3 (1/6 + ...) below 2^-16, for which fp32 is enough.
 __device__ __forceinline__ void sigmoid_pair(float a, Pair& t, Pair& s) {
@@ -140,28 +140,29 @@ __device__ __forceinline__ bool settled(Pair v, float e, float& out) {
   out = v.h + (v.l - e);
   return bf16_bits(out) == bf16_bits(v.h + (v.l + e));
 }
-// the pairs' range: |gate| <= 16, and results far from fp32's smallest and largest numbers
+// results far from fp32's smallest and largest numbers
 __device__ __forceinline__ bool in_range(float v) {
   return fabsf(v) >= 0x1p-100f && fabsf(v) < 0x1p126f;
 }
+constexpr float GATE_MAX = 80.0f;   // above it, and for results out of range, 64 bits
 
 __device__ __noinline__ float silu_mul_exact(float a, float b) {
   const float p = a * b;   // exact: two 8-bit significands
   if (p == 0.0f) return p;
-  if (fabsf(a) <= 16.0f && in_range(p)) {
+  if (fabsf(a) <= GATE_MAX && in_range(p)) {
     Pair t, s;
     sigmoid_pair(a, t, s);
     const float v = p * s.h;
     float out;
     if (in_range(v) &&
-        settled(quick_sum(v, fmaf(p, s.h, -v) + p * s.l), fabsf(v) * 0x1p-33f, out))
+        settled(quick_sum(v, fmaf(p, s.h, -v) + p * s.l), fabsf(v) * 0x1p-31f, out))
       return out;
   }
   return silu_mul_64(a, b);
 }
 __device__ __noinline__ float dsilu_mul_exact(float a, float b, float dh) {
   const float p = dh * b;
-  if (fabsf(a) <= 16.0f && (p == 0.0f || in_range(p))) {
+  if (fabsf(a) <= GATE_MAX && (p == 0.0f || in_range(p))) {
     if (p == 0.0f) return p;
     Pair t, s;
     sigmoid_pair(a, t, s);
@@ -173,41 +174,69 @@ __device__ __noinline__ float dsilu_mul_exact(float a, float b, float dh) {
     const float v = p * m.h;
     float out;
     if (in_range(v) && settled(quick_sum(v, fmaf(p, m.h, -v) + p * m.l),
-                               fabsf(p * s.h) * (fabsf(u.h) + fabsf(g.h)) * 0x1p-32f, out))
+                               fabsf(p * s.h) * (fabsf(u.h) + fabsf(g.h)) * 0x1p-30f, out))
       return out;
   }
   return dsilu_mul_64(a, b, dh);
 }
 
-// Whether an fp32 value may not round as the exact one does: its fraction is within `ulps` fp32
-// steps of a border between bf16 numbers, or it is below 2^-100 (zeros too), infinite or NaN.
-__device__ __forceinline__ bool unsettled(float v, uint32_t ulps) {
-  const uint32_t u = __float_as_uint(v);
-  return ((u + ulps - 0x8000u) & 0xffffu) <= 2 * ulps ||
-         (u & 0x7fffffffu) - 0x0d800000u >= 0x7f800000u - 0x0d800000u;
+// The fp32 values, two at a time.  Whether any of them has to be computed again is asked once for
+// all, in few instructions (these kernels are bound by the instructions they issue): values are
+// settled if
+//   their low 16 bits are more than 10 from 0x8000, that is, they lie more than 10 fp32 steps from
+//   every border between bf16 numbers;
+//   their magnitudes are between 2^-100 and the largest number (a 0 is computed again too, which
+//   returns at once); and the gates are within +-80.
+__device__ __forceinline__ float2 wide2(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+constexpr uint32_t SETTLE_STEPS = 10;
+// distance from the border plus SETTLE_STEPS, modulo 2^16, in the upper half
+__device__ __forceinline__ uint32_t border_place(float v) {
+  return __float_as_uint(v) * 0x10000u + ((0x8000u + SETTLE_STEPS) << 16);
 }
+constexpr uint32_t BORDER_END = (2 * SETTLE_STEPS + 1) << 16;
+__device__ __forceinline__ bool unsettled(float v, float gate) {
+  return border_place(v) < BORDER_END || !(fabsf(v) >= 0x1p-100f && fabsf(v) < INFINITY) ||
+         !(fabsf(gate) <= GATE_MAX);
+}
+__device__ __forceinline__ float least(float a, float b) { return fminf(fabsf(a), fabsf(b)); }
+__device__ __forceinline__ float most(float a, float b) { return fmaxf(fabsf(a), fabsf(b)); }
 
+__device__ __forceinline__ float ex2(float x) {   // off by at most two ulp
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 // 1 / d for d >= 1, off by at most one ulp (0 from 2^126 on)
 __device__ __forceinline__ float fast_rcp(float d) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
   return r;
 }
+// t = e^-a: 2^y with y = -a / ln 2 rounded, times 1 + c, c = -a - y ln 2 (ln 2 in two parts).  Off by
+// ex2's two ulp (2^-22) and one rounding: 1.25 * 2^-22.
+__device__ __forceinline__ float2 exp_neg2(float2 a) {
+  const float2 na = __fmul2_rn(a, both(-1.0f));
+  const float2 y = __fmul2_rn(na, both(0x1.715476p+0f));
+  float2 c = __ffma2_rn(y, both(-0x1.62e430p-1f), na);
+  c = __ffma2_rn(y, both(0x1.05c610p-29f), c);
+  const float2 t = make_float2(ex2(y.x), ex2(y.y));
+  return __ffma2_rn(t, c, t);
+}
 
-// silu(a) b = a b / (1 + e^-a): a b is exact, expf is off by at most one ulp (2^-23), the sum by
-// 2^-24, the reciprocal by one ulp (2^-23), the product by 2^-24: 1.5 * 2^-22 of the value, at most
-// 6 of its fp32 steps.  Where e^-a or the reciprocal leaves its range the result is 0, which is
-// unsettled.
+// silu(a) b = a b s, s = 1 / (1 + t): a b is exact; t 1.25 * 2^-22, the sum 2^-24, the reciprocal
+// 2^-23, the product 2^-24: below 2.25 * 2^-22, 9 fp32 steps.
 __device__ __forceinline__ uint32_t silu_mul2(uint32_t a, uint32_t b) {
-  const float a0 = bf16_lo(a), a1 = bf16_hi(a), b0 = bf16_lo(b), b1 = bf16_hi(b);
-  float v0 = a0 * b0 * fast_rcp(1.0f + expf(-a0));
-  float v1 = a1 * b1 * fast_rcp(1.0f + expf(-a1));
-  const bool o0 = unsettled(v0, 6), o1 = unsettled(v1, 6);
-  if (o0 || o1) {
-    if (o0) v0 = silu_mul_exact(a0, b0);
-    if (o1) v1 = silu_mul_exact(a1, b1);
+  const float2 fa = wide2(a), fb = wide2(b);
+  const float2 den = __fadd2_rn(exp_neg2(fa), both(1.0f));
+  float2 h = __fmul2_rn(__fmul2_rn(fa, fb), make_float2(fast_rcp(den.x), fast_rcp(den.y)));
+  const float far = most(h.x, h.y);
+  if (min(border_place(h.x), border_place(h.y)) < BORDER_END || !(least(h.x, h.y) >= 0x1p-100f) ||
+      !(far < INFINITY) || !(most(fa.x, fa.y) <= GATE_MAX)) {
+    if (unsettled(h.x, fa.x)) h.x = silu_mul_exact(fa.x, fb.x);
+    if (unsettled(h.y, fa.y)) h.y = silu_mul_exact(fa.y, fb.y);
   }
-  return pack_bf16x2(v0, v1);
+  return pack_bf16x2(h.x, h.y);
 }
 __device__ __forceinline__ uint4 silu_mul8(const uint4& a, const uint4& b) {
   return make_uint4(silu_mul2(a.x, b.x), silu_mul2(a.y, b.y), silu_mul2(a.z, b.z),
@@ -215,37 +244,47 @@ __device__ __forceinline__ uint4 silu_mul8(const uint4& a, const uint4& b) {
 }
 
 // All three of a pair of columns from one exponential: h = a b s, db = dh a s, da = dh b s g with
-// s = 1 / (1 + t), t = e^-a, u = a t s = a (1 - s), g = 1 + u.  s is off by 1.25 * 2^-22 (as
-// above); h and db add one rounding: 6 steps, again.  da: |dh b s| (|u| + |g|) 2.25 * 2^-22
-// (t 2^-23; s 1.25 * 2^-22; two roundings of u; one of g and two of the products).
+// u = a t s = a (1 - s), g = 1 + u.  h and db as above.  da: |dh b s| (|u| + |g|) 4 * 2^-22 (t
+// 1.25 * 2^-22; s 2 * 2^-22; two roundings of u, one of g and two of the products 2^-24 each),
+// which near the zero of silu' is many steps of da: both ends of that bound are rounded instead.
 struct Swiglu2 {
   uint32_t da, db, h;
 };
 __device__ __forceinline__ Swiglu2 swiglu_bwd2(uint32_t a, uint32_t b, uint32_t dh) {
-  float da[2], db[2], h[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float fa = i ? bf16_hi(a) : bf16_lo(a), fb = i ? bf16_hi(b) : bf16_lo(b),
-                fd = i ? bf16_hi(dh) : bf16_lo(dh);
-    const float t = expf(-fa);
-    const float s = fast_rcp(1.0f + t);
-    const float u = fa * t * s;
-    const float g = 1.0f + u;
-    const float qs = fd * fb * s;
-    h[i] = fa * fb * s;
-    db[i] = fd * fa * s;
-    da[i] = qs * g;
-    const float e = fabsf(qs) * (fabsf(u) + fabsf(g)) * 0x1.4p-21f;
-    const bool oh = unsettled(h[i], 6), ob = unsettled(db[i], 6);
-    const uint32_t ends = pack_bf16x2(da[i] - e, da[i] + e);
-    const bool oa = (ends >> 16) != (ends & 0xffffu) || !(e >= 0x1p-120f && e < INFINITY);
-    if (oh || ob || oa) {
-      if (oh) h[i] = silu_mul_exact(fa, fb);
-      if (ob) db[i] = silu_mul_exact(fa, fd);
-      if (oa) da[i] = dsilu_mul_exact(fa, fb, fd);
-    }
+  const float2 fa = wide2(a), fb = wide2(b), fd = wide2(dh);
+  const float2 t = exp_neg2(fa);
+  const float2 den = __fadd2_rn(t, both(1.0f));
+  const float2 s = make_float2(fast_rcp(den.x), fast_rcp(den.y));
+  const float2 u = __fmul2_rn(__fmul2_rn(fa, t), s);
+  const float2 g = __fadd2_rn(u, both(1.0f));
+  float2 h = __fmul2_rn(__fmul2_rn(fa, fb), s);
+  float2 db = __fmul2_rn(__fmul2_rn(fd, fa), s);
+  const float2 qs = __fmul2_rn(__fmul2_rn(fd, fb), s);
+  const float2 v = __fmul2_rn(qs, g);
+  const float2 w = make_float2((fabsf(u.x) + fabsf(g.x)) * fabsf(qs.x),
+                               (fabsf(u.y) + fabsf(g.y)) * fabsf(qs.y));
+  const uint32_t lo = pack_bf16x2(fmaf(w.x, -0x1p-20f, v.x), fmaf(w.y, -0x1p-20f, v.y));
+  const uint32_t hi = pack_bf16x2(fmaf(w.x, 0x1p-20f, v.x), fmaf(w.y, 0x1p-20f, v.y));
+  const uint32_t near = min(min(border_place(h.x), border_place(h.y)),
+                            min(border_place(db.x), border_place(db.y)));
+  const float close = fminf(fminf(least(h.x, h.y), least(db.x, db.y)), fminf(w.x, w.y));
+  const float far = fmaxf(fmaxf(most(h.x, h.y), most(db.x, db.y)), fmaxf(w.x, w.y));
+  auto fits = [](float x) { return x >= 0x1p-100f && x < INFINITY; };
+  uint32_t da = lo;
+  if (near < BORDER_END || lo != hi || !(close >= 0x1p-100f) || !(far < INFINITY) ||
+      !(most(fa.x, fa.y) <= GATE_MAX)) {
+    if (unsettled(h.x, fa.x)) h.x = silu_mul_exact(fa.x, fb.x);
+    if (unsettled(h.y, fa.y)) h.y = silu_mul_exact(fa.y, fb.y);
+    if (unsettled(db.x, fa.x)) db.x = silu_mul_exact(fa.x, fd.x);
+    if (unsettled(db.y, fa.y)) db.y = silu_mul_exact(fa.y, fd.y);
+    const uint32_t off = lo ^ hi;
+    const float x = (off & 0xffffu) || !fits(w.x) || !(fabsf(fa.x) <= GATE_MAX)
+                        ? dsilu_mul_exact(fa.x, fb.x, fd.x) : bf16_lo(lo);
+    const float y = (off >> 16) || !fits(w.y) || !(fabsf(fa.y) <= GATE_MAX)
+                        ? dsilu_mul_exact(fa.y, fb.y, fd.y) : bf16_hi(lo);
+    da = pack_bf16x2(x, y);
   }
-  return {pack_bf16x2(da[0], da[1]), pack_bf16x2(db[0], db[1]), pack_bf16x2(h[0], h[1])};
+  return {da, pack_bf16x2(db.x, db.y), pack_bf16x2(h.x, h.y)};
 }
 
 // ------------------------------------------------------------------ sources
@@ -333,6 +372,13 @@ __device__ __forceinline__ long long live_rows(const int32_t* offsets, int G, lo
   return n;
 }
 
+// 16 bytes global -> shared, asynchronously; zeros where !ok (nothing is read)
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(ok ? 16 : 0)
+               : "memory");
+}
+
 // Four blocks of a row (or of four rows), a chunk of eight values per lane in each, sixteen lanes
 // to a block: their scales and factors, by one pass of shuffles (two blocks' maxima to a
 // word) and one division, of whose lanes one divides for each block's factor and its neighbour
@@ -363,7 +409,7 @@ __device__ __forceinline__ int scale_of_lane(int lane) {
 // One warp per row; a lane takes eight values (16 bytes), half a warp a block, four chunks'
 // loads before any is used.
 template <int SRC, bool VEC>
-__global__ void __launch_bounds__(FQ_THREADS)
+__global__ void __launch_bounds__(FQ_THREADS, 4)
 fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
                 const int32_t* __restrict__ offsets, int G, long long rows, const QuantOut out,
                 int* err) {
@@ -455,141 +501,270 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
 }
 
 // ------------------------------------------------------------------ along the tokens (and rows)
-// One CTA at a time per 128 columns and 128-row block of a segment (blocks are counted from the
-// segment's first row).  A tile goes through shared memory: its rows are quantised from
-// the registers that loaded them, its columns from shared memory, two columns and sixteen rows
-// per thread.  With BOTH the tile is 128 columns of f: da, db and h from one read of a, b and dh.
-constexpr int FT_THREADS = 512;
+// Tiles of 128 columns and one 128-row block of a segment (blocks are counted from the segment's
+// first row), column tiles fastest.
+struct Blocks {
+  int first[FQ_MAX_G + 1];   // first block of every segment
+  int sum[8];
+  int bad;
+};
+struct TileAt {
+  int kb, c0, nr;            // block, first column, rows in it
+  long long r0;              // first row
+};
+__device__ __forceinline__ long long segment_start(const int32_t* offsets, int g, long long rows) {
+  return offsets ? static_cast<long long>(__ldg(offsets + g)) : (g ? rows : 0LL);
+}
+// All threads of the CTA (at least 256); false for bad offsets.
+__device__ __forceinline__ bool count_blocks(Blocks& s, const int32_t* offsets, int G,
+                                             long long rows, int* err) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) s.bad = 0;
+  __syncthreads();
+  int nb = 0;   // G <= 256: one segment per thread of the first eight warps
+  if (tid < G) {
+    const long long a = segment_start(offsets, tid, rows), b = segment_start(offsets, tid + 1, rows);
+    if (a < 0 || b < a || b > rows || (tid == 0 && a != 0)) s.bad = 1;
+    else nb = static_cast<int>((b - a + 127) / 128);
+  }
+  const int incl = warp_incl_scan(nb);
+  if (lane == 31 && warp < 8) s.sum[warp] = incl;
+  __syncthreads();
+  if (tid < G) {
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += s.sum[w];
+    s.first[tid] = before + incl - nb;
+    if (tid == G - 1) s.first[G] = before + incl;
+  }
+  __syncthreads();
+  if (s.bad && blockIdx.x == 0 && tid == 0) flag_error(err, MOE_DEVERR_BAD_OFFSETS);
+  return s.bad == 0;
+}
+__device__ __forceinline__ TileAt tile_at(const Blocks& s, const int32_t* offsets, int G,
+                                          long long rows, long long item, int gx) {
+  TileAt t;
+  t.kb = static_cast<int>(item / gx);
+  t.c0 = static_cast<int>(item - static_cast<long long>(t.kb) * gx) * 128;
+  int lo = 0, hi = G;   // first[lo] <= kb < first[lo + 1]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.first[mid] <= t.kb) lo = mid;
+    else hi = mid;
+  }
+  t.r0 = segment_start(offsets, lo, rows) + 128LL * (t.kb - s.first[lo]);
+  const long long left = segment_start(offsets, lo + 1, rows) - t.r0;
+  t.nr = left < 128 ? static_cast<int>(left) : 128;
+  return t;
+}
+
 constexpr int FT_TILE = 128 * 16;   // 16-byte pieces
 
-// The tile's columns (c0 ..) along the tokens into block kb.
-__device__ __forceinline__ void tile_columns(const uint4* tile, uint32_t (*s_max)[64], int c0,
-                                             int cols, int kb, uint8_t* codes_t, float* scales_t,
-                                             int kb_cap, int pow2) {
-  // columns c0 + 2 cp, + 1; rows 16 q .. 16 q + 15
-  const int cp = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
-  uint32_t w[16];
-  uint32_t m = 0u;
+// A tile's columns (c0 ..) along the tokens into block kb, by `64 * Q` threads of which this is
+// number `th`: two columns and 128 / Q rows each.  Joined by a barrier of the whole CTA.
+template <int Q>
+struct Columns {
+  uint32_t w[128 / Q];
+  uint32_t m;
+  __device__ __forceinline__ void read(const uint4* tile, int th, uint32_t (*s_max)[64]) {
+    const int cp = th & 63, q = th >> 6;
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(tile);
+    m = 0u;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    w[i] = words[(16 * q + i) * 64 + cp];
-    m = max_mag(m, w[i]);
-  }
-  s_max[q][cp] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max2(m, s_max[i][cp]);
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int c = c0 + 2 * cp + j;
-    if (c >= cols) continue;
-    const uint32_t amax = j ? m >> 16 : m & 0xffffu;
-    const float r = block_quotient(amax, pow2, 0);
-    uint32_t code[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {   // the column's halves of two rows' words to one
-      const uint32_t sel = j ? 0x7632 : 0x5410;
-      code[i] = codes4(__byte_perm(w[4 * i], w[4 * i + 1], sel),
-                       __byte_perm(w[4 * i + 2], w[4 * i + 3], sel), r);
+    for (int i = 0; i < 128 / Q; ++i) {
+      w[i] = words[(128 / Q * q + i) * 64 + cp];
+      m = max_mag(m, w[i]);
     }
-    *reinterpret_cast<uint4*>(codes_t + (static_cast<long long>(c) * kb_cap + kb) * 128 + 16 * q) =
-        make_uint4(code[0], code[1], code[2], code[3]);
-    if (q == 0) scales_t[static_cast<long long>(kb) * cols + c] = block_quotient(amax, pow2, 1);
+    s_max[q][cp] = m;
   }
-}
+  __device__ __forceinline__ void write(int th, uint32_t (*s_max)[64], int c0, int cols, int kb,
+                                        const QuantOut& o) {
+    const int cp = th & 63, q = th >> 6;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) m = max2(m, s_max[i][cp]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int c = c0 + 2 * cp + j;
+      if (c >= cols) continue;
+      const uint32_t amax = j ? m >> 16 : m & 0xffffu;
+      const float r = block_quotient(amax, o.pow2, 0);
+      uint32_t code[32 / Q];
+#pragma unroll
+      for (int i = 0; i < 32 / Q; ++i) {
+        auto at = [&](int k) { return j ? bf16_hi(w[4 * i + k]) : bf16_lo(w[4 * i + k]); };
+        const float2 x = __fmul2_rn(make_float2(at(0), at(1)), both(r));
+        const float2 y = __fmul2_rn(make_float2(at(2), at(3)), both(r));
+        code[i] = e4m3x2(x.x, x.y) | (e4m3x2(y.x, y.y) << 16);
+      }
+      uint8_t* dst = o.codes_t + (static_cast<long long>(c) * o.kb_cap + kb) * 128 + 128 / Q * q;
+      if constexpr (Q == 16) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
+      } else {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
+      }
+      if (q == 0) o.scales_t[static_cast<long long>(kb) * cols + c] = block_quotient(amax, o.pow2, 1);
+    }
+  }
+};
 
-// Four rows of a tile (r + 32 u) along the row, a half-warp each.
-__device__ __forceinline__ void tile_rows(const uint4* v, long long r0, int nr, int c, int cols,
-                                          const QuantOut& out) {
-  const int lane = threadIdx.x & 31, r = threadIdx.x >> 4;
+// Four blocks along the row: row and column of each from at(i) (a half-warp each).
+template <typename At>
+__device__ __forceinline__ void tile_rows(const uint4* v, const TileAt& t, int cols,
+                                          const QuantOut& out, At at) {
+  const int lane = threadIdx.x & 31;
   float f[4], quot;
   four_scales(v, out.pow2, lane, f, quot);
-  if (c < cols) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (r + 32 * u < nr)
-        *reinterpret_cast<uint2*>(out.codes + (r0 + r + 32 * u) * out.ld + c) = codes8(v[u], f[u]);
+  for (int i = 0; i < 4; ++i) {
+    const int2 rc = at(i);
+    if (rc.x < t.nr && rc.y < cols)
+      *reinterpret_cast<uint2*>(out.codes + (t.r0 + rc.x) * out.ld + rc.y) = codes8(v[i], f[i]);
   }
-  const int sb = scale_of_lane(lane), row = r + 32 * sb, c_first = c - 8 * (lane & 15);
-  if (sb >= 0 && row < nr && c_first < cols)
-    out.scales[(r0 + row) * out.kb + (c_first >> 7)] = quot;
+  const int sb = scale_of_lane(lane);
+  if (sb >= 0) {
+    const int2 rc = at(sb);
+    const int c = rc.y - 8 * (lane & 15);
+    if (rc.x < t.nr && c < cols) out.scales[(t.r0 + rc.x) * out.kb + (c >> 7)] = quot;
+  }
 }
 
-template <int SRC, bool VEC, bool BOTH>
+// Rows read by the element: any width and alignment.
+constexpr int FT_THREADS = 512;
+
+template <int SRC>
 __global__ void __launch_bounds__(FT_THREADS, 2)
+fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
+                      const int32_t* __restrict__ offsets, int G, long long rows,
+                      const QuantOut out, int* err) {
+  griddep_wait();   // see common.cuh: dependent launches
+  __shared__ uint4 tile[FT_TILE];
+  __shared__ uint32_t s_max[8][64];
+  __shared__ Blocks blocks;
+  if (!count_blocks(blocks, offsets, G, rows, err)) return;
+  const int tid = threadIdx.x;
+  const int gx = (src.cols + 127) / 128;
+  const long long total = static_cast<long long>(blocks.first[G]) * gx;
+  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
+    const TileAt t = tile_at(blocks, offsets, G, rows, item, gx);
+    const int r = tid >> 4, c = t.c0 + 8 * (tid & 15);
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r + 32 * u < t.nr) {
+        long long row = t.r0 + r + 32 * u;
+        if (src_tok) {
+          row = __ldg(src_tok + row);
+          if (row < 0 || row >= src_rows) {
+            flag_error(err, MOE_DEVERR_BAD_INDEX);
+            row = 0;
+          }
+        }
+        v[u] = value8<SRC, false>(src, row, c);
+      }
+    }
+    __syncthreads();   // the previous tile is consumed
+#pragma unroll
+    for (int u = 0; u < 4; ++u) tile[(r + 32 * u) * 16 + (tid & 15)] = v[u];
+    if (out.codes)
+      tile_rows(v, t, src.cols, out, [&](int u) { return make_int2(r + 32 * u, c); });
+    __syncthreads();
+    Columns<8> cols;
+    cols.read(tile, tid, s_max);
+    __syncthreads();
+    cols.write(tid, s_max, t.c0, src.cols, t.kb, out);
+  }
+  griddep_launch();
+}
+
+// Rows on 16 bytes: the next tile's raw pieces are on their way (cp.async) while this one is
+// worked on.  A piece is fetched, read and (SwiGLU) overwritten with its result by one thread, so
+// two sets of raw tiles are all the shared memory: x; a, b -> h, -; a, b, dh -> da, db, h.
+template <int SRC>
+struct TileGeo {
+  static constexpr int RAW = SRC == SRC_ROWS ? 1 : SRC == SRC_SWIGLU ? 2 : 3;
+  static constexpr int THREADS = SRC == SRC_SWIGLU_BWD ? 1024 : 512;
+  static constexpr int PER = FT_TILE / THREADS;         // pieces of a tile per thread
+  static constexpr int CTAS = SRC == SRC_ROWS ? 3 : 1;  // per SM
+  static constexpr int SMEM = 2 * RAW * FT_TILE * 16;
+};
+
+template <int SRC>
+__global__ void __launch_bounds__(TileGeo<SRC>::THREADS, TileGeo<SRC>::CTAS)
 fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
                   const int32_t* __restrict__ offsets, int G, long long rows, const QuantOut out,
                   const QuantOut out_h, int* err) {
   griddep_wait();   // see common.cuh: dependent launches
-  extern __shared__ uint4 tile[];   // BOTH: three tiles
-  __shared__ uint32_t s_max[BOTH ? 3 : 1][8][64];
-  __shared__ int s_first[FQ_MAX_G + 1];
-  __shared__ int s_sum[8];
-  __shared__ int s_bad;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  auto start_of = [&](int g) {
-    return offsets ? static_cast<long long>(__ldg(offsets + g)) : (g ? rows : 0LL);
-  };
-  // first block of every segment (G <= 256: one per thread of the first eight warps)
-  int nb = 0;
-  if (tid < G) {
-    const long long a = start_of(tid), b = start_of(tid + 1);
-    if (a < 0 || b < a || b > rows || (tid == 0 && a != 0)) s_bad = 1;
-    else nb = static_cast<int>((b - a + 127) / 128);
-  }
-  const int incl = warp_incl_scan(nb);
-  if (lane == 31 && warp < 8) s_sum[warp] = incl;
-  __syncthreads();
-  if (tid < G) {
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    s_first[tid] = before + incl - nb;
-    if (tid == G - 1) s_first[G] = before + incl;
-  }
-  __syncthreads();
-  if (s_bad) {
-    if (blockIdx.x == 0 && tid == 0) flag_error(err, MOE_DEVERR_BAD_OFFSETS);
-    return;
-  }
-  const int gx = ((BOTH ? src.f : src.cols) + 127) / 128;   // column tiles, fastest
-  const long long total = static_cast<long long>(s_first[G]) * gx;
-  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
-    const int kb = static_cast<int>(item / gx);
-    const int c0 = static_cast<int>(item - static_cast<long long>(kb) * gx) * 128;
-    int lo = 0, hi = G;   // s_first[lo] <= kb < s_first[lo + 1]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_first[mid] <= kb) lo = mid;
-      else hi = mid;
-    }
-    const long long r0 = start_of(lo) + 128LL * (kb - s_first[lo]);
-    const long long left = start_of(lo + 1) - r0;
-    const int nr = left < 128 ? static_cast<int>(left) : 128;
-    const int r = tid >> 4, c = c0 + 8 * (tid & 15);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    uint4 v[4];
-    if constexpr (BOTH) {
-      uint4 a[4], b[4], d[4];
+  using GE = TileGeo<SRC>;
+  constexpr int PER = GE::PER;
+  constexpr bool BWD = SRC == SRC_SWIGLU_BWD;
+  extern __shared__ uint4 raw[];   // [2][RAW][128][16]
+  __shared__ uint32_t s_max[BWD ? 32 : 8][64];
+  __shared__ Blocks blocks;
+  if (!count_blocks(blocks, offsets, G, rows, err)) return;
+  const int tid = threadIdx.x;
+  const int width = BWD ? src.f : src.cols;
+  const int gx = (width + 127) / 128;
+  const long long total = static_cast<long long>(blocks.first[G]) * gx;
+  const int r = tid >> 4, ch = tid & 15;   // pieces (r + THREADS / 16 u, ch)
+  constexpr int STEP = GE::THREADS / 16;
+  auto fetch = [&](const TileAt& t, uint4* dst) {
+    const int c = t.c0 + 8 * ch;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        a[u] = b[u] = d[u] = zero;
-        if (r + 32 * u < nr) {
-          const long long t = r0 + r + 32 * u;
-          a[u] = load8<true>(src.x + t * 2 * src.f + c, 8);
-          b[u] = load8<true>(src.x + t * 2 * src.f + src.f + c, 8);
-          d[u] = load8<true>(src.dh + t * src.f + c, 8);
+    for (int u = 0; u < PER; ++u) {
+      const int rr = r + STEP * u, at = rr * 16 + ch;
+      const bool in = rr < t.nr && c < width;
+      long long row = in ? t.r0 + rr : 0;
+      if (SRC == SRC_ROWS && src_tok && in) {
+        row = __ldg(src_tok + row);
+        if (row < 0 || row >= src_rows) {
+          flag_error(err, MOE_DEVERR_BAD_INDEX);
+          row = 0;
         }
       }
-      __syncthreads();   // the previous tiles are consumed
+      const int cc = in ? c : 0;
+      if constexpr (SRC == SRC_ROWS) {
+        cp_async16(dst + at, src.x + row * src.ld + cc, in);
+      } else {
+        const __nv_bfloat16* a = src.x + row * 2 * src.f + cc;
+        cp_async16(dst + at, a, in);
+        cp_async16(dst + FT_TILE + at, a + src.f, in);
+        if constexpr (BWD) cp_async16(dst + 2 * FT_TILE + at, src.dh + row * src.f + cc, in);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  TileAt next;
+  if (blockIdx.x < total) {
+    next = tile_at(blocks, offsets, G, rows, blockIdx.x, gx);
+    fetch(next, raw);
+  }
+  int buf = 0;
+  for (long long item = blockIdx.x; item < total; item += gridDim.x, buf ^= 1) {
+    const TileAt t = next;
+    uint4* tile = raw + buf * GE::RAW * FT_TILE;
+    // the other set was consumed before the last barrier
+    if (item + gridDim.x < total) {
+      next = tile_at(blocks, offsets, G, rows, item + gridDim.x, gx);
+      fetch(next, raw + (buf ^ 1) * GE::RAW * FT_TILE);
+    } else {
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");   // this thread's pieces of this tile
+    const int c = t.c0 + 8 * ch;
+    uint4 v[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int at = (r + 32 * u) * 16 + (tid & 15);
+    for (int u = 0; u < PER; ++u) {
+      uint4* at = tile + (r + STEP * u) * 16 + ch;
+      if constexpr (SRC == SRC_ROWS) {
+        v[u] = at[0];
+      } else if constexpr (SRC == SRC_SWIGLU) {
+        v[u] = r + STEP * u < t.nr ? silu_mul8(at[0], at[FT_TILE]) : make_uint4(0u, 0u, 0u, 0u);
+        at[0] = v[u];
+      } else {
+        const uint4 a = at[0], b = at[FT_TILE], d = at[2 * FT_TILE];
         uint32_t x[4] = {0u, 0u, 0u, 0u}, y[4] = {0u, 0u, 0u, 0u}, z[4] = {0u, 0u, 0u, 0u};
-        if (r + 32 * u < nr) {
-          const uint32_t *pa = &a[u].x, *pb = &b[u].x, *pd = &d[u].x;
+        if (r + STEP * u < t.nr) {
+          const uint32_t *pa = &a.x, *pb = &b.x, *pd = &d.x;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const Swiglu2 w = swiglu_bwd2(pa[k], pb[k], pd[k]);
@@ -598,49 +773,34 @@ fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long lo
             z[k] = w.h;
           }
         }
-        tile[at] = make_uint4(x[0], x[1], x[2], x[3]);
-        tile[FT_TILE + at] = make_uint4(y[0], y[1], y[2], y[3]);
-        tile[2 * FT_TILE + at] = make_uint4(z[0], z[1], z[2], z[3]);
+        v[u] = make_uint4(x[0], x[1], x[2], x[3]);
+        v[2 + u] = make_uint4(y[0], y[1], y[2], y[3]);
+        at[0] = v[u];
+        at[FT_TILE] = v[2 + u];
+        at[2 * FT_TILE] = make_uint4(z[0], z[1], z[2], z[3]);
       }
-      // this thread's own pieces back, for the rows of da and db
-#pragma unroll
-      for (int part = 0; part < 2; ++part) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          v[u] = tile[part * FT_TILE + (r + 32 * u) * 16 + (tid & 15)];
-        tile_rows(v, r0, nr, part * src.f + c, src.cols, out);
-      }
+    }
+    if (out.codes)
+      tile_rows(v, t, src.cols, out, [&](int i) {
+        return BWD ? make_int2(r + STEP * (i & 1), c + (i >> 1) * src.f)
+                   : make_int2(r + STEP * i, c);
+      });
+    __syncthreads();
+    if constexpr (BWD) {
+      // 512 threads each for da and db, then all of them for h
+      const int part = tid >> 9, th = tid & 511;
+      Columns<8> cols;
+      Columns<16> cols_h;
+      cols.read(tile + part * FT_TILE, th, s_max + 8 * part);
+      cols_h.read(tile + 2 * FT_TILE, tid, s_max + 16);
       __syncthreads();
-#pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        if (part == 2 && !out_h.codes_t) continue;
-        const QuantOut& o = part == 2 ? out_h : out;
-        tile_columns(tile + part * FT_TILE, s_max[part], (part == 1 ? src.f : 0) + c0,
-                     part == 2 ? src.f : src.cols, kb, o.codes_t, o.scales_t, o.kb_cap, o.pow2);
-      }
+      cols.write(th, s_max + 8 * part, part * src.f + t.c0, src.cols, t.kb, out);
+      if (out_h.codes_t) cols_h.write(tid, s_max + 16, t.c0, src.f, t.kb, out_h);
     } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        v[u] = zero;
-        if (r + 32 * u < nr) {
-          long long t = r0 + r + 32 * u;
-          if (src_tok) {
-            t = __ldg(src_tok + t);
-            if (t < 0 || t >= src_rows) {
-              flag_error(err, MOE_DEVERR_BAD_INDEX);
-              t = 0;
-            }
-          }
-          v[u] = value8<SRC, VEC>(src, t, c);
-        }
-      }
-      __syncthreads();   // the previous tile is consumed
-#pragma unroll
-      for (int u = 0; u < 4; ++u) tile[(r + 32 * u) * 16 + (tid & 15)] = v[u];
-      if (out.codes) tile_rows(v, r0, nr, c, src.cols, out);
+      Columns<8> cols;
+      cols.read(tile, tid, s_max);
       __syncthreads();
-      tile_columns(tile, s_max[0], c0, src.cols, kb, out.codes_t, out.scales_t, out.kb_cap,
-                   out.pow2);
+      cols.write(tid, s_max, t.c0, src.cols, t.kb, out);
     }
   }
   griddep_launch();
@@ -734,7 +894,7 @@ int fq_sms() {
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int SRC, bool VEC, bool BOTH = false>
+template <int SRC, bool VEC>
 cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut& o,
                          const QuantOut& oh, cudaStream_t st) {
   if (!o.codes_t) {
@@ -744,17 +904,24 @@ cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut&
                       dim3(static_cast<unsigned>(want < most ? want : most)), dim3(FQ_THREADS), 0,
                       st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, a.err);
   }
-  auto kern = fp8_tokens_kernel<SRC, VEC, BOTH>;
-  constexpr int smem = (BOTH ? 3 : 1) * FT_TILE * 16;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const long long items =
-      fp8_token_blocks(a.rows, a.G) * (((BOTH ? s.f : s.cols) + 127) / 128);
-  const long long most = static_cast<long long>(fq_sms()) * 2;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(items < most ? items : most)),
-                    dim3(FT_THREADS), smem, st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G,
-                    a.rows, o, oh, a.err);
+  const int width = VEC && SRC == SRC_SWIGLU_BWD ? s.f : s.cols;
+  const long long items = fp8_token_blocks(a.rows, a.G) * ((width + 127) / 128);
+  auto grid = [&](int per_sm) {
+    const long long most = static_cast<long long>(fq_sms()) * per_sm;
+    return dim3(static_cast<unsigned>(items < most ? items : most));
+  };
+  if constexpr (VEC) {
+    using GE = TileGeo<SRC>;
+    auto kern = fp8_tokens_kernel<SRC>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GE::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, grid(GE::CTAS), dim3(GE::THREADS), GE::SMEM, st, 1, s, a.src_tok,
+                      a.src_rows, a.offsets, a.G, a.rows, o, oh, a.err);
+  } else {
+    return launch_pdl(fp8_tokens_any_kernel<SRC>, grid(2), dim3(FT_THREADS), 0, st, 1, s, a.src_tok,
+                      a.src_rows, a.offsets, a.G, a.rows, o, a.err);
+  }
 }
 
 }  // namespace
@@ -789,7 +956,7 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, cudaStream_t st) {
                         : launch_quant<SRC_SWIGLU, false>(s, a, o, oh, st);
   // the backward reads a, b and dh once for da, db and h where the blocks of da and db do not
   // share one (f a multiple of 128); other widths are computed by the column, and h apart
-  if (a.f % 128 == 0) return launch_quant<SRC_SWIGLU_BWD, true, true>(s, a, o, oh, st);
+  if (a.f % 128 == 0) return launch_quant<SRC_SWIGLU_BWD, true>(s, a, o, oh, st);
   const cudaError_t e = launch_quant<SRC_SWIGLU_BWD, false>(s, a, o, oh, st);
   if (e != cudaSuccess || !a.h_codes_t) return e;
   s.cols = a.f;
