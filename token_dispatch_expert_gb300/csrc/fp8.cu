@@ -12,6 +12,7 @@
 //
 // All kernels are bound by memory: a bf16 value is read once (2 bytes) and one byte or, with
 // both orientations, two bytes are written.
+#include <cuda.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -379,6 +380,14 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) 
                : "memory");
 }
 
+// a box of 128 bytes x 128 rows, shared -> global (parts past the map's rows are not written)
+__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+
 // Four blocks of a row (or of four rows), a chunk of eight values per lane in each, sixteen lanes
 // to a block: their scales and factors, by one pass of shuffles (two blocks' maxima to a
 // word) and one division, of whose lanes one divides for each block's factor and its neighbour
@@ -560,7 +569,10 @@ __device__ __forceinline__ TileAt tile_at(const Blocks& s, const int32_t* offset
 constexpr int FT_TILE = 128 * 16;   // 16-byte pieces
 
 // A tile's columns (c0 ..) along the tokens into block kb, by `64 * Q` threads of which this is
-// number `th`: two columns and 128 / Q rows each.  Joined by a barrier of the whole CTA.
+// number `th`: two columns and 128 / Q rows each.  Joined by a barrier of the whole CTA.  The
+// codes go to their places, or to `box`: 128 columns of 128 bytes, 16-byte pieces XOR-swizzled by
+// the column, for a TMA store (a column's 128 codes are one line in memory, and 16 bytes of
+// 32 lines at a time halved the stores' rate).
 template <int Q>
 struct Columns {
   uint32_t w[128 / Q];
@@ -577,7 +589,7 @@ struct Columns {
     s_max[q][cp] = m;
   }
   __device__ __forceinline__ void write(int th, uint32_t (*s_max)[64], int c0, int cols, int kb,
-                                        const QuantOut& o) {
+                                        const QuantOut& o, uint8_t* box) {
     const int cp = th & 63, q = th >> 6;
 #pragma unroll
     for (int i = 0; i < Q; ++i) m = max2(m, s_max[i][cp]);
@@ -595,7 +607,10 @@ struct Columns {
         const float2 y = __fmul2_rn(make_float2(at(2), at(3)), both(r));
         code[i] = e4m3x2(x.x, x.y) | (e4m3x2(y.x, y.y) << 16);
       }
-      uint8_t* dst = o.codes_t + (static_cast<long long>(c) * o.kb_cap + kb) * 128 + 128 / Q * q;
+      constexpr int N = 128 / Q;   // codes
+      const int at = N * q, cc = 2 * cp + j;
+      uint8_t* dst = box ? box + cc * 128 + ((at & 112) ^ ((cc & 7) << 4)) + (at & 15)
+                         : o.codes_t + (static_cast<long long>(c) * o.kb_cap + kb) * 128 + at;
       if constexpr (Q == 16) {
         *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
       } else {
@@ -671,33 +686,37 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
     Columns<8> cols;
     cols.read(tile, tid, s_max);
     __syncthreads();
-    cols.write(tid, s_max, t.c0, src.cols, t.kb, out);
+    cols.write(tid, s_max, t.c0, src.cols, t.kb, out, nullptr);
   }
   griddep_launch();
 }
 
-// Rows on 16 bytes: the next tile's raw pieces are on their way (cp.async) while this one is
-// worked on.  A piece is fetched, read and (SwiGLU) overwritten with its result by one thread, so
-// two sets of raw tiles are all the shared memory: x; a, b -> h, -; a, b, dh -> da, db, h.
+// Rows on 16 bytes: the next tile's raw pieces are on their way (cp.async) while this one's columns
+// are worked on.  A piece is fetched, read and (SwiGLU) overwritten with its result by one thread,
+// and a tile's column codes overwrite the tile once it is in registers, so two sets of raw
+// tiles are all the shared memory: x; a, b -> h, -; a, b, dh -> da, db, h.
 template <int SRC>
 struct TileGeo {
   static constexpr int RAW = SRC == SRC_ROWS ? 1 : SRC == SRC_SWIGLU ? 2 : 3;
   static constexpr int THREADS = SRC == SRC_SWIGLU_BWD ? 1024 : 512;
   static constexpr int PER = FT_TILE / THREADS;         // pieces of a tile per thread
   static constexpr int CTAS = SRC == SRC_ROWS ? 3 : 1;  // per SM
-  static constexpr int SMEM = 2 * RAW * FT_TILE * 16;
+  static constexpr int SMEM = 2 * RAW * FT_TILE * 16 + 1024;
 };
 
 template <int SRC>
 __global__ void __launch_bounds__(TileGeo<SRC>::THREADS, TileGeo<SRC>::CTAS)
-fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
+fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_h,
+                  const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
                   const int32_t* __restrict__ offsets, int G, long long rows, const QuantOut out,
                   const QuantOut out_h, int* err) {
   griddep_wait();   // see common.cuh: dependent launches
   using GE = TileGeo<SRC>;
   constexpr int PER = GE::PER;
   constexpr bool BWD = SRC == SRC_SWIGLU_BWD;
-  extern __shared__ uint4 raw[];   // [2][RAW][128][16]
+  extern __shared__ uint4 dyn[];   // [2][RAW][128][16] after the next 1 KB boundary
+  uint4* raw = reinterpret_cast<uint4*>(
+      (reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
   __shared__ uint32_t s_max[BWD ? 32 : 8][64];
   __shared__ Blocks blocks;
   if (!count_blocks(blocks, offsets, G, rows, err)) return;
@@ -742,14 +761,7 @@ fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long lo
   for (long long item = blockIdx.x; item < total; item += gridDim.x, buf ^= 1) {
     const TileAt t = next;
     uint4* tile = raw + buf * GE::RAW * FT_TILE;
-    // the other set was consumed before the last barrier
-    if (item + gridDim.x < total) {
-      next = tile_at(blocks, offsets, G, rows, item + gridDim.x, gx);
-      fetch(next, raw + (buf ^ 1) * GE::RAW * FT_TILE);
-    } else {
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    asm volatile("cp.async.wait_group 1;" ::: "memory");   // this thread's pieces of this tile
+    asm volatile("cp.async.wait_all;" ::: "memory");   // this thread's pieces of this tile
     const int c = t.c0 + 8 * ch;
     uint4 v[4];
 #pragma unroll
@@ -785,7 +797,14 @@ fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long lo
         return BWD ? make_int2(r + STEP * (i & 1), c + (i >> 1) * src.f)
                    : make_int2(r + STEP * i, c);
       });
+    if (tid == 0) bulk_wait_group_read<0>();   // the last tile's codes have left the other set
     __syncthreads();
+    if (item + gridDim.x < total) {
+      next = tile_at(blocks, offsets, G, rows, item + gridDim.x, gx);
+      fetch(next, raw + (buf ^ 1) * GE::RAW * FT_TILE);
+    }
+    uint8_t* box = reinterpret_cast<uint8_t*>(tile);
+    constexpr int BOX = FT_TILE * 16;   // from one tile's to the next one's
     if constexpr (BWD) {
       // 512 threads each for da and db, then all of them for h
       const int part = tid >> 9, th = tid & 511;
@@ -794,15 +813,27 @@ fp8_tokens_kernel(const Source src, const int32_t* __restrict__ src_tok, long lo
       cols.read(tile + part * FT_TILE, th, s_max + 8 * part);
       cols_h.read(tile + 2 * FT_TILE, tid, s_max + 16);
       __syncthreads();
-      cols.write(th, s_max + 8 * part, part * src.f + t.c0, src.cols, t.kb, out);
-      if (out_h.codes_t) cols_h.write(tid, s_max + 16, t.c0, src.f, t.kb, out_h);
+      cols.write(th, s_max + 8 * part, part * src.f + t.c0, src.cols, t.kb, out, box + part * BOX);
+      if (out_h.codes_t) cols_h.write(tid, s_max + 16, t.c0, src.f, t.kb, out_h, box + 2 * BOX);
     } else {
       Columns<8> cols;
       cols.read(tile, tid, s_max);
       __syncthreads();
-      cols.write(tid, s_max, t.c0, src.cols, t.kb, out);
+      cols.write(tid, s_max, t.c0, src.cols, t.kb, out, box);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+      const uint32_t at = smem_u32(box);
+      tma_store_2d(&tm, at, 128 * t.kb, t.c0);
+      if (BWD) {
+        tma_store_2d(&tm, at + BOX, 128 * t.kb, src.f + t.c0);
+        if (out_h.codes_t) tma_store_2d(&tm_h, at + 2 * BOX, 128 * t.kb, t.c0);
+      }
+      bulk_commit_group();
     }
   }
+  if (tid == 0) bulk_wait_group_all();   // stores done before exit
   griddep_launch();
 }
 
@@ -916,8 +947,16 @@ cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut&
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GE::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, grid(GE::CTAS), dim3(GE::THREADS), GE::SMEM, st, 1, s, a.src_tok,
-                      a.src_rows, a.offsets, a.G, a.rows, o, oh, a.err);
+    CUtensorMap tm, tm_h;
+    const uint64_t len = 128ull * static_cast<uint64_t>(o.kb_cap);
+    if (!fp8_codes_map(&tm, o.codes_t, len, len, static_cast<uint64_t>(s.cols), 128))
+      return cudaErrorInvalidValue;
+    tm_h = tm;
+    if (SRC == SRC_SWIGLU_BWD && oh.codes_t &&
+        !fp8_codes_map(&tm_h, oh.codes_t, len, len, static_cast<uint64_t>(s.f), 128))
+      return cudaErrorInvalidValue;
+    return launch_pdl(kern, grid(GE::CTAS), dim3(GE::THREADS), GE::SMEM, st, 1, tm, tm_h, s,
+                      a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, oh, a.err);
   } else {
     return launch_pdl(fp8_tokens_any_kernel<SRC>, grid(2), dim3(FT_THREADS), 0, st, 1, s, a.src_tok,
                       a.src_rows, a.offsets, a.G, a.rows, o, a.err);

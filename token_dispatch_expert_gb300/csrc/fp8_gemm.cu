@@ -646,21 +646,6 @@ PFN_cuTensorMapEncodeTiled_v12000 fg_encode_fn() {
   return fn;
 }
 
-// codes [rows][ld] of which `cols` are read (zeros past them), boxes of 128 x box_rows
-bool fg_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint64_t rows,
-            uint32_t box_rows) {
-  auto enc = fg_encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {ld};
-  cuuint32_t box[2] = {FG_BK, box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
-}
-
 // The output [groups][rows][cols] with rows `ld` elements apart, 128-byte swizzle, box 128 bytes
 // x 32 rows x 1 group: a store never crosses into the next group's rows.  False where TMA
 // cannot address it (a base or a row off 16 bytes).
@@ -695,6 +680,20 @@ cudaError_t fg_launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtens
 
 }  // namespace
 
+bool fp8_codes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint64_t rows,
+                   uint32_t box_rows) {
+  auto enc = fg_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld};
+  cuuint32_t box[2] = {FG_BK, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   FgParams p{};
   p.G = a.G;
@@ -720,16 +719,16 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
     p.m_tiles = (a.K + tile_m - 1) / tile_m;
     p.kb = static_cast<int>(fp8_token_blocks(a.rows, a.G));
     const uint64_t len = 128ull * static_cast<uint64_t>(p.kb);
-    ok = fg_map(&ta, a.a, len, len, static_cast<uint64_t>(a.K), 128) &&
-         fg_map(&tb, a.b, len, len, static_cast<uint64_t>(a.N), b_rows);
+    ok = fp8_codes_map(&ta, a.a, len, len, static_cast<uint64_t>(a.K), 128) &&
+         fp8_codes_map(&tb, a.b, len, len, static_cast<uint64_t>(a.N), b_rows);
     p.tma_out = fg_out_map(&tc, a.out, a.out_fp32, static_cast<uint64_t>(a.N),
                            static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.K),
                            static_cast<uint64_t>(a.G));
   } else {
     p.kb = (a.K + 127) / 128;
-    ok = fg_map(&ta, a.a, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.lda),
+    ok = fp8_codes_map(&ta, a.a, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.lda),
                 static_cast<uint64_t>(a.rows), 128) &&
-         fg_map(&tb, a.b, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.ldb),
+         fp8_codes_map(&tb, a.b, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.ldb),
                 static_cast<uint64_t>(a.G) * static_cast<uint64_t>(a.N), b_rows);
     p.tma_out = fg_out_map(&tc, a.out, a.out_fp32, static_cast<uint64_t>(a.N),
                            static_cast<uint64_t>(a.ldo), static_cast<uint64_t>(a.rows), 1);

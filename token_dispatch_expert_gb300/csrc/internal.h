@@ -1,6 +1,7 @@
 // internal.h -- launchers shared between the library's translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -288,5 +289,10 @@ struct Fp8GemmArgs {
   int* err;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
+
+// Tensor map over codes [rows][ld] of which `cols` bytes a row are read (zeros past them): boxes of
+// 128 bytes x box_rows, 128-byte swizzle.
+bool fp8_codes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint64_t rows,
+                   uint32_t box_rows);
 
 }  // namespace moe
