@@ -47,13 +47,6 @@ cudaError_t launch_route(const moe_config_t* c, const float* logits, int32_t* to
                          int32_t* dest_row, int32_t* src_tok, int32_t* src_slot,
                          uint8_t* drop_mask, void* scratch, int* err, cudaStream_t st);
 
-// F2 from the chosen experts: chunk_cnt [E][route_chunks(T)] holds each chunk's count of every
-// expert, dest_row each slot's rank inside its chunk (-1: not routed); token-order capacity.
-cudaError_t launch_route_order(int64_t T, int E, int k, int cap, const int32_t* topk_idx,
-                               int32_t* chunk_cnt, int32_t* counts, int32_t* kept,
-                               int32_t* offsets, int32_t* dest_row, int32_t* src_tok,
-                               int32_t* src_slot, uint8_t* drop_mask, cudaStream_t st);
-
 // Group-limited routing (router.cu) and the gradient of its weights; scratch as launch_route.
 cudaError_t launch_route_groups(const moe_config_t* c, const moe_router_t* r, const float* logits,
                                 int32_t* topk_idx, float* topk_w, int32_t* counts, int32_t* kept,

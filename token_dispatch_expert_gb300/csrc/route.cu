@@ -406,21 +406,6 @@ route_assign_kernel(const int32_t* __restrict__ topk_idx, int64_t T, int k, int 
 
 }  // namespace
 
-cudaError_t launch_route_order(int64_t T, int E, int k, int cap, const int32_t* topk_idx,
-                               int32_t* chunk_cnt, int32_t* counts, int32_t* kept,
-                               int32_t* offsets, int32_t* dest_row, int32_t* src_tok,
-                               int32_t* src_slot, uint8_t* drop_mask, cudaStream_t st) {
-  const int64_t nch = route_chunks(T);
-  const cudaError_t e =
-      launch_pdl(route_scan_kernel, dim3(1), dim3(1024), 0, st, 1, chunk_cnt, nch, E, cap, counts,
-                 kept, offsets, static_cast<int32_t*>(nullptr));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(route_assign_kernel, dim3(static_cast<unsigned>((T * k + 255) / 256)),
-                    dim3(256), 0, st, 1, topk_idx, T, k, E, cap, chunk_cnt, nch, offsets, counts,
-                    static_cast<const int32_t*>(nullptr), static_cast<const int32_t*>(nullptr),
-                    dest_row, src_tok, src_slot, drop_mask);
-}
-
 cudaError_t launch_route(const moe_config_t* c, const float* logits, int32_t* topk_idx,
                          float* topk_w, int32_t* counts, int32_t* kept, int32_t* offsets,
                          int32_t* dest_row, int32_t* src_tok, int32_t* src_slot,

@@ -15,15 +15,18 @@
 // Keys with a bias are numbers of their own, so their order is defined in 64 bits: two
 // experts whose keys differ by less than the fp32 rounding error would otherwise be ordered
 // by the accident of an implementation.  The kernel computes fp32 keys, takes the choice
-// from them, and checks that every decision it made had a margin above the keys' error bound;
-// a token without that margin (measured: 0.1 - 0.3 % of tokens with 256 sigmoid scores) is
-// chosen again from 64-bit keys.
+// from them, and checks that every decision it made had a margin above the keys' error bound.
+// Where neighbours in the order are closer (one token in some thousand with 256 sigmoid scores),
+// the few candidates' 64-bit keys decide, one lane each; where two groups are, the whole choice
+// is made again from 64-bit keys.  (Doing the latter for all of them took 20 us, most of it
+// fetching the instructions of code that nothing else runs.)
 //
-// One warp per token, one CTA per 32-token chunk (32 warps).  The choice is k rounds of a
-// warp maximum (redux.sync on order-preserving 32-bit keys, then on the id among equals).
-// The chunk's histogram and the ranks inside it are bit masks as in route.cu, whose scan
-// and assign kernels follow; a single chunk (T <= 32) does their work itself, in one
-// launch.
+// One warp per token, one CTA per 32-token chunk (32 warps).  A lane sorts its E / 32 keys; the
+// choice is k rounds of a warp maximum over the lanes' heads (redux.sync on order-preserving
+// 32-bit keys, then on the id among equals), whose lane moves its list up.  The chunk's histogram
+// and the ranks inside it are bit masks (as in route.cu); order_count (a warp per expert) and
+// order_assign follow; a single chunk (T <= 32) does their work itself, in one launch.
+// Bound by latency: 4 MB of logits for 4096 tokens are 0.6 us of bandwidth.
 #include "common.cuh"
 #include "internal.h"
 
@@ -48,7 +51,6 @@ __device__ __forceinline__ unsigned long long key64(double x) {
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
-__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(FULL_MASK, v); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long v) {
   const uint32_t hi = static_cast<uint32_t>(v >> 32);
   const uint32_t top = __reduce_max_sync(FULL_MASK, hi);
@@ -59,18 +61,28 @@ __device__ __forceinline__ float warp_fmax(float v) {
   return unkey32(__reduce_max_sync(FULL_MASK, key32(v)));
 }
 
-// the best key left in the warp (0: none) and its expert (the lowest id among equals);
+// e^x and 1 / d for the keys, off by two ulp and one ulp (the weights use expf and divisions)
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 0x1.715476p+0f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float d) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return r;
+}
+
+// the best 64-bit key left in the warp (0: none) and its expert (the lowest id among equals);
 // the winner is taken out of its lane's keys
-template <int VPL, typename K>
-__device__ __forceinline__ K take_best(K* key, int lane, int& e) {
-  K mine = key[0];
+template <int VPL>
+__device__ __forceinline__ void take_best(unsigned long long* key, int lane, int& e) {
+  unsigned long long mine = key[0];
 #pragma unroll
   for (int s = 1; s < VPL; ++s) mine = key[s] > mine ? key[s] : mine;
-  const K top = warp_max(mine);
-  if (top == 0) {
-    e = -1;
-    return top;
-  }
+  const unsigned long long top = warp_max(mine);
+  e = -1;
+  if (top == 0) return;
   uint32_t id = 0xffffffffu;
 #pragma unroll
   for (int s = VPL - 1; s >= 0; --s)
@@ -80,36 +92,87 @@ __device__ __forceinline__ K take_best(K* key, int lane, int& e) {
   for (int s = 0; s < VPL; ++s)
     if (id == static_cast<uint32_t>(lane + 32 * s)) key[s] = 0;
   e = static_cast<int>(id);
-  return top;
 }
 
-// Worth of every group: lane g * L + sub scans part of group g's values (staged in shared
-// memory) and the L lanes of a group are joined.  The scan starts at a place that depends on
-// g, so that the groups of one step read different banks.  -inf: nothing in service.
+// This lane's keys in descending order, equal ones by ascending id (id = lane + 32 s).
+template <int VPL>
+struct SortedKeys {
+  uint32_t key[VPL];
+  int id[VPL];
+  __device__ __forceinline__ void order(int i, int j) {   // i < j: the larger (lower id) first
+    const bool swap = key[j] > key[i] || (key[j] == key[i] && id[j] < id[i]);
+    const uint32_t k = swap ? key[j] : key[i];
+    const int d = swap ? id[j] : id[i];
+    key[j] = swap ? key[i] : key[j];
+    id[j] = swap ? id[i] : id[j];
+    key[i] = k;
+    id[i] = d;
+  }
+  __device__ __forceinline__ void sort(int lane) {
+#pragma unroll
+    for (int s = 0; s < VPL; ++s) id[s] = lane + 32 * s;
+    // Batcher's merge exchange
+#pragma unroll
+    for (int p = 1; p < VPL; p *= 2)
+#pragma unroll
+      for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+        for (int j = k % p; j + k < VPL; j += 2 * k)
+#pragma unroll
+          for (int i = 0; i < k; ++i)
+            if ((i + j) / (2 * p) == (i + j + k) / (2 * p) && i + j + k < VPL)
+              order(i + j, i + j + k);
+  }
+  // the best one left in the warp (0: none) and its expert
+  __device__ __forceinline__ uint32_t take(int lane, int& e) {
+    const uint32_t top = __reduce_max_sync(FULL_MASK, key[0]);
+    e = static_cast<int>(__reduce_min_sync(
+        FULL_MASK, key[0] == top ? static_cast<uint32_t>(id[0]) : 0xffffffffu));
+    if ((e & 31) == lane) {
+#pragma unroll
+      for (int s = 0; s + 1 < VPL; ++s) {
+        key[s] = key[s + 1];
+        id[s] = id[s + 1];
+      }
+      key[VPL - 1] = 0u;
+    }
+    if (top == 0u) e = -1;
+    return top;
+  }
+};
+
+struct RouterParams {
+  const float* logits;
+  const float* bias;
+  int64_t T;
+  int E, k, G, per, top_groups, top2, sigmoid, renorm, cap;
+  int per_magic;           // ceil(2^16 / per): e / per = e * per_magic >> 16 for e < 256
+  int lanes_log2, turns;   // 2^lanes_log2 lanes scan a group, in `turns` steps
+  float scale;
+};
+__device__ __forceinline__ int group_of(const RouterParams& p, int e) {
+  return (e * p.per_magic) >> 16;
+}
+
+// Worth of every group: the L = 2^lanes_log2 lanes g L .. of group g each scan part of its values
+// (staged in shared memory) and are joined.  The scan starts at a place that depends on g, so that
+// the groups of one step read different banks.  -inf: nothing in service.
 template <typename F>
-__device__ __forceinline__ F group_worth(const F* val, int G, int per, int top2, int lane, int& g,
-                                         int& L) {
-  L = 1;
-  while (2 * L * G <= 32 && L < per) L *= 2;
-  g = lane / L;
-  const int sub = lane - g * L;
+__device__ __forceinline__ F group_worth(const F* val, const RouterParams& p, int lane) {
+  const int L = 1 << p.lanes_log2, g = lane >> p.lanes_log2, sub = lane & (L - 1);
   const F none = -static_cast<F>(INFINITY);
   F m1 = none, m2 = none;
-  if (g < G) {
-    const int nj = (per + L - 1) / L;
-    int j = g % nj;
-    for (int n = 0; n < nj; ++n) {
-      const int i = sub + L * j;
-      if (i < per) {
-        const F v = val[g * per + i];
-        if (v > m1) {
-          m2 = m1;
-          m1 = v;
-        } else if (v > m2) {
-          m2 = v;
-        }
+  if (g < p.G) {
+    int i = sub + L * (g < p.turns ? g : 0);
+    for (int n = 0; n < p.turns; ++n) {
+      if (i < p.per) {
+        const F v = val[g * p.per + i];
+        const F lo = v < m1 ? v : m1;
+        m1 = v > m1 ? v : m1;
+        m2 = lo > m2 ? lo : m2;
       }
-      if (++j == nj) j = 0;
+      i += L;
+      if (i >= L * p.turns) i = sub;
     }
   }
   for (int o = 1; o < L; o <<= 1) {
@@ -119,42 +182,32 @@ __device__ __forceinline__ F group_worth(const F* val, int G, int per, int top2,
     m2 = b > m2 ? b : m2;
     m2 = lo > m2 ? lo : m2;
   }
-  return (top2 && m2 != none) ? m1 + m2 : m1;
+  return (p.top2 && m2 != none) ? m1 + m2 : m1;
 }
 
 // Bit g set for each of the top_groups best groups; margin: the least worth that stays minus
 // the best that goes (+inf where nothing goes).
 template <typename F>
-__device__ __forceinline__ uint32_t choose_groups(F worth, int g, int L, int G, int top_groups,
-                                                  int lane, F& margin) {
+__device__ __forceinline__ uint32_t choose_groups(F worth, const RouterParams& p, int lane,
+                                                  F& margin) {
+  const int g = lane >> p.lanes_log2;
   int rank = 0;
-  for (int j = 0; j < G; ++j) {
-    const F o = __shfl_sync(FULL_MASK, worth, j * L);
+  for (int j = 0; j < p.G; ++j) {
+    const F o = __shfl_sync(FULL_MASK, worth, j << p.lanes_log2);
     rank += (o > worth || (o == worth && j < g)) ? 1 : 0;
   }
-  const bool head = g < G && lane == g * L;
-  const bool in = head && rank < top_groups;
-  F lo = in ? worth : static_cast<F>(INFINITY);
-  F hi = (head && !in) ? worth : -static_cast<F>(INFINITY);
-  for (int o = 16; o > 0; o >>= 1) {
-    const F a = __shfl_xor_sync(FULL_MASK, lo, o), b = __shfl_xor_sync(FULL_MASK, hi, o);
-    lo = a < lo ? a : lo;
-    hi = b > hi ? b : hi;
-  }
-  margin = hi == -static_cast<F>(INFINITY) ? static_cast<F>(INFINITY) : lo - hi;
-  uint32_t mask = 0u;
+  const bool head = g < p.G && (lane & ((1 << p.lanes_log2) - 1)) == 0;
+  const bool in = head && rank < p.top_groups;
+  // the last one in and the first one out
   const uint32_t heads = __ballot_sync(FULL_MASK, in);
-  for (int j = 0; j < G; ++j) mask |= ((heads >> (j * L)) & 1u) << j;
+  const uint32_t last = __ballot_sync(FULL_MASK, head && rank == p.top_groups - 1);
+  const uint32_t first = __ballot_sync(FULL_MASK, head && rank == p.top_groups);
+  margin = __shfl_sync(FULL_MASK, worth, __ffs(last) - 1) -
+           __shfl_sync(FULL_MASK, worth, __ffs(first) - 1);
+  uint32_t mask = 0u;
+  for (int j = 0; j < p.G; ++j) mask |= ((heads >> (j << p.lanes_log2)) & 1u) << j;
   return mask;
 }
-
-struct RouterParams {
-  const float* logits;
-  const float* bias;
-  int64_t T;
-  int E, k, G, per, top_groups, top2, sigmoid, renorm, cap;
-  float scale;
-};
 
 // The choice from 64-bit keys.  val: the token's logits (NaN already -inf), wide: room for as
 // many doubles, both this warp's own.  Lane j gets the j-th choice.
@@ -164,15 +217,18 @@ __device__ __noinline__ int choose_exact(const RouterParams p, const float* val,
   double m = 0.0, z = 0.0;
   if (!p.sigmoid) {
     float mf = -F32_MAX;
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) mf = fmaxf(mf, val[e]);
+#pragma unroll
+    for (int s = 0; s < VPL; ++s)
+      if (lane + 32 * s < p.E) mf = fmaxf(mf, val[lane + 32 * s]);
     m = static_cast<double>(warp_fmax(mf));
   }
-#pragma unroll 1
-  for (int e = lane; e < p.E; e += 32) {
-    const double l = static_cast<double>(val[e]);
-    wide[e] = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m);
-    z += wide[e];
+  double sc[VPL];   // unrolled: one 64-bit exponential's latency hides behind the others'
+#pragma unroll
+  for (int s = 0; s < VPL; ++s) {
+    const double l = lane + 32 * s < p.E ? static_cast<double>(val[lane + 32 * s]) : -INFINITY;
+    const double x = exp(p.sigmoid ? -l : l - m);
+    sc[s] = p.sigmoid ? 1.0 / (1.0 + x) : x;
+    z += sc[s];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL_MASK, z, o);
@@ -184,7 +240,7 @@ __device__ __noinline__ int choose_exact(const RouterParams p, const float* val,
     if (e >= p.E) continue;
     const bool live = val[e] > -INFINITY;
     const double l = static_cast<double>(val[e]);
-    double c = p.sigmoid ? wide[e] : wide[e] / z;
+    double c = p.sigmoid ? sc[s] : sc[s] / z;
     if (p.bias) c += static_cast<double>(__ldg(p.bias + e));
     // without a bias the experts' own order is that of the logits
     if (live) key[s] = key64(p.bias ? c : l);
@@ -192,13 +248,11 @@ __device__ __noinline__ int choose_exact(const RouterParams p, const float* val,
   }
   if (p.G > 1) {
     __syncwarp();
-    int g, L;
-    const double worth = group_worth(wide, p.G, p.per, p.top2, lane, g, L);
     double margin;
-    const uint32_t mask = choose_groups(worth, g, L, p.G, p.top_groups, lane, margin);
+    const uint32_t mask = choose_groups(group_worth(wide, p, lane), p, lane, margin);
 #pragma unroll
     for (int s = 0; s < VPL; ++s)
-      if (lane + 32 * s < p.E && !((mask >> ((lane + 32 * s) / p.per)) & 1u)) key[s] = 0ull;
+      if (lane + 32 * s < p.E && !((mask >> group_of(p, lane + 32 * s)) & 1u)) key[s] = 0ull;
   }
   int sel = -1;
   for (int j = 0; j < p.k; ++j) {
@@ -207,6 +261,35 @@ __device__ __noinline__ int choose_exact(const RouterParams p, const float* val,
     if (lane == j) sel = e;
   }
   return sel;
+}
+
+// Lane j < n holds candidate my_e: the candidates in the order of their 64-bit keys.
+__device__ __noinline__ double exp64(double x) { return exp(x); }
+__device__ __noinline__ int order_exact(const RouterParams p, const float* val, int* list, int my_e,
+                                        int n, int lane) {
+  double m = 0.0, z = 1.0;
+  if (!p.sigmoid) {   // the sum over all experts
+    float mf = -F32_MAX;
+    for (int e = lane; e < p.E; e += 32) mf = fmaxf(mf, val[e]);
+    m = static_cast<double>(warp_fmax(mf));
+    z = 0.0;
+    for (int e = lane; e < p.E; e += 32) z += exp64(static_cast<double>(val[e]) - m);
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL_MASK, z, o);
+  }
+  const int e = lane < n ? my_e : 0;
+  const double l = static_cast<double>(val[e]);
+  const double x = exp64(p.sigmoid ? -l : l - m);
+  const double c = (p.sigmoid ? 1.0 / (1.0 + x) : x / z) + static_cast<double>(__ldg(p.bias + e));
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double o = __shfl_sync(FULL_MASK, c, j);
+    const int oe = __shfl_sync(FULL_MASK, e, j);
+    rank += (o > c || (o == c && oe < e)) ? 1 : 0;
+  }
+  __syncwarp();
+  if (lane < n) list[rank] = e;
+  __syncwarp();
+  return lane < n ? list[lane] : -1;
 }
 
 template <int VPL>
@@ -218,18 +301,21 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
                     int32_t* __restrict__ src_tok, int32_t* __restrict__ src_slot,
                     uint8_t* __restrict__ drop_mask, int* err) {
   griddep_wait();   // see common.cuh: dependent launches
-  // per warp: room for 64-bit keys (the exact choice), and the fp32 values that its groups are
-  // judged by
+  // per warp: room for 64-bit keys (the exact choice), the values that its groups are judged by,
+  // and the logits
   extern __shared__ double s_dyn[];
   __shared__ int s_idx[RG_CHUNK][8];
   __shared__ uint32_t s_bits[256];
   __shared__ int s_off[257];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warps = blockDim.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * RG_CHUNK + warp;
   const int E = p.E, k = p.k;
   double* s_dbl = s_dyn + warp * 32 * VPL;
-  float* s_val = reinterpret_cast<float*>(s_dyn + RG_CHUNK * 32 * VPL) + warp * 32 * VPL;
-  for (int e = threadIdx.x; e < E; e += RG_THREADS) s_bits[e] = 0u;
+  float* s_val = reinterpret_cast<float*>(s_dyn + warps * 32 * VPL) + warp * 64 * VPL;
+  float* s_log = s_val + 32 * VPL;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) s_bits[e] = 0u;
+  if (threadIdx.x < RG_CHUNK * 8) (&s_idx[0][0])[threadIdx.x] = -1;
   float v[VPL];
 #pragma unroll
   for (int s = 0; s < VPL; ++s) {
@@ -239,11 +325,10 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
   __syncthreads();
 
   int my_e = -1;
-  bool redo = false;
-  float top = -F32_MAX, z = 0.0f;   // softmax over all experts: maximum and sum
   if (t < p.T) {
+    bool redo = false;
     bool nan_here = false;
-    float top_here = -F32_MAX;
+    float top = -F32_MAX, z = 0.0f;   // softmax over all experts: maximum and sum
 #pragma unroll
     for (int s = 0; s < VPL; ++s) {
       if (v[s] != v[s]) {
@@ -251,7 +336,8 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
         v[s] = -INFINITY;
       }
       v[s] = fminf(v[s], F32_MAX);
-      top_here = fmaxf(top_here, v[s]);
+      s_log[lane + 32 * s] = v[s];
+      top = fmaxf(top, v[s]);
     }
     if (__any_sync(FULL_MASK, nan_here) && lane == 0) flag_error(err, MOE_DEVERR_NAN_LOGIT);
     const bool keyed = p.bias != nullptr;               // keys are scores + bias
@@ -260,80 +346,83 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
 #pragma unroll
     for (int s = 0; s < VPL; ++s) sc[s] = 0.0f;
     if (!p.sigmoid && (scored || !p.renorm)) {
-      top = warp_fmax(top_here);
+      top = warp_fmax(top);
 #pragma unroll
       for (int s = 0; s < VPL; ++s) {
-        sc[s] = expf(v[s] - top);
+        sc[s] = fast_exp(v[s] - top);
         z += sc[s];
       }
-      z = warp_sum(z);
-      const float inv = 1.0f / fmaxf(z, 1e-37f);
+      z = fmaxf(warp_sum(z), 1e-37f);
+      const float inv = 1.0f / z;
 #pragma unroll
       for (int s = 0; s < VPL; ++s) sc[s] *= inv;
     } else if (scored) {
 #pragma unroll
-      for (int s = 0; s < VPL; ++s) sc[s] = 1.0f / (1.0f + expf(-v[s]));
+      for (int s = 0; s < VPL; ++s) sc[s] = fast_rcp(1.0f + fast_exp(-v[s]));
     }
-    uint32_t key[VPL];
+    SortedKeys<VPL> keys;
     float big = 0.0f;
 #pragma unroll
     for (int s = 0; s < VPL; ++s) {
       const int e = lane + 32 * s;
-      key[s] = 0u;
+      keys.key[s] = 0u;
       const bool live = v[s] > -INFINITY;
       const float c = keyed && e < E ? sc[s] + __ldg(p.bias + e) : sc[s];
       if (live) {
-        key[s] = key32(keyed ? c : v[s]);
+        keys.key[s] = key32(keyed ? c : v[s]);
         big = fmaxf(big, fabsf(c));
       }
-      if (p.G > 1 && e < E) s_val[e] = !live ? -INFINITY : scored ? c : v[s];
+      if (p.G > 1) s_val[e] = !live ? -INFINITY : scored ? c : v[s];
     }
-    // error bound of an fp32 key.  sigma: one ulp of expf and two roundings, below 2^-21 of a
-    // score <= 1.  softmax: the argument's rounding |x| 2^-24 times e^x is below 2^-25, the
-    // sum of 256 terms adds 13 roundings, the quotient two: below 2^-19.  Adding the bias
-    // rounds once more, relative to the key.
-    const float tol = scored ? (p.sigmoid ? 0x1p-21f : 0x1p-19f) + 0x1p-23f * warp_fmax(big) : 0.0f;
+    // Error bound of an fp32 key.  sigma = 1 / (1 + e^-x): the exponential is off by 2^-22 and by
+    // its argument's rounding, |x| 2^-24, of which sigma (1 - sigma) <= 1/4 reaches the result
+    // (x sigma (1 - sigma) < 0.23); the sum and the reciprocal by 0.75 * 2^-22 of it: below 2^-22.  softmax: e^x is off by 2^-22 and
+    // |x| 2^-24 of itself, the sum of 256 terms by 13 roundings more, the quotient by two:
+    // below 2^-19.  Adding the bias rounds once more, relative to the key.
+    const float tol =
+        scored ? (p.sigmoid ? 0x1p-22f : 0x1p-19f) + 0x1p-24f * warp_fmax(big) : 0.0f;
     if (p.G > 1) {
       __syncwarp();
-      int g, L;
-      const float worth = group_worth(s_val, p.G, p.per, p.top2, lane, g, L);
       float margin;
-      const uint32_t mask = choose_groups(worth, g, L, p.G, p.top_groups, lane, margin);
-      // two keys a group and the rounding of their sum, on both sides
-      if (scored && !(margin > 5.0f * tol)) redo = true;
+      const uint32_t mask = choose_groups(group_worth(s_val, p, lane), p, lane, margin);
+      // two keys a group and the rounding of their sum, on both sides; NaN: -inf on both
+      if (scored && margin <= 5.0f * tol) redo = true;
 #pragma unroll
       for (int s = 0; s < VPL; ++s)
-        if (lane + 32 * s < E && !((mask >> ((lane + 32 * s) / p.per)) & 1u)) key[s] = 0u;
+        if (lane + 32 * s < E && !((mask >> group_of(p, lane + 32 * s)) & 1u)) keys.key[s] = 0u;
     }
+    keys.sort(lane);
+    __syncwarp();
+    // the k best, and with scores in the keys every further one that may belong to them: lane j
+    // gets the j-th
     uint32_t last = 0u;
-    for (int j = 0; j < k; ++j) {
+    int last_e = -1, found = 0;
+    bool close = false;
+    for (;; ++found) {
+      if (found == (keyed ? 32 : k)) {
+        redo |= keyed;   // more candidates than lanes
+        break;
+      }
       int e;
-      const uint32_t got = take_best<VPL>(key, lane, e);
-      if (lane == j) my_e = e;
-      if (keyed && j > 0 && got != 0u && !(unkey32(last) - unkey32(got) > 2.0f * tol)) redo = true;
+      const uint32_t got = keys.take(lane, e);
+      if (got == 0u) break;
+      if (keyed && found > 0) {
+        // too close to tell, unless they are made of the same logit and the same bias
+        const bool near = unkey32(last) - unkey32(got) <= 2.0f * tol;
+        if (found >= k && !near) break;
+        if (near && (s_log[e] != s_log[last_e] || __ldg(p.bias + e) != __ldg(p.bias + last_e)))
+          close = true;
+      }
+      if (lane == found) my_e = e;
       last = got;
+      last_e = e;
     }
-    if (keyed && last != 0u) {   // the first one left out
-      int e;
-      const uint32_t got = take_best<VPL>(key, lane, e);
-      if (got != 0u && !(unkey32(last) - unkey32(got) > 2.0f * tol)) redo = true;
-    }
-    if (redo) {
-      __syncwarp();
-#pragma unroll
-      for (int s = 0; s < VPL; ++s)
-        if (lane + 32 * s < E) s_val[lane + 32 * s] = v[s];
-      my_e = choose_exact<VPL>(p, s_val, s_dbl, lane);
-    }
+    if (redo) my_e = choose_exact<VPL>(p, s_log, s_dbl, lane);
+    else if (close) my_e = order_exact(p, s_log, reinterpret_cast<int*>(s_val), my_e, found, lane);
+    if (lane >= k) my_e = -1;
 
     // weights of the chosen, one lane each
-    float my_l = -INFINITY;
-    const int at = my_e < 0 ? 0 : my_e;
-#pragma unroll
-    for (int s = 0; s < VPL; ++s) {
-      const float o = __shfl_sync(FULL_MASK, v[s], at & 31);
-      if (s == (at >> 5)) my_l = o;
-    }
+    const float my_l = my_e >= 0 ? s_log[my_e] : -INFINITY;
     const bool live = lane < k && my_e >= 0;
     float w = 0.0f;
     if (p.renorm) {
@@ -358,7 +447,7 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
       if (my_e < 0) dest_row[t * k + lane] = -1;
     }
   }
-  if (lane < 8) s_idx[warp][lane] = (t < p.T && lane < k) ? my_e : -1;
+  if (t < p.T && lane < k) s_idx[warp][lane] = my_e;
   __syncthreads();
 
   // chunk histogram as per-expert token bit masks (OR is order-free: deterministic)
@@ -373,7 +462,7 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
   const int64_t slot = (static_cast<int64_t>(blockIdx.x) * RG_CHUNK + tok) * k + j;
   if (nch > 1) {
     if (e >= 0) dest_row[slot] = rank;
-    for (int x = threadIdx.x; x < E; x += RG_THREADS)
+    for (int x = threadIdx.x; x < E; x += blockDim.x)
       chunk_cnt[static_cast<int64_t>(x) * nch + blockIdx.x] = __popc(s_bits[x]);
     griddep_launch();
     return;
@@ -419,11 +508,92 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
       src_slot[d] = static_cast<int32_t>(slot);
     }
   }
-  for (int i = threadIdx.x; i < p.T * k; i += RG_THREADS)
+  for (int i = threadIdx.x; i < p.T * k; i += blockDim.x)
     if (i >= s_off[E]) {
       src_tok[i] = -1;
       src_slot[i] = -1;
     }
+  griddep_launch();
+}
+
+// One warp per expert: its chunks' counts to their exclusive sums, its total and what is kept.
+__global__ void __launch_bounds__(256)
+order_count_kernel(int32_t* __restrict__ chunk_cnt, int64_t nch, int E, int cap,
+                   int32_t* __restrict__ counts, int32_t* __restrict__ kept) {
+  griddep_wait();   // see common.cuh: dependent launches
+  const int lane = threadIdx.x & 31;
+  const int e = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (e < E) {
+    int32_t* col = chunk_cnt + static_cast<int64_t>(e) * nch;
+    int running = 0;
+    // 256 chunks at a time, the eight loads before any store
+    for (int64_t base = 0; base < nch; base += 256) {
+      int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t c = base + 32 * i + lane;
+        v[i] = c < nch ? col[c] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int64_t c = base + 32 * i + lane;
+        const int incl = warp_incl_scan(v[i]);
+        if (c < nch) col[c] = running + incl - v[i];
+        running += __shfl_sync(FULL_MASK, incl, 31);
+      }
+    }
+    if (lane == 0) {
+      counts[e] = running;
+      kept[e] = cap > 0 && running > cap ? cap : running;
+    }
+  }
+  griddep_launch();
+}
+
+// A thread per slot; every CTA sums the kept rows to the segments' offsets itself.
+__global__ void __launch_bounds__(256)
+order_assign_kernel(const int32_t* __restrict__ topk_idx, int64_t T, int k, int E, int cap,
+                    const int32_t* __restrict__ chunk_base, int64_t nch,
+                    const int32_t* __restrict__ kept, int32_t* __restrict__ offsets,
+                    int32_t* __restrict__ dest_row, int32_t* __restrict__ src_tok,
+                    int32_t* __restrict__ src_slot, uint8_t* __restrict__ drop_mask) {
+  griddep_wait();   // see common.cuh: dependent launches
+  __shared__ int s_off[257];
+  __shared__ int s_sum[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + tid;
+  const bool in = i < T * k;
+  const int in_chunk = in ? dest_row[i] : -1;   // rank inside the chunk, or -1: not routed
+  const int e = in ? topk_idx[i] : -1;
+  const int n = tid < E ? kept[tid] : 0;
+  const int base =
+      in_chunk >= 0 ? chunk_base[static_cast<int64_t>(e) * nch + i / k / RG_CHUNK] : 0;
+  const int incl = warp_incl_scan(n);
+  if (lane == 31) s_sum[warp] = incl;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) before += w < warp ? s_sum[w] : 0;
+  if (tid < E) s_off[tid] = before + incl - n;
+  if (tid == E - 1) s_off[E] = before + incl;
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int x = tid; x <= E; x += 256) offsets[x] = s_off[x];
+  if (in) {
+    if (i >= s_off[E]) {
+      src_tok[i] = -1;
+      src_slot[i] = -1;
+    }
+    const int r = in_chunk < 0 ? -1 : base + in_chunk;
+    const bool stays = r >= 0 && (cap == 0 || r < cap);
+    const int d = stays ? s_off[e] + r : -1;
+    dest_row[i] = d;
+    drop_mask[i] = stays ? 0 : 1;
+    if (stays) {
+      src_tok[d] = static_cast<int32_t>(i / k);
+      src_slot[d] = static_cast<int32_t>(i);
+    }
+  }
   griddep_launch();
 }
 
@@ -471,16 +641,19 @@ route_groups_bwd_kernel(const RouterParams p, const int32_t* __restrict__ topk_i
     }
     top = warp_fmax(top);
     if (e >= 0) l = clean(__ldg(row + e));
+    // bit s: this lane's s-th expert is chosen
+    uint32_t chosen = 0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int ej = __shfl_sync(FULL_MASK, e, j);
+      if ((ej & 31) == lane && ej >= 0) chosen |= 1u << (ej >> 5);
+    }
     float zz = 0.0f;
 #pragma unroll
     for (int s = 0; s < VPL; ++s) {
-      bool chosen = false;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        chosen |= __shfl_sync(FULL_MASK, e, j) == lane + 32 * s;
       v[s] = expf(v[s] - top);
       zz += v[s];
-      if (!chosen) rest += v[s];
+      if (!((chosen >> s) & 1u)) rest += v[s];
     }
     z = fmaxf(warp_sum(zz), 1e-37f);
     rest = warp_sum(rest) / z;
@@ -516,18 +689,13 @@ route_groups_bwd_kernel(const RouterParams p, const int32_t* __restrict__ topk_i
     if (dense) acc = fmaf(rest, g, acc);
     if (live) d = u * acc * (p.sigmoid ? 1.0f / (1.0f + expf(l)) : 1.0f);
   }
+  // the whole row first, then the chosen experts' places
+  const float each = dense ? -dot / z : 0.0f;
 #pragma unroll
-  for (int s = 0; s < VPL; ++s) {
-    const int x = lane + 32 * s;
-    float val = dense ? -(v[s] / z) * dot : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int ej = __shfl_sync(FULL_MASK, e, j);
-      const float dj = __shfl_sync(FULL_MASK, d, j);
-      if (ej == x) val = dj;
-    }
-    if (x < E) dlogits[t * E + x] = val;
-  }
+  for (int s = 0; s < VPL; ++s)
+    if (lane + 32 * s < E) dlogits[t * E + lane + 32 * s] = dense ? v[s] * each : 0.0f;
+  __syncwarp();
+  if (e >= 0) dlogits[t * E + e] = d;
   griddep_launch();
 }
 
@@ -547,6 +715,10 @@ RouterParams router_params(const moe_config_t* c, const moe_router_t* r, const f
   p.cap = c->capacity;
   p.scale = c->route_scale;
   if (p.top_groups == p.G) p.G = 1;   // every group stays: nothing to choose
+  p.per_magic = (65536 + p.per - 1) / p.per;
+  p.lanes_log2 = 0;
+  while ((2 << p.lanes_log2) * p.G <= 32 && (1 << p.lanes_log2) < p.per) ++p.lanes_log2;
+  p.turns = (p.per + (1 << p.lanes_log2) - 1) >> p.lanes_log2;
   return p;
 }
 
@@ -560,12 +732,14 @@ cudaError_t launch_route_groups(const moe_config_t* c, const moe_router_t* r, co
   const RouterParams p = router_params(c, r, logits);
   const int64_t nch = route_chunks(c->T);
   int32_t* chunk_cnt = static_cast<int32_t*>(scratch);
-  const dim3 grid(static_cast<unsigned>(nch)), block(RG_THREADS);
+  // a short single chunk: a warp per token, at least the 256 threads of its histogram
+  const unsigned warps = nch > 1 ? 32u : static_cast<unsigned>(c->T < 8 ? 8 : c->T);
+  const dim3 grid(static_cast<unsigned>(nch)), block(32 * warps);
 #define MOE_RG_LAUNCH(V)                                                                       \
   (e = cudaFuncSetAttribute(route_groups_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                            RG_CHUNK * 32 * V * 12)) != cudaSuccess                             \
+                            RG_CHUNK * 32 * V * 16)) != cudaSuccess                             \
       ? e                                                                                       \
-      : launch_pdl(route_groups_kernel<V>, grid, block, RG_CHUNK * 32 * V * 12, st, 1, p,       \
+      : launch_pdl(route_groups_kernel<V>, grid, block, warps * 32 * V * 16, st, 1, p,          \
                    topk_idx, topk_w, dest_row, chunk_cnt, nch, counts, kept, offsets, src_tok,  \
                    src_slot, drop_mask, err)
   cudaError_t e;
@@ -575,8 +749,12 @@ cudaError_t launch_route_groups(const moe_config_t* c, const moe_router_t* r, co
   else e = MOE_RG_LAUNCH(8);
 #undef MOE_RG_LAUNCH
   if (e != cudaSuccess || nch == 1) return e;
-  return launch_route_order(c->T, c->E, c->k, c->capacity, topk_idx, chunk_cnt, counts, kept,
-                            offsets, dest_row, src_tok, src_slot, drop_mask, st);
+  e = launch_pdl(order_count_kernel, dim3(static_cast<unsigned>((c->E + 7) / 8)), dim3(256), 0, st,
+                 1, chunk_cnt, nch, c->E, c->capacity, counts, kept);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(order_assign_kernel, dim3(static_cast<unsigned>((c->T * c->k + 255) / 256)),
+                    dim3(256), 0, st, 1, topk_idx, c->T, c->k, c->E, c->capacity, chunk_cnt, nch,
+                    kept, offsets, dest_row, src_tok, src_slot, drop_mask);
 }
 
 cudaError_t launch_route_groups_bwd(const moe_config_t* c, const moe_router_t* r,
