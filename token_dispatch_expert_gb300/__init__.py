@@ -179,11 +179,20 @@ def _p(t):
 
 def _s(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream():
+    """The current stream's handle.  A small call's time is mostly the host's, and torch's own
+    accessor builds a Stream object around the handle."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None:
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
 
 
 def _check(status, where):
@@ -396,10 +405,18 @@ def make_router(score="softmax", groups=1, top_groups=None, group_top=1, renorm=
     return r
 
 
+_dtypes = {}   # name -> torch dtype
+
+
 def _typed(t, dtype, name):
     """_p for a buffer of one element type (a torch dtype's name)."""
-    if t is not None and not isinstance(t, int) and str(t.dtype) != "torch." + dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t is not None and not isinstance(t, int):
+        want = _dtypes.get(dtype)
+        if want is None:
+            import torch
+            want = _dtypes[dtype] = getattr(torch, dtype)
+        if t.dtype is not want:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     return _p(t)
 
 
@@ -466,7 +483,8 @@ def moe_fp8_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, *,
     """Quantise rows of x (bf16, rows may be strided) along the row (codes, scales) and, or, along
     the tokens of the segments (codes_t, scales_t); row p is x[src_tok[p]] when src_tok is
     given."""
-    if x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda or str(x.dtype) != "torch.bfloat16":
+    import torch
+    if x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda or x.dtype is not torch.bfloat16:
         raise ValueError("x: expected a CUDA bf16 matrix with adjacent columns")
     G = _groups(offsets)
     rows = x.shape[0] if src_tok is None else src_tok.numel()
@@ -532,13 +550,13 @@ def moe_fp8_swiglu_bwd(dh, ab, codes, scales, codes_t=None, scales_t=None, h_cod
                                     _s(stream)), "moe_fp8_swiglu_bwd")
 
 
-OUT_TYPES = {"torch.bfloat16": 0, "torch.float32": 1}
-
-
 def _out_type(t, name):
-    if str(t.dtype) not in OUT_TYPES:
-        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
-    return OUT_TYPES[str(t.dtype)]
+    import torch
+    if t.dtype is torch.bfloat16:
+        return 0
+    if t.dtype is torch.float32:
+        return 1
+    raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
 
 
 def moe_fp8_gemm(a, a_scales, b, b_scales, out, K, *, offsets=None, ws, stream=None):

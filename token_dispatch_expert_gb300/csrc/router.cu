@@ -735,19 +735,21 @@ cudaError_t launch_route_groups(const moe_config_t* c, const moe_router_t* r, co
   // a short single chunk: a warp per token, at least the 256 threads of its histogram
   const unsigned warps = nch > 1 ? 32u : static_cast<unsigned>(c->T < 8 ? 8 : c->T);
   const dim3 grid(static_cast<unsigned>(nch)), block(32 * warps);
-#define MOE_RG_LAUNCH(V)                                                                       \
-  (e = cudaFuncSetAttribute(route_groups_kernel<V>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                            RG_CHUNK * 32 * V * 16)) != cudaSuccess                             \
-      ? e                                                                                       \
-      : launch_pdl(route_groups_kernel<V>, grid, block, warps * 32 * V * 16, st, 1, p,          \
-                   topk_idx, topk_w, dest_row, chunk_cnt, nch, counts, kept, offsets, src_tok,  \
-                   src_slot, drop_mask, err)
+  auto go = [&](auto kern, int vpl) {
+    const size_t smem = static_cast<size_t>(warps) * 32 * vpl * 16;
+    if (smem > 48 * 1024) {
+      const cudaError_t a = cudaFuncSetAttribute(
+          kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (a != cudaSuccess) return a;
+    }
+    return launch_pdl(kern, grid, block, smem, st, 1, p, topk_idx, topk_w, dest_row, chunk_cnt, nch,
+                      counts, kept, offsets, src_tok, src_slot, drop_mask, err);
+  };
   cudaError_t e;
-  if (c->E <= 32) e = MOE_RG_LAUNCH(1);
-  else if (c->E <= 64) e = MOE_RG_LAUNCH(2);
-  else if (c->E <= 128) e = MOE_RG_LAUNCH(4);
-  else e = MOE_RG_LAUNCH(8);
-#undef MOE_RG_LAUNCH
+  if (c->E <= 32) e = go(route_groups_kernel<1>, 1);
+  else if (c->E <= 64) e = go(route_groups_kernel<2>, 2);
+  else if (c->E <= 128) e = go(route_groups_kernel<4>, 4);
+  else e = go(route_groups_kernel<8>, 8);
   if (e != cudaSuccess || nch == 1) return e;
   e = launch_pdl(order_count_kernel, dim3(static_cast<unsigned>((c->E + 7) / 8)), dim3(256), 0, st,
                  1, chunk_cnt, nch, c->E, c->capacity, counts, kept);
