@@ -44,7 +44,8 @@ constexpr int FG_EPI_WARPS = 8;
 constexpr int FG_BUFS = 4;                // accumulators: (block & 1) * 2 + half
 constexpr int FG_MAX_G = 256;
 constexpr uint32_t FG_TMEM_COLS = 512;
-constexpr int FG_BOX_BYTES = 32 * 128;    // a warp's piece of a finished tile: 32 rows x 128 bytes
+constexpr int FG_BOX_BYTES = 32 * 128;    // a piece of a finished tile: 32 rows x 128 bytes
+constexpr int FG_BOXES = 2;               // per epilogue warp
 constexpr long long FG_WAIT_BUDGET = 4000000000LL;
 
 template <int PAIR>
@@ -54,7 +55,7 @@ struct FgGeo {
   static constexpr int B_ROWS = FG_TILE_N / PAIR;       // this CTA's rows of b
   static constexpr int B_BYTES = B_ROWS * FG_BK;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = PAIR == 2 ? 5 : 3;
+  static constexpr int STAGES = PAIR == 2 ? 4 : 3;
 };
 
 // Scales of one block: a row's in row[], and in col[] the columns' (weight gradient) or the two
@@ -78,7 +79,7 @@ static_assert(offsetof(FgCtl, scales) % 16 == 0, "read as float4");
 
 template <int PAIR>
 constexpr size_t fg_smem() {
-  return FgGeo<PAIR>::STAGES * FgGeo<PAIR>::STAGE_BYTES + FG_EPI_WARPS * FG_BOX_BYTES +
+  return FgGeo<PAIR>::STAGES * FgGeo<PAIR>::STAGE_BYTES + FG_EPI_WARPS * FG_BOXES * FG_BOX_BYTES +
          sizeof(FgCtl) + 1024;
 }
 static_assert(fg_smem<1>() <= 232448 && fg_smem<2>() <= 232448, "227 KB per CTA");
@@ -225,7 +226,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* boxes = smem + STAGES * GE::STAGE_BYTES;
-  FgCtl* ctl = reinterpret_cast<FgCtl*>(boxes + FG_EPI_WARPS * FG_BOX_BYTES);
+  FgCtl* ctl = reinterpret_cast<FgCtl*>(boxes + FG_EPI_WARPS * FG_BOXES * FG_BOX_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem);
   volatile int* abort_flag = &ctl->abort;
@@ -318,20 +319,23 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
   const uint32_t tmem_base = ctl->tmem_base;
 
   // tile -> group, row tile, column tile; row tiles run fastest, so the CTAs at work share the
-  // group's weight rows in L2
+  // group's weight rows in L2.  Every role walks its tiles in ascending order, so the group is
+  // found by going on from the last one; with fewer than 2^16 column tiles the fp32 quotient is
+  // off by at most one, which the remainder corrects.
   auto map_tile = [&](int tile, int& g, int& mt, int& nt) {
-    int lo = 0, hi = p.G;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (ctl->tprefix[mid] <= tile) lo = mid;
-      else hi = mid;
-    }
-    g = lo;
+    while (ctl->tprefix[g + 1] <= tile) ++g;
     const int local = tile - ctl->tprefix[g];
     const int mtg =
         WG ? p.m_tiles : ceil_div(ctl->gstart[g + 1] - ctl->gstart[g], GE::TILE_M);
-    nt = local / mtg;
+    nt = static_cast<int>(__fdividef(static_cast<float>(local), static_cast<float>(mtg)));
     mt = local - nt * mtg;
+    if (mt < 0) {
+      --nt;
+      mt += mtg;
+    } else if (mt >= mtg) {
+      ++nt;
+      mt -= mtg;
+    }
   };
   auto blocks = [&](int g) { return WG ? ctl->kbpre[g + 1] - ctl->kbpre[g] : p.kb; };
 
@@ -342,8 +346,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
+      int g = 0;
       for (int tile = unit; tile < total && ok; tile += num_units) {
-        int g, mt, nt;
+        int mt, nt;
         map_tile(tile, g, mt, nt);
         const int nkb = fg_uniform(blocks(g));
         int x = fg_uniform(WG ? ctl->kbpre[g] * FG_BK : 0);
@@ -400,10 +405,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const uint64_t da0 = make_smem_desc(smem_base, 16, 1024);
         const uint64_t db0 =
             make_smem_desc(smem_base + GE::A_BYTES + h * (GE::B_BYTES / 2), 16, 1024);
+        int g = 0;
         for (int tile = unit; tile < total && ok; tile += num_units) {
           int nkb = p.kb;
           if (WG) {
-            int g, mt, nt;
+            int mt, nt;
             map_tile(tile, g, mt, nt);
             nkb = fg_uniform(blocks(g));
           }
@@ -455,8 +461,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       // -------------------------------------------------------------- scale loader (warp 2)
       uint32_t ci = 0;   // chunks loaded
       bool ok = true;
+      int g = 0;
       for (int tile = unit; tile < total && ok; tile += num_units) {
-        int g, mt, nt;
+        int mt, nt;
         map_tile(tile, g, mt, nt);
         const int nkb = blocks(g);
         const int m0 = mt * GE::TILE_M + 128 * rank;
@@ -507,8 +514,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     // ---------------------------------------------------------------- epilogue (8 warps)
     const int q = warp & 3;                          // the lane quarter this warp may read
     const int hh = (warp - FG_EPI_WARP0) >> 2;       // which 128 of the 256 columns
-    uint8_t* box = boxes + (warp - FG_EPI_WARP0) * FG_BOX_BYTES;
-    const uint32_t box_row = smem_u32(box) + lane * 128;
+    uint8_t* my_boxes = boxes + (warp - FG_EPI_WARP0) * FG_BOXES * FG_BOX_BYTES;
     // this half's two accumulators: TMEM address, barriers (the leader counts both CTAs' warps)
     const uint32_t taddr0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + 128 * hh;
     const uint32_t tfull0 = smem_u32(&ctl->tfull[hh]);
@@ -517,13 +523,14 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint32_t it = 0;   // blocks added
     uint32_t ci = 0;   // scale chunks used up
     bool ok = true;
+    int g = 0;
     for (int tile = unit; tile < total && ok; tile += num_units) {
-      int g, mt, nt;
+      int mt, nt;
       map_tile(tile, g, mt, nt);
       const int nkb = blocks(g);
-      float acc[128];
+      float2 acc[64];
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+      for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.0f, 0.0f);
       for (int left = nkb; left > 0 && ok; left -= FG_CHUNK, ++ci) {
         if (!fg_wait(smem_u32(&ctl->sfull[ci & 1u]), (ci >> 1) & 1u, abort_flag, p.err)) {
           ok = false;
@@ -556,21 +563,23 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 else mbar_arrive(tempty0 + par * 16);
               }
             }
+            const float2 s2 = make_float2(s, s);
+            auto sums = [&](int i) {
+              return make_float2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
+            };
             if constexpr (WG) {
               const float4* cs = reinterpret_cast<const float4*>(sc->col + 128 * hh + W * c);
 #pragma unroll
               for (int i = 0; i < W / 4; ++i) {
                 const float4 f = cs[i];
-                float* a = acc + W * c + 4 * i;
-                a[0] = fmaf(__uint_as_float(d[4 * i]), f.x * s, a[0]);
-                a[1] = fmaf(__uint_as_float(d[4 * i + 1]), f.y * s, a[1]);
-                a[2] = fmaf(__uint_as_float(d[4 * i + 2]), f.z * s, a[2]);
-                a[3] = fmaf(__uint_as_float(d[4 * i + 3]), f.w * s, a[3]);
+                float2* a = acc + W / 2 * c + 2 * i;
+                a[0] = __ffma2_rn(sums(2 * i), __fmul2_rn(make_float2(f.x, f.y), s2), a[0]);
+                a[1] = __ffma2_rn(sums(2 * i + 1), __fmul2_rn(make_float2(f.z, f.w), s2), a[1]);
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < W; ++i)
-                acc[W * c + i] = fmaf(__uint_as_float(d[i]), s, acc[W * c + i]);
+              for (int i = 0; i < W / 2; ++i)
+                acc[W / 2 * c + i] = __ffma2_rn(sums(i), s2, acc[W / 2 * c + i]);
             }
           }
         }
@@ -588,32 +597,39 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
       for (int part = 0; part < 128 / BOX_COLS; ++part) {
         const int n = n0 + BOX_COLS * part;
-        if (lane == 0) bulk_wait_group_read<0>();   // the last store has read the box
+        uint8_t* box = my_boxes + part % FG_BOXES * FG_BOX_BYTES;
+        const uint32_t box_row = smem_u32(box) + lane * 128;
+        if (lane == 0) bulk_wait_group_read<FG_BOXES - 1>();   // the store before last has read it
         __syncwarp();
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           uint4 v;
           if (F32) {
-            const float* x = acc + BOX_COLS * part + 4 * j;
-            v = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                           __float_as_uint(x[3]));
+            const float2* x = acc + BOX_COLS / 2 * part + 2 * j;
+            v = make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y),
+                           __float_as_uint(x[1].x), __float_as_uint(x[1].y));
           } else {
-            v = pack8(acc + BOX_COLS * part + 8 * j);
+            const float2* x = acc + BOX_COLS / 2 * part + 4 * j;
+            v = make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y),
+                           pack_bf16x2(x[2].x, x[2].y), pack_bf16x2(x[3].x, x[3].y));
           }
           st_shared_v4(box_row + ((j ^ (lane & 7)) << 4), v);
         }
         if (by_tma) {
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0 && n < p.N) {
-            tma_store_3d(&tmC, smem_u32(box), n, WG ? lrow0 : ctl->gstart[g] + lrow0, WG ? g : 0);
+          if (lane == 0) {   // a group even where there is nothing to store: one per box
+            if (n < p.N)
+              tma_store_3d(&tmC, smem_u32(box), n, WG ? lrow0 : ctl->gstart[g] + lrow0,
+                           WG ? g : 0);
             bulk_commit_group();
           }
-        } else if (n < p.N) {
+        } else {
           __syncwarp();
           const long long row =
               WG ? static_cast<long long>(g) * p.K + lrow0 : ctl->gstart[g] + lrow0;
-          copy_box<F32>(box, p.out, row * p.ldo + n, p.ldo, nr, p.N - n, lane);
+          if (n < p.N) copy_box<F32>(box, p.out, row * p.ldo + n, p.ldo, nr, p.N - n, lane);
+          if (lane == 0) bulk_commit_group();   // empty: one group per box, as above
           __syncwarp();
         }
       }
