@@ -192,24 +192,30 @@ __device__ __forceinline__ void copy_box(const uint8_t* box, void* out, long lon
                                          long long ldo, int nr, int nc, int lane) {
   const uint8_t* src = box + (lane & 3) * 4;
   const int piece = lane >> 2;
-  if (F32) {
-    float* dst = static_cast<float*>(out) + off + lane;
-    for (int i = 0; i < nr; ++i)
-      if (lane < nc)
-        dst[i * ldo] = *reinterpret_cast<const float*>(src + i * 128 + ((piece ^ (i & 7)) << 4));
-  } else {
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out) + off + 2 * lane;
-    const bool two = 2 * lane + 1 < nc, one = 2 * lane < nc;
-    for (int i = 0; i < nr; ++i) {
-      const uint32_t w =
-          *reinterpret_cast<const uint32_t*>(src + i * 128 + ((piece ^ (i & 7)) << 4));
-      __nv_bfloat16* d = dst + i * ldo;
-      if (two && (reinterpret_cast<uintptr_t>(d) & 3u) == 0) {
-        *reinterpret_cast<uint32_t*>(d) = w;
-      } else {
-        if (one) *reinterpret_cast<uint16_t*>(d) = static_cast<uint16_t>(w);
-        if (two) *reinterpret_cast<uint16_t*>(d + 1) = static_cast<uint16_t>(w >> 16);
+  constexpr int SIZE = F32 ? 4 : 2;
+  uint8_t* dst = static_cast<uint8_t*>(out) + off * SIZE + 4 * lane;
+  const long long step = ldo * SIZE;
+  const bool one = F32 ? lane < nc : 2 * lane < nc;      // of this lane's columns, any in the row
+  const bool two = F32 || 2 * lane + 1 < nc;             // bf16: both
+  // 4-byte stores: always possible in fp32, in bf16 where every row starts on 4 bytes
+  const bool wide = F32 || ((reinterpret_cast<uintptr_t>(dst) | static_cast<uintptr_t>(step)) & 3u) == 0;
+#pragma unroll 1
+  for (int i0 = 0; i0 < nr; i0 += 8) {   // eight rows' reads before their stores
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = *reinterpret_cast<const uint32_t*>(src + (i0 + i) * 128 + ((piece ^ i) << 4));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (one && i0 + i < nr) {
+        if (wide && two) {
+          *reinterpret_cast<uint32_t*>(dst) = w[i];
+        } else {
+          *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w[i]);
+          if (two) *reinterpret_cast<uint16_t*>(dst + 2) = static_cast<uint16_t>(w[i] >> 16);
+        }
       }
+      dst += step;
     }
   }
 }
@@ -726,7 +732,11 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.err = a.err;
   // pairs: weight gradients of more than 128 rows; products whose average segment fills more
   // than three quarters of a pair's 256 rows
-  const bool pair = a.wgrad ? a.K > 128 : a.rows >= 192 * static_cast<int64_t>(a.G);
+  // pairs: weight gradients of more than 128 rows (201 us against 212 for one CTA at 2048 x 768 of
+  // 128 experts), products with 768 rows or more to the average segment.  Below, a pair's
+  // padding of the last tile outweighs its cheaper operands (231 us against 249 at 512 rows of
+  // 1536 x 2048, but 204 against 185 at 1024 rows of 28672 x 4096)
+  const bool pair = a.wgrad ? a.K > 128 : a.rows >= 768 * static_cast<int64_t>(a.G);
   const uint32_t b_rows = pair ? 64 : 256;   // a box of b
   CUtensorMap ta, tb, tc;
   bool ok;
