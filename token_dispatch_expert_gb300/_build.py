@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(OUT_DIR, "libmoe_gb300.so")
 OBJ_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["route.cu", "router.cu", "dispatch.cu", "grouped_gemm.cu", "mx.cu", "fp8.cu",
-           "fp8_gemm.cu", "moe_api.cu"]
+           "fp8_gemm.cu", "fp8_few.cu", "moe_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -282,6 +282,9 @@ struct Fp8GemmArgs {
   int* err;
 };
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st);
+// the product for few rows (fp8_few.cu), and whether it is one
+bool fp8_few_rows(const Fp8GemmArgs& a);
+cudaError_t launch_fp8_few(const Fp8GemmArgs& a, cudaStream_t st);
 
 // Tensor map over codes [rows][ld] of which `cols` bytes a row are read (zeros past them): boxes of
 // 128 bytes x box_rows, 128-byte swizzle.
