@@ -312,8 +312,17 @@ PRODUCTS = [  # segment lengths, N, K
     ([17], 2048, 7168), ([260, 140], 128, 4096)]
 
 
+# few rows: 16- and 64-row tiles, segments of several of them, blocks shared by 2, 4 and 8 CTAs,
+# more tiles than SMs
+FEW = [
+    ([1], 128, 1024), ([16], 130, 2048), ([3], 1000, 4100), ([0, 2, 0, 5, 0, 0], 384, 7168),
+    ([40] + [0] * 7, 257, 1024), ([16, 1, 17, 0], 520, 2048), ([64], 250, 1024), ([33], 77, 7000),
+    ([150, 0, 3, 0, 1], 130, 1030), ([200] + [0] * 30 + [1], 128, 1152), ([1] * 40, 1000, 300),
+    ([30, 40, 0, 26], 4096, 520), ([2] * 256, 64, 130)]
+
+
 @pytest.mark.parametrize("fp32", [False, True])
-@pytest.mark.parametrize("lengths,N,K", PRODUCTS)
+@pytest.mark.parametrize("lengths,N,K", PRODUCTS + FEW)
 def test_product(lengths, N, K, fp32):
     off = offsets_of(lengths)
     R, G = off[-1], len(lengths)
@@ -355,6 +364,42 @@ def test_product_dense_strided_and_part_of_the_rows():
     tde.moe_fp8_gemm(a, dev(sa), b, dev(sb), out, K, offsets=odev([0, 77]), ws=ws)
     assert (out[77:] == 5).all()
     check_product(f64(out[:77]), (A @ B.T)[:77], (np.abs(A) @ np.abs(B.T))[:77], 2, True, "part")
+
+
+@pytest.mark.parametrize("R,K", [(9, 4096), (50, 1024)])
+def test_few_rows_strided_bad_and_repeated(R, K):
+    """An output inside a wider one; a row of NaN codes in the middle of a tile; the same bits from
+    every call and from a captured one."""
+    N, KB = 130, K // 128
+    av, sa = operand((R, K), 7, (R, KB))
+    bv, sb = operand((1, N, K), 8, (1, 2, KB))
+    a, b, ws = to_codes(av, K), to_codes(bv, K), ws_new()
+    a.view(torch.uint8)[4] = 0x7f
+    A = av * ref.spread(sa.astype(np.float64), K, 1)
+    B = bv[0] * ref.spread(ref.spread(sb[0].astype(np.float64), N, 0), K, 1)
+    rows = [r for r in range(R) if r != 4]
+    for dt in (torch.bfloat16, torch.float32):
+        wide = torch.zeros((R, N + 9), dtype=dt, device="cuda")
+        args = (a, dev(sa), b, dev(sb), wide[:, 3:3 + N], K)
+        tde.moe_fp8_gemm(*args, ws=ws)
+        first = wide.clone()
+        assert torch.isnan(wide[4, 3:3 + N]).all()
+        assert (wide[:, :3] == 0).all() and (wide[:, 3 + N:] == 0).all()
+        check_product(f64(wide[:, 3:3 + N])[rows], (A @ B.T)[rows],
+                      (np.abs(A) @ np.abs(B.T))[rows], KB, dt == torch.float32, "few")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            tde.moe_fp8_gemm(*args, ws=ws)
+        for _ in range(3):
+            wide.zero_()
+            graph.replay()
+            assert same_bits(wide, first)
+    assert tde.moe_status(ws)[1] == 0
+
+
+def same_bits(x, y):
+    return bool((x.view(torch.uint8) == y.view(torch.uint8)).all())
 
 
 def test_product_keeps_a_bad_row_to_itself():
