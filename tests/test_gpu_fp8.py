@@ -312,13 +312,14 @@ PRODUCTS = [  # segment lengths, N, K
     ([17], 2048, 7168), ([260, 140], 128, 4096)]
 
 
-# few rows: 16- and 64-row tiles, segments of several of them, blocks shared by 2, 4 and 8 CTAs,
-# more tiles than SMs
+# few rows: segments of several 16-row tiles, blocks shared by 2, 4 and 8 CTAs (in two rounds,
+# too), more tiles than SMs
 FEW = [
     ([1], 128, 1024), ([16], 130, 2048), ([3], 1000, 4100), ([0, 2, 0, 5, 0, 0], 384, 7168),
     ([40] + [0] * 7, 257, 1024), ([16, 1, 17, 0], 520, 2048), ([64], 250, 1024), ([33], 77, 7000),
     ([150, 0, 3, 0, 1], 130, 1030), ([200] + [0] * 30 + [1], 128, 1152), ([1] * 40, 1000, 300),
-    ([30, 40, 0, 26], 4096, 520), ([2] * 256, 64, 130)]
+    ([30, 40, 0, 26], 4096, 520), ([2] * 256, 64, 130),
+    ([13], 200, 12400), ([29, 1, 1, 1], 2294, 3100)]
 
 
 @pytest.mark.parametrize("fp32", [False, True])
@@ -366,7 +367,7 @@ def test_product_dense_strided_and_part_of_the_rows():
     check_product(f64(out[:77]), (A @ B.T)[:77], (np.abs(A) @ np.abs(B.T))[:77], 2, True, "part")
 
 
-@pytest.mark.parametrize("R,K", [(9, 4096), (50, 1024)])
+@pytest.mark.parametrize("R,K", [(9, 4096), (50, 1024), (11, 12800)])
 def test_few_rows_strided_bad_and_repeated(R, K):
     """An output inside a wider one; a row of NaN codes in the middle of a tile; the same bits from
     every call and from a captured one."""

@@ -2,16 +2,19 @@
 // read for a handful of tokens.
 //
 // The operands change places: D[n][t] = sum_kb sb[kb] sa[t][kb] sum_k b[n][k] a[t][k], the tensor
-// core's 128 rows are weight rows and its columns the tokens (16, or 64), so that a tile's rows
-// are all work and its accumulators small: eight of them rotate in TMEM, and one epilogue warp
-// per lane quarter adds them up, scaled, one thread per weight row.
+// core's 128 rows are weight rows and its 16 columns the tokens, so that a tile's rows are all
+// work and its accumulators small: eight of them rotate in TMEM, and one epilogue warp per lane
+// quarter adds them up, scaled, one thread per weight row.
 //
-// Bound by the weights' bytes.  Bandwidth wants bytes in flight: a stage is 128 weight rows x 128
-// bytes (16 KB) and the tokens' 2 or 8 KB, and 10 or 7 of them fill shared memory, 160 KB of
-// weights a CTA on its way (fp8_gemm's 48 KB stages had 96 KB, and 4.1 TB/s).  Where the 128-row
-// tiles are fewer than the SMs, clusters of 2, 4 or 8 CTAs share a tile's blocks: each sums its
-// part of them, sends each CTA of the cluster the columns that it owns through distributed shared
-// memory, and every owner adds the parts in rank order and stores its columns.
+// Bound by the weights' bytes, and in small calls by the chain of one tile's blocks.  A stage is
+// 128 weight rows x 128 bytes (16 KB) and the tokens' 2 KB; ten of them, 160 KB of weights a CTA
+// on its way, read eight experts of 4096 x 7168 for one token in 47 us, 5.0 TB/s with the launch
+// (fp8_gemm's three 48 KB stages: 57 us, 4.1 TB/s).
+//
+// Where one tile's blocks are many and the tiles few, clusters of 2, 4 or 8 CTAs share a tile's
+// blocks: each sums its part of them, sends each CTA of the cluster the columns that it owns
+// through distributed shared memory, and every owner adds the parts in rank order and stores its
+// columns (one row by 256 x 16384: 41.6 us alone, 27.4, 19.1 and 17.2 us by 2, 4 and 8).
 #include <cuda.h>
 
 #include <cstddef>
@@ -27,19 +30,15 @@ constexpr int FW_BUFS = 8;      // accumulators
 constexpr int FW_CHUNK = 4;     // blocks whose scales are loaded and freed together
 constexpr int FW_CHUNKS = 4;
 
-template <int NT>   // tokens of a tile
-struct FwGeo {
-  static constexpr int W_BYTES = 128 * FG_BK;
-  static constexpr int T_BYTES = NT * FG_BK;
-  static constexpr int STAGE_BYTES = W_BYTES + T_BYTES;   // a multiple of 1 KB
-  static constexpr int STAGES = NT == 16 ? 10 : 7;
-  static constexpr int PART_BYTES = NT * 128 * 4;
-  static constexpr uint32_t TMEM_COLS = FW_BUFS * NT;     // 128 or 512
-};
+constexpr int NT = 16;          // tokens of a tile
+constexpr int FW_W_BYTES = 128 * FG_BK;
+constexpr int FW_STAGE_BYTES = FW_W_BYTES + NT * FG_BK;   // a multiple of 1 KB
+constexpr int FW_STAGES = 10;
+constexpr int FW_PART_BYTES = NT * 128 * 4;
+constexpr uint32_t FW_TMEM_COLS = FW_BUFS * NT;
 
-template <int NT>
 struct FwCtl {
-  uint64_t full[10], empty[10], tfull[FW_BUFS], tempty[FW_BUFS], sfull[FW_CHUNKS],
+  uint64_t full[FW_STAGES], empty[FW_STAGES], tfull[FW_BUFS], tempty[FW_BUFS], sfull[FW_CHUNKS],
       sempty[FW_CHUNKS], pfull, pempty, drain;
   uint32_t tmem_base;
   int abort, bad;
@@ -49,12 +48,8 @@ struct FwCtl {
   float sb[FW_CHUNKS][FW_CHUNK];
 };
 
-template <int NT>
-constexpr size_t fw_smem() {
-  return FwGeo<NT>::STAGES * FwGeo<NT>::STAGE_BYTES + FwGeo<NT>::PART_BYTES + sizeof(FwCtl<NT>) +
-         1024;
-}
-static_assert(fw_smem<16>() <= 232448 && fw_smem<64>() <= 232448, "227 KB per CTA");
+constexpr size_t FW_SMEM = FW_STAGES * FW_STAGE_BYTES + FW_PART_BYTES + sizeof(FwCtl) + 1024;
+static_assert(FW_SMEM <= 232448, "227 KB per CTA");
 
 struct FwParams {
   int G, N, rows, kb, nb;
@@ -80,8 +75,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 
-// a store to, and an arrival (releasing this thread's stores to the cluster) in, another CTA's
-// shared memory
+// a store to, and an arrival (releasing to the cluster the stores ordered before it) in, another
+// CTA's shared memory
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -122,19 +117,17 @@ __device__ __forceinline__ void store1(void* out, long long at, float v) {
 }
 
 // tmW: the weights' codes [G N][K], box 128 x 128; tmT: the rows' codes, box 128 x NT.
-template <int NT, bool F32>
+template <bool F32>
 __global__ void __launch_bounds__(FW_THREADS, 1)
 fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
                const FwParams p) {
   griddep_wait();   // see common.cuh: dependent launches
-  using GE = FwGeo<NT>;
-  constexpr int STAGES = GE::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   // parts of this CTA's columns, by the rank that summed them: [split][NT / split][128]
-  float* part = reinterpret_cast<float*>(smem + STAGES * GE::STAGE_BYTES);
-  FwCtl<NT>* ctl = reinterpret_cast<FwCtl<NT>*>(smem + STAGES * GE::STAGE_BYTES + GE::PART_BYTES);
+  float* part = reinterpret_cast<float*>(smem + FW_STAGES * FW_STAGE_BYTES);
+  FwCtl* ctl = reinterpret_cast<FwCtl*>(smem + FW_STAGES * FW_STAGE_BYTES + FW_PART_BYTES);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem);
   volatile int* abort_flag = &ctl->abort;
@@ -143,7 +136,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
   const int unit = blockIdx.x / split, num_units = gridDim.x / split;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < FW_STAGES; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 1);
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
@@ -155,7 +148,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       mbar_init(smem_u32(&ctl->sfull[b]), 32);
       mbar_init(smem_u32(&ctl->sempty[b]), 4);
     }
-    mbar_init(smem_u32(&ctl->pfull), 128 * split);
+    mbar_init(smem_u32(&ctl->pfull), 4 * split);
     mbar_init(smem_u32(&ctl->pempty), 4 * split);
     mbar_init(smem_u32(&ctl->drain), 1);
     fence_mbar_init();
@@ -201,7 +194,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     }
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&ctl->tmem_base), GE::TMEM_COLS);
+    tmem_alloc(smem_u32(&ctl->tmem_base), FW_TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -240,23 +233,23 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           break;
         }
         if (fg_elect()) {
-          const uint32_t sw = smem_base + s * GE::STAGE_BYTES;
+          const uint32_t sw = smem_base + s * FW_STAGE_BYTES;
           const uint32_t full = smem_u32(&ctl->full[s]);
-          mbar_arrive_expect_tx(full, GE::STAGE_BYTES);
+          mbar_arrive_expect_tx(full, FW_STAGE_BYTES);
           tma_load_2d(sw, &tmW, full, (kb_lo + kb) * FG_BK, wrow);
-          tma_load_2d(sw + GE::W_BYTES, &tmT, full, (kb_lo + kb) * FG_BK, trow);
+          tma_load_2d(sw + FW_W_BYTES, &tmT, full, (kb_lo + kb) * FG_BK, trow);
         }
         __syncwarp();
-        if (++s == STAGES) {
+        if (++s == FW_STAGES) {
           s = 0;
           ph ^= 1u;
         }
       }
     }
     griddep_launch();
-    for (int i = 0; i < STAGES && ok; ++i) {   // every copy of this CTA has been consumed
+    for (int i = 0; i < FW_STAGES && ok; ++i) {   // every copy of this CTA has been consumed
       if (!fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err)) break;
-      if (++s == STAGES) {
+      if (++s == FW_STAGES) {
         s = 0;
         ph ^= 1u;
       }
@@ -269,7 +262,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
     bool ok = true;
     const uint32_t tmem = static_cast<uint32_t>(fg_uniform(static_cast<int>(tmem_base)));
     const uint64_t da0 = make_smem_desc(smem_base, 16, 1024);
-    const uint64_t db0 = make_smem_desc(smem_base + GE::W_BYTES, 16, 1024);
+    const uint64_t db0 = make_smem_desc(smem_base + FW_W_BYTES, 16, 1024);
     for (int tile = unit; tile < total && ok; tile += num_units) {
       for (int kb = 0; kb < nkb; ++kb, ++it) {
         const uint32_t buf = it % FW_BUFS;
@@ -280,8 +273,8 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         }
         tc_fence_after();
         if (fg_elect()) {
-          const uint64_t da = da0 + static_cast<uint32_t>(s * (GE::STAGE_BYTES >> 4));
-          const uint64_t db = db0 + static_cast<uint32_t>(s * (GE::STAGE_BYTES >> 4));
+          const uint64_t da = da0 + static_cast<uint32_t>(s * (FW_STAGE_BYTES >> 4));
+          const uint64_t db = db0 + static_cast<uint32_t>(s * (FW_STAGE_BYTES >> 4));
 #pragma unroll
           for (uint32_t kk = 0; kk < FG_BK / 32; ++kk)   // 32 bytes on, in 16-byte units
             fg_mma(tmem + buf * NT, da + 2 * kk, db + 2 * kk, fg_idesc(128, NT), kk != 0);
@@ -289,7 +282,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           tc_commit(smem_u32(&ctl->empty[s]));
         }
         __syncwarp();
-        if (++s == STAGES) {
+        if (++s == FW_STAGES) {
           s = 0;
           ph ^= 1u;
         }
@@ -361,8 +354,7 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           }
           tc_fence_after();
           uint32_t d[NT];
-          if constexpr (NT == 16) tmem_ld16(taddr + buf * NT, d);
-          else tmem_ld64(taddr + buf * NT, d);
+          tmem_ld16(taddr + buf * NT, d);
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
@@ -404,8 +396,9 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
                                static_cast<uint32_t>(owner)),
                    (t & 1) ? acc[t / 2].y : acc[t / 2].x);
       }
-      for (int r = 0; r < split; ++r)
-        arrive_cluster(mapa_shared(smem_u32(&ctl->pfull), static_cast<uint32_t>(r)));
+      __syncwarp();
+      if (lane < split)
+        arrive_cluster(mapa_shared(smem_u32(&ctl->pfull), static_cast<uint32_t>(lane)));
       if (!fw_wait_cluster(smem_u32(&ctl->pfull), round & 1u, abort_flag, p.err)) break;
       for (int i = 0; i < own; ++i) {
         float v = 0.0f;
@@ -415,34 +408,37 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
           store1<F32>(p.out, static_cast<long long>(row0 + t) * p.ldo + n, v);
       }
       __syncwarp();
-      if (lane == 0)
-        for (int r = 0; r < split; ++r)
-          arrive_cluster(mapa_shared(smem_u32(&ctl->pempty), static_cast<uint32_t>(r)));
+      if (lane < split)
+        arrive_cluster(mapa_shared(smem_u32(&ctl->pempty), static_cast<uint32_t>(lane)));
     }
   }
   tc_fence_before();
   if (split > 1) cluster_sync_all();   // nobody leaves while the others may write to it
   else __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, GE::TMEM_COLS);
+  if (warp == 1) tmem_dealloc(tmem_base, FW_TMEM_COLS);
 }
 
-template <int NT, bool F32>
-cudaError_t fw_launch(const CUtensorMap& tw, const CUtensorMap& tt, const FwParams& p, int sms,
+template <bool F32>
+cudaError_t fw_launch(const CUtensorMap& tw, const CUtensorMap& tt, const FwParams& p, int units,
                       cudaStream_t st) {
-  auto kern = fp8_few_kernel<NT, F32>;
+  auto kern = fp8_few_kernel<F32>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(fw_smem<NT>()));
+                                             static_cast<int>(FW_SMEM));
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(sms / p.split * p.split)), dim3(FW_THREADS),
-                    fw_smem<NT>(), st, static_cast<unsigned>(p.split), tw, tt, p);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(units * p.split)), dim3(FW_THREADS), FW_SMEM,
+                    st, static_cast<unsigned>(p.split), tw, tt, p);
 }
 
 }  // namespace
 
-// Few rows, in all or to a segment on average: products bound by the weights' bytes.
+// Up to 16 rows in all, or 8 to the average segment, which leaves uneven segments room in their
+// 16-row tile.  One row to each of eight experts of 4096 x 7168 takes 47 us here and 57 us in
+// fp8_gemm's kernel; 8 or 16 rows to each of 128 experts of 1536 x 2048 85 and 87 us here, 91 and
+// 94 us there; with 24 rows, two tiles to each, 99 us here and 97 us there, with 64 rows 181 and
+// 95 us.  (A 64-row tile was never the best.)
 bool fp8_few_rows(const Fp8GemmArgs& a) {
-  return !a.wgrad && (a.rows <= 64 || a.rows <= 32 * static_cast<int64_t>(a.G));
+  return !a.wgrad && (a.rows <= 16 || a.rows <= 8 * static_cast<int64_t>(a.G));
 }
 
 cudaError_t launch_fp8_few(const Fp8GemmArgs& a, cudaStream_t st) {
@@ -459,27 +455,27 @@ cudaError_t launch_fp8_few(const Fp8GemmArgs& a, cudaStream_t st) {
   p.out = a.out;
   p.ldo = a.ldo;
   p.err = a.err;
-  // up to 16 rows in all, or 8 to a segment on average: 16-token tiles
-  const bool small = a.rows <= 16 || a.rows <= 8 * static_cast<int64_t>(a.G);
   int dev = 0, sms = 148;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // clusters where the tiles (one token tile to every segment that can have rows) are fewer than
-  // the SMs, of at least four blocks to a CTA
+  // Clusters while all the tiles (one token tile to every segment that can have rows) still run at
+  // once and 12 blocks are left to a CTA: one row by 4096 x 7168 takes 25.2 us alone, 21.1 by 2,
+  // 19.1 by 4 and, in two rounds, 29.3 us by 8; with 8 blocks, 4096 x 1024, 13 us alone, 15 by 2.
   const int64_t tiles = (a.rows < a.G ? a.rows : a.G) * p.w_tiles;
   p.split = 1;
-  while (p.split < 8 && tiles * p.split < sms && p.kb >= 8 * p.split) p.split *= 2;
+  while (p.split < 8 && tiles * 2 * p.split <= sms && p.kb >= 24 * p.split) p.split *= 2;
+  // no more units than there can be tiles: a segment has at most one that is not full
+  const int64_t most = (a.rows < a.G ? a.rows : a.G) + a.rows / NT;
+  const int64_t units = most * p.w_tiles;
+  const int fit = sms / p.split;
   CUtensorMap tw, tt;
   if (!fp8_codes_map(&tw, a.b, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.ldb),
                      static_cast<uint64_t>(a.G) * static_cast<uint64_t>(a.N), 128) ||
       !fp8_codes_map(&tt, a.a, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.lda),
-                     static_cast<uint64_t>(a.rows), small ? 16 : 64))
+                     static_cast<uint64_t>(a.rows), NT))
     return cudaErrorInvalidValue;
-  if (small)
-    return a.out_fp32 ? fw_launch<16, true>(tw, tt, p, sms, st)
-                      : fw_launch<16, false>(tw, tt, p, sms, st);
-  return a.out_fp32 ? fw_launch<64, true>(tw, tt, p, sms, st)
-                    : fw_launch<64, false>(tw, tt, p, sms, st);
+  const int n = units < fit ? static_cast<int>(units) : fit;
+  return a.out_fp32 ? fw_launch<true>(tw, tt, p, n, st) : fw_launch<false>(tw, tt, p, n, st);
 }
 
 }  // namespace moe

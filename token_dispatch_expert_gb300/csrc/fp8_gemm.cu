@@ -647,12 +647,11 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
   p.out = a.out;
   p.ldo = a.ldo;
   p.err = a.err;
-  // pairs: weight gradients of more than 128 rows; products whose average segment fills more
-  // than three quarters of a pair's 256 rows
   // pairs: weight gradients of more than 128 rows (201 us against 212 for one CTA at 2048 x 768 of
   // 128 experts), products with 768 rows or more to the average segment.  Below, a pair's
-  // padding of the last tile outweighs its cheaper operands (231 us against 249 at 512 rows of
-  // 1536 x 2048, but 204 against 185 at 1024 rows of 28672 x 4096)
+  // padding of the last tile outweighs its cheaper operands where segments are uneven (249 us
+  // against 231 for one CTA at 512 rows on average of 1536 x 2048, but 185 against 204 at 1024
+  // rows of 28672 x 4096)
   const bool pair = a.wgrad ? a.K > 128 : a.rows >= 768 * static_cast<int64_t>(a.G);
   const uint32_t b_rows = pair ? 64 : 256;   // a box of b
   CUtensorMap ta, tb, tc;
