@@ -10,10 +10,21 @@
 // whatever kernel writes them: the rounding to 4 significant bits is the only one that
 // matters.  A NaN in a block makes the whole block NaN, an infinity makes the others 0.
 //
-// All kernels are bound by memory: a bf16 value is read once (2 bytes) and one byte or, with
-// both orientations, two bytes are written.
+// By their bytes these kernels belong to memory: a bf16 value is read once (2 bytes) and one byte
+// or, with both orientations, two bytes are written.  What they reach, and what holds them up, at
+// 6.7 TB/s for a copy:
+//   rows in order, 21,240 x 6656           6.2 TB/s, 69 us: memory
+//   rows 32,768 x 7168 gathered from 4096  3.8 TB/s, 78 us; moving the same bytes without any
+//                                          arithmetic takes 66 us: every row passes L2 eight times
+//   both ways, 16,382 x 2056               3.8 TB/s, 36 us: barriers between the two orientations
+//   SwiGLU, rows 65,536 x 768              4.0 TB/s, 63 us: the instructions issued, at 50 of
+//                                          which an exactly rounded h and its code come
+//   its backward, both ways, 16,383 x 1408 2.4 TB/s, 107 us: instructions, about 100 a column for
+//                                          three values and five codes
 #include <cuda.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -290,7 +301,8 @@ __device__ __forceinline__ Swiglu2 swiglu_bwd2(uint32_t a, uint32_t b, uint32_t 
 
 // ------------------------------------------------------------------ sources
 // What a quantiser reads: eight consecutive values of a row, as packed bf16; columns at or past
-// `cols` are 0.  VEC: every row starts on 16 bytes and a chunk never crosses an end.
+// `cols` are 0.  W: what is loaded at once, 8 values (every row starts on 16 bytes and a chunk
+// never crosses an end), 2 (on 4 bytes, an even width) or 1.
 enum { SRC_ROWS, SRC_SWIGLU, SRC_SWIGLU_BWD };
 
 struct Source {
@@ -301,51 +313,77 @@ struct Source {
   int cols;                  // columns quantised: C, f, or 2f
 };
 
-template <bool VEC>
+__device__ __forceinline__ uint32_t load1(const __nv_bfloat16* p) {
+  return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p)));
+}
+__device__ __forceinline__ uint32_t load2(const __nv_bfloat16* p) {
+  return __ldg(reinterpret_cast<const uint32_t*>(p));
+}
+template <int W>
 __device__ __forceinline__ uint4 load8(const __nv_bfloat16* p, int n) {
-  if constexpr (VEC) {
+  if constexpr (W == 8) {
     return __ldg(reinterpret_cast<const uint4*>(p));
   } else {
-    const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < n ? __ldg(u + 2 * i) : 0u;
-      const uint32_t hi = 2 * i + 1 < n ? __ldg(u + 2 * i + 1) : 0u;
-      w[i] = lo | (hi << 16);
+      if constexpr (W == 2) {
+        w[i] = 2 * i < n ? load2(p + 2 * i) : 0u;
+      } else {
+        const uint32_t lo = 2 * i < n ? load1(p + 2 * i) : 0u;
+        const uint32_t hi = 2 * i + 1 < n ? load1(p + 2 * i + 1) : 0u;
+        w[i] = lo | (hi << 16);
+      }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-template <int SRC, bool VEC>
+template <int SRC, int W>
 __device__ __forceinline__ uint4 value8(const Source& s, long long row, int c) {
   const int n = s.cols - c;
   if (n <= 0) return make_uint4(0u, 0u, 0u, 0u);
   if constexpr (SRC == SRC_ROWS) {
-    return load8<VEC>(s.x + row * s.ld + c, n);
+    return load8<W>(s.x + row * s.ld + c, n);
   } else {
     const __nv_bfloat16* ab = s.x + row * 2 * s.f;
     if constexpr (SRC == SRC_SWIGLU)
-      return silu_mul8(load8<VEC>(ab + c, n), load8<VEC>(ab + s.f + c, n));
-    // one column at a time, wherever the halves meet; full blocks of 128 columns have kernels of
-    // their own
+      return silu_mul8(load8<W>(ab + c, n), load8<W>(ab + s.f + c, n));
+    // da or db, wherever the halves meet: the other is computed too and dropped.  Widths of whole
+    // blocks have code of their own
     const __nv_bfloat16* dh = s.dh + row * s.f;
-    auto bits = [](const __nv_bfloat16* p) {
-      return static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p)));
-    };
     uint32_t w[4];
+    if constexpr (W == 8) {
+      const bool first = c < s.f;
+      const int k = first ? c : c - s.f;
+      const uint4 a = load8<8>(ab + k, 8), b = load8<8>(ab + s.f + k, 8), d = load8<8>(dh + k, 8);
+      const uint32_t *pa = &a.x, *pb = &b.x, *pd = &d.x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int cc = c + i;
-      uint32_t r = 0u;
-      if (cc < s.cols) {
-        const int k = cc < s.f ? cc : cc - s.f;
-        const Swiglu2 x = swiglu_bwd2(bits(ab + k), bits(ab + s.f + k), bits(dh + k));
-        r = (cc < s.f ? x.da : x.db) & 0xffffu;
+      for (int i = 0; i < 4; ++i) {
+        const Swiglu2 x = swiglu_bwd2(pa[i], pb[i], pd[i]);
+        w[i] = first ? x.da : x.db;
       }
-      if (i & 1) w[i / 2] |= r << 16;
-      else w[i / 2] = r;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c0 = c + 2 * i, c1 = c0 + 1;
+        w[i] = 0u;
+        if (c0 >= s.cols) continue;
+        const int k0 = c0 < s.f ? c0 : c0 - s.f;
+        uint32_t a, b, d;
+        if constexpr (W == 2) {   // an even f: a pair lies in one half
+          a = load2(ab + k0);
+          b = load2(ab + s.f + k0);
+          d = load2(dh + k0);
+        } else {                  // (cols = 2 f is even, so c1 is there too)
+          const int k1 = c1 < s.f ? c1 : c1 - s.f;
+          a = load1(ab + k0) | (load1(ab + k1) << 16);
+          b = load1(ab + s.f + k0) | (load1(ab + s.f + k1) << 16);
+          d = load1(dh + k0) | (load1(dh + k1) << 16);
+        }
+        const Swiglu2 x = swiglu_bwd2(a, b, d);
+        w[i] = ((c0 < s.f ? x.da : x.db) & 0xffffu) | ((c1 < s.f ? x.da : x.db) & 0xffff0000u);
+      }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -416,8 +454,9 @@ __device__ __forceinline__ int scale_of_lane(int lane) {
 
 // ------------------------------------------------------------------ along the rows
 // One warp per row; a lane takes eight values (16 bytes), half a warp a block, four chunks'
-// loads before any is used.
-template <int SRC, bool VEC>
+// loads before any is used.  W = 128: the backward of a width of whole blocks, where a chunk's
+// values of da and db come from one computation.
+template <int SRC, int W>
 __global__ void __launch_bounds__(FQ_THREADS, 4)
 fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
                 const int32_t* __restrict__ offsets, int G, long long rows, const QuantOut out,
@@ -440,7 +479,7 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
         continue;
       }
     }
-    constexpr bool BOTH = SRC == SRC_SWIGLU_BWD && VEC;   // two chunks of da, two of db
+    constexpr bool BOTH = SRC == SRC_SWIGLU_BWD && W == 128;   // two chunks of da, two of db
     const int span = BOTH ? src.f : src.cols;
     for (int c0 = 0; c0 < span; c0 += BOTH ? 512 : 1024) {
       uint4 v[4];
@@ -454,9 +493,9 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
           col[2 + i] = src.f + c;
           a[i] = b[i] = d[i] = make_uint4(0u, 0u, 0u, 0u);
           if (c < src.f) {
-            a[i] = load8<true>(src.x + t * 2 * src.f + c, 8);
-            b[i] = load8<true>(src.x + t * 2 * src.f + src.f + c, 8);
-            d[i] = load8<true>(src.dh + t * src.f + c, 8);
+            a[i] = load8<8>(src.x + t * 2 * src.f + c, 8);
+            b[i] = load8<8>(src.x + t * 2 * src.f + src.f + c, 8);
+            d[i] = load8<8>(src.dh + t * src.f + c, 8);
           } else {
             col[i] = col[2 + i] = 1 << 28;   // past every column
           }
@@ -474,15 +513,15 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
           v[i] = make_uint4(x[0], x[1], x[2], x[3]);
           v[2 + i] = make_uint4(y[0], y[1], y[2], y[3]);
         }
-      } else if constexpr (SRC == SRC_SWIGLU && VEC) {
+      } else if constexpr (SRC == SRC_SWIGLU && W == 8) {
         uint4 a[4], b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           col[i] = c0 + 256 * i + 8 * lane;
           a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
           if (col[i] < src.cols) {
-            a[i] = load8<true>(src.x + t * 2 * src.f + col[i], 8);
-            b[i] = load8<true>(src.x + t * 2 * src.f + src.f + col[i], 8);
+            a[i] = load8<8>(src.x + t * 2 * src.f + col[i], 8);
+            b[i] = load8<8>(src.x + t * 2 * src.f + src.f + col[i], 8);
           }
         }
 #pragma unroll
@@ -492,7 +531,7 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           col[i] = c0 + 256 * i + 8 * lane;
-          v[i] = value8<SRC, VEC>(src, t, col[i]);
+          v[i] = value8<SRC, W>(src, t, col[i]);
         }
       }
       float r[4], quot;
@@ -588,15 +627,17 @@ struct Columns {
     }
     s_max[q][cp] = m;
   }
-  __device__ __forceinline__ void write(int th, uint32_t (*s_max)[64], int c0, int cols, int kb,
-                                        const QuantOut& o, uint8_t* box) {
+  // columns from c0 of a part of `width` columns that begins at `first` of all `cols`
+  __device__ __forceinline__ void write(int th, uint32_t (*s_max)[64], int c0, int first,
+                                        int width, int cols, int kb, const QuantOut& o,
+                                        uint8_t* box) {
     const int cp = th & 63, q = th >> 6;
 #pragma unroll
     for (int i = 0; i < Q; ++i) m = max2(m, s_max[i][cp]);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int c = c0 + 2 * cp + j;
-      if (c >= cols) continue;
+      if (c0 + 2 * cp + j >= width) continue;
+      const int c = first + c0 + 2 * cp + j;
       const uint32_t amax = j ? m >> 16 : m & 0xffffu;
       const float r = block_quotient(amax, o.pow2, 0);
       uint32_t code[32 / Q];
@@ -642,10 +683,10 @@ __device__ __forceinline__ void tile_rows(const uint4* v, const TileAt& t, int c
   }
 }
 
-// Rows read by the element: any width and alignment.
+// Rows read by one or two elements: any width and alignment.
 constexpr int FT_THREADS = 512;
 
-template <int SRC>
+template <int SRC, int W>
 __global__ void __launch_bounds__(FT_THREADS, 2)
 fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
                       const int32_t* __restrict__ offsets, int G, long long rows,
@@ -674,7 +715,7 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
             row = 0;
           }
         }
-        v[u] = value8<SRC, false>(src, row, c);
+        v[u] = value8<SRC, W>(src, row, c);
       }
     }
     __syncthreads();   // the previous tile is consumed
@@ -686,51 +727,54 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
     Columns<8> cols;
     cols.read(tile, tid, s_max);
     __syncthreads();
-    cols.write(tid, s_max, t.c0, src.cols, t.kb, out, nullptr);
+    cols.write(tid, s_max, t.c0, 0, src.cols, src.cols, t.kb, out, nullptr);
   }
   griddep_launch();
 }
 
-// Rows on 16 bytes: the next tile's raw pieces are on their way (cp.async) while this one's columns
-// are worked on.  A piece is fetched, read and (SwiGLU) overwritten with its result by one thread,
-// and a tile's column codes overwrite the tile once it is in registers, so two sets of raw
-// tiles are all the shared memory: x; a, b -> h, -; a, b, dh -> da, db, h.
+// Rows on 16 bytes.  A piece of a tile is fetched (cp.async), read and turned into its result by
+// one thread.  Rows: the next tile is on its way into the other of two buffers while this one's
+// columns are worked on.  SwiGLU: a and b, read by their own threads alone, make room for the next
+// tile's as soon as h stands in a buffer of its own.  Backward: da, db and h overwrite a, b and
+// dh.  A tile's column codes overwrite the tile once it is in registers.  So one CTA takes 64,
+// 96 or 96 KB, and three or two CTAs to an SM work while another waits (the backward in one CTA of
+// 1024 threads with the next tile under way took 118 us at 16383 x 1408).
 template <int SRC>
 struct TileGeo {
-  static constexpr int RAW = SRC == SRC_ROWS ? 1 : SRC == SRC_SWIGLU ? 2 : 3;
-  static constexpr int THREADS = SRC == SRC_SWIGLU_BWD ? 1024 : 512;
-  static constexpr int PER = FT_TILE / THREADS;         // pieces of a tile per thread
-  static constexpr int CTAS = SRC == SRC_ROWS ? 3 : 1;  // per SM
-  static constexpr int SMEM = 2 * RAW * FT_TILE * 16 + 1024;
+  static constexpr int PER = FT_TILE / FT_THREADS;      // pieces of a tile per thread
+  static constexpr int CTAS = SRC == SRC_ROWS ? 3 : 2;  // per SM
+  static constexpr int BUFS = SRC == SRC_ROWS ? 2 : 3;
+  static constexpr int SMEM = BUFS * FT_TILE * 16 + 1024;
 };
 
+// tm, tm_b, tm_h: codes_t of rows, h or da; of db; of the backward's h.
 template <int SRC>
-__global__ void __launch_bounds__(TileGeo<SRC>::THREADS, TileGeo<SRC>::CTAS)
-fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_h,
-                  const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
+__global__ void __launch_bounds__(FT_THREADS, TileGeo<SRC>::CTAS)
+fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_b,
+                  const __grid_constant__ CUtensorMap tm_h, const Source src,
+                  const int32_t* __restrict__ src_tok, long long src_rows,
                   const int32_t* __restrict__ offsets, int G, long long rows, const QuantOut out,
                   const QuantOut out_h, int* err) {
   griddep_wait();   // see common.cuh: dependent launches
   using GE = TileGeo<SRC>;
   constexpr int PER = GE::PER;
   constexpr bool BWD = SRC == SRC_SWIGLU_BWD;
-  extern __shared__ uint4 dyn[];   // [2][RAW][128][16] after the next 1 KB boundary
-  uint4* raw = reinterpret_cast<uint4*>(
+  extern __shared__ uint4 dyn[];   // [BUFS][128][16] after the next 1 KB boundary
+  uint4* bufs = reinterpret_cast<uint4*>(
       (reinterpret_cast<uintptr_t>(dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ uint32_t s_max[BWD ? 32 : 8][64];
+  __shared__ uint32_t s_max[BWD ? 24 : 8][64];
   __shared__ Blocks blocks;
   if (!count_blocks(blocks, offsets, G, rows, err)) return;
   const int tid = threadIdx.x;
   const int width = BWD ? src.f : src.cols;
   const int gx = (width + 127) / 128;
   const long long total = static_cast<long long>(blocks.first[G]) * gx;
-  const int r = tid >> 4, ch = tid & 15;   // pieces (r + THREADS / 16 u, ch)
-  constexpr int STEP = GE::THREADS / 16;
+  const int r = tid >> 4, ch = tid & 15;   // pieces (r + 32 u, ch)
   auto fetch = [&](const TileAt& t, uint4* dst) {
     const int c = t.c0 + 8 * ch;
 #pragma unroll
     for (int u = 0; u < PER; ++u) {
-      const int rr = r + STEP * u, at = rr * 16 + ch;
+      const int rr = r + 32 * u, at = rr * 16 + ch;
       const bool in = rr < t.nr && c < width;
       long long row = in ? t.r0 + rr : 0;
       if (SRC == SRC_ROWS && src_tok && in) {
@@ -755,71 +799,86 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
   TileAt next;
   if (blockIdx.x < total) {
     next = tile_at(blocks, offsets, G, rows, blockIdx.x, gx);
-    fetch(next, raw);
+    fetch(next, bufs);
   }
   int buf = 0;
   for (long long item = blockIdx.x; item < total; item += gridDim.x, buf ^= 1) {
     const TileAt t = next;
-    uint4* tile = raw + buf * GE::RAW * FT_TILE;
+    const bool more = item + gridDim.x < total;
+    uint4* raw = bufs + (SRC == SRC_ROWS ? buf * FT_TILE : 0);
+    uint4* tile = SRC == SRC_SWIGLU ? bufs + 2 * FT_TILE : raw;
     asm volatile("cp.async.wait_all;" ::: "memory");   // this thread's pieces of this tile
     const int c = t.c0 + 8 * ch;
     uint4 v[4];
+    if constexpr (BWD) {
+#pragma unroll 1
+      for (int u = 0; u < PER; u += 2) {   // two rows at a time
 #pragma unroll
-    for (int u = 0; u < PER; ++u) {
-      uint4* at = tile + (r + STEP * u) * 16 + ch;
-      if constexpr (SRC == SRC_ROWS) {
-        v[u] = at[0];
-      } else if constexpr (SRC == SRC_SWIGLU) {
-        v[u] = r + STEP * u < t.nr ? silu_mul8(at[0], at[FT_TILE]) : make_uint4(0u, 0u, 0u, 0u);
-        at[0] = v[u];
-      } else {
-        const uint4 a = at[0], b = at[FT_TILE], d = at[2 * FT_TILE];
-        uint32_t x[4] = {0u, 0u, 0u, 0u}, y[4] = {0u, 0u, 0u, 0u}, z[4] = {0u, 0u, 0u, 0u};
-        if (r + STEP * u < t.nr) {
-          const uint32_t *pa = &a.x, *pb = &b.x, *pd = &d.x;
+        for (int i = 0; i < 2; ++i) {
+          const int rr = r + 32 * (u + i);
+          uint4* at = raw + rr * 16 + ch;
+          const uint4 a = at[0], b = at[FT_TILE], d = at[2 * FT_TILE];
+          uint32_t x[4] = {0u, 0u, 0u, 0u}, y[4] = {0u, 0u, 0u, 0u}, z[4] = {0u, 0u, 0u, 0u};
+          if (rr < t.nr && c < width) {
+            const uint32_t *pa = &a.x, *pb = &b.x, *pd = &d.x;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const Swiglu2 w = swiglu_bwd2(pa[k], pb[k], pd[k]);
-            x[k] = w.da;
-            y[k] = w.db;
-            z[k] = w.h;
+            for (int k = 0; k < 4; ++k) {
+              const Swiglu2 w = swiglu_bwd2(pa[k], pb[k], pd[k]);
+              x[k] = w.da;
+              y[k] = w.db;
+              z[k] = w.h;
+            }
           }
+          v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+          v[2 + i] = make_uint4(y[0], y[1], y[2], y[3]);
+          at[0] = v[i];
+          at[FT_TILE] = v[2 + i];
+          at[2 * FT_TILE] = make_uint4(z[0], z[1], z[2], z[3]);
         }
-        v[u] = make_uint4(x[0], x[1], x[2], x[3]);
-        v[2 + u] = make_uint4(y[0], y[1], y[2], y[3]);
-        at[0] = v[u];
-        at[FT_TILE] = v[2 + u];
-        at[2 * FT_TILE] = make_uint4(z[0], z[1], z[2], z[3]);
+        if (out.codes)
+          tile_rows(v, t, src.cols, out, [&](int i) {
+            return make_int2(r + 32 * (u + (i & 1)), c + (i >> 1) * src.f);
+          });
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < PER; ++u) {
+        const uint4* at = raw + (r + 32 * u) * 16 + ch;
+        v[u] = SRC == SRC_ROWS ? at[0]
+               : r + 32 * u < t.nr && c < width ? silu_mul8(at[0], at[FT_TILE]) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (out.codes)
+        tile_rows(v, t, src.cols, out, [&](int i) { return make_int2(r + 32 * i, c); });
+      if (tid == 0) bulk_wait_group_read<0>();   // the last tile's codes have left their buffer
     }
-    if (out.codes)
-      tile_rows(v, t, src.cols, out, [&](int i) {
-        return BWD ? make_int2(r + STEP * (i & 1), c + (i >> 1) * src.f)
-                   : make_int2(r + STEP * i, c);
-      });
-    if (tid == 0) bulk_wait_group_read<0>();   // the last tile's codes have left the other set
     __syncthreads();
-    if (item + gridDim.x < total) {
+    if constexpr (SRC == SRC_SWIGLU) {
+#pragma unroll
+      for (int u = 0; u < PER; ++u) tile[(r + 32 * u) * 16 + ch] = v[u];
+      __syncthreads();
+    }
+    if (!BWD && more) {
       next = tile_at(blocks, offsets, G, rows, item + gridDim.x, gx);
-      fetch(next, raw + (buf ^ 1) * GE::RAW * FT_TILE);
+      fetch(next, SRC == SRC_ROWS ? bufs + (buf ^ 1) * FT_TILE : raw);
     }
     uint8_t* box = reinterpret_cast<uint8_t*>(tile);
     constexpr int BOX = FT_TILE * 16;   // from one tile's to the next one's
+    Columns<8> cols;
+    cols.read(tile, tid, s_max);
     if constexpr (BWD) {
-      // 512 threads each for da and db, then all of them for h
-      const int part = tid >> 9, th = tid & 511;
-      Columns<8> cols;
-      Columns<16> cols_h;
-      cols.read(tile + part * FT_TILE, th, s_max + 8 * part);
-      cols_h.read(tile + 2 * FT_TILE, tid, s_max + 16);
+      Columns<8> cols_b;
+      cols_b.read(tile + FT_TILE, tid, s_max + 8);
       __syncthreads();
-      cols.write(th, s_max + 8 * part, part * src.f + t.c0, src.cols, t.kb, out, box + part * BOX);
-      if (out_h.codes_t) cols_h.write(tid, s_max + 16, t.c0, src.f, t.kb, out_h, box + 2 * BOX);
+      cols.write(tid, s_max, t.c0, 0, src.f, src.cols, t.kb, out, box);
+      cols_b.write(tid, s_max + 8, t.c0, src.f, src.f, src.cols, t.kb, out, box + BOX);
+      if (out_h.codes_t) {
+        cols.read(tile + 2 * FT_TILE, tid, s_max + 16);
+        __syncthreads();
+        cols.write(tid, s_max + 16, t.c0, 0, src.f, src.f, t.kb, out_h, box + 2 * BOX);
+      }
     } else {
-      Columns<8> cols;
-      cols.read(tile, tid, s_max);
       __syncthreads();
-      cols.write(tid, s_max, t.c0, src.cols, t.kb, out, box);
+      cols.write(tid, s_max, t.c0, 0, src.cols, src.cols, t.kb, out, box);
     }
     fence_proxy_async_smem();
     __syncthreads();
@@ -827,10 +886,16 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
       const uint32_t at = smem_u32(box);
       tma_store_2d(&tm, at, 128 * t.kb, t.c0);
       if (BWD) {
-        tma_store_2d(&tm, at + BOX, 128 * t.kb, src.f + t.c0);
+        tma_store_2d(&tm_b, at + BOX, 128 * t.kb, t.c0);
         if (out_h.codes_t) tma_store_2d(&tm_h, at + 2 * BOX, 128 * t.kb, t.c0);
       }
       bulk_commit_group();
+      if (BWD) bulk_wait_group_read<0>();
+    }
+    if (BWD && more) {
+      next = tile_at(blocks, offsets, G, rows, item + gridDim.x, gx);
+      __syncthreads();   // the codes have left the buffers
+      fetch(next, raw);
     }
   }
   if (tid == 0) bulk_wait_group_all();   // stores done before exit
@@ -840,9 +905,9 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
 // ------------------------------------------------------------------ weights
 // One CTA per 128 x 128 block of W [G][N][K]: one scale, the codes row-major and, for the data
 // gradient's product, transposed (its block scales transposed with them).
-template <bool VEC>
+template <int W>
 __global__ void __launch_bounds__(FQ_THREADS)
-fp8_weights_kernel(const __nv_bfloat16* __restrict__ W, int N, int K, int nb, int kb,
+fp8_weights_kernel(const __nv_bfloat16* __restrict__ w, int N, int K, int nb, int kb,
                    uint8_t* __restrict__ codes, long long ld, float* __restrict__ scales,
                    uint8_t* __restrict__ codes_t, long long ld_t, float* __restrict__ scales_t,
                    int pow2) {
@@ -862,7 +927,7 @@ fp8_weights_kernel(const __nv_bfloat16* __restrict__ W, int N, int K, int nb, in
   for (int u = 0; u < 8; ++u) {
     const int n = n0 + (tid >> 4) + 16 * u;
     v[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (n < N && c < K) v[u] = load8<VEC>(W + (g * N + n) * K + c, K - c);
+    if (n < N && c < K) v[u] = load8<W>(w + (g * N + n) * K + c, K - c);
     m = max2(m, max_mag8(v[u]));
   }
   m = max(m & 0xffffu, m >> 16);
@@ -923,44 +988,81 @@ int fq_sms() {
   return sms;
 }
 
-bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool on(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-template <int SRC, bool VEC>
-cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut& o,
-                         const QuantOut& oh, cudaStream_t st) {
-  if (!o.codes_t) {
-    const long long want = (a.rows + FQ_THREADS / 32 - 1) / (FQ_THREADS / 32);
-    const long long most = static_cast<long long>(fq_sms()) * 8;
-    return launch_pdl(fp8_rows_kernel<SRC, VEC>,
-                      dim3(static_cast<unsigned>(want < most ? want : most)), dim3(FQ_THREADS), 0,
-                      st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, a.err);
-  }
-  const int width = VEC && SRC == SRC_SWIGLU_BWD ? s.f : s.cols;
+template <int SRC, int W>
+cudaError_t launch_rows(const Source& s, const Fp8QuantArgs& a, const QuantOut& o,
+                        cudaStream_t st) {
+  const long long want = (a.rows + FQ_THREADS / 32 - 1) / (FQ_THREADS / 32);
+  const long long most = static_cast<long long>(fq_sms()) * 8;
+  return launch_pdl(fp8_rows_kernel<SRC, W>, dim3(static_cast<unsigned>(want < most ? want : most)),
+                    dim3(FQ_THREADS), 0, st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o,
+                    a.err);
+}
+
+template <int SRC, int W>
+cudaError_t launch_tokens(const Source& s, const Fp8QuantArgs& a, const QuantOut& o,
+                          const QuantOut& oh, cudaStream_t st) {
+  constexpr bool BWD = SRC == SRC_SWIGLU_BWD;
+  const int width = BWD && W == 8 ? s.f : s.cols;
   const long long items = fp8_token_blocks(a.rows, a.G) * ((width + 127) / 128);
   auto grid = [&](int per_sm) {
     const long long most = static_cast<long long>(fq_sms()) * per_sm;
     return dim3(static_cast<unsigned>(items < most ? items : most));
   };
-  if constexpr (VEC) {
+  if constexpr (W == 8) {
     using GE = TileGeo<SRC>;
     auto kern = fp8_tokens_kernel<SRC>;
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GE::SMEM);
     if (e != cudaSuccess) return e;
-    CUtensorMap tm, tm_h;
+    CUtensorMap tm, tm_b, tm_h;
     const uint64_t len = 128ull * static_cast<uint64_t>(o.kb_cap);
-    if (!fp8_codes_map(&tm, o.codes_t, len, len, static_cast<uint64_t>(s.cols), 128))
+    auto map = [&](CUtensorMap* m, uint8_t* codes) {   // `width` rows: what a last box has past them stays unwritten
+      return fp8_codes_map(m, codes, len, len, static_cast<uint64_t>(width), 128);
+    };
+    if (!map(&tm, o.codes_t)) return cudaErrorInvalidValue;
+    tm_b = tm_h = tm;
+    if (BWD && (!map(&tm_b, o.codes_t + static_cast<uint64_t>(s.f) * len) ||
+                (oh.codes_t && !map(&tm_h, oh.codes_t))))
       return cudaErrorInvalidValue;
-    tm_h = tm;
-    if (SRC == SRC_SWIGLU_BWD && oh.codes_t &&
-        !fp8_codes_map(&tm_h, oh.codes_t, len, len, static_cast<uint64_t>(s.f), 128))
-      return cudaErrorInvalidValue;
-    return launch_pdl(kern, grid(GE::CTAS), dim3(GE::THREADS), GE::SMEM, st, 1, tm, tm_h, s,
+    return launch_pdl(kern, grid(GE::CTAS), dim3(FT_THREADS), GE::SMEM, st, 1, tm, tm_b, tm_h, s,
                       a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, oh, a.err);
   } else {
-    return launch_pdl(fp8_tokens_any_kernel<SRC>, grid(2), dim3(FT_THREADS), 0, st, 1, s, a.src_tok,
-                      a.src_rows, a.offsets, a.G, a.rows, o, a.err);
+    return launch_pdl(fp8_tokens_any_kernel<SRC, W>, grid(2), dim3(FT_THREADS), 0, st, 1, s,
+                      a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, a.err);
   }
+}
+
+// One kernel where all that is asked for can come from it.
+template <int SRC, int W>
+cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut& o,
+                         const QuantOut& oh, cudaStream_t st) {
+  return o.codes_t ? launch_tokens<SRC, W>(s, a, o, oh, st) : launch_rows<SRC, W>(s, a, o, st);
+}
+
+// The backward reads a, b and dh once for da, db and h.  Where the blocks of da and db share one (f
+// no multiple of 128) the tiles of 128 columns do not hold whole blocks of a row: the row codes
+// come from a launch of their own (131 of 224 us at 16383 x 1376, where the backward by single
+// columns took 439).
+cudaError_t launch_bwd8(const Source& s, const Fp8QuantArgs& a, QuantOut o, const QuantOut& oh,
+                        cudaStream_t st) {
+  const bool whole = s.f % 128 == 0;
+  if (o.codes_t) {
+    QuantOut ot = o;
+    if (!whole) ot.codes = nullptr;
+    const cudaError_t e = launch_tokens<SRC_SWIGLU_BWD, 8>(s, a, ot, oh, st);
+    if (e != cudaSuccess || whole) return e;
+  }
+  return whole ? launch_rows<SRC_SWIGLU_BWD, 128>(s, a, o, st)
+               : launch_rows<SRC_SWIGLU_BWD, 8>(s, a, o, st);
+}
+
+// Calls go(integral constant) with what can be loaded at once: 8, 2 or 1 values.
+template <typename Go>
+cudaError_t by_width(bool eight, bool two, Go go) {
+  if (eight) return go(std::integral_constant<int, 8>());
+  return two ? go(std::integral_constant<int, 2>()) : go(std::integral_constant<int, 1>());
 }
 
 }  // namespace
@@ -985,22 +1087,24 @@ cudaError_t launch_fp8_quant(const Fp8QuantArgs& a, cudaStream_t st) {
   oh.codes = nullptr;
   oh.codes_t = static_cast<uint8_t*>(a.h_codes_t);
   oh.scales_t = a.h_scales_t;
-  if (a.src == FP8_SRC_ROWS) {
-    const bool vec = on16(a.x) && a.ldx % 8 == 0 && a.C % 8 == 0;
-    return vec ? launch_quant<SRC_ROWS, true>(s, a, o, oh, st)
-               : launch_quant<SRC_ROWS, false>(s, a, o, oh, st);
-  }
-  if (a.src == FP8_SRC_SWIGLU)
-    return a.f % 8 == 0 ? launch_quant<SRC_SWIGLU, true>(s, a, o, oh, st)
-                        : launch_quant<SRC_SWIGLU, false>(s, a, o, oh, st);
-  // the backward reads a, b and dh once for da, db and h where the blocks of da and db do not
-  // share one (f a multiple of 128); other widths are computed by the column, and h apart
-  if (a.f % 128 == 0) return launch_quant<SRC_SWIGLU_BWD, true>(s, a, o, oh, st);
-  const cudaError_t e = launch_quant<SRC_SWIGLU_BWD, false>(s, a, o, oh, st);
+  if (a.src == FP8_SRC_ROWS)
+    return by_width(on(a.x, 16) && a.ldx % 8 == 0 && a.C % 8 == 0,
+                    on(a.x, 4) && a.ldx % 2 == 0 && a.C % 2 == 0, [&](auto w) {
+                      return launch_quant<SRC_ROWS, decltype(w)::value>(s, a, o, oh, st);
+                    });
+  auto swiglu = [&](const Source& src, const QuantOut& out) {
+    return by_width(a.f % 8 == 0, a.f % 2 == 0, [&](auto w) {
+      return launch_quant<SRC_SWIGLU, decltype(w)::value>(src, a, out, oh, st);
+    });
+  };
+  if (a.src == FP8_SRC_SWIGLU) return swiglu(s, o);
+  if (a.f % 8 == 0) return launch_bwd8(s, a, o, oh, st);
+  // other widths: h apart
+  const cudaError_t e = a.f % 2 == 0 ? launch_quant<SRC_SWIGLU_BWD, 2>(s, a, o, oh, st)
+                                     : launch_quant<SRC_SWIGLU_BWD, 1>(s, a, o, oh, st);
   if (e != cudaSuccess || !a.h_codes_t) return e;
   s.cols = a.f;
-  return a.f % 8 == 0 ? launch_quant<SRC_SWIGLU, true>(s, a, oh, oh, st)
-                      : launch_quant<SRC_SWIGLU, false>(s, a, oh, oh, st);
+  return swiglu(s, oh);
 }
 
 cudaError_t launch_fp8_weights(const void* W, int G, int N, int K, void* codes, int64_t ld,
@@ -1013,7 +1117,9 @@ cudaError_t launch_fp8_weights(const void* W, int G, int N, int K, void* codes, 
                       N, K, nb, kb, static_cast<uint8_t*>(codes), ld, scales,
                       static_cast<uint8_t*>(codes_t), ld_t, scales_t, pow2);
   };
-  return on16(W) && K % 8 == 0 ? go(fp8_weights_kernel<true>) : go(fp8_weights_kernel<false>);
+  return by_width(on(W, 16) && K % 8 == 0, on(W, 4) && K % 2 == 0, [&](auto w) {
+    return go(fp8_weights_kernel<decltype(w)::value>);
+  });
 }
 
 }  // namespace moe
