@@ -69,6 +69,7 @@ struct FgCtl {
   int gstart[FG_MAX_G + 1];
   int tprefix[FG_MAX_G + 1];    // tiles before each group
   int kbpre[FG_MAX_G + 1];      // wgrad: token blocks before each group
+  int order[FG_MAX_G];          // wgrad: the groups by their number of blocks, most first
   FgScales scales[2][FG_CHUNK];
 };
 static_assert(offsetof(FgCtl, scales) % 16 == 0, "read as float4");
@@ -149,7 +150,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* boxes = smem + STAGES * GE::STAGE_BYTES;
   FgCtl* ctl = reinterpret_cast<FgCtl*>(boxes + FG_EPI_WARPS * FG_BOXES * FG_BOX_BYTES);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // as uniform values, here and below, the product's epilogue needs no spills (wide product 824 ->
+  // 786 us); the weight gradient's is 1% slower with them
+  const int warp = WG ? threadIdx.x >> 5 : fg_uniform(threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   const uint32_t smem_base = smem_u32(smem);
   volatile int* abort_flag = &ctl->abort;
   const int rank = PAIR == 2 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -233,20 +237,36 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       tmem_relinquish();
     }
   }
+  if (WG) {
+    for (int g = threadIdx.x; g < p.G; g += FG_THREADS) {
+      auto blocks_of = [&](int i) { return ceil_div(ctl->gstart[i + 1] - ctl->gstart[i], 128); };
+      const int n = blocks_of(g);
+      int before = 0;
+      for (int i = 0; i < p.G; ++i) {
+        const int m = blocks_of(i);
+        before += m > n || (m == n && i < g);
+      }
+      ctl->order[before] = g;
+    }
+  }
   tc_fence_before();
   if (PAIR == 2) cluster_sync_all();
   else __syncthreads();
   tc_fence_after();
   const int total = fg_uniform(ctl->bad ? 0 : ctl->tprefix[p.G]);
-  const uint32_t tmem_base = ctl->tmem_base;
+  const uint32_t tmem_base =
+      WG ? ctl->tmem_base : static_cast<uint32_t>(fg_uniform(static_cast<int>(ctl->tmem_base)));
 
   // tile -> group, row tile, column tile; row tiles run fastest, so the CTAs at work share the
   // group's weight rows in L2.  Every role walks its tiles in ascending order, so the group is
   // found by going on from the last one; with fewer than 2^16 column tiles the fp32 quotient is
-  // off by at most one, which the remainder corrects.
+  // off by at most one, which the remainder corrects.  The weight gradient's groups have equally
+  // many tiles and unequal ones: its order is the longest first.
+  int pos = 0;
   auto map_tile = [&](int tile, int& g, int& mt, int& nt) {
-    while (ctl->tprefix[g + 1] <= tile) ++g;
-    const int local = tile - ctl->tprefix[g];
+    while (ctl->tprefix[pos + 1] <= tile) ++pos;
+    g = WG ? ctl->order[pos] : pos;
+    const int local = tile - ctl->tprefix[pos];
     const int mtg =
         WG ? p.m_tiles : ceil_div(ctl->gstart[g + 1] - ctl->gstart[g], GE::TILE_M);
     nt = static_cast<int>(__fdividef(static_cast<float>(local), static_cast<float>(mtg)));
@@ -259,6 +279,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       mt -= mtg;
     }
   };
+  // tiles are dealt out in rounds, the weight gradient's in turns from the first unit to the last
+  // and back, so that nobody gets the longest of every round
+  const int first_step = WG ? 2 * (num_units - unit) - 1 : num_units;
+  auto next_step = [&](int step) { return WG ? 2 * num_units - step : step; };
   auto blocks = [&](int g) { return WG ? ctl->kbpre[g + 1] - ctl->kbpre[g] : p.kb; };
 
   if (warp < FG_EPI_WARP0) {
@@ -268,9 +292,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      int g = 0;
-      for (int tile = unit; tile < total && ok; tile += num_units) {
-        int mt, nt;
+      for (int tile = unit, step = first_step; tile < total && ok;
+           tile += step, step = next_step(step)) {
+        int g, mt, nt;
         map_tile(tile, g, mt, nt);
         const int nkb = fg_uniform(blocks(g));
         int x = fg_uniform(WG ? ctl->kbpre[g] * FG_BK : 0);
@@ -327,18 +351,18 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         const uint64_t da0 = make_smem_desc(smem_base, 16, 1024);
         const uint64_t db0 =
             make_smem_desc(smem_base + GE::A_BYTES + h * (GE::B_BYTES / 2), 16, 1024);
-        int g = 0;
-        for (int tile = unit; tile < total && ok; tile += num_units) {
+        for (int tile = unit, step = first_step; tile < total && ok;
+           tile += step, step = next_step(step)) {
           int nkb = p.kb;
           if (WG) {
-            int mt, nt;
+            int g, mt, nt;
             map_tile(tile, g, mt, nt);
             nkb = fg_uniform(blocks(g));
           }
           for (int kb = 0; kb < nkb; ++kb, ++it) {
             const uint32_t buf = (it & 1u) * 2u + h;
-            if (!fg_wait(smem_u32(&ctl->tempty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag, p.err) ||
-                !fg_wait(smem_u32(&ctl->full[s]), ph, abort_flag, p.err)) {
+            if (!fg_wait(smem_u32(&ctl->full[s]), ph, abort_flag, p.err) ||
+                !fg_wait(smem_u32(&ctl->tempty[buf]), ((it >> 1) & 1u) ^ 1u, abort_flag, p.err)) {
               ok = false;
               break;
             }
@@ -383,9 +407,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       // -------------------------------------------------------------- scale loader (warp 2)
       uint32_t ci = 0;   // chunks loaded
       bool ok = true;
-      int g = 0;
-      for (int tile = unit; tile < total && ok; tile += num_units) {
-        int mt, nt;
+      for (int tile = unit, step = first_step; tile < total && ok;
+           tile += step, step = next_step(step)) {
+        int g, mt, nt;
         map_tile(tile, g, mt, nt);
         const int nkb = blocks(g);
         const int m0 = mt * GE::TILE_M + 128 * rank;
@@ -445,9 +469,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     uint32_t it = 0;   // blocks added
     uint32_t ci = 0;   // scale chunks used up
     bool ok = true;
-    int g = 0;
-    for (int tile = unit; tile < total && ok; tile += num_units) {
-      int mt, nt;
+    for (int tile = unit, step = first_step; tile < total && ok;
+           tile += step, step = next_step(step)) {
+      int g, mt, nt;
       map_tile(tile, g, mt, nt);
       const int nkb = blocks(g);
       float2 acc[64];
