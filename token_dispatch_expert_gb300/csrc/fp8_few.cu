@@ -316,7 +316,8 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
         const bool in = k0 + j < nkb;
 #pragma unroll
         for (int t = lane >> 2; t < NT; t += 8)   // rows past the segment's get 0
-          cp_async4(&ctl->sa[c][j][t], sa + static_cast<long long>(t) * p.kb + k0 + j, in && t < nt);
+          cp_async4(&ctl->sa[c][j][t], sa + static_cast<long long>(t) * p.kb + k0 + j,
+                    in && t < nt);
         if (lane < FW_CHUNK) cp_async4(&ctl->sb[c][j], sb + k0 + j, in);
         cp_async_arrive(smem_u32(&ctl->sfull[c]));
       }

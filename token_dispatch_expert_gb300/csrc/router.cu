@@ -26,7 +26,9 @@
 // 32-bit keys, then on the id among equals), whose lane moves its list up.  The chunk's histogram
 // and the ranks inside it are bit masks (as in route.cu); order_count (a warp per expert) and
 // order_assign follow; a single chunk (T <= 32) does their work itself, in one launch.
-// Bound by latency: 4 MB of logits for 4096 tokens are 0.6 us of bandwidth.
+// Bound by latency: 4 MB of logits for 4096 tokens are 0.6 us of bandwidth.  One token over 256
+// experts takes 7 us with the call, 4096 tokens 13.5 us in three launches; the gradient for 8192
+// tokens of 128 softmax scores 5.2 us, 1.7 TB/s.
 #include "common.cuh"
 #include "internal.h"
 
@@ -376,9 +378,10 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
     }
     // Error bound of an fp32 key.  sigma = 1 / (1 + e^-x): the exponential is off by 2^-22 and by
     // its argument's rounding, |x| 2^-24, of which sigma (1 - sigma) <= 1/4 reaches the result
-    // (x sigma (1 - sigma) < 0.23); the sum and the reciprocal by 0.75 * 2^-22 of it: below 2^-22.  softmax: e^x is off by 2^-22 and
-    // |x| 2^-24 of itself, the sum of 256 terms by 13 roundings more, the quotient by two:
-    // below 2^-19.  Adding the bias rounds once more, relative to the key.
+    // (x sigma (1 - sigma) < 0.23); the sum and the reciprocal by 0.75 * 2^-22 of it: below
+    // 2^-22.  softmax: e^x is off by 2^-22 and |x| 2^-24 of itself, the sum of 256 terms by 13
+    // roundings more, the quotient by two: below 2^-19.  Adding the bias rounds once more,
+    // relative to the key.
     const float tol =
         scored ? (p.sigmoid ? 0x1p-22f : 0x1p-19f) + 0x1p-24f * warp_fmax(big) : 0.0f;
     if (p.G > 1) {
