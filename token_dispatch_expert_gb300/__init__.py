@@ -170,11 +170,11 @@ def _p(t):
         return None
     if isinstance(t, int):
         return t
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"expected a contiguous tensor, got strides {tuple(t.stride())}")
-    return t.data_ptr()
+    raise ValueError(f"expected a contiguous tensor, got strides {tuple(t.stride())}")
 
 
 def _s(stream):
@@ -185,14 +185,21 @@ def _s(stream):
     return stream.cuda_stream
 
 
+_raw_stream = None
+
+
 def _current_stream():
     """The current stream's handle.  A small call's time is mostly the host's, and torch's own
     accessor builds a Stream object around the handle."""
-    import torch
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        dev = getattr(torch._C, "_cuda_getDevice", None)
+        torch.cuda.init()
+        _raw_stream = ((lambda: torch.cuda.current_stream().cuda_stream)
+                       if raw is None or dev is None else (lambda: raw(dev())))
+    return _raw_stream()
 
 
 def _check(status, where):
@@ -408,15 +415,17 @@ def make_router(score="softmax", groups=1, top_groups=None, group_top=1, renorm=
 _dtypes = {}   # name -> torch dtype
 
 
+def _dtype(name):
+    import torch
+    return _dtypes.setdefault(name, getattr(torch, name))
+
+
 def _typed(t, dtype, name):
     """_p for a buffer of one element type (a torch dtype's name)."""
-    if t is not None and not isinstance(t, int):
-        want = _dtypes.get(dtype)
-        if want is None:
-            import torch
-            want = _dtypes[dtype] = getattr(torch, dtype)
-        if t.dtype is not want:
-            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t is None:
+        return None
+    if not isinstance(t, int) and t.dtype is not (_dtypes.get(dtype) or _dtype(dtype)):
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     return _p(t)
 
 
@@ -450,7 +459,7 @@ def moe_fp8_token_blocks(rows, G) -> int:
 
 
 def _shape(name, t, shape):
-    if tuple(t.shape) != shape:
+    if t.shape != shape:   # (a tuple's comparison: half the cost of building one)
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
 
 
@@ -483,8 +492,8 @@ def moe_fp8_quantize(x, codes=None, scales=None, codes_t=None, scales_t=None, *,
     """Quantise rows of x (bf16, rows may be strided) along the row (codes, scales) and, or, along
     the tokens of the segments (codes_t, scales_t); row p is x[src_tok[p]] when src_tok is
     given."""
-    import torch
-    if x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda or x.dtype is not torch.bfloat16:
+    if (x.dim() != 2 or x.stride(1) != 1 or not x.is_cuda or
+            x.dtype is not (_dtypes.get("bfloat16") or _dtype("bfloat16"))):
         raise ValueError("x: expected a CUDA bf16 matrix with adjacent columns")
     G = _groups(offsets)
     rows = x.shape[0] if src_tok is None else src_tok.numel()
@@ -551,10 +560,9 @@ def moe_fp8_swiglu_bwd(dh, ab, codes, scales, codes_t=None, scales_t=None, h_cod
 
 
 def _out_type(t, name):
-    import torch
-    if t.dtype is torch.bfloat16:
+    if t.dtype is (_dtypes.get("bfloat16") or _dtype("bfloat16")):
         return 0
-    if t.dtype is torch.float32:
+    if t.dtype is (_dtypes.get("float32") or _dtype("float32")):
         return 1
     raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
 
