@@ -499,3 +499,99 @@ def test_repeatable_and_captured():
     torch.cuda.synchronize()
     for a, b in zip(first, cap):
         assert torch.equal(a, b)
+
+
+def test_swiglu_backward_against_differences():
+    """[da | db] against central differences of silu(a) b in 64 bits: half a step of bf16 and of
+    E4M3 (2^-8 and 2^-4, relative; below its normal numbers 2^-10 of the scale); the differences
+    are off by h^2 / 6 of a third derivative (below 2)."""
+    R, f, h = 40, 96, 1e-4
+    ab, dh = normal((R, 2 * f), 31), normal((R, f), 32)
+    c, ws = [codes_new((R, 2 * f)), torch.empty((R, 2), device="cuda")], ws_new()
+    tde.moe_fp8_swiglu_bwd(dh, ab, *c, ws=ws)
+    a, b, d = f64(ab)[:, :f], f64(ab)[:, f:], f64(dh)
+
+    def fn(a, b):
+        return a / (1 + np.exp(-a)) * b
+    want = np.hstack([d * (fn(a + h, b) - fn(a - h, b)),
+                      d * (fn(a, b + h) - fn(a, b - h))]) / (2 * h)
+    s = ref.spread(f64(c[1]), 2 * f, 1)
+    slack = np.hstack([np.abs(d * b), np.abs(d)]) * (h * h / 3) + 1e-11
+    bound = (np.abs(want) + slack) * (2.0 ** -4 * (1 + 2.0 ** -8) + 2.0 ** -8 + 2.0 ** -20)
+    assert (np.abs(f64(c[0]) * s - want) <= bound + slack + s * 2.0 ** -10).all()
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 elements: rows, columns along the tokens, an output's strided rows."""
+    R, C = 300_001, 7168
+    ws, B = ws_new(), tde.moe_fp8_token_blocks(R, 1)
+    x = torch.randn((R, C), device="cuda", dtype=torch.bfloat16)
+    c = [codes_new((R, C)), torch.empty((R, 56), device="cuda"), codes_new((C, 128 * B)),
+         torch.empty((B, C), device="cuda")]
+    tde.moe_fp8_quantize(x, *c, ws=ws)
+    at = slice(R - 130, R)
+    check_rows(c[0][at], c[1][at], f64(x[at]), False)
+    rows = [codes_new((R, C)), torch.empty((R, 56), device="cuda")]
+    tde.moe_fp8_quantize(x, *rows, ws=ws)
+    assert torch.equal(rows[0].view(torch.uint8)[at], c[0].view(torch.uint8)[at])
+    assert torch.equal(rows[1], c[1])
+    check_tokens(c[2][C - 3:], c[3][:, C - 3:], f64(x[:, C - 3:]), [0, R], False)
+    del x, c, rows
+    M, N, K, ld = 300, 130, 256, 1 << 23
+    av, sa = operand((M, K), 41, (M, 2))
+    bv, sb = operand((1, N, K), 42, (1, 2, 2))
+    out = torch.zeros((M, ld), device="cuda", dtype=torch.bfloat16)
+    for lo, n in ((0, M), (M - 9, 9)):
+        part = out[lo:, ld - N:]
+        part.zero_()
+        tde.moe_fp8_gemm(to_codes(av[lo:], K), dev(sa[lo:]), to_codes(bv, K), dev(sb), part, K,
+                         ws=ws)
+        A = av[lo:] * ref.spread(sa[lo:].astype(np.float64), K, 1)
+        Bv = bv[0] * ref.spread(ref.spread(sb[0].astype(np.float64), N, 0), K, 1)
+        check_product(f64(part), A @ Bv.T, np.abs(A) @ np.abs(Bv.T), 2, False, n)
+    assert tde.moe_status(ws)[1] == 0
+    del out, part
+    torch.cuda.empty_cache()
+
+
+def test_weights_past_32_bits():
+    """More than 2^31 elements of weights and of their gradients: the last expert's."""
+    G, N, K = 160, 2048, 7168
+    ws = ws_new()
+    w = torch.zeros((G, N, K), device="cuda", dtype=torch.bfloat16)
+    w[-1] = normal((N, K), 51, 0.05)
+    q = [codes_new((G, N, K)), torch.empty((G, 16, 56), device="cuda"), codes_new((G, K, N)),
+         torch.empty((G, 56, 16), device="cuda")]
+    tde.moe_fp8_quantize_weights(w, *q)
+    codes, scales = ref.quantise_weights(f64(w[-1]))
+    same(f64(q[0][-1]), codes, "codes")
+    same(f64(q[2][-1]), codes.T, "codes_t")
+    same(f64(q[1][-1]), scales, "scales")
+    del w
+    Bv = codes[:64] * ref.spread(ref.spread(scales, N, 0), K, 1)[:64]
+    for R in (3, 1400):
+        av, sa = operand((R, K), R, (R, 56))
+        out = torch.empty((R, N), device="cuda", dtype=torch.bfloat16)
+        tde.moe_fp8_gemm(to_codes(av, K), dev(sa), *q[:2], out, K, offsets=odev([0] * G + [R]),
+                         ws=ws)
+        A = av * ref.spread(sa.astype(np.float64), K, 1)
+        check_product(f64(out[:, :64]), A @ Bv.T, np.abs(A) @ np.abs(Bv.T), 56, False, R)
+    del q
+    R, off = 200, odev([0] * G + [200])
+    x, y = normal((R, N), 52), normal((R, K), 53)
+    B = tde.moe_fp8_token_blocks(R, G)
+    ops = []
+    for t, C in ((x, N), (y, K)):
+        c = [codes_new((C, 128 * B)), torch.empty((B, C), device="cuda")]
+        tde.moe_fp8_quantize(t, codes_t=c[0], scales_t=c[1], offsets=off, ws=ws)
+        ops += c
+    dw = torch.full((G, N, K), float("nan"), device="cuda", dtype=torch.bfloat16)
+    tde.moe_fp8_wgrad(*ops, dw, offsets=off, rows=R, ws=ws)
+    assert (dw[G - 2] == 0).all() and (dw[0] == 0).all()
+    qa, sa = ref.quantise_tokens(f64(x)[:, -40:], [0, R])
+    qb, sb = ref.quantise_tokens(f64(y), [0, R])
+    A, Bv = qa * np.repeat(sa, 128, 0).T, qb * np.repeat(sb, 128, 0).T
+    check_product(f64(dw[-1, -40:]), A @ Bv.T, np.abs(A) @ np.abs(Bv).T, 2, False, "dw")
+    assert tde.moe_status(ws)[1] == 0
+    del dw
+    torch.cuda.empty_cache()
