@@ -17,10 +17,11 @@
 //   rows in order, 21,240 x 6656           6.2 TB/s, 69 us: memory
 //   rows 32,768 x 7168 gathered from 4096  3.8 TB/s, 78 us; moving the same bytes without any
 //                                          arithmetic takes 66 us: every row passes L2 eight times
-//   both ways, 16,382 x 2056               3.8 TB/s, 36 us: barriers between the two orientations
-//   SwiGLU, rows 65,536 x 768              4.0 TB/s, 63 us: the instructions issued, at 50 of
+//   both ways, 16,382 x 2056               4.2 TB/s, 32 us: instructions, and barriers between the
+//                                          two orientations
+//   SwiGLU, rows 65,536 x 768              4.1 TB/s, 62 us: the instructions issued, at 50 of
 //                                          which an exactly rounded h and its code come
-//   its backward, both ways, 16,383 x 1408 2.4 TB/s, 107 us: instructions, about 100 a column for
+//   its backward, both ways, 16,383 x 1408 2.5 TB/s, 104 us: instructions, about 100 a column for
 //                                          three values and five codes
 #include <cuda.h>
 #include <cuda_fp8.h>
@@ -563,12 +564,12 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
 // first row), column tiles fastest.
 struct Blocks {
   int first[FQ_MAX_G + 1];   // first block of every segment
+  int start[FQ_MAX_G + 1];   // first row
   int sum[8];
   int bad;
 };
 struct TileAt {
-  int kb, c0, nr;            // block, first column, rows in it
-  long long r0;              // first row
+  int kb, c0, nr, r0;        // block, first column, rows in it, the first of them
 };
 __device__ __forceinline__ long long segment_start(const int32_t* offsets, int g, long long rows) {
   return offsets ? static_cast<long long>(__ldg(offsets + g)) : (g ? rows : 0LL);
@@ -585,6 +586,8 @@ __device__ __forceinline__ bool count_blocks(Blocks& s, const int32_t* offsets, 
     const long long b = segment_start(offsets, tid + 1, rows);
     if (a < 0 || b < a || b > rows || (tid == 0 && a != 0)) s.bad = 1;
     else nb = static_cast<int>((b - a + 127) / 128);
+    s.start[tid] = static_cast<int>(a);
+    if (tid == G - 1) s.start[G] = static_cast<int>(b);
   }
   const int incl = warp_incl_scan(nb);
   if (lane == 31 && warp < 8) s.sum[warp] = incl;
@@ -599,22 +602,37 @@ __device__ __forceinline__ bool count_blocks(Blocks& s, const int32_t* offsets, 
   if (s.bad && blockIdx.x == 0 && tid == 0) flag_error(err, MOE_DEVERR_BAD_OFFSETS);
   return s.bad == 0;
 }
-__device__ __forceinline__ TileAt tile_at(const Blocks& s, const int32_t* offsets, int G,
-                                          long long rows, long long item, int gx) {
-  TileAt t;
-  t.kb = static_cast<int>(item / gx);
-  t.c0 = static_cast<int>(item - static_cast<long long>(t.kb) * gx) * 128;
-  int lo = 0, hi = G;   // first[lo] <= kb < first[lo + 1]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (s.first[mid] <= t.kb) lo = mid;
-    else hi = mid;
+// A CTA's tiles, `step` apart, from number `item`: the column tile, block and segment go on from the
+// last tile's (a division and a search for each took a fifth of the instructions of the quantiser
+// without SwiGLU).
+struct Walk {
+  int cx, kb, g;             // column tile, block, segment
+  int dc, dk, gx;
+  __device__ __forceinline__ Walk(long long item, int step, int gx_) : g(0), gx(gx_) {
+    kb = static_cast<int>(item / gx);
+    cx = static_cast<int>(item - static_cast<long long>(kb) * gx);
+    dk = step / gx;
+    dc = step - dk * gx;
   }
-  t.r0 = segment_start(offsets, lo, rows) + 128LL * (t.kb - s.first[lo]);
-  const long long left = segment_start(offsets, lo + 1, rows) - t.r0;
-  t.nr = left < 128 ? static_cast<int>(left) : 128;
-  return t;
-}
+  __device__ __forceinline__ void next() {
+    kb += dk;
+    cx += dc;
+    if (cx >= gx) {
+      cx -= gx;
+      ++kb;
+    }
+  }
+  // (kb below the number of blocks)
+  __device__ __forceinline__ TileAt at(const Blocks& s) {
+    while (s.first[g + 1] <= kb) ++g;
+    TileAt t;
+    t.kb = kb;
+    t.c0 = cx * 128;
+    t.r0 = s.start[g] + 128 * (kb - s.first[g]);
+    t.nr = min(s.start[g + 1] - t.r0, 128);
+    return t;
+  }
+};
 
 constexpr int FT_TILE = 128 * 16;   // 16-byte pieces
 
@@ -691,7 +709,8 @@ __device__ __forceinline__ void tile_rows(const uint4* v, const TileAt& t, int c
   if (sb >= 0) {
     const int2 rc = at(sb);
     const int c = rc.y - 8 * (lane & 15);
-    if (rc.x < t.nr && c < cols) out.scales[(t.r0 + rc.x) * out.kb + (c >> 7)] = quot;
+    if (rc.x < t.nr && c < cols)
+      out.scales[static_cast<long long>(t.r0 + rc.x) * out.kb + (c >> 7)] = quot;
   }
 }
 
@@ -711,15 +730,16 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
   const int tid = threadIdx.x;
   const int gx = (src.cols + 127) / 128;
   const long long total = static_cast<long long>(blocks.first[G]) * gx;
-  for (long long item = blockIdx.x; item < total; item += gridDim.x) {
-    const TileAt t = tile_at(blocks, offsets, G, rows, item, gx);
+  Walk walk(blockIdx.x, gridDim.x, gx);
+  for (long long item = blockIdx.x; item < total; item += gridDim.x, walk.next()) {
+    const TileAt t = walk.at(blocks);
     const int r = tid >> 4, c = t.c0 + 8 * (tid & 15);
     uint4 v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       v[u] = make_uint4(0u, 0u, 0u, 0u);
       if (r + 32 * u < t.nr) {
-        long long row = t.r0 + r + 32 * u;
+        int row = t.r0 + r + 32 * u;
         if (src_tok) {
           row = __ldg(src_tok + row);
           if (row < 0 || row >= src_rows) {
@@ -788,7 +808,7 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
     for (int u = 0; u < PER; ++u) {
       const int rr = r + 32 * u, at = rr * 16 + ch;
       const bool in = rr < t.nr && c < width;
-      long long row = in ? t.r0 + rr : 0;
+      int row = in ? t.r0 + rr : 0;
       if (SRC == SRC_ROWS && src_tok && in) {
         row = __ldg(src_tok + row);
         if (row < 0 || row >= src_rows) {
@@ -800,17 +820,18 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
       if constexpr (SRC == SRC_ROWS) {
         cp_async16(dst + at, src.x + row * src.ld + cc, in);
       } else {
-        const __nv_bfloat16* a = src.x + row * 2 * src.f + cc;
+        const __nv_bfloat16* a = src.x + static_cast<long long>(row) * (2 * src.f) + cc;
         cp_async16(dst + at, a, in);
         cp_async16(dst + FT_TILE + at, a + src.f, in);
-        if constexpr (BWD) cp_async16(dst + 2 * FT_TILE + at, src.dh + row * src.f + cc, in);
+        if constexpr (BWD) cp_async16(dst + 2 * FT_TILE + at, src.dh + static_cast<long long>(row) * src.f + cc, in);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+  Walk walk(blockIdx.x, gridDim.x, gx);
   TileAt next;
   if (blockIdx.x < total) {
-    next = tile_at(blocks, offsets, G, rows, blockIdx.x, gx);
+    next = walk.at(blocks);
     fetch(next, bufs);
   }
   int buf = 0;
@@ -871,7 +892,8 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
       __syncthreads();
     }
     if (!BWD && more) {
-      next = tile_at(blocks, offsets, G, rows, item + gridDim.x, gx);
+      walk.next();
+      next = walk.at(blocks);
       fetch(next, SRC == SRC_ROWS ? bufs + (buf ^ 1) * FT_TILE : raw);
     }
     uint8_t* box = reinterpret_cast<uint8_t*>(tile);
@@ -906,7 +928,8 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
       if (BWD) bulk_wait_group_read<0>();
     }
     if (BWD && more) {
-      next = tile_at(blocks, offsets, G, rows, item + gridDim.x, gx);
+      walk.next();
+      next = walk.at(blocks);
       __syncthreads();   // the codes have left the buffers
       fetch(next, raw);
     }
@@ -1057,7 +1080,7 @@ cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut&
 
 // The backward reads a, b and dh once for da, db and h.  Where the blocks of da and db share one (f
 // no multiple of 128) the tiles of 128 columns do not hold whole blocks of a row: the row codes
-// come from a launch of their own (131 of 224 us at 16383 x 1376, where the backward by single
+// come from a launch of their own (131 of 221 us at 16383 x 1376, where the backward by single
 // columns took 439).
 cudaError_t launch_bwd8(const Source& s, const Fp8QuantArgs& a, QuantOut o, const QuantOut& oh,
                         cudaStream_t st) {
