@@ -14,13 +14,13 @@
 // or, with both orientations, two bytes are written.  What they reach, and what holds them up, at
 // 6.7 TB/s for a copy:
 //   weights 8 x 4096 x 7168 and transposes 6.5 TB/s, 144 us: memory
-//   rows in order, 21,240 x 6656           6.2 TB/s, 69 us: memory
-//   rows 32,768 x 7168 gathered from 4096  3.8 TB/s, 78 us; moving the same bytes without any
-//                                          arithmetic takes 66 us: every row passes L2 eight times
+//   rows in order, 21,240 x 6656           6.6 TB/s, 64 us: memory
+//   rows 32,768 x 7168 gathered from 4096  4.5 TB/s, 67 us: every row passes L2 eight times, and
+//                                          moving the bytes without any arithmetic took 66 us
 //   both ways, 16,382 x 2056               4.2 TB/s, 32 us: instructions, and barriers between the
 //                                          two orientations
-//   SwiGLU, rows 65,536 x 768              4.1 TB/s, 62 us: the instructions issued, at 50 of
-//                                          which an exactly rounded h and its code come
+//   SwiGLU, rows 65,536 x 768              4.1 TB/s, 62 us: instructions, 34 a column for an
+//                                          exactly rounded h and its code
 //   its backward, both ways, 16,383 x 1408 2.5 TB/s, 104 us: instructions, about 100 a column for
 //                                          three values and five codes
 #include <cuda.h>
@@ -559,6 +559,89 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
   griddep_launch();
 }
 
+// Plain rows on 16 bytes: a lane's pieces come through a ring in shared memory that it alone writes
+// (cp.async) and reads, so that two spans of 1024 columns are under way while one is worked on,
+// with nothing to wait for but the lane's own copies.  (Loaded into registers, as above: 77 us
+// instead of 67 for 32,768 gathered rows of 7168, 69 instead of 64 for 21,240 rows of 6656 in
+// order.  The SwiGLU, with two inputs to a column and bound by its instructions, is 10% slower
+// this way.)  A grid of four waves: the rows are spread evenly.
+constexpr int FR_STAGES = 3;
+constexpr int FR_CTAS = 4;   // per SM
+constexpr int FR_SMEM = FR_STAGES * 4 * FQ_THREADS * 16;
+
+__global__ void __launch_bounds__(FQ_THREADS, FR_CTAS)
+fp8_rows_ring_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
+                     const int32_t* __restrict__ offsets, int G, long long rows,
+                     const QuantOut out, int* err) {
+  griddep_wait();   // see common.cuh: dependent launches
+  extern __shared__ uint4 dyn[];   // [FR_STAGES][4][FQ_THREADS]
+  uint4* mine = dyn + threadIdx.x;
+  const int lane = threadIdx.x & 31;
+  const long long gw = (static_cast<long long>(blockIdx.x) * FQ_THREADS + threadIdx.x) >> 5;
+  const long long nw = (static_cast<long long>(gridDim.x) * FQ_THREADS) >> 5;
+  const long long n_rows = live_rows(offsets, G, rows, err, gw == 0 && lane == 0);
+  // the next fetch: its row, source row and first column, and the source of the row after it
+  long long fp = gw, ft = gw, ft_next = gw + nw;
+  int fc = 0, f_stage = 0;
+  if (src_tok) {
+    if (gw < n_rows) ft = __ldg(src_tok + gw);
+    if (gw + nw < n_rows) ft_next = __ldg(src_tok + gw + nw);
+  }
+  auto fetch = [&]() {
+    if (fp < n_rows) {
+      const bool ok = !src_tok || (ft >= 0 && ft < src_rows);
+      const __nv_bfloat16* row = src.x + (ok ? ft : 0) * src.ld + fc + 8 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool in = ok && fc + 256 * i + 8 * lane < src.cols;
+        cp_async16(mine + (f_stage * 4 + i) * FQ_THREADS, in ? row + 256 * i : src.x, in);
+      }
+      if (++f_stage == FR_STAGES) f_stage = 0;
+      fc += 1024;
+      if (fc >= src.cols) {
+        fc = 0;
+        fp += nw;
+        ft = ft_next;
+        ft_next = fp + nw;
+        if (src_tok && ft_next < n_rows) ft_next = __ldg(src_tok + ft_next);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < FR_STAGES - 1; ++i) fetch();
+  int stage = 0;
+  for (long long p = gw; p < n_rows; p += nw) {
+    bool live = true;   // its source is a row (the ring holds zeros if not)
+    if (src_tok) {
+      const long long t = __ldg(src_tok + p);
+      live = t >= 0 && t < src_rows;
+      if (!live && lane == 0) flag_error(err, MOE_DEVERR_BAD_INDEX);
+    }
+    for (int c0 = 0; c0 < src.cols; c0 += 1024) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(FR_STAGES - 2) : "memory");
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mine[(stage * 4 + i) * FQ_THREADS];
+      if (++stage == FR_STAGES) stage = 0;
+      float r[4], quot;
+      four_scales(v, out.pow2, lane, r, quot);
+      fetch();   // to where the span before this one was
+      if (!live) continue;
+      const int c = c0 + 8 * lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + 256 * i < src.cols)
+          __stcs(reinterpret_cast<uint2*>(out.codes + p * out.ld + c + 256 * i),
+                 codes8(v[i], r[i]));
+      const int sb = scale_of_lane(lane);
+      const int cs = c0 + 256 * sb + 8 * (lane & 16);   // its block's first column
+      if (sb >= 0 && cs < src.cols) out.scales[p * out.kb + (cs >> 7)] = quot;
+    }
+  }
+  griddep_launch();
+}
+
 // ------------------------------------------------------------------ along the tokens (and rows)
 // Tiles of 128 columns and one 128-row block of a segment (blocks are counted from the segment's
 // first row), column tiles fastest.
@@ -1030,10 +1113,20 @@ template <int SRC, int W>
 cudaError_t launch_rows(const Source& s, const Fp8QuantArgs& a, const QuantOut& o,
                         cudaStream_t st) {
   const long long want = (a.rows + FQ_THREADS / 32 - 1) / (FQ_THREADS / 32);
-  const long long most = static_cast<long long>(fq_sms()) * 8;
-  return launch_pdl(fp8_rows_kernel<SRC, W>, dim3(static_cast<unsigned>(want < most ? want : most)),
-                    dim3(FQ_THREADS), 0, st, 1, s, a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o,
-                    a.err);
+  auto grid = [&](int per_sm) {
+    const long long most = static_cast<long long>(fq_sms()) * per_sm;
+    return dim3(static_cast<unsigned>(want < most ? want : most));
+  };
+  if constexpr (SRC == SRC_ROWS && W == 8) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        fp8_rows_ring_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FR_SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(fp8_rows_ring_kernel, grid(4 * FR_CTAS), dim3(FQ_THREADS), FR_SMEM, st, 1, s,
+                      a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, a.err);
+  } else {
+    return launch_pdl(fp8_rows_kernel<SRC, W>, grid(8), dim3(FQ_THREADS), 0, st, 1, s, a.src_tok,
+                      a.src_rows, a.offsets, a.G, a.rows, o, a.err);
+  }
 }
 
 template <int SRC, int W>
