@@ -19,7 +19,7 @@
 //                                          moving the bytes without any arithmetic took 66 us
 //   both ways, 16,382 x 2056               4.2 TB/s, 32 us: instructions, and barriers between the
 //                                          two orientations
-//   SwiGLU, rows 65,536 x 768              4.1 TB/s, 62 us: instructions, 34 a column for an
+//   SwiGLU, rows 65,536 x 768              4.5 TB/s, 57 us: instructions, about 30 a column for an
 //                                          exactly rounded h and its code
 //   its backward, both ways, 16,383 x 1408 2.5 TB/s, 104 us: instructions, about 100 a column for
 //                                          three values and five codes
@@ -523,20 +523,6 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
           v[i] = make_uint4(x[0], x[1], x[2], x[3]);
           v[2 + i] = make_uint4(y[0], y[1], y[2], y[3]);
         }
-      } else if constexpr (SRC == SRC_SWIGLU && W == 8) {
-        uint4 a[4], b[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          col[i] = c0 + 256 * i + 8 * lane;
-          a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (col[i] < src.cols) {
-            a[i] = load8<8>(src.x + t * 2 * src.f + col[i], 8);
-            b[i] = load8<8>(src.x + t * 2 * src.f + src.f + col[i], 8);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = col[i] < src.cols ? silu_mul8(a[i], b[i]) : a[i];
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -637,6 +623,68 @@ fp8_rows_ring_kernel(const Source src, const int32_t* __restrict__ src_tok, long
       const int sb = scale_of_lane(lane);
       const int cs = c0 + 256 * sb + 8 * (lane & 16);   // its block's first column
       if (sb >= 0 && cs < src.cols) out.scales[p * out.kb + (cs >> 7)] = quot;
+    }
+  }
+  griddep_launch();
+}
+
+// The SwiGLU of widths of 8: a warp takes four chunks of 256 columns at a time, one after another
+// over the rows' ends, so that no width leaves places of four_scales() empty (65,536 rows of 768
+// columns 57 us, in spans of 1024 columns 62; 32,768 rows of 1408 58 and 61; but 16,384 rows of
+// 2048 40 and 38.5).
+__global__ void __launch_bounds__(FQ_THREADS, 4)
+fp8_swiglu_rows_kernel(const Source src, const int32_t* __restrict__ offsets, int G,
+                       long long rows, const QuantOut out, int* err) {
+  griddep_wait();   // see common.cuh: dependent launches
+  const int lane = threadIdx.x & 31;
+  const long long gw = (static_cast<long long>(blockIdx.x) * FQ_THREADS + threadIdx.x) >> 5;
+  const long long nw = (static_cast<long long>(gridDim.x) * FQ_THREADS) >> 5;
+  const uint32_t n_rows =
+      static_cast<uint32_t>(live_rows(offsets, G, rows, err, gw == 0 && lane == 0));
+  const int nch = (src.f + 255) / 256;
+  uint32_t row = static_cast<uint32_t>(4 * gw / nch);
+  int ch = static_cast<int>(4 * gw - static_cast<long long>(row) * nch);
+  // from the end of a warp's four chunks to its next ones
+  const uint32_t skip_rows = static_cast<uint32_t>(4 * (nw - 1) / nch);
+  const int skip = static_cast<int>(4 * (nw - 1) - static_cast<long long>(skip_rows) * nch);
+  while (row < n_rows) {
+    uint4 a[4], b[4];
+    uint32_t at[4];
+    int col[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      at[i] = row;
+      col[i] = row < n_rows ? 256 * ch + 8 * lane : src.f;
+      a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (col[i] < src.f) {
+        const __nv_bfloat16* x = src.x + static_cast<long long>(row) * (2 * src.f) + col[i];
+        a[i] = __ldcs(reinterpret_cast<const uint4*>(x));
+        b[i] = __ldcs(reinterpret_cast<const uint4*>(x + src.f));
+      }
+      if (++ch == nch) {
+        ch = 0;
+        ++row;
+      }
+    }
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = col[i] < src.f ? silu_mul8(a[i], b[i]) : a[i];
+    float r[4], quot;
+    four_scales(v, out.pow2, lane, r, quot);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col[i] < src.f)
+        __stcs(reinterpret_cast<uint2*>(out.codes + static_cast<long long>(at[i]) * out.ld + col[i]), codes8(v[i], r[i]));
+    const int sb = scale_of_lane(lane);
+    const uint32_t p = sb == 1 ? at[1] : sb == 2 ? at[2] : sb == 3 ? at[3] : at[0];
+    const int c =
+        (sb == 1 ? col[1] : sb == 2 ? col[2] : sb == 3 ? col[3] : col[0]) - 8 * (lane & 15);
+    if (sb >= 0 && c < src.f) out.scales[static_cast<long long>(p) * out.kb + (c >> 7)] = quot;
+    row += skip_rows;
+    ch += skip;
+    if (ch >= nch) {
+      ch -= nch;
+      ++row;
     }
   }
   griddep_launch();
@@ -1123,6 +1171,9 @@ cudaError_t launch_rows(const Source& s, const Fp8QuantArgs& a, const QuantOut& 
     if (e != cudaSuccess) return e;
     return launch_pdl(fp8_rows_ring_kernel, grid(4 * FR_CTAS), dim3(FQ_THREADS), FR_SMEM, st, 1, s,
                       a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, a.err);
+  } else if constexpr (SRC == SRC_SWIGLU && W == 8) {
+    return launch_pdl(fp8_swiglu_rows_kernel, grid(8), dim3(FQ_THREADS), 0, st, 1, s, a.offsets,
+                      a.G, a.rows, o, a.err);
   } else {
     return launch_pdl(fp8_rows_kernel<SRC, W>, grid(8), dim3(FQ_THREADS), 0, st, 1, s, a.src_tok,
                       a.src_rows, a.offsets, a.G, a.rows, o, a.err);
