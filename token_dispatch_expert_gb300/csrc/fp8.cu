@@ -272,6 +272,14 @@ __device__ __forceinline__ uint4 silu_mul8(const uint4& a, const uint4& b) {
 struct Swiglu2 {
   uint32_t da, db, h;
 };
+// One of a pair of da: its two ends' bf16 if they agree and can be trusted, else computed again.
+__device__ __forceinline__ float dsilu_mul_settled(uint32_t lo, uint32_t hi, int shift, float w,
+                                                   float a, float b, float dh) {
+  if (((lo ^ hi) >> shift & 0xffffu) || !(w >= 0x1p-100f && w < INFINITY) ||
+      !(fabsf(a) <= GATE_MAX))
+    return dsilu_mul_exact(a, b, dh);
+  return __uint_as_float((lo >> shift) << 16);
+}
 __device__ __forceinline__ Swiglu2 swiglu_bwd2(uint32_t a, uint32_t b, uint32_t dh) {
   const float2 fa = wide2(a), fb = wide2(b), fd = wide2(dh);
   const float2 t = exp_neg2(fa);
@@ -291,7 +299,6 @@ __device__ __forceinline__ Swiglu2 swiglu_bwd2(uint32_t a, uint32_t b, uint32_t 
                             min(border_place(db.x), border_place(db.y)));
   const float close = fminf(fminf(least(h.x, h.y), least(db.x, db.y)), fminf(w.x, w.y));
   const float far = fmaxf(fmaxf(most(h.x, h.y), most(db.x, db.y)), fmaxf(w.x, w.y));
-  auto fits = [](float x) { return x >= 0x1p-100f && x < INFINITY; };
   uint32_t da = lo;
   if (near < BORDER_END || lo != hi || !(close >= 0x1p-100f) || !(far < INFINITY) ||
       !(most(fa.x, fa.y) <= GATE_MAX)) {
@@ -299,14 +306,35 @@ __device__ __forceinline__ Swiglu2 swiglu_bwd2(uint32_t a, uint32_t b, uint32_t 
     if (unsettled(h.y, fa.y)) h.y = silu_mul_exact(fa.y, fb.y);
     if (unsettled(db.x, fa.x)) db.x = silu_mul_exact(fa.x, fd.x);
     if (unsettled(db.y, fa.y)) db.y = silu_mul_exact(fa.y, fd.y);
-    const uint32_t off = lo ^ hi;
-    const float x = (off & 0xffffu) || !fits(w.x) || !(fabsf(fa.x) <= GATE_MAX)
-                        ? dsilu_mul_exact(fa.x, fb.x, fd.x) : bf16_lo(lo);
-    const float y = (off >> 16) || !fits(w.y) || !(fabsf(fa.y) <= GATE_MAX)
-                        ? dsilu_mul_exact(fa.y, fb.y, fd.y) : bf16_hi(lo);
-    da = pack_bf16x2(x, y);
+    da = pack_bf16x2(dsilu_mul_settled(lo, hi, 0, w.x, fa.x, fb.x, fd.x),
+                     dsilu_mul_settled(lo, hi, 16, w.y, fa.y, fb.y, fd.y));
   }
   return {da, pack_bf16x2(db.x, db.y), pack_bf16x2(h.x, h.y)};
+}
+
+// da alone (db alone is silu_mul2(a, dh))
+__device__ __forceinline__ uint32_t dsilu_mul2(uint32_t a, uint32_t b, uint32_t dh) {
+  const float2 fa = wide2(a), fb = wide2(b), fd = wide2(dh);
+  const float2 t = exp_neg2(fa);
+  const float2 den = __fadd2_rn(t, both(1.0f));
+  const float2 s = make_float2(fast_rcp(den.x), fast_rcp(den.y));
+  const float2 u = __fmul2_rn(__fmul2_rn(fa, t), s);
+  const float2 g = __fadd2_rn(u, both(1.0f));
+  const float2 qs = __fmul2_rn(__fmul2_rn(fd, fb), s);
+  const float2 v = __fmul2_rn(qs, g);
+  const float2 w = make_float2((fabsf(u.x) + fabsf(g.x)) * fabsf(qs.x),
+                               (fabsf(u.y) + fabsf(g.y)) * fabsf(qs.y));
+  const uint32_t lo = pack_bf16x2(fmaf(w.x, -0x1p-20f, v.x), fmaf(w.y, -0x1p-20f, v.y));
+  const uint32_t hi = pack_bf16x2(fmaf(w.x, 0x1p-20f, v.x), fmaf(w.y, 0x1p-20f, v.y));
+  if (lo == hi && fminf(w.x, w.y) >= 0x1p-100f && fmaxf(w.x, w.y) < INFINITY &&
+      most(fa.x, fa.y) <= GATE_MAX)
+    return lo;
+  return pack_bf16x2(dsilu_mul_settled(lo, hi, 0, w.x, fa.x, fb.x, fd.x),
+                     dsilu_mul_settled(lo, hi, 16, w.y, fa.y, fb.y, fd.y));
+}
+__device__ __forceinline__ uint4 dsilu_mul8(const uint4& a, const uint4& b, const uint4& dh) {
+  return make_uint4(dsilu_mul2(a.x, b.x, dh.x), dsilu_mul2(a.y, b.y, dh.y),
+                    dsilu_mul2(a.z, b.z, dh.z), dsilu_mul2(a.w, b.w, dh.w));
 }
 
 // ------------------------------------------------------------------ sources
@@ -359,41 +387,23 @@ __device__ __forceinline__ uint4 value8(const Source& s, long long row, int c) {
     const __nv_bfloat16* ab = s.x + row * 2 * s.f;
     if constexpr (SRC == SRC_SWIGLU)
       return silu_mul8(load8<W>(ab + c, n), load8<W>(ab + s.f + c, n));
-    // da or db, wherever the halves meet: the other is computed too and dropped.  Widths of whole
-    // blocks have code of their own
+    // a chunk of da, of db, or (where the halves meet inside it) of both; widths of whole blocks
+    // have code of their own
     const __nv_bfloat16* dh = s.dh + row * s.f;
+    if (c + 8 <= s.f)
+      return dsilu_mul8(load8<W>(ab + c, 8), load8<W>(ab + s.f + c, 8), load8<W>(dh + c, 8));
+    if (c >= s.f) return silu_mul8(load8<W>(ab + c - s.f, n), load8<W>(dh + c - s.f, n));
     uint32_t w[4];
-    if constexpr (W == 8) {
-      const bool first = c < s.f;
-      const int k = first ? c : c - s.f;
-      const uint4 a = load8<8>(ab + k, 8), b = load8<8>(ab + s.f + k, 8), d = load8<8>(dh + k, 8);
-      const uint32_t *pa = &a.x, *pb = &b.x, *pd = &d.x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const Swiglu2 x = swiglu_bwd2(pa[i], pb[i], pd[i]);
-        w[i] = first ? x.da : x.db;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c0 = c + 2 * i, c1 = c0 + 1;
-        w[i] = 0u;
-        if (c0 >= s.cols) continue;
-        const int k0 = c0 < s.f ? c0 : c0 - s.f;
-        uint32_t a, b, d;
-        if constexpr (W == 2) {   // an even f: a pair lies in one half
-          a = load2(ab + k0);
-          b = load2(ab + s.f + k0);
-          d = load2(dh + k0);
-        } else {                  // (cols = 2 f is even, so c1 is there too)
-          const int k1 = c1 < s.f ? c1 : c1 - s.f;
-          a = load1(ab + k0) | (load1(ab + k1) << 16);
-          b = load1(ab + s.f + k0) | (load1(ab + s.f + k1) << 16);
-          d = load1(dh + k0) | (load1(dh + k1) << 16);
-        }
-        const Swiglu2 x = swiglu_bwd2(a, b, d);
-        w[i] = ((c0 < s.f ? x.da : x.db) & 0xffffu) | ((c1 < s.f ? x.da : x.db) & 0xffff0000u);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int c0 = c + 2 * i, c1 = c0 + 1;
+      w[i] = 0u;
+      if (c0 >= s.cols) continue;   // (cols = 2 f is even)
+      const int k0 = c0 < s.f ? c0 : c0 - s.f, k1 = c1 < s.f ? c1 : c1 - s.f;
+      const Swiglu2 x = swiglu_bwd2(load1(ab + k0) | (load1(ab + k1) << 16),
+                                    load1(ab + s.f + k0) | (load1(ab + s.f + k1) << 16),
+                                    load1(dh + k0) | (load1(dh + k1) << 16));
+      w[i] = ((c0 < s.f ? x.da : x.db) & 0xffffu) | ((c1 < s.f ? x.da : x.db) & 0xffff0000u);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -1224,8 +1234,7 @@ cudaError_t launch_quant(const Source& s, const Fp8QuantArgs& a, const QuantOut&
 
 // The backward reads a, b and dh once for da, db and h.  Where the blocks of da and db share one (f
 // no multiple of 128) the tiles of 128 columns do not hold whole blocks of a row: the row codes
-// come from a launch of their own (131 of 221 us at 16383 x 1376, where the backward by single
-// columns took 439).
+// come from a launch of their own (84 of 174 us at 16383 x 1376).
 cudaError_t launch_bwd8(const Source& s, const Fp8QuantArgs& a, QuantOut o, const QuantOut& oh,
                         cudaStream_t st) {
   const bool whole = s.f % 128 == 0;
