@@ -15,8 +15,8 @@
 // 6.7 TB/s for a copy:
 //   weights 8 x 4096 x 7168 and transposes 6.5 TB/s, 144 us: memory
 //   rows in order, 21,240 x 6656           6.6 TB/s, 64 us: memory
-//   rows 32,768 x 7168 gathered from 4096  4.5 TB/s, 67 us: every row passes L2 eight times, and
-//                                          moving the bytes without any arithmetic took 66 us
+//   rows 32,768 x 7168 gathered from 4096  4.7 TB/s, 63 us: every row passes L2 eight times;
+//                                          instructions
 //   both ways, 16,382 x 2056               4.2 TB/s, 32 us: instructions, and barriers between the
 //                                          two orientations
 //   SwiGLU, rows 65,536 x 768              4.5 TB/s, 57 us: instructions, about 30 a column for an
@@ -431,11 +431,13 @@ __device__ __forceinline__ long long live_rows(const int32_t* offsets, int G, lo
   return n;
 }
 
-// 16 bytes global -> shared, asynchronously; zeros where !ok (nothing is read)
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
-               "r"(ok ? 16 : 0)
+// 16 bytes global -> shared, asynchronously, of which the first n are read and the rest zeros
+__device__ __forceinline__ void cp_async_n(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool ok) {
+  cp_async_n(smem_u32(dst), src, ok ? 16 : 0);
 }
 
 // a box of 128 bytes x 128 rows, shared -> global (parts past the map's rows are not written)
@@ -558,7 +560,7 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
 // Plain rows on 16 bytes: a lane's pieces come through a ring in shared memory that it alone writes
 // (cp.async) and reads, so that two spans of 1024 columns are under way while one is worked on,
 // with nothing to wait for but the lane's own copies.  (Loaded into registers, as above: 77 us
-// instead of 67 for 32,768 gathered rows of 7168, 69 instead of 64 for 21,240 rows of 6656 in
+// instead of 63 for 32,768 gathered rows of 7168, 69 instead of 64 for 21,240 rows of 6656 in
 // order.  The SwiGLU, with two inputs to a column and bound by its instructions, is 10% slower
 // this way.)  A grid of four waves: the rows are spread evenly.
 constexpr int FR_STAGES = 3;
@@ -571,7 +573,8 @@ fp8_rows_ring_kernel(const Source src, const int32_t* __restrict__ src_tok, long
                      const QuantOut out, int* err) {
   griddep_wait();   // see common.cuh: dependent launches
   extern __shared__ uint4 dyn[];   // [FR_STAGES][4][FQ_THREADS]
-  uint4* mine = dyn + threadIdx.x;
+  const uint4* mine = dyn + threadIdx.x;
+  const uint32_t mine_addr = smem_u32(mine);
   const int lane = threadIdx.x & 31;
   const long long gw = (static_cast<long long>(blockIdx.x) * FQ_THREADS + threadIdx.x) >> 5;
   const long long nw = (static_cast<long long>(gridDim.x) * FQ_THREADS) >> 5;
@@ -587,10 +590,17 @@ fp8_rows_ring_kernel(const Source src, const int32_t* __restrict__ src_tok, long
     if (fp < n_rows) {
       const bool ok = !src_tok || (ft >= 0 && ft < src_rows);
       const __nv_bfloat16* row = src.x + (ok ? ft : 0) * src.ld + fc + 8 * lane;
+      const uint32_t dst = mine_addr + f_stage * (4 * FQ_THREADS * 16);
+      if (fc + 1024 <= src.cols) {   // the whole span: constant distances
+        const int n = ok ? 16 : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool in = ok && fc + 256 * i + 8 * lane < src.cols;
-        cp_async16(mine + (f_stage * 4 + i) * FQ_THREADS, in ? row + 256 * i : src.x, in);
+        for (int i = 0; i < 4; ++i) cp_async_n(dst + i * (FQ_THREADS * 16), row + 256 * i, n);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = ok && fc + 256 * i + 8 * lane < src.cols;
+          cp_async_n(dst + i * (FQ_THREADS * 16), in ? row + 256 * i : src.x, in ? 16 : 0);
+        }
       }
       if (++f_stage == FR_STAGES) f_stage = 0;
       fc += 1024;
@@ -625,11 +635,17 @@ fp8_rows_ring_kernel(const Source src, const int32_t* __restrict__ src_tok, long
       fetch();   // to where the span before this one was
       if (!live) continue;
       const int c = c0 + 8 * lane;
+      uint8_t* to = out.codes + p * out.ld + c;
+      if (c0 + 1024 <= src.cols) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (c + 256 * i < src.cols)
-          __stcs(reinterpret_cast<uint2*>(out.codes + p * out.ld + c + 256 * i),
-                 codes8(v[i], r[i]));
+        for (int i = 0; i < 4; ++i)
+          __stcs(reinterpret_cast<uint2*>(to + 256 * i), codes8(v[i], r[i]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + 256 * i < src.cols)
+            __stcs(reinterpret_cast<uint2*>(to + 256 * i), codes8(v[i], r[i]));
+      }
       const int sb = scale_of_lane(lane);
       const int cs = c0 + 256 * sb + 8 * (lane & 16);   // its block's first column
       if (sb >= 0 && cs < src.cols) out.scales[p * out.kb + (cs >> 7)] = quot;
