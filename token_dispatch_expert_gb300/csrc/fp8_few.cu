@@ -433,13 +433,17 @@ cudaError_t fw_launch(const CUtensorMap& tw, const CUtensorMap& tt, const FwPara
 
 }  // namespace
 
-// Up to 16 rows in all, or 8 to the average segment, which leaves uneven segments room in their
-// 16-row tile.  One row to each of eight experts of 4096 x 7168 takes 47 us here and 57 us in
-// fp8_gemm's kernel; 8 or 16 rows to each of 128 experts of 1536 x 2048 85 and 87 us here, 91 and
-// 94 us there; with 24 rows, two tiles to each, 99 us here and 97 us there, with 64 rows 181 and
-// 95 us.  (A 64-row tile was never the best.)
+// Up to 16 rows in all; up to 64, or 2 to the average segment, if there are no more than 8 to it.
+// One row to each of eight experts of 4096 x 7168 takes 47 us here and 57 us in fp8_gemm's kernel;
+// 4 rows to each of 128 experts of 1536 x 2048 85 us here and 91 us there, to each of 256 of 512 x
+// 1024 40 and 46 us, 8 rows to each of 8 of 2048 x 4096 23 and 31 us.  With 16 rows to each the two
+// are even, and with 64, four tiles, 181 us here and 95 us there.  The host does not see the
+// segments: where one of 128 has half of 1024 rows, 76 us here and 73 us there, and all 2048 rows
+// in one of 256 of 4096 x 7168 389 and 61 us, hence the lower bound for many rows.
 bool fp8_few_rows(const Fp8GemmArgs& a) {
-  return !a.wgrad && (a.rows <= 16 || a.rows <= 8 * static_cast<int64_t>(a.G));
+  const int64_t G = a.G;
+  return !a.wgrad &&
+         (a.rows <= 16 || (a.rows <= 8 * G && a.rows <= (2 * G > 64 ? 2 * G : 64)));
 }
 
 cudaError_t launch_fp8_few(const Fp8GemmArgs& a, cudaStream_t st) {
