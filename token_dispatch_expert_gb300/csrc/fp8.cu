@@ -680,7 +680,9 @@ fp8_swiglu_rows_kernel(const Source src, const int32_t* __restrict__ offsets, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       at[i] = row;
-      col[i] = row < n_rows ? 256 * ch + 8 * lane : src.f;
+      // past the last row: past every width by more than a block, so that no code and no scale of
+      // it is stored
+      col[i] = row < n_rows ? 256 * ch + 8 * lane : 1 << 28;
       a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
       if (col[i] < src.f) {
         const __nv_bfloat16* x = src.x + static_cast<long long>(row) * (2 * src.f) + col[i];
@@ -700,7 +702,9 @@ fp8_swiglu_rows_kernel(const Source src, const int32_t* __restrict__ offsets, in
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (col[i] < src.f)
-        __stcs(reinterpret_cast<uint2*>(out.codes + static_cast<long long>(at[i]) * out.ld + col[i]), codes8(v[i], r[i]));
+        __stcs(reinterpret_cast<uint2*>(out.codes + static_cast<long long>(at[i]) * out.ld +
+                                        col[i]),
+               codes8(v[i], r[i]));
     const int sb = scale_of_lane(lane);
     const uint32_t p = sb == 1 ? at[1] : sb == 2 ? at[2] : sb == 3 ? at[3] : at[0];
     const int c =
