@@ -167,11 +167,7 @@ def test_weights(G, N, K):
             x.bytes()
 
 
-@pytest.mark.parametrize("fp32", [False, True])
-@pytest.mark.parametrize("lengths,dead,N,K", [
-    ([3], 2, 130, 200), ([5, 0, 9], 1, 64, 300), ([70, 0, 131], 6, 257, 136),   # few rows; tiles
-    ([1600], 40, 264, 128)])                                                    # pairs
-def test_product(lengths, dead, N, K, fp32):
+def product_inside(lengths, dead, N, K, fp32, ld, col=0):
     off, G = offsets_of(lengths), len(lengths)
     live, rows = off[-1], off[-1] + dead
     KB, NB, dt = -(-K // 128), -(-N // 128), torch.float32 if fp32 else torch.bfloat16
@@ -180,18 +176,36 @@ def test_product(lengths, dead, N, K, fp32):
     ws = ws_new()
     a, b = to_codes(av, up(K, 16)), to_codes(bv, up(K, 16))
     A = av * ref.spread(sa.astype(np.float64), K, 1)
-    for ld in (N, N + 1):
-        out = Guarded((rows, ld), dt)
-        tde.moe_fp8_gemm(a, dev(sa), b, dev(sb), out.t[:, :N], K, offsets=odev(off), ws=ws)
-        got = f64(out.t)[:live, :N]
-        for g in range(G):
-            r = slice(off[g], off[g + 1])
-            B = bv[g] * ref.spread(ref.spread(sb[g].astype(np.float64), N, 0), K, 1)
-            check_product(got[r], A[r] @ B.T, np.abs(A[r]) @ np.abs(B).T, KB, fp32, f"ld {ld}")
-        raw = out.bytes()
-        untouched(raw[live:], "out")
-        untouched(raw[:, N * dt.itemsize:], "out")
+    out = Guarded((rows, ld), dt)
+    tde.moe_fp8_gemm(a, dev(sa), b, dev(sb), out.t[:, col:col + N], K, offsets=odev(off), ws=ws)
+    got = f64(out.t[:live, col:col + N])
+    for g in range(G):
+        r = slice(off[g], off[g + 1])
+        B = bv[g] * ref.spread(ref.spread(sb[g].astype(np.float64), N, 0), K, 1)
+        check_product(got[r], A[r] @ B.T, np.abs(A[r]) @ np.abs(B).T, KB, fp32, f"ld {ld}")
+    raw = out.bytes()
+    untouched(raw[live:], "out")
+    untouched(raw[:, :col * dt.itemsize], "out")
+    untouched(raw[:, (col + N) * dt.itemsize:], "out")
     assert tde.moe_status(ws)[1] == 0
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("lengths,dead,N,K", [
+    ([3], 2, 130, 200), ([5, 0, 9], 1, 64, 300), ([70, 0, 131], 6, 257, 136),   # few rows; tiles
+    ([1600], 40, 264, 128)])                                                    # pairs
+def test_product(lengths, dead, N, K, fp32):
+    for ld in (N, N + 1):
+        product_inside(lengths, dead, N, K, fp32, ld)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("N", [1, 63, 65, 130, 250, 257, 321])
+@pytest.mark.parametrize("lengths", [[70, 0, 131], [1600], [9]])
+def test_product_inside_rows_on_16_bytes(lengths, N, fp32):
+    """Columns off 16 bytes of an output whose rows lie on them: the next columns stay as they are."""
+    for ld, col in ((up(N, 8), 0), (up(N, 8) + 24, 8)):
+        product_inside(lengths, 3, N, 200, fp32, ld, col)
 
 
 @pytest.mark.parametrize("fp32", [False, True])

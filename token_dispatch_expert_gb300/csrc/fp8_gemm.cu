@@ -24,8 +24,9 @@
 // Tiles are 256 x 256 on a CTA pair (cta_group::2, each CTA holding 128 rows of A and of B, which
 // halves the operand bytes per multiply-add) or 128 x 256 on one CTA, where a pair's second half
 // would mostly be padding.  A finished tile leaves through shared memory, one 32 x 128-byte box
-// per warp, by TMA stores that overlap the next tile; boxes that a segment's end cuts, and
-// outputs whose rows TMA cannot address, are copied row by row from the same box.
+// per warp, by TMA stores that overlap the next tile; boxes that a segment's end cuts, or a
+// row's end off 16 bytes, and outputs whose rows TMA cannot address, are copied row by row from the
+// same box.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -99,6 +100,7 @@ struct FgParams {
   void* out;
   long long ldo;
   int tma_out;                  // the output map is usable
+  int tma_edge;                 // and may clip a row's end: N lies on 16 bytes
   int* err;
 };
 
@@ -546,10 +548,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       if (!ok || nr == 0 || n0 >= p.N) continue;
       // through the box, 128 bytes of a row at a time
       constexpr int BOX_COLS = F32 ? 32 : 64;
-      const bool by_tma = p.tma_out && (WG || nr == 32);
 #pragma unroll
       for (int part = 0; part < 128 / BOX_COLS; ++part) {
         const int n = n0 + BOX_COLS * part;
+        // a TMA store clips a row's end at 16 bytes only: where N lies off them, the last box
+        // would write up to 14 bytes of a wider output's next columns
+        const bool by_tma =
+            p.tma_out && (WG || nr == 32) && (p.tma_edge || n + BOX_COLS <= p.N);
         uint8_t* box = my_boxes + part % FG_BOXES * FG_BOX_BYTES;
         const uint32_t box_row = smem_u32(box) + lane * 128;
         if (lane == 0) bulk_wait_group_read<FG_BOXES - 1>();   // the store before last has read it
@@ -707,6 +712,7 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
                            static_cast<uint64_t>(a.ldo), static_cast<uint64_t>(a.rows), 1);
   }
   if (!ok) return cudaErrorInvalidValue;
+  p.tma_edge = a.N % (a.out_fp32 ? 4 : 8) == 0;
   if (!p.tma_out) tc = ta;   // a valid map that no store uses
   auto go = [&](auto wg, auto f32) {
     return pair ? fg_launch<decltype(wg)::value, decltype(f32)::value, 2>(ta, tb, tc, p, st)
