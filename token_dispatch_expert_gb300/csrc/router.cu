@@ -388,8 +388,9 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
       __syncwarp();
       float margin;
       const uint32_t mask = choose_groups(group_worth(s_val, p, lane), p, lane, margin);
-      // two keys a group and the rounding of their sum, on both sides; NaN: -inf on both
-      if (scored && margin <= 5.0f * tol) redo = true;
+      // On either side two keys, tol each, and the rounding of their sum, of up to twice the largest
+      // key: 2 * 2^-24 big, at most 2 tol.  NaN: -inf on both.
+      if (scored && margin <= 8.0f * tol) redo = true;
 #pragma unroll
       for (int s = 0; s < VPL; ++s)
         if (lane + 32 * s < E && !((mask >> group_of(p, lane + 32 * s)) & 1u)) keys.key[s] = 0u;
