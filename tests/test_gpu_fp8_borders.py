@@ -149,6 +149,31 @@ def test_gathered_rows(form):
     assert tde.moe_status(ws)[1] == 0
 
 
+@pytest.mark.parametrize("C", [264, 262, 263, 8])
+def test_a_bad_source_row_is_skipped_along_the_row_and_read_as_row_0_along_the_tokens(C):
+    """The same codes and scales from each form, whichever outputs are asked for together."""
+    T, n, bad = 40, 151, [0, 31, 32, 77, 90, 150]
+    off = offsets_of([90, 0, 61])
+    x, ws = normal((T, C), 4), ws_new()
+    src = np.random.default_rng(0).integers(1, T, n).astype(np.int32)
+    src[bad] = [T, -1, 2 ** 30, -2 ** 31, T, -5]
+    good = np.setdiff1d(np.arange(n), bad)
+    v = f64(x)[np.where((src < 0) | (src >= T), 0, src)]
+    for form in FORMS:
+        r = Outputs(n, 3, C, *form)
+        tde.moe_fp8_quantize(x, *r.args(), offsets=odev(off), src_tok=dev(src), ws=ws)
+        assert tde.moe_status(ws)[1] == tde.DEVERR["BAD_INDEX"]
+        if r.row:
+            q, s = ref.quantise_rows(v)
+            same(f64(r.row[0].t[good, :C]), q[good], "codes")
+            same(f64(r.row[1].t[good]), s[good], "scales")
+            untouched(r.row[0].bytes()[bad], "codes of a bad row")
+            untouched(r.row[1].bytes()[bad], "scales of a bad row")
+        if r.tok:
+            r.row = None
+            r.check(v, off, False, "tokens")
+
+
 @pytest.mark.parametrize("G,N,K", [(1, 1, 1), (2, 130, 100), (3, 17, 257), (1, 300, 128)])
 def test_weights(G, N, K):
     w = normal((G, N, K), N + K, 0.02)

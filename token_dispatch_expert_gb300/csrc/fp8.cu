@@ -896,6 +896,7 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
     const TileAt t = walk.at(blocks);
     const int r = tid >> 4, c = t.c0 + 8 * (tid & 15);
     uint4 v[4];
+    uint32_t bad = 0u;   // bit u: the row's source is none (read as row 0, and no row codes)
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       v[u] = make_uint4(0u, 0u, 0u, 0u);
@@ -906,6 +907,7 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
           if (row < 0 || row >= src_rows) {
             flag_error(err, MOE_DEVERR_BAD_INDEX);
             row = 0;
+            bad |= 1u << u;
           }
         }
         v[u] = value8<SRC, W>(src, row, c);
@@ -915,7 +917,9 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
 #pragma unroll
     for (int u = 0; u < 4; ++u) tile[(r + 32 * u) * 16 + (tid & 15)] = v[u];
     if (out.codes)
-      tile_rows(v, t, src.cols, out, [&](int u) { return make_int2(r + 32 * u, c); });
+      tile_rows(v, t, src.cols, out, [&](int u) {
+        return make_int2((bad >> u) & 1u ? 128 : r + 32 * u, c);
+      });
     __syncthreads();
     Columns<8> cols;
     cols.read(tile, tid, s_max);
@@ -984,7 +988,8 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
         const __nv_bfloat16* a = src.x + static_cast<long long>(row) * (2 * src.f) + cc;
         cp_async16(dst + at, a, in);
         cp_async16(dst + FT_TILE + at, a + src.f, in);
-        if constexpr (BWD) cp_async16(dst + 2 * FT_TILE + at, src.dh + static_cast<long long>(row) * src.f + cc, in);
+        if constexpr (BWD)
+          cp_async16(dst + 2 * FT_TILE + at, src.dh + static_cast<long long>(row) * src.f + cc, in);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -1042,8 +1047,24 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
         else v[u] = r + 32 * u < t.nr && c < width ? silu_mul8(at[0], at[FT_TILE])
                                                    : make_uint4(0u, 0u, 0u, 0u);
       }
-      if (out.codes)
-        tile_rows(v, t, src.cols, out, [&](int i) { return make_int2(r + 32 * i, c); });
+      if (out.codes) {
+        if (SRC == SRC_ROWS && src_tok) {
+          // rows without a source (read as row 0) get no row codes; on a path of its own, since the
+          // question costs rows in order 1% on theirs
+          uint32_t bad = 0u;
+#pragma unroll
+          for (int u = 0; u < PER; ++u)
+            if (r + 32 * u < t.nr) {
+              const int row = __ldg(src_tok + t.r0 + r + 32 * u);
+              if (row < 0 || row >= src_rows) bad |= 1u << u;
+            }
+          tile_rows(v, t, src.cols, out, [&](int i) {
+            return make_int2((bad >> i) & 1u ? 128 : r + 32 * i, c);
+          });
+        } else {
+          tile_rows(v, t, src.cols, out, [&](int i) { return make_int2(r + 32 * i, c); });
+        }
+      }
       if (tid == 0) bulk_wait_group_read<0>();   // the last tile's codes have left their buffer
     }
     __syncthreads();
