@@ -179,7 +179,7 @@ def _p(t):
 
 def _s(stream):
     if stream is None:
-        return _current_stream()
+        return _raw_stream() if _raw_stream else _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -207,8 +207,7 @@ def _check(status, where):
         raise MoEError(status, where)
 
 
-def _cfg(cfg):
-    return ctypes.byref(cfg)
+_cfg = ctypes.byref
 
 
 # --------------------------------------------------------------------------- host helpers
@@ -429,24 +428,89 @@ def _typed(t, dtype, name):
     return _p(t)
 
 
+def _buf(t, dtype, n, name):
+    """_p for a buffer of at least n elements of a torch dtype (None: one byte an element): what a
+    kernel takes for int32 or fp32 must not be another type, and all that it writes must be there."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.element_size() != 1 if dtype is None else t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype or 'one byte an element'}, got {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    return _p(t)
+
+
+class _Buffers:
+    """The buffers of one entry point: their names, and their torch dtypes (looked up once)."""
+
+    def __init__(self, *names):
+        self.names = names
+        self.dtypes = None
+
+    def _load(self):
+        import torch
+        i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
+        kind = dict(logits=f32, topk_w=f32, dw=f32, dlogits=f32, dy=bf, yp=bf, dyp=bf,
+                    drop_mask=torch.uint8)
+        t = torch.Tensor
+        self.numel, self.contiguous, self.data_ptr = t.numel, t.is_contiguous, t.data_ptr
+        self.dtypes = [kind.get(n, i32) for n in self.names]
+
+    def __call__(self, tensors, sizes):
+        """_buf for each.  The usual call, tensors of just these types and sizes, is told by
+        comparing lists, which takes less of a small call's time than a call of _buf for each."""
+        if self.dtypes is None:
+            self._load()
+        try:
+            if ([t.dtype for t in tensors] == self.dtypes
+                    and list(map(self.numel, tensors)) == sizes
+                    and all([t.is_cuda for t in tensors])
+                    and all(map(self.contiguous, tensors))):
+                return map(self.data_ptr, tensors)
+        except AttributeError:   # an address among them
+            pass
+        return [_buf(t, None if name == "drop_mask" else dt, n, name)
+                for t, dt, n, name in zip(tensors, self.dtypes, sizes, self.names)]
+
+
+_route_buffers = _Buffers("logits", "topk_idx", "topk_w", "counts", "kept", "offsets", "dest_row",
+                          "src_tok", "src_slot", "drop_mask")
+_route_bwd_buffers = _Buffers("logits", "topk_idx", "dw", "dlogits")
+_combine_dw_buffers = _Buffers("dy", "yp", "topk_w", "dest_row", "dyp", "dw")
+
+
+def _check_bias(bias, E):
+    if bias is not None and not isinstance(bias, int) and bias.numel() < E:
+        raise ValueError(f"bias: expected {E} elements, got {bias.numel()}")
+
+
 def moe_route_groups(cfg, router, logits, topk_idx, topk_w, counts, kept, offsets, dest_row,
                      src_tok, src_slot, drop_mask, ws, stream=None):
-    _check(lib().moe_route_groups(_cfg(cfg), _cfg(router), _typed(logits, "float32", "logits"),
-                                  _p(topk_idx), _p(topk_w), _p(counts), _p(kept), _p(offsets),
-                                  _p(dest_row), _p(src_tok), _p(src_slot), _p(drop_mask), _p(ws),
-                                  _s(stream)), "moe_route_groups")
+    T, E = cfg.T, cfg.E
+    n = T * cfg.k
+    if router.bias:
+        _check_bias(getattr(router, "_keep", None), E)
+    ptrs = _route_buffers((logits, topk_idx, topk_w, counts, kept, offsets, dest_row, src_tok,
+                           src_slot, drop_mask), [T * E, n, n, E, E, E + 1, n, n, n, n])
+    _check(lib().moe_route_groups(_cfg(cfg), _cfg(router), *ptrs, _p(ws), _s(stream)),
+           "moe_route_groups")
 
 
 def moe_route_groups_bwd(cfg, router, logits, topk_idx, dw, dlogits, ws, stream=None):
-    _check(lib().moe_route_groups_bwd(_cfg(cfg), _cfg(router), _typed(logits, "float32", "logits"),
-                                      _p(topk_idx), _typed(dw, "float32", "dw"), _p(dlogits),
-                                      _p(ws), _s(stream)), "moe_route_groups_bwd")
+    T, E = cfg.T, cfg.E
+    n = T * cfg.k
+    # (the bias is not read: the choice is given)
+    ptrs = _route_bwd_buffers((logits, topk_idx, dw, dlogits), [T * E, n, n, T * E])
+    _check(lib().moe_route_groups_bwd(_cfg(cfg), _cfg(router), *ptrs, _p(ws), _s(stream)),
+           "moe_route_groups_bwd")
 
 
 def moe_combine_bwd_dw(cfg, dy, yp, topk_w, dest_row, dyp, dw, ws, stream=None):
-    _check(lib().moe_combine_bwd_dw(_cfg(cfg), _p(dy), _p(yp), _p(topk_w), _p(dest_row), _p(dyp),
-                                    _typed(dw, "float32", "dw"), _p(ws), _s(stream)),
-           "moe_combine_bwd_dw")
+    n = cfg.T * cfg.k
+    # (yp and dyp: as many rows as dest_row names, which the host does not see)
+    ptrs = _combine_dw_buffers((dy, yp, topk_w, dest_row, dyp, dw),
+                               [cfg.T * cfg.d, 0, n, n, 0, n])
+    _check(lib().moe_combine_bwd_dw(_cfg(cfg), *ptrs, _p(ws), _s(stream)), "moe_combine_bwd_dw")
 
 
 # ------------------------------------------------- 8-bit operands, a scale per block of 128
