@@ -9,7 +9,8 @@ The tokens are made in pairs of groups whose true worths differ by a few fp32 st
 import numpy as np
 import pytest
 
-from test_gpu_router import check
+from gpu_util import np_i
+from test_gpu_router import call, check
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,35 @@ def test_uneven_biases_of_several_units(group_top):
     for base in (5.0, 17.0):
         check(l, 8, score="sigmoid", groups=8, top_groups=4, group_top=group_top,
               bias=(base - s).astype(np.float32))
+
+
+def lane_sums(v, E):
+    """fp32 sums of [T, E] as a warp forms them: a lane adds the experts lane + 32 s in ascending
+    order, then the lanes are added in five rounds of pairs."""
+    p = np.zeros((v.shape[0], 256), np.float32)
+    p[:, :E] = v
+    lanes = np.zeros((v.shape[0], 32), np.float32)
+    for s in range(8):
+        lanes = lanes + p[:, 32 * s:32 * s + 32]
+    for o in (16, 8, 4, 2, 1):
+        lanes = lanes + lanes[:, np.arange(32) ^ o]
+    return lanes[:, 0]
+
+
+@pytest.mark.parametrize("E", [64, 256])
+def test_softmax_weights_are_normalised_by_expf(E):
+    """One logit of 0, the others one x: the largest weight is 1 / z, z = 1 + (E - 1) e^x summed in
+    fp32, with e^x off by at most one ulp (expf).  An exponential whose argument is scaled to base 2
+    in fp32 first is off by up to three."""
+    x = np.random.default_rng(E).uniform(-5.5, -2.8, 400).astype(np.float32)
+    l = np.repeat(x[:, None], E, 1)
+    l[np.arange(400), np.arange(400) % E] = 0
+    _, _, _, _, r = call(l, 1, score="softmax", renorm=False)
+    w = np_i(r["topk_w"])[:, 0]
+    near = np.exp(x.astype(np.float64)).astype(np.float32)
+    got = np.zeros(400, bool)
+    for e in (np.nextafter(near, np.float32(0)), near, np.nextafter(near, np.float32(1))):
+        v = np.repeat(e[:, None], E, 1)
+        v[np.arange(400), np.arange(400) % E] = 1
+        got |= w == np.float32(1) / lane_sums(v, E)
+    assert got.all(), np.flatnonzero(~got)

@@ -351,7 +351,8 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
       top = warp_fmax(top);
 #pragma unroll
       for (int s = 0; s < VPL; ++s) {
-        sc[s] = fast_exp(v[s] - top);
+        // without renorm z also divides the weights, as in the gradient: expf
+        sc[s] = p.renorm ? fast_exp(v[s] - top) : expf(v[s] - top);
         z += sc[s];
       }
       z = fmaxf(warp_sum(z), 1e-37f);
