@@ -797,13 +797,16 @@ struct Walk {
 
 constexpr int FT_TILE = 128 * 16;   // 16-byte pieces
 
-// A tile's columns (c0 ..) along the tokens into block kb, by `64 * Q` threads of which this is
-// number `th`: two columns and 128 / Q rows each.  Joined by a barrier of the whole CTA.  The
-// codes go to their places, or to `box`: 128 columns of 128 bytes, 16-byte pieces XOR-swizzled by
-// the column, for a TMA store (a column's 128 codes are one line in memory, and 16 bytes of
-// 32 lines at a time halved the stores' rate).
-template <int Q>
+constexpr int FT_THREADS = 512;
+
+// A tile's columns (c0 ..) along the tokens into block kb, by FT_THREADS threads of which this is
+// number `th`: two columns and 16 rows (one 16-byte piece of codes) each.  Joined by a barrier of the
+// whole CTA.  The codes go to their places, or to `box`: 128 columns of 128 bytes, 16-byte pieces
+// XOR-swizzled by the column, for a TMA store (a column's 128 codes are one line in memory, and 16
+// bytes of 32 lines at a time halved the stores' rate).
 struct Columns {
+  static constexpr int Q = FT_THREADS / 64;
+  static_assert(128 / Q == 16, "a thread's codes are one 16-byte piece");
   uint32_t w[128 / Q];
   uint32_t m;
   __device__ __forceinline__ void read(const uint4* tile, int th, uint32_t (*s_max)[64]) {
@@ -842,11 +845,7 @@ struct Columns {
       const int at = N * q, cc = 2 * cp + j;
       uint8_t* dst = box ? box + cc * 128 + ((at & 112) ^ ((cc & 7) << 4)) + (at & 15)
                          : o.codes_t + (static_cast<long long>(c) * o.kb_cap + kb) * 128 + at;
-      if constexpr (Q == 16) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(code[0], code[1]);
-      } else {
-        *reinterpret_cast<uint4*>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
-      }
+      *reinterpret_cast<uint4*>(dst) = make_uint4(code[0], code[1], code[2], code[3]);
       if (q == 0)
         o.scales_t[static_cast<long long>(kb) * cols + c] = block_quotient(amax, o.pow2, 1);
     }
@@ -876,8 +875,6 @@ __device__ __forceinline__ void tile_rows(const uint4* v, const TileAt& t, int c
 }
 
 // Rows read by one or two elements: any width and alignment.
-constexpr int FT_THREADS = 512;
-
 template <int SRC, int W>
 __global__ void __launch_bounds__(FT_THREADS, 2)
 fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, long long src_rows,
@@ -921,7 +918,7 @@ fp8_tokens_any_kernel(const Source src, const int32_t* __restrict__ src_tok, lon
         return make_int2((bad >> u) & 1u ? 128 : r + 32 * u, c);
       });
     __syncthreads();
-    Columns<8> cols;
+    Columns cols;
     cols.read(tile, tid, s_max);
     __syncthreads();
     cols.write(tid, s_max, t.c0, 0, src.cols, src.cols, t.kb, out, nullptr);
@@ -1080,10 +1077,10 @@ fp8_tokens_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant_
     }
     uint8_t* box = reinterpret_cast<uint8_t*>(tile);
     constexpr int BOX = FT_TILE * 16;   // from one tile's to the next one's
-    Columns<8> cols;
+    Columns cols;
     cols.read(tile, tid, s_max);
     if constexpr (BWD) {
-      Columns<8> cols_b;
+      Columns cols_b;
       cols_b.read(tile + FT_TILE, tid, s_max + 8);
       __syncthreads();
       cols.write(tid, s_max, t.c0, 0, src.f, src.cols, t.kb, out, box);
