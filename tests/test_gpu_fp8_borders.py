@@ -103,6 +103,12 @@ def test_swiglu_rows(f, dead):
     assert tde.moe_status(ws)[1] == 0
 
 
+@pytest.mark.parametrize("f", [776, 896, 1000, 1016, 2040])
+def test_swiglu_rows_of_four_chunks(f):
+    """Widths whose chunks of 256 columns come in fours, the last of them short."""
+    test_swiglu_rows(f, 3)
+
+
 @pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("lengths,dead", [([1], 0), ([2], 2), ([7, 0, 128], 5), ([129, 3, 0, 61], 1),
                                           ([0, 0], 3)])

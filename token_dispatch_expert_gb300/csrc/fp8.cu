@@ -535,6 +535,20 @@ fp8_rows_kernel(const Source src, const int32_t* __restrict__ src_tok, long long
           v[i] = make_uint4(x[0], x[1], x[2], x[3]);
           v[2 + i] = make_uint4(y[0], y[1], y[2], y[3]);
         }
+      } else if constexpr (SRC == SRC_SWIGLU && W == 8) {   // all loads before the arithmetic
+        uint4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          col[i] = c0 + 256 * i + 8 * lane;
+          a[i] = b[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (col[i] < src.cols) {
+            a[i] = load8<8>(src.x + t * 2 * src.f + col[i], 8);
+            b[i] = load8<8>(src.x + t * 2 * src.f + src.f + col[i], 8);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = col[i] < src.cols ? silu_mul8(a[i], b[i]) : a[i];
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -654,10 +668,12 @@ fp8_rows_ring_kernel(const Source src, const int32_t* __restrict__ src_tok, long
   griddep_launch();
 }
 
-// The SwiGLU of widths of 8: a warp takes four chunks of 256 columns at a time, one after another
-// over the rows' ends, so that no width leaves places of four_scales() empty (65,536 rows of 768
-// columns 57 us, in spans of 1024 columns 62; 32,768 rows of 1408 58 and 61; but 16,384 rows of
-// 2048 40 and 38.5).
+// The SwiGLU of widths of 8 whose chunks of 256 columns do not come in fours: a warp takes four
+// chunks at a time, one after another over the rows' ends, so that no place of four_scales() stays
+// empty (65,536 rows of 768 columns 56.4 us, in spans of 1024 columns 61.8; 32,768 rows of 1408 57.4
+// and 60.7).  Where they do, fp8_rows_kernel's spans are the same chunks with less arithmetic
+// (65,536 rows of 2048 133.4 us, here 140.4; 16,384 rows of 2048 37.9 and 39.0; 4096 rows of 1024
+// 7.5 and 8.6; 40,000 rows of 1000 46.3 and 47.4).
 __global__ void __launch_bounds__(FQ_THREADS, 4)
 fp8_swiglu_rows_kernel(const Source src, const int32_t* __restrict__ offsets, int G,
                        long long rows, const QuantOut out, int* err) {
@@ -1220,6 +1236,9 @@ cudaError_t launch_rows(const Source& s, const Fp8QuantArgs& a, const QuantOut& 
     return launch_pdl(fp8_rows_ring_kernel, grid(4 * FR_CTAS), dim3(FQ_THREADS), FR_SMEM, st, 1, s,
                       a.src_tok, a.src_rows, a.offsets, a.G, a.rows, o, a.err);
   } else if constexpr (SRC == SRC_SWIGLU && W == 8) {
+    if ((s.f + 255) / 256 % 4 == 0)   // (see fp8_swiglu_rows_kernel)
+      return launch_pdl(fp8_rows_kernel<SRC, W>, grid(8), dim3(FQ_THREADS), 0, st, 1, s, a.src_tok,
+                        a.src_rows, a.offsets, a.G, a.rows, o, a.err);
     return launch_pdl(fp8_swiglu_rows_kernel, grid(8), dim3(FQ_THREADS), 0, st, 1, s, a.offsets,
                       a.G, a.rows, o, a.err);
   } else {
