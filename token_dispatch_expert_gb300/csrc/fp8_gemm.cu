@@ -100,7 +100,7 @@ struct FgParams {
   void* out;
   long long ldo;
   int tma_out;                  // the output map is usable
-  int tma_edge;                 // and may clip a row's end: N lies on 16 bytes
+  int tma_last;                 // product: the last column at which a box may begin to be stored by it
   int* err;
 };
 
@@ -552,9 +552,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
       for (int part = 0; part < 128 / BOX_COLS; ++part) {
         const int n = n0 + BOX_COLS * part;
         // a TMA store clips a row's end at 16 bytes only: where N lies off them, the last box
-        // would write up to 14 bytes of a wider output's next columns
-        const bool by_tma =
-            p.tma_out && (WG || nr == 32) && (p.tma_edge || n + BOX_COLS <= p.N);
+        // would write up to 14 bytes of a wider output's next columns (tma_last)
+        const bool by_tma = WG ? p.tma_out : nr == 32 && n <= p.tma_last;
         uint8_t* box = my_boxes + part % FG_BOXES * FG_BOX_BYTES;
         const uint32_t box_row = smem_u32(box) + lane * 128;
         if (lane == 0) bulk_wait_group_read<FG_BOXES - 1>();   // the store before last has read it
@@ -712,7 +711,8 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs& a, cudaStream_t st) {
                            static_cast<uint64_t>(a.ldo), static_cast<uint64_t>(a.rows), 1);
   }
   if (!ok) return cudaErrorInvalidValue;
-  p.tma_edge = a.N % (a.out_fp32 ? 4 : 8) == 0;
+  const int edge = a.out_fp32 ? 4 : 8, box_cols = a.out_fp32 ? 32 : 64;
+  p.tma_last = !p.tma_out ? -1 : a.N % edge == 0 ? a.N : a.N - box_cols;
   if (!p.tma_out) tc = ta;   // a valid map that no store uses
   auto go = [&](auto wg, auto f32) {
     return pair ? fg_launch<decltype(wg)::value, decltype(f32)::value, 2>(ta, tb, tc, p, st)
