@@ -247,13 +247,16 @@ fp8_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ 
       }
     }
     griddep_launch();
+    const int s_end = s;
+    const uint32_t ph_end = ph;
     for (int i = 0; i < FW_STAGES && ok; ++i) {   // every copy of this CTA has been consumed
-      if (!fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err)) break;
+      ok = fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err);
       if (++s == FW_STAGES) {
         s = 0;
         ph ^= 1u;
       }
     }
+    if (!ok) fg_drain_copies<FW_STAGES>(ctl->full, s_end, ph_end);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
     int s = 0;

@@ -339,13 +339,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
       }
       griddep_launch();
+      const int s_end = s;
+      const uint32_t ph_end = ph;
       for (int i = 0; i < STAGES && ok; ++i) {   // every copy of this CTA has been consumed
-        if (!fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err)) break;
+        ok = fg_wait(smem_u32(&ctl->empty[s]), ph ^ 1u, abort_flag, p.err);
         if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
         }
       }
+      // (the leader's barriers count both CTAs' bytes, and neither leaves before the other)
+      if (!ok && rank == 0) fg_drain_copies<STAGES>(ctl->full, s_end, ph_end);
     } else if (warp & 1) {
       // -------------------------------------------------------------- MMA issuers (the leader's)
       // warp 1 the tile's left half, warp 3 the right one, so that neither waits for the other's

@@ -17,6 +17,19 @@ __device__ __forceinline__ bool fg_wait(uint32_t bar, uint32_t parity, volatile 
   if (__all_sync(FULL_MASK, mbar_try_wait(bar, parity))) return true;
   return __all_sync(FULL_MASK, mbar_wait_bounded(bar, parity, abort, err, FG_WAIT_BUDGET));
 }
+// After giving up: waits, again with a limit, until the copies issued into a ring of N stages have
+// landed, so that none arrives in the shared memory of a CTA that has left.  `s`, `ph`: the stage that
+// would have been filled next and its parity; the stages before it were filled last with that parity,
+// the others with the opposite one (or never: such a wait returns at once).
+template <int N>
+__device__ __forceinline__ void fg_drain_copies(const uint64_t* full, int s, uint32_t ph) {
+  const long long t0 = clock64();
+#pragma unroll 1
+  for (int j = 0; j < N; ++j)
+    while (!mbar_try_wait(smem_u32(full + j), j < s ? ph : ph ^ 1u) &&
+           clock64() - t0 < FG_WAIT_BUDGET / 4) {
+    }
+}
 // One thread of the warp, in a form that leaves the code around it warp-uniform: the operands of
 // tcgen05.mma and of the TMA copies are uniform registers, and in a branch on the lane's number
 // each of them was moved there first, about 100 cycles per MMA.
