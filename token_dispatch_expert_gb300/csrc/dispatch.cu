@@ -322,7 +322,7 @@ cudaError_t launch_combine_bwd(const void* dy, const void* yp, const float* logi
                                float* dlogits, int* err, cudaStream_t st) {
   const int grid = grid_warps(T);
 #define MOE_COMBINE_BWD(KM)                                                                   \
-  launch_pdl(combine_bwd_kernel<KM, false>, dim3(grid), dim3(THREADS), 0, st, 1,                     \
+  launch_pdl(combine_bwd_kernel<KM, false>, dim3(grid), dim3(THREADS), 0, st, 1,              \
              static_cast<const uint4*>(dy), static_cast<const uint4*>(yp), logits, topk_idx,   \
              topk_w, dest_row, T, E, k, d / 8, gate, scale, rows_cap,                          \
              static_cast<uint4*>(dyp), dlogits, err, static_cast<float*>(nullptr))

@@ -13,15 +13,19 @@
 // By their bytes these kernels belong to memory: a bf16 value is read once (2 bytes) and one byte
 // or, with both orientations, two bytes are written.  What they reach, and what holds them up, at
 // 6.7 TB/s for a copy:
-//   weights 8 x 4096 x 7168 and transposes 6.5 TB/s, 144 us: memory
+//   weights 8 x 4096 x 7168 and transposes 6.5 TB/s, 145 us: memory
 //   rows in order, 21,240 x 6656           6.6 TB/s, 64 us: memory
-//   rows 32,768 x 7168 gathered from 4096  4.7 TB/s, 63 us: every row passes L2 eight times;
+//   rows 32,768 x 7168 gathered from 4096  4.7 TB/s, 64 us: every row passes L2 eight times;
 //                                          instructions
-//   both ways, 16,382 x 2056               4.2 TB/s, 32 us: instructions, and barriers between the
+//   along the tokens alone, 16,382 x 2056  4.4 TB/s, 23 us: as the next
+//   both ways, 16,382 x 2056               4.2 TB/s, 33 us: instructions, and barriers between the
 //                                          two orientations
 //   SwiGLU, rows 65,536 x 768              4.5 TB/s, 57 us: instructions, about 30 a column for an
 //                                          exactly rounded h and its code
-//   its backward, both ways, 16,383 x 1408 2.5 TB/s, 104 us: instructions, about 100 a column for
+//   both ways, 16,383 x 1408               3.0 TB/s, 47 us: instructions
+//   its backward, rows alone, 16,383 x 1408
+//                                          2.8 TB/s, 66 us: instructions
+//   its backward, both ways with h         2.5 TB/s, 102 us: instructions, about 100 a column for
 //                                          three values and five codes
 #include <cuda.h>
 #include <cuda_fp8.h>

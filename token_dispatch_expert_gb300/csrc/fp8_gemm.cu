@@ -17,9 +17,10 @@
 // Measured: 2048 rows by 28672 x 4096 of two experts 177 us, 2.7 PFLOP/s at 1.9 GHz (840 cycles a
 // block); without the additions it takes 153 us, without MMAs 162, without either 124, the rate
 // of the operand loads (53 bytes an SM and cycle from L2).  8192 rows of eight experts 785 us, and
-// 915 us (2.1 PFLOP/s) for as long as the power cap holds the clock down.  65,536 rows over 128
-// experts by 1536 x 2048 222 us, 1.9 PFLOP/s; weight gradients 2048 x 768 of 128 experts 193 us,
-// 3.0 TB/s, where the additions are twice as many and the tiles short (135 us without them).
+// 905 us (2.1 PFLOP/s) for as long as the power cap holds the clock down.  65,536 rows over 128
+// experts by 1536 x 2048 222 us in a short run, 240 us (1.7 PFLOP/s) in a long one; weight gradients
+// 2048 x 768 of 128 experts 194 us, 3.0 TB/s, where the additions are twice as many and the tiles
+// short (135 us without them).
 //
 // Tiles are 256 x 256 on a CTA pair (cta_group::2, each CTA holding 128 rows of A and of B, which
 // halves the operand bytes per multiply-add) or 128 x 256 on one CTA, where a pair's second half
