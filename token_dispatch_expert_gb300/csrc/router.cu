@@ -385,15 +385,15 @@ route_groups_kernel(const RouterParams p, int32_t* __restrict__ topk_idx,
     // 2^-22.  softmax: e^x is off by 2^-22 and |x| 2^-24 of itself, the sum of 256 terms by 13
     // roundings more, the quotient by two: below 2^-19.  Adding the bias rounds once more,
     // relative to the key.
-    const float tol =
-        scored ? (p.sigmoid ? 0x1p-22f : 0x1p-19f) + 0x1p-24f * warp_fmax(big) : 0.0f;
+    const float largest = scored ? warp_fmax(big) : 0.0f;
+    const float tol = scored ? (p.sigmoid ? 0x1p-22f : 0x1p-19f) + 0x1p-24f * largest : 0.0f;
     if (p.G > 1) {
       __syncwarp();
       float margin;
       const uint32_t mask = choose_groups(group_worth(s_val, p, lane), p, lane, margin);
-      // On either side two keys, tol each, and the rounding of their sum, of up to twice the largest
-      // key: 2 * 2^-24 big, at most 2 tol.  NaN: -inf on both.
-      if (scored && margin <= 8.0f * tol) redo = true;
+      // On either side two keys, tol each, and the rounding of their sum, which is at most twice the
+      // largest key: 2 * 2^-24 of that.  NaN: -inf on both.
+      if (scored && margin <= 4.0f * tol + 0x1p-22f * largest) redo = true;
 #pragma unroll
       for (int s = 0; s < VPL; ++s)
         if (lane + 32 * s < E && !((mask >> group_of(p, lane + 32 * s)) & 1u)) keys.key[s] = 0u;
