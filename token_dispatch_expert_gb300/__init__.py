@@ -124,8 +124,10 @@ def lib() -> ctypes.CDLL:
             "moe_grouped_ffn_bwd_mx": ([cfgp] + [P] * 12, I32),
             "moe_layer_bwd_mx": ([cfgp] + [P] * 15, I32),
             "moe_layer_bwd": ([cfgp] + [P] * 16, I32),
-            "moe_route_groups": ([cfgp, ctypes.POINTER(MoERouterC)] + [P] * 12, I32),
-            "moe_route_groups_bwd": ([cfgp, ctypes.POINTER(MoERouterC)] + [P] * 6, I32),
+            # (the structs by address: an int converts faster than a byref, and the binding has
+            # read their fields before)
+            "moe_route_groups": ([P] * 14, I32),
+            "moe_route_groups_bwd": ([P] * 8, I32),
             "moe_combine_bwd_dw": ([cfgp] + [P] * 8, I32),
             "moe_fp8_token_blocks": ([I64, I32], I64),
             "moe_fp8_quantize": ([ctypes.POINTER(_QuantC)] + [P] * 9, I32),
@@ -208,6 +210,7 @@ def _check(status, where):
 
 
 _cfg = ctypes.byref
+_addr = ctypes.addressof
 
 
 # --------------------------------------------------------------------------- host helpers
@@ -492,16 +495,18 @@ def moe_route_groups(cfg, router, logits, topk_idx, topk_w, counts, kept, offset
         _check_bias(getattr(router, "_keep", None), E)
     ptrs = _route_buffers((logits, topk_idx, topk_w, counts, kept, offsets, dest_row, src_tok,
                            src_slot, drop_mask), [T * E, n, n, E, E, E + 1, n, n, n, n])
-    _check(lib().moe_route_groups(_cfg(cfg), _cfg(router), *ptrs, _p(ws), _s(stream)),
+    _check(lib().moe_route_groups(_addr(cfg), _addr(router), *ptrs, _p(ws), _s(stream)),
            "moe_route_groups")
 
 
 def moe_route_groups_bwd(cfg, router, logits, topk_idx, dw, dlogits, ws, stream=None):
     T, E = cfg.T, cfg.E
     n = T * cfg.k
+    if not isinstance(router, MoERouterC):
+        raise TypeError(f"router: expected a MoERouterC, got {type(router).__name__}")
     # (the bias is not read: the choice is given)
     ptrs = _route_bwd_buffers((logits, topk_idx, dw, dlogits), [T * E, n, n, T * E])
-    _check(lib().moe_route_groups_bwd(_cfg(cfg), _cfg(router), *ptrs, _p(ws), _s(stream)),
+    _check(lib().moe_route_groups_bwd(_addr(cfg), _addr(router), *ptrs, _p(ws), _s(stream)),
            "moe_route_groups_bwd")
 
 
