@@ -28,9 +28,9 @@
 // order_assign follow; a single chunk (T <= 32) does their work itself, in one launch.
 // Not bound by bytes: 4 MB of logits for 4096 tokens are 0.6 us of bandwidth.  One token over 256
 // experts takes 3.8 us on the device and 7.7 us with the call, which the host bounds.  4096 tokens
-// take 13.4 to 14.4 us in three launches: about 1640 warp instructions a token on 128 SMs, 67% of their issue
-// slots, then two launches that wait for all chunks of the one before.  The gradient for 8192 tokens
-// of 128 softmax scores takes 5.5 us with the call, most of it the launch.
+// take 13.4 to 14.4 us in three launches: about 1640 warp instructions a token on 128 SMs, 67% of
+// their issue slots, then two launches that wait for all chunks of the one before.  The gradient for
+// 8192 tokens of 128 softmax scores takes 5.5 us with the call, most of it the launch.
 #include "common.cuh"
 #include "internal.h"
 
