@@ -610,6 +610,121 @@ moe_status_t moe_fp8_wgrad(const moe_fp8_wgrad_t *g, const void *a, const float 
                            void *dW, void *ws, void *stream);
 
 /*
+ * ---- Normalisation of rows, and activations held in 8 bits for the backward pass.
+ *
+ * Checkpoint of rows: codes [rows][ld] bytes and fp32 scales [rows][ceil(C/128)], one for each
+ * block of 128 along the row (the last one may be shorter).  With amax the block's largest
+ * magnitude, held at or above 2^-110:
+ *   MOE_CKPT_INT8  scale amax / 127, code = the whole number nearest to v * (127 / amax), ties to
+ *                  even, the product rounded once: a value is off by at most half a scale
+ *   MOE_CKPT_E4M3  scale and code as moe_fp8_quantize's along the row (pow2 = 0), so that the row
+ *                  codes of a product's operand are its checkpoint
+ * with quotients correctly rounded in fp32.  A value is restored as code * scale in fp32, and
+ * rounded once more where it is stored as bf16.  A block that holds a NaN or an infinity restores
+ * as NaN throughout.  ld is a multiple of 16 and at least C; what lies past C is neither written
+ * nor read.
+ *
+ * `live` (device, one int32, 4-byte aligned; NULL: all rows): the number of rows that hold
+ * something, &offsets[E] for the rows of the expert segments.  Rows behind it are neither read nor
+ * written.  A number outside [0, rows] is held to that range and sets MOE_DEVERR_BAD_OFFSETS.
+ * rows < 2^31 - 2^15, C < 2^24.  `ws` as for the 8-bit operands: it holds the error word.
+ */
+typedef enum { MOE_CKPT_INT8 = 0, MOE_CKPT_E4M3 = 1 } moe_ckpt_t;
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind_t;
+
+typedef struct {
+    int64_t rows;
+    int32_t C;            /* columns                                                      */
+    int32_t kind;         /* moe_norm_kind_t                                              */
+    float eps;            /* finite, >= 0; forward only                                   */
+    int32_t x_type;       /* moe_out_t of x, residual and total; of add and dx            */
+    int32_t y_type;       /* of y; of dy                                                  */
+    int32_t p_type;       /* of gamma and beta                                            */
+    int32_t g_type;       /* of dgamma and dbeta                                          */
+    int32_t format;       /* moe_ckpt_t                                                   */
+    int64_t ldx;          /* elements between rows of x, >= C                             */
+    int64_t ld_add;       /* of residual; of add                                          */
+    int64_t ld_y;         /* of y; of dy                                                  */
+    int64_t ld_out;       /* of total; of dx                                              */
+    int64_t ld_codes;     /* bytes between rows of codes                                  */
+} moe_norm_t;
+
+/*
+ * Normalise rows.  v = x, or x + residual (summed in fp32, rounded to x_type); m = mean of v, 0
+ * with MOE_NORM_RMS; rstd = 1 / sqrt(mean of (v - m)^2 + eps):
+ *   y = (v - m) * rstd * gamma + beta        (gamma or beta NULL: 1 or 0; fp32, rounded once)
+ *   total = v (only with residual), mean = m [rows] (not with MOE_NORM_RMS), rstd [rows], and the
+ *   checkpoint of v (codes, scales); each of these may be NULL.
+ * Statistics are fp32: squares of magnitudes above 2^63 overflow.  A constant row with eps = 0 is
+ * NaN.  Rows of x, residual, y and total may be strided and need only their elements' alignment
+ * (off 16 bytes, or with a width off 8, accesses are narrower); gamma, beta, mean, rstd, codes and
+ * scales are dense.  total may be x or residual itself, and y may be x or residual.
+ */
+moe_status_t moe_norm(const moe_norm_t *p, const void *x, const void *residual_or_null,
+                      const void *gamma_or_null, const void *beta_or_null, void *y,
+                      void *total_or_null, float *mean_or_null, float *rstd_or_null,
+                      void *codes_or_null, float *scales_or_null, void *stream);
+
+/* Bytes of moe_norm_bwd's ws: the error word and the partial sums over the rows.  -1 for invalid
+ * or unsupported sizes.  Host-only. */
+int64_t moe_norm_ws_size(int64_t rows, int32_t C);
+
+/*
+ * Gradient of moe_norm.  With xhat = (v - mean) * rstd and G = dy * gamma:
+ *   dx = rstd * (G - mean(G) - xhat * mean(G * xhat)) + add      (no mean(G) with MOE_NORM_RMS)
+ *   dgamma = sum over the rows of dy * xhat, dbeta = sum over the rows of dy
+ * v: rows of x_type at x, or with x_scales their checkpoint, whose codes are at x (ld_codes).  mean
+ * and rstd are moe_norm's, of v itself; mean is NULL with MOE_NORM_RMS.  dx is the gradient of x
+ * and of residual alike; add (NULL: none) is the gradient that reaches v by another way, the
+ * stream's own.  dgamma and dbeta may be NULL; with rows = 0 they are zeros.  Sums over the rows
+ * are fp32, in an order that rows, C and the device alone decide: the same bits every time.  dx may
+ * be add or dy itself.  ws: moe_norm_ws_size bytes; its contents need not be kept.
+ */
+moe_status_t moe_norm_bwd(const moe_norm_t *p, const void *dy, const void *x,
+                          const float *x_scales_or_null, const float *mean, const float *rstd,
+                          const void *gamma_or_null, const void *add_or_null, void *dx,
+                          void *dgamma_or_null, void *dbeta_or_null, void *ws, void *stream);
+
+/* y of moe_norm again, from the checkpoint of v and v's statistics. */
+moe_status_t moe_ckpt_norm(const moe_norm_t *p, const void *codes, const float *scales,
+                           const float *mean, const float *rstd, const void *gamma_or_null,
+                           const void *beta_or_null, void *y, void *stream);
+
+typedef struct {
+    int64_t rows;
+    int32_t C;            /* columns; [a | b]: 2f                                         */
+    int32_t format;       /* moe_ckpt_t                                                   */
+    int32_t x_type;       /* moe_out_t of x (SwiGLU: not used)                            */
+    int64_t ldx;          /* elements between rows of x, >= C (SwiGLU: not used)          */
+    int64_t ld;           /* bytes between rows of codes                                  */
+} moe_ckpt_rows_t;
+
+/* Rows x into their checkpoint, and back. */
+moe_status_t moe_ckpt_save(const moe_ckpt_rows_t *p, const void *x, const int32_t *live_or_null,
+                           void *codes, float *scales, void *ws, void *stream);
+moe_status_t moe_ckpt_load(const moe_ckpt_rows_t *p, const void *codes, const float *scales,
+                           const int32_t *live_or_null, void *x, void *ws, void *stream);
+
+/* From the checkpoint of [a | b] (C = 2f): ab [rows][2f] bf16 and h = silu(a) * b [rows][f] bf16,
+ * h from the fp32 values that the codes stand for.  Either may be NULL.  ab and h are what
+ * moe_grouped_ffn_bwd and its variants read. */
+moe_status_t moe_ckpt_swiglu(const moe_ckpt_rows_t *p, const void *codes, const float *scales,
+                             const int32_t *live_or_null, void *ab_or_null, void *h_or_null,
+                             void *ws, void *stream);
+
+/* Backward of h = silu(a) * b from dh [rows][f] bf16 and the checkpoint of [a | b]:
+ * da = dh b silu'(a), db = dh silu(a) -> dab [rows][2f] bf16, and h (NULL: not wanted). */
+moe_status_t moe_ckpt_swiglu_bwd(const moe_ckpt_rows_t *p, const void *dh, const void *codes,
+                                 const float *scales, const int32_t *live_or_null, void *dab,
+                                 void *h_or_null, void *ws, void *stream);
+
+/* moe_combine_bwd_dw with yp [T*k][d] from its checkpoint. */
+moe_status_t moe_ckpt_combine_bwd(const moe_config_t *cfg, const void *dy, const void *codes,
+                                  int64_t ld, const float *scales, int32_t format,
+                                  const float *topk_w, const int32_t *dest_row, void *dyp,
+                                  float *dw, void *ws, void *stream);
+
+/*
  * Whole forward: route -> permute -> grouped FFN -> (shared expert) -> combine.
  *   logits [T,E] fp32, x [T,d], W1, W2 (W1s, W2s if ffn_shared > 0, else may be NULL)
  *   y [T,d] out.  ctx (moe_workspace_size bytes) receives the saved tensors listed in

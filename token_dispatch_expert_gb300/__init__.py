@@ -28,6 +28,8 @@ __all__ = [
     "MoERouterC", "make_router", "moe_route_groups", "moe_route_groups_bwd", "moe_combine_bwd_dw",
     "FP8_WS_BYTES", "moe_fp8_token_blocks", "moe_fp8_quantize", "moe_fp8_quantize_weights",
     "moe_fp8_swiglu", "moe_fp8_swiglu_bwd", "moe_fp8_gemm", "moe_fp8_wgrad", "Fp8MoELayer",
+    "moe_norm", "moe_norm_ws_size", "moe_norm_bwd", "moe_ckpt_norm", "moe_ckpt_save",
+    "moe_ckpt_load", "moe_ckpt_swiglu", "moe_ckpt_swiglu_bwd", "moe_ckpt_combine_bwd",
     "moe_status", "moe_status_string", "moe_selftest_wait_timeout", "moe_gemm_clock_trace",
     "moe_gemm_clock_read", "ctx_views", "MoELayer", "CTX_FIELDS",
 ]
@@ -75,6 +77,19 @@ class _Fp8GemmC(ctypes.Structure):
 class _Fp8WgradC(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("G", ctypes.c_int32), ("M", ctypes.c_int32),
                 ("N", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
+class _NormC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_type", ctypes.c_int32), ("y_type", ctypes.c_int32),
+                ("p_type", ctypes.c_int32), ("g_type", ctypes.c_int32),
+                ("format", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ld_add", ctypes.c_int64),
+                ("ld_y", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("ld_codes", ctypes.c_int64)]
+
+
+class _CkptC(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("x_type", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ld", ctypes.c_int64)]
 
 
 class MoEError(RuntimeError):
@@ -136,6 +151,15 @@ def lib() -> ctypes.CDLL:
             "moe_fp8_swiglu_bwd": ([ctypes.POINTER(_ActC)] + [P] * 11, I32),
             "moe_fp8_gemm": ([ctypes.POINTER(_Fp8GemmC)] + [P] * 8, I32),
             "moe_fp8_wgrad": ([ctypes.POINTER(_Fp8WgradC)] + [P] * 8, I32),
+            "moe_norm": ([P] * 12, I32),
+            "moe_norm_ws_size": ([I64, I32], I64),
+            "moe_norm_bwd": ([P] * 13, I32),
+            "moe_ckpt_norm": ([P] * 9, I32),
+            "moe_ckpt_save": ([P] * 7, I32),
+            "moe_ckpt_load": ([P] * 7, I32),
+            "moe_ckpt_swiglu": ([P] * 8, I32),
+            "moe_ckpt_swiglu_bwd": ([P] * 9, I32),
+            "moe_ckpt_combine_bwd": ([P, P, P, I64, P, I32, P, P, P, P, P, P], I32),
             "moe_status": ([P, P, ctypes.POINTER(ctypes.c_int32)], I32),
             "moe_gemm_clock_trace": ([I32], I32),
             "moe_gemm_clock_read": ([ctypes.POINTER(ctypes.c_uint64)] * 3, I32),
@@ -677,6 +701,246 @@ def moe_fp8_wgrad(a, a_scales, b, b_scales, dw, *, offsets=None, rows=None, ws, 
                                _typed(b_scales, "float32", "b_scales"),
                                _typed(offsets, "int32", "offsets"), _p(dw), _p(ws), _s(stream)),
            "moe_fp8_wgrad")
+
+
+# --------------------------------------------------- normalisation and 8-bit checkpoints of rows
+NORMS = {"layer": 0, "rms": 1}
+_row_types = {}   # torch dtype -> moe_out_t
+_formats = {}     # torch dtype of the codes -> moe_ckpt_t
+
+
+def _load_row_types():
+    import torch
+    _row_types.update({torch.bfloat16: 0, torch.float32: 1})
+    _formats.update({torch.int8: 0, torch.float8_e4m3fn: 1})
+
+
+def _row_type(t, name):
+    """moe_out_t of a tensor."""
+    if not _row_types:
+        _load_row_types()
+    k = _row_types.get(t.dtype)
+    if k is None:
+        raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
+    return k
+
+
+def _rows(t, name, shape, kind=None):
+    """(pointer, moe_out_t, elements between rows) of a matrix whose rows may be strided; kind: the
+    type that it has to be of."""
+    k = _row_type(t, name)
+    if kind is not None and k != kind:
+        raise ValueError(f"{name}: expected {'float32' if kind else 'bfloat16'}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: expected a matrix with adjacent columns")
+    if not t.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
+    return t.data_ptr(), k, ld if shape[0] > 1 else shape[1]
+
+
+def _vector(t, name, n, dtype="float32"):
+    """_p of n elements of one type."""
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
+    return _typed(t, dtype, name)
+
+
+def _params(C, a, b, names):
+    """(type, pointer, pointer) of two vectors of one type, each of which may be missing."""
+    kind = 0
+    for t, name in ((a, names[0]), (b, names[1])):
+        if t is not None:
+            kind = _row_type(t, name)
+            if t.numel() != C:
+                raise ValueError(f"{name}: expected {C} elements, got {t.numel()}")
+    if a is not None and b is not None and a.dtype is not b.dtype:
+        raise ValueError(f"{names[1]}: expected {a.dtype}, got {b.dtype}")
+    return kind, _p(a), _p(b)
+
+
+def _checkpoint(codes, scales, rows, C):
+    """(format, bytes between rows, pointer, pointer) of a checkpoint of [rows, C]."""
+    if not _formats:
+        _load_row_types()
+    fmt = _formats.get(codes.dtype)
+    if fmt is None:
+        raise ValueError(f"codes: expected int8 or float8_e4m3fn, got {codes.dtype}")
+    ld = codes.shape[-1]
+    _shape("codes", codes, (rows, ld))
+    _shape("scales", scales, (rows, (C + 127) // 128))
+    return fmt, ld, _p(codes), _typed(scales, "float32", "scales")
+
+
+def _live(offsets):
+    """Address of the last of the segments' offsets: the number of live rows."""
+    if offsets is None:
+        return None
+    return _typed(offsets, "int32", "offsets") + 4 * (offsets.numel() - 1)
+
+
+def _kind(kind):
+    k = NORMS.get(kind)
+    if k is None:
+        raise ValueError(f"kind: expected 'layer' or 'rms', got {kind!r}")
+    return k
+
+
+def moe_norm(x, y, gamma=None, beta=None, *, residual=None, total=None, mean=None, rstd=None,
+             codes=None, scales=None, eps=1e-5, kind="layer", stream=None):
+    """y = normalised rows of x (or of x + residual, written to total) times gamma plus beta; mean
+    and rstd [rows] and the 8-bit checkpoint (codes, scales) of what was normalised are for the
+    backward pass.  kind: "layer" or "rms" (no mean).  x, residual and total are of one type, y of
+    its own (bf16 or fp32), rows may be strided."""
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: expected a matrix, got {len(shape)} dimensions")
+    rows, C = shape
+    px, xt, ldx = _rows(x, "x", shape)
+    py, yt, ldy = _rows(y, "y", shape)
+    pr = pt = pc = ps = None
+    ldr = ldt = fmt = ldc = 0
+    if residual is not None:
+        pr, _, ldr = _rows(residual, "residual", shape, xt)
+    if total is not None:
+        pt, _, ldt = _rows(total, "total", shape, xt)
+    if codes is not None:
+        fmt, ldc, pc, ps = _checkpoint(codes, scales, rows, C)
+    elif scales is not None:
+        raise ValueError("scales: given without codes")
+    kt, pg, pb = _params(C, gamma, beta, ("gamma", "beta"))
+    p = _NormC(rows, C, _kind(kind), eps, xt, yt, kt, 0, fmt, ldx, ldr, ldy, ldt, ldc)
+    _check(lib().moe_norm(_addr(p), px, pr, pg, pb, py, pt, _vector(mean, "mean", rows),
+                          _vector(rstd, "rstd", rows), pc, ps, _s(stream)), "moe_norm")
+
+
+def moe_norm_ws_size(rows, C) -> int:
+    """Bytes of the workspace of moe_norm_bwd."""
+    return lib().moe_norm_ws_size(int(rows), int(C))
+
+
+def moe_norm_bwd(dy, x, mean, rstd, dx, dgamma=None, dbeta=None, *, gamma=None, scales=None,
+                 add=None, kind="layer", ws, stream=None):
+    """Gradient of moe_norm: dx (plus add, the gradient that reaches the rows by another way),
+    dgamma and dbeta.  x: the rows that were normalised, or with scales the codes of their
+    checkpoint.  dx and add are of one type (x's, if x is not codes); mean is None for kind="rms"."""
+    shape = dy.shape
+    if len(shape) != 2:
+        raise ValueError(f"dy: expected a matrix, got {len(shape)} dimensions")
+    rows, C = shape
+    py, yt, ldy = _rows(dy, "dy", shape)
+    pd, xt, ldd = _rows(dx, "dx", shape)
+    pa = ps = None
+    lda = ldx = fmt = ldc = 0
+    if scales is None:
+        px, _, ldx = _rows(x, "x", shape, xt)
+    else:
+        fmt, ldc, px, ps = _checkpoint(x, scales, rows, C)
+    if add is not None:
+        pa, _, lda = _rows(add, "add", shape, xt)
+    kt, pg, _ = _params(C, gamma, None, ("gamma", ""))
+    gt, pdg, pdb = _params(C, dgamma, dbeta, ("dgamma", "dbeta"))
+    if (dgamma is not None or dbeta is not None) and not isinstance(ws, int):
+        need = moe_norm_ws_size(rows, C)
+        if ws.numel() * ws.element_size() < need:
+            raise ValueError(f"ws: expected {need} bytes, got {ws.numel() * ws.element_size()}")
+    p = _NormC(rows, C, _kind(kind), 0.0, xt, yt, kt, gt, fmt, ldx, lda, ldy, ldd, ldc)
+    _check(lib().moe_norm_bwd(_addr(p), py, px, ps, _vector(mean, "mean", rows),
+                              _vector(rstd, "rstd", rows), pg, pa, pd, pdg, pdb, _p(ws),
+                              _s(stream)), "moe_norm_bwd")
+
+
+def moe_ckpt_norm(codes, scales, mean, rstd, y, gamma=None, beta=None, *, kind="layer",
+                  stream=None):
+    """moe_norm's y again, from the checkpoint and the statistics of what was normalised."""
+    shape = y.shape
+    if len(shape) != 2:
+        raise ValueError(f"y: expected a matrix, got {len(shape)} dimensions")
+    rows, C = shape
+    py, yt, ldy = _rows(y, "y", shape)
+    fmt, ldc, pc, ps = _checkpoint(codes, scales, rows, C)
+    kt, pg, pb = _params(C, gamma, beta, ("gamma", "beta"))
+    p = _NormC(rows, C, _kind(kind), 0.0, yt, yt, kt, 0, fmt, 0, 0, ldy, 0, ldc)
+    _check(lib().moe_ckpt_norm(_addr(p), pc, ps, _vector(mean, "mean", rows),
+                               _vector(rstd, "rstd", rows), pg, pb, py, _s(stream)),
+           "moe_ckpt_norm")
+
+
+def moe_ckpt_save(x, codes, scales, *, offsets=None, ws, stream=None):
+    """Rows of x (bf16 or fp32) into 8 bits: codes int8 or float8_e4m3fn [rows, ld], scales [rows,
+    ceil(C / 128)].  offsets: the segments' offsets, whose last entry says how many rows are
+    live."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected a matrix, got {x.dim()} dimensions")
+    rows, C = x.shape
+    px, xt, ldx = _rows(x, "x", x.shape)
+    fmt, ld, pc, ps = _checkpoint(codes, scales, rows, C)
+    p = _CkptC(rows, C, fmt, xt, ldx, ld)
+    _check(lib().moe_ckpt_save(_addr(p), px, _live(offsets), pc, ps, _p(ws), _s(stream)),
+           "moe_ckpt_save")
+
+
+def moe_ckpt_load(codes, scales, x, *, offsets=None, ws, stream=None):
+    """The rows x (bf16 or fp32) that a checkpoint stands for."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected a matrix, got {x.dim()} dimensions")
+    rows, C = x.shape
+    px, xt, ldx = _rows(x, "x", x.shape)
+    fmt, ld, pc, ps = _checkpoint(codes, scales, rows, C)
+    p = _CkptC(rows, C, fmt, xt, ldx, ld)
+    _check(lib().moe_ckpt_load(_addr(p), pc, ps, _live(offsets), px, _p(ws), _s(stream)),
+           "moe_ckpt_load")
+
+
+def moe_ckpt_swiglu(codes, scales, ab=None, h=None, *, offsets=None, ws, stream=None):
+    """ab = [a | b] (bf16) and h = silu(a) * b (bf16) from the checkpoint of [a | b]."""
+    if ab is None and h is None:
+        raise ValueError("ab, h: expected at least one of them")
+    rows = codes.shape[0]
+    C = ab.shape[-1] if ab is not None else 2 * h.shape[-1]
+    if C % 2:
+        raise ValueError(f"ab: expected an even number of columns, got {C}")
+    if ab is not None:
+        _shape("ab", ab, (rows, C))
+    if h is not None:
+        _shape("h", h, (rows, C // 2))
+    fmt, ld, pc, ps = _checkpoint(codes, scales, rows, C)
+    p = _CkptC(rows, C, fmt, 0, C, ld)
+    _check(lib().moe_ckpt_swiglu(_addr(p), pc, ps, _live(offsets), _typed(ab, "bfloat16", "ab"),
+                                 _typed(h, "bfloat16", "h"), _p(ws), _s(stream)),
+           "moe_ckpt_swiglu")
+
+
+def moe_ckpt_swiglu_bwd(dh, codes, scales, dab, h=None, *, offsets=None, ws, stream=None):
+    """dab = [da | db] of h = silu(a) * b (bf16), and h, from dh (bf16) and the checkpoint of
+    [a | b]."""
+    if dh.dim() != 2:
+        raise ValueError(f"dh: expected a matrix, got {dh.dim()} dimensions")
+    rows, f = dh.shape
+    _shape("dab", dab, (rows, 2 * f))
+    if h is not None:
+        _shape("h", h, (rows, f))
+    fmt, ld, pc, ps = _checkpoint(codes, scales, rows, 2 * f)
+    p = _CkptC(rows, 2 * f, fmt, 0, 2 * f, ld)
+    _check(lib().moe_ckpt_swiglu_bwd(_addr(p), _typed(dh, "bfloat16", "dh"), pc, ps,
+                                     _live(offsets), _typed(dab, "bfloat16", "dab"),
+                                     _typed(h, "bfloat16", "h"), _p(ws), _s(stream)),
+           "moe_ckpt_swiglu_bwd")
+
+
+_ckpt_combine_buffers = _Buffers("dy", "topk_w", "dest_row", "dyp", "dw")
+
+
+def moe_ckpt_combine_bwd(cfg, dy, codes, scales, topk_w, dest_row, dyp, dw, ws, stream=None):
+    """moe_combine_bwd_dw with the experts' outputs from their checkpoint."""
+    n = cfg.T * cfg.k
+    fmt, ld, pc, ps = _checkpoint(codes, scales, n, cfg.d)
+    pdy, pw, pr, pdyp, pdw = _ckpt_combine_buffers((dy, topk_w, dest_row, dyp, dw),
+                                                   [cfg.T * cfg.d, n, n, n * cfg.d, n])
+    _check(lib().moe_ckpt_combine_bwd(_addr(cfg), pdy, pc, ld, ps, fmt, pw, pr, pdyp, pdw, _p(ws),
+                                      _s(stream)), "moe_ckpt_combine_bwd")
 
 
 def moe_status(ws, stream=None):

@@ -291,4 +291,76 @@ cudaError_t launch_fp8_few(const Fp8GemmArgs& a, cudaStream_t st);
 bool fp8_codes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint64_t rows,
                    uint32_t box_rows);
 
+// ----------------------------------------------------------------- rows: norm.cu, norm_bwd.cu, ckpt.cu
+// n / per for the items of rows of `per` items each, by a multiplication: with m = floor(2^64 /
+// per) + 1 the high half of n m is exact while n * per < 2^64 (here both are far below).
+struct RowDiv {
+  uint64_t m;
+  int per;
+  explicit RowDiv(int per_row)
+      : m(per_row == 1 ? 0 : ~static_cast<uint64_t>(0) / static_cast<uint64_t>(per_row) + 1),
+        per(per_row) {}
+#ifdef __CUDACC__
+  __device__ __forceinline__ int64_t row(int64_t n) const {
+    return per == 1 ? n : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(n), m));
+  }
+#endif
+};
+
+// Rows and what is done with them; types are RowType (rows8.cuh), distances in elements.
+struct NormArgs {
+  const void* x;          // the rows, or their codes
+  const void* add;        // residual, or the stream's gradient; may be null
+  const void* gamma;      // may be null
+  const void* beta;       // may be null
+  void* y;                // y; backward: dy (read)
+  void* out;              // the sum, may be null; backward: dv
+  float* mean;            // may be null
+  float* rstd;            // may be null
+  void* codes;            // may be null
+  float* scales;
+  const float* x_scales;  // of x's codes
+  void* dgamma;           // may be null
+  void* dbeta;            // may be null
+  float* part;            // the rows' sums of the CTAs
+  int64_t rows, ldx, ld_add, ld_y, ld_out, ld_codes;
+  int C, blocks;          // blocks: ceil(C / 128)
+  int kind, format;
+  int src_type;           // of x
+  int x_type;             // of x, add and out (backward from codes: of add and out)
+  int y_type, p_type, g_type;
+  float eps;
+};
+int norm_vector(const NormArgs& a);
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_ckpt_norm(const NormArgs& a, cudaStream_t st);
+// the CTAs whose sums the backward's workspace holds, and the floats of each
+constexpr int NORM_PARTS = 608;
+__host__ __device__ inline int64_t norm_part_floats(int64_t C) { return 2 * ((C + 63) / 64 * 64); }
+cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st);
+
+struct CkptArgs {
+  const void* x;          // rows to save
+  void* codes;
+  float* scales;
+  const void* codes_in;
+  const float* scales_in;
+  void* out;              // restored rows, [a | b], or [da | db]; may be null beside h
+  void* h;                // may be null
+  const void* dh;
+  const int32_t* live;    // rows that are live, on the device; null: all
+  int64_t rows, ldx, ld;
+  int C, blocks, format, x_type;
+  int* err;
+};
+cudaError_t launch_ckpt_save(const CkptArgs& a, cudaStream_t st);
+cudaError_t launch_ckpt_load(const CkptArgs& a, cudaStream_t st);
+// C: columns of [a | b]; dh: null restores [a | b] and h, else [da | db] and h
+cudaError_t launch_ckpt_swiglu(const CkptArgs& a, cudaStream_t st);
+cudaError_t launch_ckpt_combine_bwd(const void* dy, const void* codes, int64_t ld,
+                                    const float* scales, int format, const float* topk_w,
+                                    const int32_t* dest_row, int64_t T, int k, int d,
+                                    int64_t rows_cap, void* dyp, float* dw, int* err,
+                                    cudaStream_t st);
+
 }  // namespace moe

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "rows8.cuh"
 
 using namespace moe;
 
@@ -1122,6 +1123,240 @@ moe_status_t moe_fp8_wgrad(const moe_fp8_wgrad_t* g, const void* a, const float*
   x.out_fp32 = fp32;
   x.err = static_cast<int*>(ws);
   return cuda_status(launch_fp8_gemm(x, static_cast<cudaStream_t>(stream)));
+}
+
+// ------------------------------------------------- normalisation and 8-bit checkpoints of rows
+static bool row_type_ok(int32_t t) { return t == MOE_OUT_BF16 || t == MOE_OUT_FP32; }
+static bool format_ok(int32_t f) { return f == MOE_CKPT_INT8 || f == MOE_CKPT_E4M3; }
+// rows that may be strided: aligned to their elements
+static bool rows_ok(const void* p, int64_t ld, int64_t C, int32_t type) {
+  return p && reinterpret_cast<uintptr_t>(p) % (type == MOE_OUT_FP32 ? 4 : 2) == 0 && ld >= C;
+}
+static bool opt_ok(const void* p) { return !p || aligned16(p); }
+
+// what every call checks of its sizes; rows = 0 passes
+static moe_status_t validate_rows(int64_t rows, int64_t C) {
+  if (rows < 0 || C < 1) return MOE_ERR_INVALID_ARG;
+  return rows >= FP8_MAX_ROWS || C >= FP8_MAX_DIM ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+static moe_status_t validate_norm(const moe_norm_t* p) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  const moe_status_t s = validate_rows(p->rows, p->C);
+  if (s != MOE_OK) return s;
+  if ((p->kind != MOE_NORM_LAYER && p->kind != MOE_NORM_RMS) || !row_type_ok(p->x_type) ||
+      !row_type_ok(p->y_type) || !row_type_ok(p->p_type) || !row_type_ok(p->g_type) ||
+      !format_ok(p->format))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+static NormArgs norm_args(const moe_norm_t* p) {
+  NormArgs a{};
+  a.rows = p->rows;
+  a.ldx = p->ldx;
+  a.ld_add = p->ld_add;
+  a.ld_y = p->ld_y;
+  a.ld_out = p->ld_out;
+  a.ld_codes = p->ld_codes;
+  a.C = p->C;
+  a.blocks = (p->C + 127) / 128;
+  a.kind = p->kind;
+  a.format = p->format;
+  a.src_type = a.x_type = p->x_type;
+  a.y_type = p->y_type;
+  a.p_type = p->p_type;
+  a.g_type = p->g_type;
+  a.eps = p->eps;
+  return a;
+}
+
+moe_status_t moe_norm(const moe_norm_t* p, const void* x, const void* residual, const void* gamma,
+                      const void* beta, void* y, void* total, float* mean, float* rstd, void* codes,
+                      float* scales, void* stream) {
+  const moe_status_t s = validate_norm(p);
+  if (s != MOE_OK) return s;
+  if (!std::isfinite(p->eps) || p->eps < 0.0f) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!rows_ok(x, p->ldx, p->C, p->x_type) || !rows_ok(y, p->ld_y, p->C, p->y_type) ||
+      (residual && !rows_ok(residual, p->ld_add, p->C, p->x_type)) ||
+      (total && (!residual || !rows_ok(total, p->ld_out, p->C, p->x_type))) || !opt_ok(gamma) ||
+      !opt_ok(beta) || !opt_ok(mean) || !opt_ok(rstd) || (mean && p->kind == MOE_NORM_RMS) ||
+      !pair_ok(codes, scales, true) || (codes && !ld_ok(p->ld_codes, p->C)))
+    return MOE_ERR_INVALID_ARG;
+  NormArgs a = norm_args(p);
+  a.x = x;
+  a.add = residual;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.y = y;
+  a.out = total;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.codes = codes;
+  a.scales = scales;
+  return cuda_status(launch_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+int64_t moe_norm_ws_size(int64_t rows, int32_t C) {
+  if (validate_rows(rows, C) != MOE_OK) return -1;
+  const int64_t parts = rows < NORM_PARTS ? rows : NORM_PARTS;
+  return static_cast<int64_t>(WS_HEADER_BYTES) + parts * norm_part_floats(C) * 4;
+}
+
+moe_status_t moe_norm_bwd(const moe_norm_t* p, const void* dy, const void* x, const float* x_scales,
+                          const float* mean, const float* rstd, const void* gamma, const void* add,
+                          void* dx, void* dgamma, void* dbeta, void* ws, void* stream) {
+  const moe_status_t s = validate_norm(p);
+  if (s != MOE_OK) return s;
+  if (!opt_ok(dgamma) || !opt_ok(dbeta)) return MOE_ERR_INVALID_ARG;
+  const bool layer = p->kind == MOE_NORM_LAYER;
+  if (p->rows > 0) {
+    if (!rows_ok(dy, p->ld_y, p->C, p->y_type) || !rows_ok(dx, p->ld_out, p->C, p->x_type) ||
+        (add && !rows_ok(add, p->ld_add, p->C, p->x_type)) || !opt_ok(gamma) || !ptrs_ok(rstd, ws) ||
+        (layer ? !ptrs_ok(mean) : mean != nullptr))
+      return MOE_ERR_INVALID_ARG;
+    if (x_scales ? !ptrs_ok(x, x_scales) || !ld_ok(p->ld_codes, p->C)
+                 : !rows_ok(x, p->ldx, p->C, p->x_type))
+      return MOE_ERR_INVALID_ARG;
+  } else if (!dgamma && !dbeta) {
+    return MOE_OK;
+  }
+  NormArgs a = norm_args(p);
+  a.x = x;
+  if (x_scales) {
+    a.src_type = code_type(p->format);
+    a.ldx = p->ld_codes;
+    a.x_scales = x_scales;
+  }
+  a.y = const_cast<void*>(dy);
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.gamma = gamma;
+  a.add = add;
+  a.out = dx;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.part = ws ? at<float>(ws, WS_HEADER_BYTES) : nullptr;
+  return cuda_status(launch_norm_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_ckpt_norm(const moe_norm_t* p, const void* codes, const float* scales,
+                           const float* mean, const float* rstd, const void* gamma,
+                           const void* beta, void* y, void* stream) {
+  const moe_status_t s = validate_norm(p);
+  if (s != MOE_OK) return s;
+  if (p->rows == 0) return MOE_OK;
+  if (!ptrs_ok(codes, scales, rstd) || !ld_ok(p->ld_codes, p->C) ||
+      (p->kind == MOE_NORM_LAYER ? !ptrs_ok(mean) : mean != nullptr) || !opt_ok(gamma) ||
+      !opt_ok(beta) || !rows_ok(y, p->ld_y, p->C, p->y_type))
+    return MOE_ERR_INVALID_ARG;
+  NormArgs a = norm_args(p);
+  a.x = codes;
+  a.src_type = code_type(p->format);
+  a.ldx = p->ld_codes;
+  a.x_scales = scales;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.gamma = gamma;
+  a.beta = beta;
+  a.y = y;
+  return cuda_status(launch_ckpt_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+static moe_status_t validate_ckpt(const moe_ckpt_rows_t* p, const int32_t* live) {
+  if (!p) return MOE_ERR_INVALID_ARG;
+  const moe_status_t s = validate_rows(p->rows, p->C);
+  if (s != MOE_OK) return s;
+  if (!format_ok(p->format) || !row_type_ok(p->x_type) ||
+      (reinterpret_cast<uintptr_t>(live) & 3u) || !ld_ok(p->ld, p->C))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+static CkptArgs ckpt_args(const moe_ckpt_rows_t* p, const int32_t* live, void* ws) {
+  CkptArgs a{};
+  a.live = live;
+  a.rows = p->rows;
+  a.ldx = p->ldx;
+  a.ld = p->ld;
+  a.C = p->C;
+  a.blocks = (p->C + 127) / 128;
+  a.format = p->format;
+  a.x_type = p->x_type;
+  a.err = static_cast<int*>(ws);
+  return a;
+}
+
+moe_status_t moe_ckpt_save(const moe_ckpt_rows_t* p, const void* x, const int32_t* live, void* codes,
+                           float* scales, void* ws, void* stream) {
+  const moe_status_t s = validate_ckpt(p, live);
+  if (s != MOE_OK || p->rows == 0) return s;
+  if (!rows_ok(x, p->ldx, p->C, p->x_type) || !ptrs_ok(codes, scales, ws))
+    return MOE_ERR_INVALID_ARG;
+  CkptArgs a = ckpt_args(p, live, ws);
+  a.x = x;
+  a.codes = codes;
+  a.scales = scales;
+  return cuda_status(launch_ckpt_save(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_ckpt_load(const moe_ckpt_rows_t* p, const void* codes, const float* scales,
+                           const int32_t* live, void* x, void* ws, void* stream) {
+  const moe_status_t s = validate_ckpt(p, live);
+  if (s != MOE_OK || p->rows == 0) return s;
+  if (!rows_ok(x, p->ldx, p->C, p->x_type) || !ptrs_ok(codes, scales, ws))
+    return MOE_ERR_INVALID_ARG;
+  CkptArgs a = ckpt_args(p, live, ws);
+  a.codes_in = codes;
+  a.scales_in = scales;
+  a.out = x;
+  return cuda_status(launch_ckpt_load(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_ckpt_swiglu(const moe_ckpt_rows_t* p, const void* codes, const float* scales,
+                             const int32_t* live, void* ab, void* h, void* ws, void* stream) {
+  const moe_status_t s = validate_ckpt(p, live);
+  if (s != MOE_OK) return s;
+  if (p->C % 2) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!ptrs_ok(codes, scales, ws) || (!ab && !h) || !opt_ok(ab) || !opt_ok(h))
+    return MOE_ERR_INVALID_ARG;
+  CkptArgs a = ckpt_args(p, live, ws);
+  a.codes_in = codes;
+  a.scales_in = scales;
+  a.out = ab;
+  a.h = h;
+  return cuda_status(launch_ckpt_swiglu(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_ckpt_swiglu_bwd(const moe_ckpt_rows_t* p, const void* dh, const void* codes,
+                                 const float* scales, const int32_t* live, void* dab, void* h,
+                                 void* ws, void* stream) {
+  const moe_status_t s = validate_ckpt(p, live);
+  if (s != MOE_OK) return s;
+  if (p->C % 2) return MOE_ERR_INVALID_ARG;
+  if (p->rows == 0) return MOE_OK;
+  if (!ptrs_ok(dh, codes, scales, dab, ws) || !opt_ok(h)) return MOE_ERR_INVALID_ARG;
+  CkptArgs a = ckpt_args(p, live, ws);
+  a.dh = dh;
+  a.codes_in = codes;
+  a.scales_in = scales;
+  a.out = dab;
+  a.h = h;
+  return cuda_status(launch_ckpt_swiglu(a, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_ckpt_combine_bwd(const moe_config_t* cfg, const void* dy, const void* codes,
+                                  int64_t ld, const float* scales, int32_t format,
+                                  const float* topk_w, const int32_t* dest_row, void* dyp, float* dw,
+                                  void* ws, void* stream) {
+  const moe_status_t s = validate(cfg);
+  if (s != MOE_OK) return s;
+  if (!format_ok(format) || !ld_ok(ld, cfg->d) ||
+      !ptrs_ok(dy, codes, scales, topk_w, dest_row, dyp, dw, ws))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_status(launch_ckpt_combine_bwd(dy, codes, ld, scales, format, topk_w, dest_row, cfg->T,
+                                             cfg->k, cfg->d, cfg->T * cfg->k, dyp, dw,
+                                             static_cast<int*>(ws),
+                                             static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,331 @@
+// norm.cu -- layer norm and root-mean-square norm of rows, their gradient, and the normalised
+// rows again from a row's 8-bit checkpoint.
+//
+//   v = x, or x + residual rounded to the rows' type;  m = mean of v (0 for the RMS norm)
+//   rstd = 1 / sqrt(mean of (v - m)^2 + eps);  xhat = (v - m) rstd;  y = xhat gamma + beta
+//   G = dy gamma;  dv = rstd (G - mean G - xhat mean(G xhat)) + add   (no mean G for the RMS norm)
+//   dgamma = sum over the rows of dy xhat,  dbeta = sum over the rows of dy
+//
+// The statistics take two passes over a row that stays in registers: the mean first, then the
+// squares around it, with the mean of the differences as its correction (which also mends the
+// rounding of the first sum), all in fp32.  By their bytes these kernels belong to memory: 4 bytes
+// an element forward for bf16 rows (9 with a residual and a checkpoint), 6 backward (8 with the
+// stream's gradient).
+#include "rows8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int MAX_WARPS = 16;    // of a row that stays in registers: 16 * 4 chunks of 256 columns
+
+struct Shared {
+  float2 part[2][MAX_WARPS];
+};
+
+// Sums of (a, b) over the warps that share a row: every thread gets them.  `turn` alternates
+// between two buffers, so that one barrier a sum is enough.
+__device__ __forceinline__ float2 row_sum(float a, float b, Shared& sh, int turn, int warp, int nw) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if (nw == 1) return make_float2(a, b);
+  if ((threadIdx.x & 31) == 0) sh.part[turn][warp] = make_float2(a, b);
+  __syncthreads();
+  float sa = 0.0f, sb = 0.0f;
+  for (int i = 0; i < nw; ++i) {   // the same order in every thread
+    const float2 p = sh.part[turn][i];
+    sa += p.x;
+    sb += p.y;
+  }
+  return make_float2(sa, sb);
+}
+
+__device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t ld, int size) {
+  return static_cast<const uint8_t*>(p) + row * ld * size;
+}
+__device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t ld, int size) {
+  return static_cast<uint8_t*>(p) + row * ld * size;
+}
+
+// v of one chunk: x, or the sum with the residual rounded to the rows' type
+template <int V>
+__device__ __forceinline__ void stream_values(float* f, const NormArgs& a, const void* xr,
+                                              const void* rr, int chunk, int lane) {
+  load_values<V>(f, xr, a.x_type, chunk, a.C, lane);
+  if (!rr) return;
+  float g[8];
+  load_values<V>(g, rr, a.x_type, chunk, a.C, lane);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    f[j] += g[j];
+    if (a.x_type == ROW_BF16) f[j] = __bfloat162float(__float2bfloat16_rn(f[j]));
+  }
+}
+
+// xhat gamma + beta of a chunk whose xhat is in f
+template <int V>
+__device__ __forceinline__ void affine_store(float* f, const NormArgs& a, void* yr, int chunk,
+                                             int lane) {
+  float p[8];
+  if (a.gamma) {
+    load_values<V>(p, a.gamma, a.p_type, chunk, a.C, lane);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= p[j];
+  }
+  if (a.beta) {
+    load_values<V>(p, a.beta, a.p_type, chunk, a.C, lane);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] += p[j];
+  }
+  store_values<V>(yr, a.y_type, chunk, a.C, lane, f);
+}
+
+// nw warps share a row, N chunks to a warp; with nw = 1 the CTA's warps have rows of their own.
+template <int V, int N>
+__global__ void __launch_bounds__(32 * MAX_WARPS)
+norm_kernel(const __grid_constant__ NormArgs a, int nw) {
+  griddep_wait();   // see common.cuh: dependent launches
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = nw == 1 ? 0 : warp;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (nw == 1 ? blockDim.x >> 5 : 1);
+  const int xs = row_size(a.x_type);
+  for (int64_t row = nw == 1 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+       row < a.rows; row += step) {
+    const void* xr = row_at(a.x, row, a.ldx, xs);
+    const void* rr = a.add ? row_at(a.add, row, a.ld_add, xs) : nullptr;
+    float f[N][8];
+    int chunk[N];
+    {
+      Raw8 x[N], r[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        chunk[i] = (i * nw + w) * CHUNK;
+        load_raw<V>(x[i], xr, a.x_type, chunk[i], a.C, lane);
+      }
+      if (rr) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) load_raw<V>(r[i], rr, a.x_type, chunk[i], a.C, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        unpack_raw<V>(x[i], a.x_type, f[i]);
+        if (rr) {
+          float g[8];
+          unpack_raw<V>(r[i], a.x_type, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            f[i][j] += g[j];
+            if (a.x_type == ROW_BF16) f[i][j] = __bfloat162float(__float2bfloat16_rn(f[i][j]));
+          }
+        }
+      }
+    }
+    if (a.out) {
+      void* tr = row_at(a.out, row, a.ld_out, xs);
+#pragma unroll
+      for (int i = 0; i < N; ++i) store_values<V>(tr, a.x_type, chunk[i], a.C, lane, f[i]);
+    }
+    float mean = 0.0f;
+    if (a.kind == MOE_NORM_LAYER) {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t += f[i][j];
+        s += t;
+      }
+      mean = row_sum(s, 0.0f, sh, 0, w, nw).x / static_cast<float>(a.C);
+    }
+    float s = 0.0f, q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float t = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = elem_col<V>(chunk[i], lane, j) < a.C ? f[i][j] - mean : 0.0f;
+        t += d;
+        u = fmaf(d, d, u);
+      }
+      s += t;
+      q += u;
+    }
+    const float2 sq = row_sum(s, q, sh, 1, w, nw);
+    const float shift = a.kind == MOE_NORM_LAYER ? sq.x / static_cast<float>(a.C) : 0.0f;
+    const float var = fmaxf(sq.y / static_cast<float>(a.C) - shift * shift, 0.0f);
+    const float rstd = rsqrtf((sq.y != sq.y ? sq.y : var) + a.eps);
+    if (lane == 0 && w == 0) {
+      if (a.mean) a.mean[row] = mean + shift;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if (a.codes)
+      save_chunks<V, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
+                        chunk, a.C, lane, f);
+    void* yr = row_at(a.y, row, a.ld_y, row_size(a.y_type));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] = ((f[i][j] - mean) - shift) * rstd;
+      affine_store<V>(f[i], a, yr, chunk[i], lane);
+    }
+    // with several warps to a row: part[0] of the next row is written only after all have read
+    // part[1] of this one at their next barrier, and part[1] after part[0]'s; the RMS norm sums
+    // through part[1] alone
+    if (nw > 1 && a.kind != MOE_NORM_LAYER) __syncthreads();
+  }
+  griddep_launch();
+}
+
+// Rows of more columns than stay in registers: three passes, the second and third from L2.
+template <int V>
+__global__ void __launch_bounds__(32 * MAX_WARPS)
+norm_wide_kernel(const __grid_constant__ NormArgs a) {
+  griddep_wait();
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  const int xs = row_size(a.x_type);
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const void* xr = row_at(a.x, row, a.ldx, xs);
+    const void* rr = a.add ? row_at(a.add, row, a.ld_add, xs) : nullptr;
+    float f[1][8];
+    float mean = 0.0f, s = 0.0f, q = 0.0f;
+    if (a.kind == MOE_NORM_LAYER) {
+      for (int c = warp * CHUNK; c < a.C; c += nw * CHUNK) {
+        stream_values<V>(f[0], a, xr, rr, c, lane);
+        float t = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t += f[0][j];
+        s += t;
+      }
+      mean = row_sum(s, 0.0f, sh, 0, warp, nw).x / static_cast<float>(a.C);
+      s = 0.0f;
+    }
+    for (int c = warp * CHUNK; c < a.C; c += nw * CHUNK) {
+      stream_values<V>(f[0], a, xr, rr, c, lane);
+      float t = 0.0f, u = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = elem_col<V>(c, lane, j) < a.C ? f[0][j] - mean : 0.0f;
+        t += d;
+        u = fmaf(d, d, u);
+      }
+      s += t;
+      q += u;
+    }
+    const float2 sq = row_sum(s, q, sh, 1, warp, nw);
+    const float shift = a.kind == MOE_NORM_LAYER ? sq.x / static_cast<float>(a.C) : 0.0f;
+    const float var = fmaxf(sq.y / static_cast<float>(a.C) - shift * shift, 0.0f);
+    const float rstd = rsqrtf((sq.y != sq.y ? sq.y : var) + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[row] = mean + shift;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    void* tr = a.out ? row_at(a.out, row, a.ld_out, xs) : nullptr;
+    void* yr = row_at(a.y, row, a.ld_y, row_size(a.y_type));
+    // (a thread writes only elements that it alone reads: the outputs may be the inputs' rows)
+    for (int c = warp * CHUNK; c < a.C; c += nw * CHUNK) {
+      stream_values<V>(f[0], a, xr, rr, c, lane);
+      if (tr) store_values<V>(tr, a.x_type, c, a.C, lane, f[0]);
+      if (a.codes)
+        save_chunks<V, 1>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
+                          &c, a.C, lane, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[0][j] = ((f[0][j] - mean) - shift) * rstd;
+      affine_store<V>(f[0], a, yr, c, lane);
+    }
+    __syncthreads();
+  }
+  griddep_launch();
+}
+
+// Normalised rows from a checkpoint and the statistics: element by element, a warp takes N
+// chunks of 256 columns, going on over the rows' ends.
+template <int V, int N>
+__global__ void __launch_bounds__(256)
+ckpt_norm_kernel(const __grid_constant__ NormArgs a, RowDiv div) {
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t items = a.rows * div.per;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * N;
+  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * N; i0 < items;
+       i0 += step) {
+    int64_t row = div.row(i0);
+    int k = static_cast<int>(i0 - row * div.per);
+    Raw8 raw[N];
+    float sc[N][8 / V], mean[N], rstd[N];
+    int64_t at[N];
+    int chunk[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      at[i] = row;
+      chunk[i] = k * CHUNK;
+      if (i0 + i < items) {
+        load_raw<V>(raw[i], row_at(a.x, row, a.ldx, 1), a.src_type, chunk[i], a.C, lane);
+        load_scales<V>(sc[i], a.x_scales + row * a.blocks, 0, chunk[i], a.C, lane);
+        mean[i] = a.kind == MOE_NORM_LAYER ? a.mean[row] : 0.0f;
+        rstd[i] = a.rstd[row];
+      }
+      if (++k == div.per) { k = 0; ++row; }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i0 + i >= items) break;
+      float f[8];
+      unpack_raw<V>(raw[i], a.src_type, f);
+      scale_values<V>(f, sc[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean[i]) * rstd[i];
+      affine_store<V>(f, a, row_at(a.y, at[i], a.ld_y, row_size(a.y_type)), chunk[i], lane);
+    }
+  }
+  griddep_launch();
+}
+
+
+}  // namespace
+
+// The widest vectors that every row's address, distance and width allow.
+int norm_vector(const NormArgs& a) {
+  const int xs = row_size(a.x_type), ys = row_size(a.y_type);
+  for (int v : {8, 2})
+    if (a.C % v == 0 && rows_fit(a.x, a.ldx, row_size(a.src_type), v) &&
+        rows_fit(a.add, a.ld_add, xs, v) && rows_fit(a.out, a.ld_out, xs, v) &&
+        rows_fit(a.y, a.ld_y, ys, v) && rows_fit(a.codes, a.ld_codes, 1, v))
+      return v;
+  return 1;
+}
+
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
+  const int chunks = (a.C + CHUNK - 1) / CHUNK;
+  const int v = norm_vector(a);
+  const int64_t most = static_cast<int64_t>(1) << 30;
+  if (chunks > 4 * MAX_WARPS) {
+    const dim3 grid(static_cast<unsigned>(a.rows < most ? a.rows : most));
+    if (v == 8) return launch_pdl(norm_wide_kernel<8>, grid, dim3(512), 0, st, 1, a);
+    if (v == 2) return launch_pdl(norm_wide_kernel<2>, grid, dim3(512), 0, st, 1, a);
+    return launch_pdl(norm_wide_kernel<1>, grid, dim3(512), 0, st, 1, a);
+  }
+  const int n = chunks == 1 ? 1 : chunks == 2 ? 2 : 4;
+  const int nw = (chunks + n - 1) / n;
+  const int warps = nw == 1 ? 4 : nw;
+  const int64_t ctas = nw == 1 ? (a.rows + 3) / 4 : a.rows;
+  const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(32 * warps);
+#define MOE_NORM(V, N) launch_pdl(norm_kernel<V, N>, grid, block, 0, st, 1, a, nw)
+#define MOE_NORM_N(V) (n == 1 ? MOE_NORM(V, 1) : n == 2 ? MOE_NORM(V, 2) : MOE_NORM(V, 4))
+  return v == 8 ? MOE_NORM_N(8) : v == 2 ? MOE_NORM_N(2) : MOE_NORM_N(1);
+#undef MOE_NORM_N
+#undef MOE_NORM
+}
+
+cudaError_t launch_ckpt_norm(const NormArgs& a, cudaStream_t st) {
+  const int v = norm_vector(a);
+  const RowDiv div((a.C + CHUNK - 1) / CHUNK);
+  const int64_t items = a.rows * div.per, need = (items + 8 * 2 - 1) / (8 * 2);
+  const int64_t most = static_cast<int64_t>(1) << 30;
+  const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(256);
+  if (v == 8) return launch_pdl(ckpt_norm_kernel<8, 2>, grid, block, 0, st, 1, a, div);
+  if (v == 2) return launch_pdl(ckpt_norm_kernel<2, 2>, grid, block, 0, st, 1, a, div);
+  return launch_pdl(ckpt_norm_kernel<1, 2>, grid, block, 0, st, 1, a, div);
+}
+
+}  // namespace moe

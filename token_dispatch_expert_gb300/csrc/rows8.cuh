@@ -1,0 +1,347 @@
+// rows8.cuh -- how the normalisation and the 8-bit checkpoints read and write rows.
+//
+// A warp takes a row in chunks of 256 columns, eight to a lane, as vectors of V adjacent
+// elements: element j of a lane is column
+//     chunk + (j / V) * 32 V + lane * V + j % V.
+// V = 8 makes 16-byte accesses of bf16 and 8-byte ones of codes; rows off that alignment, or of
+// another width, take V = 2 or 1, whose accesses of a warp are still contiguous.  A block of 128
+// columns is half a chunk: lanes 0-15 or 16-31 with V = 8, elements 0-3 or 4-7 of every lane with
+// V = 2 and 1.  Bytes are kept as they were loaded (Raw8) until they are used, so that the loads
+// of several rows or chunks can be under way together whatever their type; types are arguments,
+// the same for a whole launch, so their branches are uniform.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+constexpr int CHUNK = 256;
+
+// Element types of rows: the public ones, then codes.
+enum RowType : int { ROW_BF16 = MOE_OUT_BF16, ROW_FP32 = MOE_OUT_FP32, ROW_INT8 = 2, ROW_E4M3 = 3 };
+__host__ __device__ inline int code_type(int format) {
+  return format == MOE_CKPT_INT8 ? ROW_INT8 : ROW_E4M3;
+}
+
+struct Raw8 {
+  uint32_t w[8];
+};
+
+template <int V>
+__device__ __forceinline__ int elem_col(int chunk, int lane, int j) {
+  return chunk + (j / V) * 32 * V + lane * V + j % V;
+}
+
+// The bytes of a lane's eight elements of the row at `row`; columns from C on are zeros.
+template <int V>
+__device__ __forceinline__ void load_raw(Raw8& r, const void* row, int type, int chunk, int C,
+                                         int lane) {
+  const uint8_t* p = static_cast<const uint8_t*>(row);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.w[j] = 0;
+  if (V == 8) {
+    const int c = chunk + 8 * lane;
+    if (c >= C) return;
+    if (type == ROW_BF16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 2 * static_cast<int64_t>(c));
+      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else if (type == ROW_FP32) {
+      const uint4* q = reinterpret_cast<const uint4*>(p + 4 * static_cast<int64_t>(c));
+      const uint4 v = q[0], u = q[1];
+      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+      r.w[4] = u.x; r.w[5] = u.y; r.w[6] = u.z; r.w[7] = u.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + c);
+      r.w[0] = v.x; r.w[1] = v.y;
+    }
+  } else if (V == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = elem_col<V>(chunk, lane, 2 * i);
+      if (c >= C) continue;
+      if (type == ROW_BF16) {
+        r.w[i] = *reinterpret_cast<const uint32_t*>(p + 2 * static_cast<int64_t>(c));
+      } else if (type == ROW_FP32) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * static_cast<int64_t>(c));
+        r.w[2 * i] = v.x; r.w[2 * i + 1] = v.y;
+      } else {
+        r.w[i] = *reinterpret_cast<const uint16_t*>(p + c);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = elem_col<V>(chunk, lane, j);
+      if (c >= C) continue;
+      if (type == ROW_BF16) r.w[j] = *reinterpret_cast<const uint16_t*>(p + 2 * static_cast<int64_t>(c));
+      else if (type == ROW_FP32) r.w[j] = *reinterpret_cast<const uint32_t*>(p + 4 * static_cast<int64_t>(c));
+      else r.w[j] = p[c];
+    }
+  }
+}
+
+// Byte i of w as a number: with the sign bit flipped it is a whole number from 0 to 255 above
+// 128, which as the low byte of 2^23 makes 2^23 + code + 128, so that one addition gives the code.
+__device__ __forceinline__ float int8_value(uint32_t flipped, int i) {
+  return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440u | static_cast<uint32_t>(i))) -
+         8388736.0f;
+}
+__device__ __forceinline__ float2 e4m3_values(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu),
+                                                   __NV_E4M3);
+  return __half22float2(__half2(h));
+}
+
+// The values of a lane's eight elements (of codes: the numbers they are, without the scale).
+template <int V>
+__device__ __forceinline__ void unpack_raw(const Raw8& r, int type, float* f) {
+  if (type == ROW_FP32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(r.w[j]);
+  } else if (type == ROW_BF16) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      f[j] = V == 1 ? bf16_lo(r.w[j]) : (j & 1) ? bf16_hi(r.w[j / 2]) : bf16_lo(r.w[j / 2]);
+  } else if (type == ROW_INT8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t w = V == 8 ? r.w[j / 4] : V == 2 ? r.w[j / 2] : r.w[j];
+      f[j] = int8_value(w ^ 0x80808080u, V == 8 ? j % 4 : V == 2 ? j % 2 : 0);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const uint32_t two = V == 8 ? r.w[j / 4] >> (8 * (j % 4))
+                                  : V == 2 ? r.w[j / 2] : r.w[j] | (r.w[j + 1] << 8);
+      const float2 v = e4m3_values(two);
+      f[j] = v.x; f[j + 1] = v.y;
+    }
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_values(float* f, const void* row, int type, int chunk, int C,
+                                            int lane) {
+  Raw8 r;
+  load_raw<V>(r, row, type, chunk, C, lane);
+  unpack_raw<V>(r, type, f);
+}
+
+// Store a lane's eight values, rounded to nearest where the type is bf16.
+template <int V>
+__device__ __forceinline__ void store_values(void* row, int type, int chunk, int C, int lane,
+                                             const float* f) {
+  uint8_t* p = static_cast<uint8_t*>(row);
+  if (V == 8) {
+    const int c = chunk + 8 * lane;
+    if (c >= C) return;
+    if (type == ROW_BF16) {
+      *reinterpret_cast<uint4*>(p + 2 * static_cast<int64_t>(c)) = pack8(f);
+    } else {
+      float4* q = reinterpret_cast<float4*>(p + 4 * static_cast<int64_t>(c));
+      q[0] = make_float4(f[0], f[1], f[2], f[3]);
+      q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+  } else if (V == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = elem_col<V>(chunk, lane, 2 * i);
+      if (c >= C) continue;
+      if (type == ROW_BF16)
+        *reinterpret_cast<uint32_t*>(p + 2 * static_cast<int64_t>(c)) = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+      else
+        *reinterpret_cast<float2*>(p + 4 * static_cast<int64_t>(c)) = make_float2(f[2 * i], f[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = elem_col<V>(chunk, lane, j);
+      if (c >= C) continue;
+      if (type == ROW_BF16)
+        *reinterpret_cast<__nv_bfloat16*>(p + 2 * static_cast<int64_t>(c)) = __float2bfloat16_rn(f[j]);
+      else
+        *reinterpret_cast<float*>(p + 4 * static_cast<int64_t>(c)) = f[j];
+    }
+  }
+}
+
+// Multiply a lane's codes by their blocks' scales.  `first` is the column of the checkpoint's row
+// at which the chunk's column 0 lies (blocks count from the row's start, so a part of a row that
+// does not start at a block's border has blocks that end inside a vector's neighbours, but never
+// inside a vector: V divides `first` and 128).
+template <int V>
+__device__ __forceinline__ void load_scales(float* s, const float* row_scales, int first, int chunk,
+                                            int C, int lane) {
+#pragma unroll
+  for (int i = 0; i < 8 / V; ++i) {
+    const int c = elem_col<V>(chunk, lane, i * V);
+    s[i] = c < C ? row_scales[(first + c) >> 7] : 0.0f;
+  }
+}
+template <int V>
+__device__ __forceinline__ void scale_values(float* f, const float* s) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] *= s[j / V];
+}
+
+// ------------------------------------------------------------------ saving a block
+// s = amax / top, r = top / amax with amax = max(max |v|, 2^-110), each one correctly rounded
+// quotient; int8 codes are the whole number nearest to v * r (ties to even), the product rounded
+// once; E4M3 codes are E4M3(fp32(v * r)), as the quantisers of the products' operands make them.
+constexpr float CKPT_AMAX_FLOOR = 0x1p-110f;
+__device__ __forceinline__ float ckpt_top(int format) {
+  return format == MOE_CKPT_INT8 ? 127.0f : 448.0f;
+}
+// of two magnitudes the larger; a NaN wins
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// The largest magnitudes of a lane's block(s): m[0] for V = 8 (the lane's half), m[0] and m[1]
+// for V = 2 and 1; complete after block_max over the warp.
+template <int V>
+__device__ __forceinline__ void lane_max(const float* f, float* m) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) a = max_nan(a, fabsf(f[4 * h + j]));
+    m[h] = a;
+  }
+  if (V == 8) m[0] = m[1] = max_nan(m[0], m[1]);
+}
+
+// scale and factor of a block
+__device__ __forceinline__ void block_scale(float amax, int format, float& scale, float& factor) {
+  const float top = ckpt_top(format);
+  if (amax < CKPT_AMAX_FLOOR) amax = CKPT_AMAX_FLOOR;
+  scale = __fdiv_rn(amax, top);
+  factor = __fdiv_rn(top, amax);
+}
+
+// The low byte of the result is the code: 1.5 * 2^23 + v * r, rounded once, holds the product's
+// nearest whole number in its low bits (|v * r| < 127.5, so no code passes 127).
+__device__ __forceinline__ uint32_t int8_code(float v, float r) {
+  return __float_as_uint(fmaf(v, r, 12582912.0f));
+}
+__device__ __forceinline__ uint32_t e4m3_code2(float a, float b) {   // a in the low byte
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE,
+                                                        __NV_E4M3));
+}
+
+// Store a lane's eight codes; r: the factor of elements 0-3 and of 4-7.  A factor that is not a
+// positive number (a block with a NaN or an infinity) makes int8 codes of zero, which the block's
+// scale then turns into NaN.
+template <int V>
+__device__ __forceinline__ void store_codes(void* row, int format, int chunk, int C, int lane,
+                                            const float* f, const float* r) {
+  uint8_t* p = static_cast<uint8_t*>(row);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* g = f + 4 * h;
+    if (format == MOE_CKPT_INT8) {
+      const uint32_t lo = __byte_perm(int8_code(g[0], r[h]), int8_code(g[1], r[h]), 0x0040);
+      const uint32_t hi = __byte_perm(int8_code(g[2], r[h]), int8_code(g[3], r[h]), 0x0040);
+      w[h] = r[h] > 0.0f ? __byte_perm(lo, hi, 0x5410) : 0u;
+    } else {
+      w[h] = e4m3_code2(g[0] * r[h], g[1] * r[h]) | (e4m3_code2(g[2] * r[h], g[3] * r[h]) << 16);
+    }
+  }
+  if (V == 8) {
+    const int c = chunk + 8 * lane;
+    if (c < C) *reinterpret_cast<uint2*>(p + c) = make_uint2(w[0], w[1]);
+  } else if (V == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = elem_col<V>(chunk, lane, 2 * i);
+      if (c < C) *reinterpret_cast<uint16_t*>(p + c) = static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2)));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = elem_col<V>(chunk, lane, j);
+      if (c < C) p[c] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
+    }
+  }
+}
+
+// Quantise N chunks that the warp holds (f[i]: the lane's values of chunk[i]; columns from C on
+// are zeros) into a row's codes and scales.  With V = 8 the maxima of four blocks' halves go
+// through one set of shuffles: lanes exchange all but a share of the chunks at each step, so that
+// each lane ends with one block, divides once for it, and the factors are handed back.
+template <int V, int N>
+__device__ __forceinline__ void save_chunks(void* codes, float* scales, int format,
+                                            const int* chunk, int C, int lane,
+                                            const float (*f)[8]) {
+  float m[N][2];
+#pragma unroll
+  for (int i = 0; i < N; ++i) lane_max<V>(f[i], m[i]);
+  if (V == 8) {
+    float sc, fa, r[N];
+    if (N == 4) {
+      const bool b3 = lane & 8, b2 = lane & 4;
+      float a = b3 ? m[2 % N][0] : m[0][0], b = b3 ? m[3 % N][0] : m[1 % N][0];
+      a = max_nan(a, __shfl_xor_sync(FULL_MASK, b3 ? m[0][0] : m[2 % N][0], 8));
+      b = max_nan(b, __shfl_xor_sync(FULL_MASK, b3 ? m[1 % N][0] : m[3 % N][0], 8));
+      float q = b2 ? b : a;
+      q = max_nan(q, __shfl_xor_sync(FULL_MASK, b2 ? a : b, 4));
+      q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, 2));
+      q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, 1));
+      block_scale(q, format, sc, fa);
+      const int mine = (b3 ? 2 : 0) + (b2 ? 1 : 0);
+      const int c = (mine == 0 ? chunk[0] : mine == 1 ? chunk[1 % N]
+                                          : mine == 2 ? chunk[2 % N] : chunk[3 % N]) +
+                    128 * (lane >> 4);
+      if ((lane & 3) == 0 && c < C) scales[c >> 7] = sc;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        r[i] = __shfl_sync(FULL_MASK, fa, (lane & 16) | (i / 2 * 8) | (i % 2 * 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float q = m[i][0];
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, o));
+        block_scale(q, format, sc, r[i]);
+        const int c = chunk[i] + 128 * (lane >> 4);
+        if ((lane & 15) == 0 && c < C) scales[c >> 7] = sc;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float both[2] = {r[i], r[i]};
+      store_codes<V>(codes, format, chunk[i], C, lane, f[i], both);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float r[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float q = m[i][h], sc;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, o));
+        block_scale(q, format, sc, r[h]);
+        const int c = chunk[i] + 128 * h;
+        if (lane == 0 && c < C) scales[c >> 7] = sc;
+      }
+      store_codes<V>(codes, format, chunk[i], C, lane, f[i], r);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host: which V
+// Rows at p, `ld` elements of `size` bytes apart.
+inline bool rows_fit(const void* p, int64_t ld, int size, int v) {
+  const int64_t a = v == 8 ? (size == 1 ? 8 : 16) : static_cast<int64_t>(v) * size;
+  return !p || (reinterpret_cast<uintptr_t>(p) % a == 0 && (ld * size) % a == 0);
+}
+__host__ __device__ inline int row_size(int type) { return type == ROW_BF16 ? 2 : type == ROW_FP32 ? 4 : 1; }
+
+}  // namespace moe
