@@ -4,6 +4,8 @@
 // A checkpoint is one code a value and one fp32 scale for each block of 128 along the row
 // (rows8.cuh).  Everything here is memory's: 3 bytes a value to save bf16 rows or to restore them,
 // 10 a column of the SwiGLU's gradient, 3 a value of the combine's.
+#include <type_traits>
+
 #include "rows8.cuh"
 
 namespace moe {
@@ -22,77 +24,69 @@ __device__ __forceinline__ int64_t live_rows(const CkptArgs& a) {
 }
 
 // Save: a warp takes N chunks of 256 columns, going on over the rows' ends.
-template <int V, int N>
+template <int V, int N, int X, int FORMAT>
 __global__ void __launch_bounds__(THREADS)
 save_kernel(const __grid_constant__ CkptArgs a, RowDiv div) {
   griddep_wait();   // see common.cuh: dependent launches
   const int lane = threadIdx.x & 31;
   const int64_t items = live_rows(a) * div.per;
   const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * N;
-  const int xs = row_size(a.x_type);
+  constexpr int XS = X == ROW_BF16 ? 2 : 4;
   for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N; i0 < items;
        i0 += step) {
     int64_t row = div.row(i0);
     int k = static_cast<int>(i0 - row * div.per);
     Raw8 raw[N];
-    int64_t at[N];
+    void* codes[N];
+    float* scales[N];
     int chunk[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      at[i] = row;
       chunk[i] = i0 + i < items ? k * CHUNK : a.C;   // (a chunk that starts at C has no columns)
-      if (i0 + i < items)
-        load_raw<V>(raw[i], static_cast<const uint8_t*>(a.x) + row * a.ldx * xs, a.x_type, chunk[i],
-                    a.C, lane);
+      load_raw<V>(raw[i], static_cast<const uint8_t*>(a.x) + row * a.ldx * XS, X, chunk[i], a.C, lane);
+      codes[i] = static_cast<uint8_t*>(a.codes) + row * a.ld;
+      scales[i] = a.scales + row * a.blocks;
       if (++k == div.per) { k = 0; ++row; }
     }
+    float f[N][8];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i0 + i >= items) break;
-      float f[1][8];
-      unpack_raw<V>(raw[i], a.x_type, f[0]);
-      save_chunks<V, 1>(static_cast<uint8_t*>(a.codes) + at[i] * a.ld, a.scales + at[i] * a.blocks,
-                        a.format, &chunk[i], a.C, lane, f);
-    }
+    for (int i = 0; i < N; ++i) unpack_raw<V>(raw[i], X, f[i]);
+    save_chunks<V, N>(codes, scales, FORMAT, chunk, a.C, lane, f);
   }
   griddep_launch();
 }
 
-template <int V, int N>
+template <int V, int N, int X, int FORMAT>
 __global__ void __launch_bounds__(THREADS)
 load_kernel(const __grid_constant__ CkptArgs a, RowDiv div) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int64_t items = live_rows(a) * div.per;
   const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * N;
-  const int type = code_type(a.format), xs = row_size(a.x_type);
+  constexpr int XS = X == ROW_BF16 ? 2 : 4, TYPE = FORMAT == MOE_CKPT_INT8 ? ROW_INT8 : ROW_E4M3;
   for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N; i0 < items;
        i0 += step) {
     int64_t row = div.row(i0);
     int k = static_cast<int>(i0 - row * div.per);
     Raw8 raw[N];
     float sc[N][8 / V];
-    int64_t at[N];
+    uint8_t* out[N];
     int chunk[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      at[i] = row;
-      chunk[i] = k * CHUNK;
-      if (i0 + i < items) {
-        load_raw<V>(raw[i], static_cast<const uint8_t*>(a.codes_in) + row * a.ld, type, chunk[i],
-                    a.C, lane);
-        load_scales<V>(sc[i], a.scales_in + row * a.blocks, 0, chunk[i], a.C, lane);
-      }
+      out[i] = static_cast<uint8_t*>(a.out) + row * a.ldx * XS;
+      chunk[i] = i0 + i < items ? k * CHUNK : a.C;
+      load_raw<V>(raw[i], static_cast<const uint8_t*>(a.codes_in) + row * a.ld, TYPE, chunk[i], a.C,
+                  lane);
+      load_scales<V>(sc[i], a.scales_in + row * a.blocks, 0, chunk[i], a.C, lane);
       if (++k == div.per) { k = 0; ++row; }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (i0 + i >= items) break;
       float f[8];
-      unpack_raw<V>(raw[i], type, f);
+      unpack_raw<V>(raw[i], TYPE, f);
       scale_values<V>(f, sc[i]);
-      store_values<V>(static_cast<uint8_t*>(a.out) + at[i] * a.ldx * xs, a.x_type, chunk[i], a.C,
-                      lane, f);
+      store_values<V>(out[i], X, chunk[i], a.C, lane, f);
     }
   }
   griddep_launch();
@@ -101,7 +95,7 @@ load_kernel(const __grid_constant__ CkptArgs a, RowDiv div) {
 // [a | b] and h, or with BACK [da | db] and h from dh: f = C / 2 columns, a warp takes N chunks of
 // 256 of them.  With s = sigma(a): h = a s b, da = dh b s (1 + a (1 - s)), db = dh a s, from the
 // 32-bit restored values, each rounded once.
-template <int V, int N, bool BACK>
+template <int V, int N, bool BACK, int TYPE>
 __global__ void __launch_bounds__(THREADS)
 swiglu_kernel(const __grid_constant__ CkptArgs p, RowDiv div) {
   griddep_wait();
@@ -109,7 +103,6 @@ swiglu_kernel(const __grid_constant__ CkptArgs p, RowDiv div) {
   const int f = p.C / 2;
   const int64_t items = live_rows(p) * div.per;
   const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * N;
-  const int type = code_type(p.format);
   for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N; i0 < items;
        i0 += step) {
     int64_t row = div.row(i0);
@@ -125,8 +118,8 @@ swiglu_kernel(const __grid_constant__ CkptArgs p, RowDiv div) {
       if (i0 + i < items) {
         const uint8_t* codes = static_cast<const uint8_t*>(p.codes_in) + row * p.ld;
         const float* scales = p.scales_in + row * p.blocks;
-        load_raw<V>(ra[i], codes, type, chunk[i], f, lane);
-        load_raw<V>(rb[i], codes + f, type, chunk[i], f, lane);
+        load_raw<V>(ra[i], codes, TYPE, chunk[i], f, lane);
+        load_raw<V>(rb[i], codes + f, TYPE, chunk[i], f, lane);
         if (BACK)
           load_raw<V>(rd[i], static_cast<const __nv_bfloat16*>(p.dh) + row * f, ROW_BF16, chunk[i],
                       f, lane);
@@ -139,8 +132,8 @@ swiglu_kernel(const __grid_constant__ CkptArgs p, RowDiv div) {
     for (int i = 0; i < N; ++i) {
       if (i0 + i >= items) break;
       float a[8], b[8], h[8];
-      unpack_raw<V>(ra[i], type, a);
-      unpack_raw<V>(rb[i], type, b);
+      unpack_raw<V>(ra[i], TYPE, a);
+      unpack_raw<V>(rb[i], TYPE, b);
       scale_values<V>(a, sa[i]);
       scale_values<V>(b, sb[i]);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at[i] * p.C;
@@ -251,6 +244,17 @@ int sm_count() {
   return sms;
 }
 
+// f(the rows' type, the format) as constants
+template <typename F>
+cudaError_t by_types(const CkptArgs& a, F f) {
+  using Bf16 = std::integral_constant<int, ROW_BF16>;
+  using Fp32 = std::integral_constant<int, ROW_FP32>;
+  using Int8 = std::integral_constant<int, MOE_CKPT_INT8>;
+  using E4m3 = std::integral_constant<int, MOE_CKPT_E4M3>;
+  if (a.x_type == ROW_BF16) return a.format == MOE_CKPT_INT8 ? f(Bf16(), Int8()) : f(Bf16(), E4m3());
+  return a.format == MOE_CKPT_INT8 ? f(Fp32(), Int8()) : f(Fp32(), E4m3());
+}
+
 dim3 item_grid(int64_t rows, int per, int n) {
   const int64_t need = (rows * per + WARPS * n - 1) / (WARPS * n);
   const int64_t most = static_cast<int64_t>(1) << 30;
@@ -262,38 +266,52 @@ dim3 item_grid(int64_t rows, int per, int n) {
 cudaError_t launch_ckpt_save(const CkptArgs& a, cudaStream_t st) {
   const RowDiv div((a.C + CHUNK - 1) / CHUNK);
   const int xs = row_size(a.x_type);
-#define MOE_SAVE(V, N) \
-  launch_pdl(save_kernel<V, N>, item_grid(a.rows, div.per, N), dim3(THREADS), 0, st, 1, a, div)
-  if (a.C % 8 == 0 && rows_fit(a.x, a.ldx, xs, 8)) return MOE_SAVE(8, 4);
-  if (a.C % 2 == 0 && rows_fit(a.x, a.ldx, xs, 2)) return MOE_SAVE(2, 2);
-  return MOE_SAVE(1, 2);
-#undef MOE_SAVE
+  auto go = [&](auto kern, int n) {
+    return launch_pdl(kern, item_grid(a.rows, div.per, n), dim3(THREADS), 0, st, 1, a, div);
+  };
+  auto pick = [&](auto x, auto format) {
+    constexpr int X = decltype(x)::value, F = decltype(format)::value;
+    if (a.C % 8 == 0 && rows_fit(a.x, a.ldx, xs, 8)) return go(save_kernel<8, 4, X, F>, 4);
+    if (a.C % 2 == 0 && rows_fit(a.x, a.ldx, xs, 2)) return go(save_kernel<2, 2, X, F>, 2);
+    return go(save_kernel<1, 2, X, F>, 2);
+  };
+  return by_types(a, pick);
 }
 
 cudaError_t launch_ckpt_load(const CkptArgs& a, cudaStream_t st) {
   const RowDiv div((a.C + CHUNK - 1) / CHUNK);
   const int xs = row_size(a.x_type);
-#define MOE_LOAD(V, N) \
-  launch_pdl(load_kernel<V, N>, item_grid(a.rows, div.per, N), dim3(THREADS), 0, st, 1, a, div)
-  if (a.C % 8 == 0 && rows_fit(a.out, a.ldx, xs, 8)) return MOE_LOAD(8, 4);
-  if (a.C % 2 == 0 && rows_fit(a.out, a.ldx, xs, 2)) return MOE_LOAD(2, 2);
-  return MOE_LOAD(1, 2);
-#undef MOE_LOAD
+  auto go = [&](auto kern, int n) {
+    return launch_pdl(kern, item_grid(a.rows, div.per, n), dim3(THREADS), 0, st, 1, a, div);
+  };
+  auto pick = [&](auto x, auto format) {
+    constexpr int X = decltype(x)::value, F = decltype(format)::value;
+    if (a.C % 8 == 0 && rows_fit(a.out, a.ldx, xs, 8)) return go(load_kernel<8, 4, X, F>, 4);
+    if (a.C % 2 == 0 && rows_fit(a.out, a.ldx, xs, 2)) return go(load_kernel<2, 2, X, F>, 2);
+    return go(load_kernel<1, 2, X, F>, 2);
+  };
+  return by_types(a, pick);
 }
 
 cudaError_t launch_ckpt_swiglu(const CkptArgs& a, cudaStream_t st) {
   const int f = a.C / 2;
   const RowDiv div((f + CHUNK - 1) / CHUNK);
-#define MOE_SWIGLU(V, N)                                                                        \
-  (a.dh ? launch_pdl(swiglu_kernel<V, N, true>, item_grid(a.rows, div.per, N), dim3(THREADS), 0, \
-                     st, 1, a, div)                                                              \
-        : launch_pdl(swiglu_kernel<V, N, false>, item_grid(a.rows, div.per, N), dim3(THREADS),   \
-                     0, st, 1, a, div))
-  // (dh, [a | b] and h are dense from 16-byte addresses: the width alone decides)
-  if (f % 8 == 0) return MOE_SWIGLU(8, 2);
-  if (f % 2 == 0) return MOE_SWIGLU(2, 1);
-  return MOE_SWIGLU(1, 1);
-#undef MOE_SWIGLU
+  auto go = [&](auto kern, int n) {
+    return launch_pdl(kern, item_grid(a.rows, div.per, n), dim3(THREADS), 0, st, 1, a, div);
+  };
+  auto pick = [&](auto back, auto format) {
+    constexpr bool B = decltype(back)::value;
+    constexpr int T = decltype(format)::value == MOE_CKPT_INT8 ? ROW_INT8 : ROW_E4M3;
+    // (dh, [a | b] and h are dense from 16-byte addresses: the width alone decides)
+    if (f % 8 == 0) return go(swiglu_kernel<8, 2, B, T>, 2);
+    if (f % 2 == 0) return go(swiglu_kernel<2, 1, B, T>, 1);
+    return go(swiglu_kernel<1, 1, B, T>, 1);
+  };
+  using Int8 = std::integral_constant<int, MOE_CKPT_INT8>;
+  using E4m3 = std::integral_constant<int, MOE_CKPT_E4M3>;
+  if (a.dh)
+    return a.format == MOE_CKPT_INT8 ? pick(std::true_type(), Int8()) : pick(std::true_type(), E4m3());
+  return a.format == MOE_CKPT_INT8 ? pick(std::false_type(), Int8()) : pick(std::false_type(), E4m3());
 }
 
 cudaError_t launch_ckpt_combine_bwd(const void* dy, const void* codes, int64_t ld,

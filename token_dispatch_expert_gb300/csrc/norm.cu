@@ -16,36 +16,6 @@
 namespace moe {
 namespace {
 
-constexpr int MAX_WARPS = 16;    // of a row that stays in registers: 16 * 4 chunks of 256 columns
-
-struct Shared {
-  float2 part[2][MAX_WARPS];
-};
-
-// Sums of (a, b) over the warps that share a row: every thread gets them.  `turn` alternates
-// between two buffers, so that one barrier a sum is enough.
-__device__ __forceinline__ float2 row_sum(float a, float b, Shared& sh, int turn, int warp, int nw) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (nw == 1) return make_float2(a, b);
-  if ((threadIdx.x & 31) == 0) sh.part[turn][warp] = make_float2(a, b);
-  __syncthreads();
-  float sa = 0.0f, sb = 0.0f;
-  for (int i = 0; i < nw; ++i) {   // the same order in every thread
-    const float2 p = sh.part[turn][i];
-    sa += p.x;
-    sb += p.y;
-  }
-  return make_float2(sa, sb);
-}
-
-__device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t ld, int size) {
-  return static_cast<const uint8_t*>(p) + row * ld * size;
-}
-__device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t ld, int size) {
-  return static_cast<uint8_t*>(p) + row * ld * size;
-}
-
 // v of one chunk: x, or the sum with the residual rounded to the rows' type
 template <int V>
 __device__ __forceinline__ void stream_values(float* f, const NormArgs& a, const void* xr,
@@ -84,7 +54,8 @@ template <int V, int N>
 __global__ void __launch_bounds__(32 * MAX_WARPS)
 norm_kernel(const __grid_constant__ NormArgs a, int nw) {
   griddep_wait();   // see common.cuh: dependent launches
-  __shared__ Shared sh;
+  __shared__ RowSums sh;
+  row_sum_init(sh);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int w = nw == 1 ? 0 : warp;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (nw == 1 ? blockDim.x >> 5 : 1);
@@ -135,7 +106,7 @@ norm_kernel(const __grid_constant__ NormArgs a, int nw) {
         for (int j = 0; j < 8; ++j) t += f[i][j];
         s += t;
       }
-      mean = row_sum(s, 0.0f, sh, 0, w, nw).x / static_cast<float>(a.C);
+      mean = row_sum1(s, sh, 0, w, nw) / static_cast<float>(a.C);
     }
     float s = 0.0f, q = 0.0f;
 #pragma unroll
@@ -150,7 +121,7 @@ norm_kernel(const __grid_constant__ NormArgs a, int nw) {
       s += t;
       q += u;
     }
-    const float2 sq = row_sum(s, q, sh, 1, w, nw);
+    const float2 sq = row_sum2(s, q, sh, 1, w, nw);
     const float shift = a.kind == MOE_NORM_LAYER ? sq.x / static_cast<float>(a.C) : 0.0f;
     const float var = fmaxf(sq.y / static_cast<float>(a.C) - shift * shift, 0.0f);
     const float rstd = rsqrtf((sq.y != sq.y ? sq.y : var) + a.eps);
@@ -159,7 +130,7 @@ norm_kernel(const __grid_constant__ NormArgs a, int nw) {
       if (a.rstd) a.rstd[row] = rstd;
     }
     if (a.codes)
-      save_chunks<V, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
+      save_row_chunks<V, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
                         chunk, a.C, lane, f);
     void* yr = row_at(a.y, row, a.ld_y, row_size(a.y_type));
 #pragma unroll
@@ -176,12 +147,150 @@ norm_kernel(const __grid_constant__ NormArgs a, int nw) {
   griddep_launch();
 }
 
+// The same for rows of whole 16-byte vectors, through shared memory: the rows that follow are
+// fetched while one is worked on.  nw warps share a row, N chunks to a warp; slots: 1 (the widest
+// rows: no fetching ahead) to 3.
+template <int N, int X, bool ADD>
+__global__ void __launch_bounds__(32 * MAX_WARPS)
+norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
+  griddep_wait();
+  __shared__ RowSums sh;
+  extern __shared__ __align__(16) uint8_t ring[];
+  row_sum_init(sh);
+  constexpr int XS = X == ROW_BF16 ? 2 : 4, BYTES = CHUNK * XS, PARTS = ADD ? 2 : 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int w = nw == 1 ? 0 : warp;
+  const bool layer = a.kind == MOE_NORM_LAYER;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (nw == 1 ? warps : 1);
+  const int64_t first = nw == 1 ? static_cast<int64_t>(blockIdx.x) * warps + warp : blockIdx.x;
+  uint8_t* const mine = ring + warp * (N * PARTS * BYTES);
+  const int slot_bytes = warps * (N * PARTS * BYTES);
+  int chunk[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    chunk[i] = (i * nw + w) * CHUNK;
+    if (chunk[i] + 8 * lane >= a.C)
+      for (int s = 0; s < slots; ++s)
+#pragma unroll
+        for (int t = 0; t < PARTS; ++t) clear_chunk(mine + s * slot_bytes + (i * PARTS + t) * BYTES, X, lane);
+  }
+  const uint8_t* xr = static_cast<const uint8_t*>(row_at(a.x, first, a.ldx, XS));
+  const uint8_t* rr = ADD ? static_cast<const uint8_t*>(row_at(a.add, first, a.ld_add, XS)) : nullptr;
+  const int64_t x_step = step * a.ldx * XS, r_step = step * a.ld_add * XS;
+  int64_t next = first;
+  auto fetch = [&](int slot) {
+    if (next < a.rows) {
+      uint8_t* to = mine + slot * slot_bytes;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        copy_chunk(to + i * PARTS * BYTES, xr, X, chunk[i], a.C, lane);
+        if (ADD) copy_chunk(to + (i * PARTS + 1) * BYTES, rr, X, chunk[i], a.C, lane);
+      }
+      xr += x_step;
+      if (ADD) rr += r_step;
+      next += step;
+    }
+    copy_commit();
+  };
+  for (int s = 0; s + 1 < slots; ++s) fetch(s);
+  int slot = 0, ahead = slots - 1;
+  const float over = 1.0f / static_cast<float>(a.C);
+  for (int64_t row = first; row < a.rows; row += step) {
+    fetch(ahead);
+    if (++ahead == slots) ahead = 0;
+    copy_wait(slots - 1);
+    const uint8_t* from = mine + slot * slot_bytes;
+    if (++slot == slots) slot = 0;
+    float2 f[N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      slot_values(f[i], from + i * PARTS * BYTES, X, lane);
+      if (ADD) {
+        float2 r[4];
+        slot_values(r, from + (i * PARTS + 1) * BYTES, X, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[i][j] = __fadd2_rn(f[i][j], r[j]);
+          if (X == ROW_BF16) {
+            const uint32_t u = pack_bf16x2(f[i][j].x, f[i][j].y);
+            f[i][j] = make_float2(bf16_lo(u), bf16_hi(u));
+          }
+        }
+      }
+    }
+    if (ADD && a.out) {
+      void* tr = row_at(a.out, row, a.ld_out, XS);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = chunk[i] + 8 * lane;
+        if (c < a.C) store_pairs(tr, X, c, f[i]);
+      }
+    }
+    float mean = 0.0f;
+    if (layer) {
+      float2 s = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        s = __fadd2_rn(s, __fadd2_rn(__fadd2_rn(f[i][0], f[i][1]), __fadd2_rn(f[i][2], f[i][3])));
+      // (a quotient, not a product: exact for a constant row)
+      mean = row_sum1(s.x + s.y, sh, 0, w, nw) / static_cast<float>(a.C);
+    }
+    // (columns past the row's end must not count as differences from the mean)
+    float2 s = both(0.0f), q = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (chunk[i] + 8 * lane < a.C) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 d = __fadd2_rn(f[i][j], both(-mean));
+          s = __fadd2_rn(s, d);
+          q = __ffma2_rn(d, d, q);
+        }
+      }
+    const float2 sq = row_sum2(s.x + s.y, q.x + q.y, sh, 1, w, nw);
+    const float shift = layer ? sq.x * over : 0.0f;
+    const float var = fmaxf(sq.y * over - shift * shift, 0.0f);
+    const float rstd = rsqrtf((sq.y != sq.y ? sq.y : var) + a.eps);
+    if (lane == 0 && w == 0) {
+      if (a.mean) a.mean[row] = mean + shift;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+    if (a.codes)
+      save_row_chunks<8, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
+                            chunk, a.C, lane, reinterpret_cast<const float(*)[8]>(f));
+    void* yr = row_at(a.y, row, a.ld_y, row_size(a.y_type));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = chunk[i] + 8 * lane;
+      if (c >= a.C) continue;
+      float2 p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        f[i][j] = __fmul2_rn(__fadd2_rn(__fadd2_rn(f[i][j], both(-mean)), both(-shift)), both(rstd));
+      if (a.gamma) {
+        vector_values(p, a.gamma, a.p_type, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i][j] = __fmul2_rn(f[i][j], p[j]);
+      }
+      if (a.beta) {
+        vector_values(p, a.beta, a.p_type, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i][j] = __fadd2_rn(f[i][j], p[j]);
+      }
+      store_pairs(yr, a.y_type, c, f[i]);
+    }
+    if (nw > 1 && !layer) __syncthreads();   // (as in norm_kernel)
+  }
+  griddep_launch();
+}
+
 // Rows of more columns than stay in registers: three passes, the second and third from L2.
 template <int V>
 __global__ void __launch_bounds__(32 * MAX_WARPS)
 norm_wide_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
-  __shared__ Shared sh;
+  __shared__ RowSums sh;
+  row_sum_init(sh);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int xs = row_size(a.x_type);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -197,7 +306,7 @@ norm_wide_kernel(const __grid_constant__ NormArgs a) {
         for (int j = 0; j < 8; ++j) t += f[0][j];
         s += t;
       }
-      mean = row_sum(s, 0.0f, sh, 0, warp, nw).x / static_cast<float>(a.C);
+      mean = row_sum1(s, sh, 0, warp, nw) / static_cast<float>(a.C);
       s = 0.0f;
     }
     for (int c = warp * CHUNK; c < a.C; c += nw * CHUNK) {
@@ -212,7 +321,7 @@ norm_wide_kernel(const __grid_constant__ NormArgs a) {
       s += t;
       q += u;
     }
-    const float2 sq = row_sum(s, q, sh, 1, warp, nw);
+    const float2 sq = row_sum2(s, q, sh, 1, warp, nw);
     const float shift = a.kind == MOE_NORM_LAYER ? sq.x / static_cast<float>(a.C) : 0.0f;
     const float var = fmaxf(sq.y / static_cast<float>(a.C) - shift * shift, 0.0f);
     const float rstd = rsqrtf((sq.y != sq.y ? sq.y : var) + a.eps);
@@ -227,7 +336,7 @@ norm_wide_kernel(const __grid_constant__ NormArgs a) {
       stream_values<V>(f[0], a, xr, rr, c, lane);
       if (tr) store_values<V>(tr, a.x_type, c, a.C, lane, f[0]);
       if (a.codes)
-        save_chunks<V, 1>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
+        save_row_chunks<V, 1>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
                           &c, a.C, lane, f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[0][j] = ((f[0][j] - mean) - shift) * rstd;
@@ -295,6 +404,38 @@ int norm_vector(const NormArgs& a) {
   return 1;
 }
 
+namespace {
+template <int N, int X, bool ADD>
+cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
+  auto kern = norm_ring_kernel<N, X, ADD>;
+  const int warps = nw == 1 ? 4 : nw;
+  const int slot = warps * N * CHUNK * row_size(X) * (ADD ? 2 : 1);
+  // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
+  int per = (N == 4 ? 640 : 1024) / (32 * warps);
+  if (per < 1) per = 1;
+  while (per > 1 && per * 2 * slot > ROW_SMEM) --per;
+  const int slots = per * 3 * slot <= ROW_SMEM ? 3 : per * 2 * slot <= ROW_SMEM ? 2 : 1;
+  const int64_t ctas = nw == 1 ? (a.rows + warps - 1) / warps : a.rows;
+  const int64_t most = static_cast<int64_t>(row_sms()) * per;
+  const int smem = slots * slot;
+  if (smem > 47 * 1024) {   // (the kernel has a little of its own)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(32 * warps), smem,
+                    st, 1, a, nw, slots);
+}
+// Chunks to a warp: four where that leaves few of them empty, else two.
+template <int X, bool ADD>
+cudaError_t launch_norm_rows(const NormArgs& a, int chunks, cudaStream_t st) {
+  if (chunks == 1) return launch_norm_ring<1, X, ADD>(a, 1, st);
+  const int fours = (chunks + 3) / 4, twos = (chunks + 1) / 2;
+  if (chunks == 2 || (twos <= MAX_WARPS && 8 * (4 * fours - chunks) > chunks))
+    return launch_norm_ring<2, X, ADD>(a, twos, st);
+  return launch_norm_ring<4, X, ADD>(a, fours, st);
+}
+}  // namespace
+
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
   const int chunks = (a.C + CHUNK - 1) / CHUNK;
   const int v = norm_vector(a);
@@ -305,6 +446,13 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     if (v == 2) return launch_pdl(norm_wide_kernel<2>, grid, dim3(512), 0, st, 1, a);
     return launch_pdl(norm_wide_kernel<1>, grid, dim3(512), 0, st, 1, a);
   }
+  if (v == 8) {
+    if (a.x_type == ROW_BF16)
+      return a.add ? launch_norm_rows<ROW_BF16, true>(a, chunks, st)
+                   : launch_norm_rows<ROW_BF16, false>(a, chunks, st);
+    return a.add ? launch_norm_rows<ROW_FP32, true>(a, chunks, st)
+                 : launch_norm_rows<ROW_FP32, false>(a, chunks, st);
+  }
   const int n = chunks == 1 ? 1 : chunks == 2 ? 2 : 4;
   const int nw = (chunks + n - 1) / n;
   const int warps = nw == 1 ? 4 : nw;
@@ -312,7 +460,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(32 * warps);
 #define MOE_NORM(V, N) launch_pdl(norm_kernel<V, N>, grid, block, 0, st, 1, a, nw)
 #define MOE_NORM_N(V) (n == 1 ? MOE_NORM(V, 1) : n == 2 ? MOE_NORM(V, 2) : MOE_NORM(V, 4))
-  return v == 8 ? MOE_NORM_N(8) : v == 2 ? MOE_NORM_N(2) : MOE_NORM_N(1);
+  return v == 2 ? MOE_NORM_N(2) : MOE_NORM_N(1);
 #undef MOE_NORM_N
 #undef MOE_NORM
 }

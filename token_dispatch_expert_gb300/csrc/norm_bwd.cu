@@ -10,35 +10,6 @@
 namespace moe {
 namespace {
 
-constexpr int MAX_WARPS = 16;
-
-struct Shared {
-  float2 part[2][MAX_WARPS];
-};
-
-__device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t ld, int size) {
-  return static_cast<const uint8_t*>(p) + row * ld * size;
-}
-__device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t ld, int size) {
-  return static_cast<uint8_t*>(p) + row * ld * size;
-}
-
-// Sums over the warps of a row; one barrier, `turn` alternates from row to row.
-__device__ __forceinline__ float2 row_sum(float a, float b, Shared& sh, int turn, int warp, int nw) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if (nw == 1) return make_float2(a, b);
-  if ((threadIdx.x & 31) == 0) sh.part[turn][warp] = make_float2(a, b);
-  __syncthreads();
-  float sa = 0.0f, sb = 0.0f;
-  for (int i = 0; i < nw; ++i) {
-    const float2 p = sh.part[turn][i];
-    sa += p.x;
-    sb += p.y;
-  }
-  return make_float2(sa, sb);
-}
-
 // v -> xhat of a chunk
 template <int V>
 __device__ __forceinline__ void xhat_values(float* x, const Raw8& raw, const float* sc,
@@ -54,7 +25,8 @@ template <int V, int N>
 __global__ void __launch_bounds__(32 * MAX_WARPS)
 norm_bwd_kernel(const __grid_constant__ NormArgs a, int nw) {
   griddep_wait();   // see common.cuh: dependent launches
-  __shared__ Shared sh;
+  __shared__ RowSums sh;
+  row_sum_init(sh);
   extern __shared__ float columns[];   // with nw = 1: the warps' sums over the rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int w = nw == 1 ? 0 : warp;
@@ -110,7 +82,7 @@ norm_bwd_kernel(const __grid_constant__ NormArgs a, int nw) {
       c1 += s;
       c2 += t;
     }
-    const float2 c = row_sum(c1, c2, sh, turn, w, nw);
+    const float2 c = row_sum2(c1, c2, sh, turn, w, nw);
     turn ^= 1;
     c1 = a.kind == MOE_NORM_LAYER ? c.x * over : 0.0f;
     c2 = c.y * over;
@@ -161,13 +133,200 @@ norm_bwd_kernel(const __grid_constant__ NormArgs a, int nw) {
   }
 }
 
+// The same for rows of whole 16-byte vectors, through shared memory: dy, v (with its scales), add
+// and the statistics of the rows that follow are fetched while one is worked on; gamma stays
+// there too, but for the widest rows, whose slots leave it no room.  With up to two chunks to a
+// warp a row's G and xhat stay in registers between the two passes over it, with four they are
+// computed again, from the slot.  S: the type of v or its codes, X: of add and dx, Y: of dy.
+template <int N, int S, int X, int Y>
+__global__ void __launch_bounds__(N == 1 ? 256 : 32 * MAX_WARPS, N == 1 ? 3 : 1)
+norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
+  griddep_wait();
+  __shared__ RowSums sh;
+  extern __shared__ __align__(16) uint8_t ring[];
+  row_sum_init(sh);
+  constexpr bool GAMMA = N < 4, KEEP = N < 4, CODES = S == ROW_INT8 || S == ROW_E4M3;
+  constexpr int XS = X == ROW_BF16 ? 2 : 4, YS = Y == ROW_BF16 ? 2 : 4;
+  constexpr int SS = CODES ? 1 : S == ROW_BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int w = nw == 1 ? 0 : warp;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (nw == 1 ? warps : 1);
+  const int64_t first = nw == 1 ? static_cast<int64_t>(blockIdx.x) * warps + warp : blockIdx.x;
+  const float over = 1.0f / static_cast<float>(a.C);
+  const bool layer = a.kind == MOE_NORM_LAYER, add = a.add != nullptr;
+  // a warp's part of a slot: per chunk dy, v, its scales and add, then the statistics
+  constexpr int AT_X = CHUNK * YS, AT_SC = AT_X + CHUNK * SS, AT_ADD = AT_SC + (CODES ? 128 : 0);
+  const int chunk_bytes = AT_ADD + (add ? CHUNK * XS : 0), warp_bytes = N * chunk_bytes + 256;
+  const int slot_bytes = warps * warp_bytes;
+  uint8_t* const mine = ring + warp * warp_bytes;
+  uint8_t* const gam = ring + slots * slot_bytes + warp * N * CHUNK * 4;   // fp32
+  float2 dg[N][4], db[N][4];
+  int chunk[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    chunk[i] = (i * nw + w) * CHUNK;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = both(0.0f);
+    const int c = chunk[i] + 8 * lane;
+    float2 p[4] = {both(1.0f), both(1.0f), both(1.0f), both(1.0f)};
+    if (c < a.C) {
+      if (GAMMA && a.gamma) vector_values(p, a.gamma, a.p_type, c);
+    } else {
+      for (int s = 0; s < slots; ++s) {
+        uint8_t* z = mine + s * slot_bytes + i * chunk_bytes;
+        clear_chunk(z, Y, lane);
+        clear_chunk(z + AT_X, S, lane);
+        if (CODES) *reinterpret_cast<float*>(z + AT_SC + 4 * lane) = 0.0f;
+        if (add) clear_chunk(z + AT_ADD, X, lane);
+      }
+    }
+    if (!GAMMA) continue;
+    *reinterpret_cast<float4*>(gam + i * 1024 + 16 * lane) = make_float4(p[0].x, p[0].y, p[1].x, p[1].y);
+    *reinterpret_cast<float4*>(gam + i * 1024 + 512 + 16 * lane) =
+        make_float4(p[2].x, p[2].y, p[3].x, p[3].y);
+  }
+  const uint8_t* yr = static_cast<const uint8_t*>(row_at(static_cast<const void*>(a.y), first, a.ld_y, YS));
+  const uint8_t* xr = static_cast<const uint8_t*>(row_at(a.x, first, a.ldx, SS));
+  const uint8_t* ar = static_cast<const uint8_t*>(row_at(a.add, first, a.ld_add, XS));
+  const int64_t y_step = step * a.ld_y * YS, x_step = step * a.ldx * SS, a_step = step * a.ld_add * XS;
+  int64_t next = first;
+  auto fetch = [&](int slot) {
+    if (next < a.rows) {
+      uint8_t* to = mine + slot * slot_bytes;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        uint8_t* t = to + i * chunk_bytes;
+        copy_chunk(t, yr, Y, chunk[i], a.C, lane);
+        copy_chunk(t + AT_X, xr, S, chunk[i], a.C, lane);
+        const int c = chunk[i] + 8 * lane;
+        if (CODES && c < a.C)
+          copy_async4(smem_u32(t + AT_SC + 4 * lane), a.x_scales + next * a.blocks + (c >> 7));
+        if (add) copy_chunk(t + AT_ADD, ar, X, chunk[i], a.C, lane);
+      }
+      const uint32_t st = smem_u32(to + N * chunk_bytes + 8 * lane);
+      if (layer) copy_async4(st, a.mean + next);
+      copy_async4(st + 4, a.rstd + next);
+      yr += y_step;
+      xr += x_step;
+      ar += a_step;
+      next += step;
+    }
+    copy_commit();
+  };
+  // G and xhat of a chunk in a slot
+  auto values = [&](const uint8_t* t, int i, float2 st, float2* g, float2* xh, bool sums) {
+    float2 p[4];
+    slot_values(g, t, Y, lane);
+    slot_values(xh, t + AT_X, S, lane);
+    if (CODES) {
+      const float sc = *reinterpret_cast<const float*>(t + AT_SC + 4 * lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) xh[j] = __fmul2_rn(xh[j], both(sc));
+    }
+    if (GAMMA) {
+      slot_values(p, gam + i * 1024, ROW_FP32, lane);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = both(1.0f);
+      if (a.gamma && chunk[i] + 8 * lane < a.C) vector_values(p, a.gamma, a.p_type, chunk[i] + 8 * lane);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      xh[j] = __fmul2_rn(__fadd2_rn(xh[j], both(-st.x)), both(st.y));
+      if (sums) {
+        dg[i][j] = __ffma2_rn(g[j], xh[j], dg[i][j]);
+        db[i][j] = __fadd2_rn(db[i][j], g[j]);
+      }
+      g[j] = __fmul2_rn(g[j], p[j]);
+    }
+  };
+  for (int s = 0; s + 1 < slots; ++s) fetch(s);
+  int slot = 0, ahead = slots - 1, turn = 0;
+  for (int64_t row = first; row < a.rows; row += step) {
+    fetch(ahead);
+    if (++ahead == slots) ahead = 0;
+    copy_wait(slots - 1);
+    const uint8_t* from = mine + slot * slot_bytes;
+    if (++slot == slots) slot = 0;
+    float2 st = *reinterpret_cast<const float2*>(from + N * chunk_bytes + 8 * lane);
+    if (!layer) st.x = 0.0f;
+    float2 g[KEEP ? N : 1][4], xh[KEEP ? N : 1][4], c1 = both(0.0f), c2 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int k = KEEP ? i : 0;
+      values(from + i * chunk_bytes, i, st, g[k], xh[k], true);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c1 = __fadd2_rn(c1, g[k][j]);
+        c2 = __ffma2_rn(g[k][j], xh[k][j], c2);
+      }
+    }
+    const float2 c = row_sum2(c1.x + c1.y, c2.x + c2.y, sh, turn, w, nw);
+    turn ^= 1;
+    const float m1 = layer ? -c.x * over : 0.0f, m2 = -c.y * over;
+    void* dr = row_at(a.out, row, a.ld_out, XS);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int k = KEEP ? i : 0;
+      if (!KEEP) values(from + i * chunk_bytes, i, st, g[k], xh[k], false);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        g[k][j] = __fmul2_rn(__ffma2_rn(xh[k][j], both(m2), __fadd2_rn(g[k][j], both(m1))), both(st.y));
+      if (add) {
+        float2 p[4];
+        slot_values(p, from + i * chunk_bytes + AT_ADD, X, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[k][j] = __fadd2_rn(g[k][j], p[j]);
+      }
+      const int col = chunk[i] + 8 * lane;
+      if (col < a.C) store_pairs(dr, X, col, g[k]);
+    }
+  }
+  griddep_launch();
+  if (!a.part) return;
+  const int64_t wide = norm_part_floats(a.C) / 2;
+  float* out = a.part + 2 * wide * blockIdx.x;
+  if (nw == 1) {
+    // the warps' sums one after another, so that their order is fixed (the copies are done: every
+    // group up to the last row's was waited for, and those behind it are empty)
+    float2* columns = reinterpret_cast<float2*>(ring);
+    __syncthreads();
+    for (int k = 0; k < warps; ++k) {
+      if (warp == k) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2* p = columns + (i * 4 + j) * 64 + lane;
+            if (k > 0) {
+              dg[i][j] = __fadd2_rn(dg[i][j], p[0]);
+              db[i][j] = __fadd2_rn(db[i][j], p[32]);
+            }
+            p[0] = dg[i][j];
+            p[32] = db[i][j];
+          }
+      }
+      __syncthreads();
+    }
+    if (warp + 1 != warps) return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int c = chunk[i] + 8 * lane;
+    if (c >= a.C) continue;
+    store_pairs(out, ROW_FP32, c, dg[i]);
+    store_pairs(out + wide, ROW_FP32, c, db[i]);
+  }
+}
+
 // Rows of more columns than stay in registers: two passes over the row, and the sums over the
 // CTA's rows in its part of the workspace.
 template <int V>
 __global__ void __launch_bounds__(32 * MAX_WARPS)
 norm_bwd_wide_kernel(const __grid_constant__ NormArgs a) {
   griddep_wait();
-  __shared__ Shared sh;
+  __shared__ RowSums sh;
+  row_sum_init(sh);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int xs = row_size(a.x_type), ys = row_size(a.y_type), ss = row_size(a.src_type);
   const float over = 1.0f / static_cast<float>(a.C);
@@ -230,7 +389,7 @@ norm_bwd_wide_kernel(const __grid_constant__ NormArgs a) {
         store_values<V>(row_at(a.out, row, a.ld_out, xs), a.x_type, k, a.C, lane, d);
       }
       if (pass == 0) {
-        c = row_sum(c1, c2, sh, turn, warp, nw);
+        c = row_sum2(c1, c2, sh, turn, warp, nw);
         turn ^= 1;
         c.x = a.kind == MOE_NORM_LAYER ? c.x * over : 0.0f;
         c.y *= over;
@@ -267,11 +426,49 @@ norm_sum_kernel(const float* part, int parts, int64_t wide, int C, void* dgamma,
   griddep_launch();
 }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
+template <int N, int S, int X, int Y>
+cudaError_t launch_ring(const NormArgs& a, int nw, cudaStream_t st, int* parts) {
+  auto kern = norm_bwd_ring_kernel<N, S, X, Y>;
+  const int warps = nw == 1 ? 8 : nw;
+  const int chunk = CHUNK * (row_size(Y) + row_size(S) + (a.add ? row_size(X) : 0)) +
+                    (a.x_scales ? 128 : 0);
+  const int slot = warps * (N * chunk + 256), gam = N < 4 ? warps * N * CHUNK * 4 : 0;
+  // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
+  int per = (N == 1 ? 768 : 512) / (32 * warps);
+  if (per < 1) per = 1;
+  if (per > NORM_PARTS / 152) per = NORM_PARTS / 152;
+  while (per > 1 && per * (2 * slot + gam) > ROW_SMEM) --per;
+  int slots = 4;
+  while (slots > 1 && per * (slots * slot + gam) > ROW_SMEM) --slots;
+  const int smem = slots * slot + gam;
+  if (smem > 47 * 1024) {   // (the kernel has a little of its own)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t ctas = nw == 1 ? (a.rows + warps - 1) / warps : a.rows;
+  int64_t most = static_cast<int64_t>(row_sms()) * per;
+  if (most > NORM_PARTS) most = NORM_PARTS;
+  *parts = static_cast<int>(ctas < most ? ctas : most);
+  return launch_pdl(kern, dim3(*parts), dim3(32 * warps), smem, st, 1, a, nw, slots);
+}
+template <int S, int X, int Y>
+cudaError_t launch_rows(const NormArgs& a, int chunks, cudaStream_t st, int* parts) {
+  if (chunks == 1) return launch_ring<1, S, X, Y>(a, 1, st, parts);
+  if (chunks <= 2 * MAX_WARPS) return launch_ring<2, S, X, Y>(a, (chunks + 1) / 2, st, parts);
+  return launch_ring<4, S, X, Y>(a, (chunks + 3) / 4, st, parts);
+}
+// the types of a stream in bf16, or in fp32 with gradients of either type
+template <int S, int X>
+cudaError_t launch_stream(const NormArgs& a, int chunks, cudaStream_t st, int* parts) {
+  if constexpr (X == ROW_FP32)
+    if (a.y_type == ROW_FP32) return launch_rows<S, X, ROW_FP32>(a, chunks, st, parts);
+  return launch_rows<S, X, ROW_BF16>(a, chunks, st, parts);
+}
+template <int X>
+cudaError_t launch_source(const NormArgs& a, int chunks, cudaStream_t st, int* parts) {
+  if (a.src_type == ROW_INT8) return launch_stream<ROW_INT8, X>(a, chunks, st, parts);
+  if (a.src_type == ROW_E4M3) return launch_stream<ROW_E4M3, X>(a, chunks, st, parts);
+  return launch_stream<X, X>(a, chunks, st, parts);
 }
 
 }  // namespace
@@ -286,11 +483,15 @@ cudaError_t launch_norm_bwd(const NormArgs& in, cudaStream_t st) {
   int parts = 0;
   if (a.rows > 0) {
     const bool wide = chunks > 4 * MAX_WARPS;
+    if (v == 8 && !wide && (a.x_type == ROW_FP32 || a.y_type == ROW_BF16)) {
+      e = a.x_type == ROW_BF16 ? launch_source<ROW_BF16>(a, chunks, st, &parts)
+                               : launch_source<ROW_FP32>(a, chunks, st, &parts);
+    } else {
     const int n = chunks == 1 ? 1 : chunks <= 2 * MAX_WARPS ? 2 : 4;
     const int nw = chunks <= 2 ? 1 : (chunks + n - 1) / n;
     const int warps = wide ? MAX_WARPS : nw == 1 ? 4 : nw;
     const int64_t ctas = nw == 1 ? (a.rows + 3) / 4 : a.rows;
-    int64_t cap = static_cast<int64_t>(sm_count()) * (warps > 8 ? 1 : 16 / warps);
+    int64_t cap = static_cast<int64_t>(row_sms()) * (warps > 8 ? 1 : 16 / warps);
     if (cap > NORM_PARTS) cap = NORM_PARTS;
     parts = static_cast<int>(ctas < cap ? ctas : cap);
     const dim3 grid(parts), block(32 * warps);
@@ -299,9 +500,11 @@ cudaError_t launch_norm_bwd(const NormArgs& in, cudaStream_t st) {
 #define MOE_NORM_N(V)                                                                \
   (wide ? launch_pdl(norm_bwd_wide_kernel<V>, grid, block, 0, st, 1, a)              \
         : n == 1 ? MOE_NORM(V, 1) : n == 2 ? MOE_NORM(V, 2) : MOE_NORM(V, 4))
-    e = v == 8 ? MOE_NORM_N(8) : v == 2 ? MOE_NORM_N(2) : MOE_NORM_N(1);
+    e = v == 8 ? launch_pdl(norm_bwd_wide_kernel<8>, grid, dim3(512), 0, st, 1, a)
+        : v == 2 ? MOE_NORM_N(2) : MOE_NORM_N(1);
 #undef MOE_NORM_N
 #undef MOE_NORM
+    }
     if (e != cudaSuccess) return e;
   }
   if (!sums) return e;

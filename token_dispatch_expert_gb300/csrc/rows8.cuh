@@ -187,6 +187,111 @@ __device__ __forceinline__ void scale_values(float* f, const float* s) {
   for (int j = 0; j < 8; ++j) f[j] *= s[j / V];
 }
 
+// ------------------------------------------------------------------ rows through shared memory
+// A kernel that goes from row to row fetches the next rows while it works on one: every thread
+// copies (cp.async) just the bytes that it will read itself into slots of its own, so the copies
+// need no barrier, and as many rows are under way as there are slots, whatever the registers.
+// Eight adjacent columns to a lane (V = 8).  A chunk's bytes in a slot: 512 for bf16, 1024 for
+// fp32 (the lanes' first 16 bytes, then their second ones: no bank conflicts), 256 for codes.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// until at most `n` of the thread's newest groups are under way (0 <= n <= 3)
+__device__ __forceinline__ void copy_wait(int n) {
+  if (n == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+__device__ __forceinline__ void copy_chunk(uint8_t* slot, const void* row, int type, int chunk, int C,
+                                           int lane) {
+  const int c = chunk + 8 * lane;
+  if (c >= C) return;
+  const uint8_t* p = static_cast<const uint8_t*>(row);
+  const uint32_t at = smem_u32(slot);
+  if (type == ROW_BF16) {
+    copy_async16(at + 16 * lane, p + 2 * static_cast<int64_t>(c));
+  } else if (type == ROW_FP32) {
+    copy_async16(at + 16 * lane, p + 4 * static_cast<int64_t>(c));
+    copy_async16(at + 512 + 16 * lane, p + 4 * static_cast<int64_t>(c) + 16);
+  } else {
+    copy_async8(at + 8 * lane, p + c);
+  }
+}
+// The bytes of a lane whose columns lie past the row's end are never copied: they are made zeros
+// once.
+__device__ __forceinline__ void clear_chunk(uint8_t* slot, int type, int lane) {
+  if (type == ROW_BF16 || type == ROW_FP32)
+    *reinterpret_cast<uint4*>(slot + 16 * lane) = make_uint4(0, 0, 0, 0);
+  if (type == ROW_FP32) *reinterpret_cast<uint4*>(slot + 512 + 16 * lane) = make_uint4(0, 0, 0, 0);
+  if (type != ROW_BF16 && type != ROW_FP32)
+    *reinterpret_cast<uint2*>(slot + 8 * lane) = make_uint2(0, 0);
+}
+// a lane's eight values in a slot, as pairs (of codes: without the scale)
+__device__ __forceinline__ void slot_values(float2* v, const uint8_t* slot, int type, int lane) {
+  if (type == ROW_BF16) {
+    const uint4 r = *reinterpret_cast<const uint4*>(slot + 16 * lane);
+    v[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+    v[1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
+    v[2] = make_float2(bf16_lo(r.z), bf16_hi(r.z));
+    v[3] = make_float2(bf16_lo(r.w), bf16_hi(r.w));
+  } else if (type == ROW_FP32) {
+    const float4 a = *reinterpret_cast<const float4*>(slot + 16 * lane);
+    const float4 b = *reinterpret_cast<const float4*>(slot + 512 + 16 * lane);
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+  } else {
+    const uint2 r = *reinterpret_cast<const uint2*>(slot + 8 * lane);
+    Raw8 raw;
+    raw.w[0] = r.x;
+    raw.w[1] = r.y;
+    float f[8];
+    if (type == ROW_INT8) unpack_raw<8>(raw, ROW_INT8, f);
+    else unpack_raw<8>(raw, ROW_E4M3, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = make_float2(f[2 * j], f[2 * j + 1]);
+  }
+}
+// a lane's eight values of a vector at `p` (the parameters), as pairs; c < C
+__device__ __forceinline__ void vector_values(float2* v, const void* p, int type, int c) {
+  if (type == ROW_BF16) {
+    const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + 2 * static_cast<int64_t>(c));
+    v[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+    v[1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
+    v[2] = make_float2(bf16_lo(r.z), bf16_hi(r.z));
+    v[3] = make_float2(bf16_lo(r.w), bf16_hi(r.w));
+  } else {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const uint8_t*>(p) + 4 * static_cast<int64_t>(c));
+    const float4 a = q[0], b = q[1];
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+  }
+}
+__device__ __forceinline__ void store_pairs(void* row, int type, int c, const float2* v) {
+  if (type == ROW_BF16) {
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(row) + 2 * static_cast<int64_t>(c)) =
+        make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                   pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+  } else {
+    float4* q = reinterpret_cast<float4*>(static_cast<uint8_t*>(row) + 4 * static_cast<int64_t>(c));
+    q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  }
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // ------------------------------------------------------------------ saving a block
 // s = amax / top, r = top / amax with amax = max(max |v|, 2^-110), each one correctly rounded
 // quotient; int8 codes are the whole number nearest to v * r (ties to even), the product rounded
@@ -271,12 +376,13 @@ __device__ __forceinline__ void store_codes(void* row, int format, int chunk, in
   }
 }
 
-// Quantise N chunks that the warp holds (f[i]: the lane's values of chunk[i]; columns from C on
-// are zeros) into a row's codes and scales.  With V = 8 the maxima of four blocks' halves go
-// through one set of shuffles: lanes exchange all but a share of the chunks at each step, so that
-// each lane ends with one block, divides once for it, and the factors are handed back.
+// Quantise N chunks that the warp holds (f[i]: the lane's values of chunk[i] of the row whose codes
+// and scales are at codes[i] and scales[i]; columns from C on are zeros, a chunk that starts at C
+// is none).  With V = 8 the maxima of four chunks go through one set of shuffles: lanes exchange
+// all but a share of the chunks at each step, so that each lane ends with one block, divides once
+// for it, and the factors are handed back.
 template <int V, int N>
-__device__ __forceinline__ void save_chunks(void* codes, float* scales, int format,
+__device__ __forceinline__ void save_chunks(void* const* codes, float* const* scales, int format,
                                             const int* chunk, int C, int lane,
                                             const float (*f)[8]) {
   float m[N][2];
@@ -284,24 +390,33 @@ __device__ __forceinline__ void save_chunks(void* codes, float* scales, int form
   for (int i = 0; i < N; ++i) lane_max<V>(f[i], m[i]);
   if (V == 8) {
     float sc, fa, r[N];
-    if (N == 4) {
+    if (N == 4 || N == 2) {
       const bool b3 = lane & 8, b2 = lane & 4;
-      float a = b3 ? m[2 % N][0] : m[0][0], b = b3 ? m[3 % N][0] : m[1 % N][0];
-      a = max_nan(a, __shfl_xor_sync(FULL_MASK, b3 ? m[0][0] : m[2 % N][0], 8));
-      b = max_nan(b, __shfl_xor_sync(FULL_MASK, b3 ? m[1 % N][0] : m[3 % N][0], 8));
-      float q = b2 ? b : a;
-      q = max_nan(q, __shfl_xor_sync(FULL_MASK, b2 ? a : b, 4));
+      float q;
+      if (N == 4) {
+        float a = b3 ? m[2 % N][0] : m[0][0], b = b3 ? m[3 % N][0] : m[1 % N][0];
+        a = max_nan(a, __shfl_xor_sync(FULL_MASK, b3 ? m[0][0] : m[2 % N][0], 8));
+        b = max_nan(b, __shfl_xor_sync(FULL_MASK, b3 ? m[1 % N][0] : m[3 % N][0], 8));
+        q = max_nan(b2 ? b : a, __shfl_xor_sync(FULL_MASK, b2 ? a : b, 4));
+      } else {
+        q = max_nan(b3 ? m[1 % N][0] : m[0][0],
+                    __shfl_xor_sync(FULL_MASK, b3 ? m[0][0] : m[1 % N][0], 8));
+        q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, 4));
+      }
       q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, 2));
       q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, 1));
       block_scale(q, format, sc, fa);
-      const int mine = (b3 ? 2 : 0) + (b2 ? 1 : 0);
-      const int c = (mine == 0 ? chunk[0] : mine == 1 ? chunk[1 % N]
-                                          : mine == 2 ? chunk[2 % N] : chunk[3 % N]) +
-                    128 * (lane >> 4);
-      if ((lane & 3) == 0 && c < C) scales[c >> 7] = sc;
+      int c = b3 ? chunk[N == 4 ? 2 % N : 1 % N] : chunk[0];
+      float* to = b3 ? scales[N == 4 ? 2 % N : 1 % N] : scales[0];
+      if (N == 4 && b2) {
+        c = b3 ? chunk[3 % N] : chunk[1 % N];
+        to = b3 ? scales[3 % N] : scales[1 % N];
+      }
+      c += 128 * (lane >> 4);
+      if ((lane & (N == 4 ? 3 : 7)) == 0 && c < C) to[c >> 7] = sc;
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        r[i] = __shfl_sync(FULL_MASK, fa, (lane & 16) | (i / 2 * 8) | (i % 2 * 4));
+        r[i] = __shfl_sync(FULL_MASK, fa, (lane & 16) | (N == 4 ? i / 2 * 8 + i % 2 * 4 : i * 8));
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -310,30 +425,91 @@ __device__ __forceinline__ void save_chunks(void* codes, float* scales, int form
         for (int o = 8; o > 0; o >>= 1) q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, o));
         block_scale(q, format, sc, r[i]);
         const int c = chunk[i] + 128 * (lane >> 4);
-        if ((lane & 15) == 0 && c < C) scales[c >> 7] = sc;
+        if ((lane & 15) == 0 && c < C) scales[i][c >> 7] = sc;
       }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float both[2] = {r[i], r[i]};
-      store_codes<V>(codes, format, chunk[i], C, lane, f[i], both);
+      const float r2[2] = {r[i], r[i]};
+      store_codes<V>(codes[i], format, chunk[i], C, lane, f[i], r2);
     }
   } else {
+    // blocks 0 and 1 of a chunk: after the first exchange a lane keeps one of them
+    const bool up = lane & 16;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float r[2];
+      float q = max_nan(up ? m[i][1] : m[i][0],
+                        __shfl_xor_sync(FULL_MASK, up ? m[i][0] : m[i][1], 16));
+      float sc, fa;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float q = m[i][h], sc;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, o));
-        block_scale(q, format, sc, r[h]);
-        const int c = chunk[i] + 128 * h;
-        if (lane == 0 && c < C) scales[c >> 7] = sc;
-      }
-      store_codes<V>(codes, format, chunk[i], C, lane, f[i], r);
+      for (int o = 8; o > 0; o >>= 1) q = max_nan(q, __shfl_xor_sync(FULL_MASK, q, o));
+      block_scale(q, format, sc, fa);
+      const int c = chunk[i] + 128 * (lane >> 4);
+      if ((lane & 15) == 0 && c < C) scales[i][c >> 7] = sc;
+      const float r[2] = {__shfl_sync(FULL_MASK, fa, 0), __shfl_sync(FULL_MASK, fa, 16)};
+      store_codes<V>(codes[i], format, chunk[i], C, lane, f[i], r);
     }
   }
+}
+template <int V, int N>
+__device__ __forceinline__ void save_row_chunks(void* codes, float* scales, int format,
+                                                const int* chunk, int C, int lane,
+                                                const float (*f)[8]) {
+  void* c[N];
+  float* s[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    c[i] = codes;
+    s[i] = scales;
+  }
+  save_chunks<V, N>(c, s, format, chunk, C, lane, f);
+}
+
+// ------------------------------------------------------------------ sums over a row
+constexpr int MAX_WARPS = 16;   // of a row that stays in registers: 16 * 4 chunks of 256 columns
+
+struct RowSums {
+  float part[2][2][MAX_WARPS];   // [buffer][which sum][warp]
+};
+// Before the first sum: the parts that no warp writes are zeros, so that they are read by fours.
+__device__ __forceinline__ void row_sum_init(RowSums& sh) {
+  for (int i = threadIdx.x; i < 4 * MAX_WARPS; i += blockDim.x) (&sh.part[0][0][0])[i] = 0.0f;
+  __syncthreads();
+}
+__device__ __forceinline__ float row_total(const float* part, int nw) {
+  float s = 0.0f;
+  for (int i = 0; i < nw; i += 4) {
+    const float4 p = *reinterpret_cast<const float4*>(part + i);
+    s += (p.x + p.y) + (p.z + p.w);
+  }
+  return s;
+}
+// Sums over the nw warps that share a row: every thread gets them, added in one order.  `turn`
+// alternates between two buffers, so that one barrier a sum is enough.
+__device__ __forceinline__ float row_sum1(float a, RowSums& sh, int turn, int warp, int nw) {
+  a = warp_sum(a);
+  if (nw == 1) return a;
+  if ((threadIdx.x & 31) == 0) sh.part[turn][0][warp] = a;
+  __syncthreads();
+  return row_total(sh.part[turn][0], nw);
+}
+// of two numbers at once: the halves of the warp take one each after the first exchange
+__device__ __forceinline__ float2 row_sum2(float a, float b, RowSums& sh, int turn, int warp, int nw) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane & 16;
+  float v = (up ? b : a) + __shfl_xor_sync(FULL_MASK, up ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+  if (nw == 1) return make_float2(__shfl_sync(FULL_MASK, v, 0), __shfl_sync(FULL_MASK, v, 16));
+  if ((lane & 15) == 0) sh.part[turn][lane >> 4][warp] = v;
+  __syncthreads();
+  return make_float2(row_total(sh.part[turn][0], nw), row_total(sh.part[turn][1], nw));
+}
+__device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t ld, int size) {
+  return static_cast<const uint8_t*>(p) + row * ld * size;
+}
+__device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t ld, int size) {
+  return static_cast<uint8_t*>(p) + row * ld * size;
 }
 
 // ------------------------------------------------------------------ host: which V
@@ -343,5 +519,13 @@ inline bool rows_fit(const void* p, int64_t ld, int size, int v) {
   return !p || (reinterpret_cast<uintptr_t>(p) % a == 0 && (ld * size) % a == 0);
 }
 __host__ __device__ inline int row_size(int type) { return type == ROW_BF16 ? 2 : type == ROW_FP32 ? 4 : 1; }
+
+constexpr int ROW_SMEM = 216 * 1024;   // of an SM's shared memory, for the rows in flight
+inline int row_sms() {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
 
 }  // namespace moe
