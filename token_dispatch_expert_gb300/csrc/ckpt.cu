@@ -12,6 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int SLOTS = 3;
 
 __device__ __forceinline__ int64_t live_rows(const CkptArgs& a) {
   if (!a.live) return a.rows;
@@ -23,142 +24,335 @@ __device__ __forceinline__ int64_t live_rows(const CkptArgs& a) {
   return n;
 }
 
-// Save: a warp takes N chunks of 256 columns, going on over the rows' ends.
+// N rows at a time: with N = 4 one division and one set of shuffles serve four blocks.
 template <int V, int N, int X, int FORMAT>
-__global__ void __launch_bounds__(THREADS)
-save_kernel(const __grid_constant__ CkptArgs a, RowDiv div) {
+__global__ void __launch_bounds__(WALK_THREADS)
+save_kernel(const __grid_constant__ CkptArgs a, int per, int groups) {
   griddep_wait();   // see common.cuh: dependent launches
   const int lane = threadIdx.x & 31;
-  const int64_t items = live_rows(a) * div.per;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * N;
+  const Walk w = walk_start(per, groups);
+  const int64_t live = w.any ? live_rows(a) : 0;
   constexpr int XS = X == ROW_BF16 ? 2 : 4;
-  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N; i0 < items;
-       i0 += step) {
-    int64_t row = div.row(i0);
-    int k = static_cast<int>(i0 - row * div.per);
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) + w.row * a.ldx * XS;
+  uint8_t* codes = static_cast<uint8_t*>(a.codes) + w.row * a.ld;
+  float* scales = a.scales + w.row * a.blocks;
+  const int64_t x_step = w.groups * a.ldx * XS, c_step = w.groups * a.ld, s_step = w.groups * a.blocks;
+  for (int64_t row = w.row; row < live; row += N * w.groups) {
     Raw8 raw[N];
-    void* codes[N];
-    float* scales[N];
+    void* to[N];
+    float* ts[N];
     int chunk[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      chunk[i] = i0 + i < items ? k * CHUNK : a.C;   // (a chunk that starts at C has no columns)
-      load_raw<V>(raw[i], static_cast<const uint8_t*>(a.x) + row * a.ldx * XS, X, chunk[i], a.C, lane);
-      codes[i] = static_cast<uint8_t*>(a.codes) + row * a.ld;
-      scales[i] = a.scales + row * a.blocks;
-      if (++k == div.per) { k = 0; ++row; }
+      chunk[i] = row + i * w.groups < live ? w.chunk : a.C;   // (a chunk at C has no columns)
+      to[i] = codes;
+      ts[i] = scales;
+      load_raw<V>(raw[i], x, X, chunk[i], a.C, lane);
+      x += x_step;
+      codes += c_step;
+      scales += s_step;
     }
     float f[N][8];
 #pragma unroll
     for (int i = 0; i < N; ++i) unpack_raw<V>(raw[i], X, f[i]);
-    save_chunks<V, N>(codes, scales, FORMAT, chunk, a.C, lane, f);
+    save_chunks<V, N>(to, ts, FORMAT, chunk, a.C, lane, f);
   }
   griddep_launch();
 }
 
 template <int V, int N, int X, int FORMAT>
-__global__ void __launch_bounds__(THREADS)
-load_kernel(const __grid_constant__ CkptArgs a, RowDiv div) {
+__global__ void __launch_bounds__(WALK_THREADS)
+load_kernel(const __grid_constant__ CkptArgs a, int per, int groups) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t items = live_rows(a) * div.per;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * N;
+  const Walk w = walk_start(per, groups);
+  const int64_t live = w.any ? live_rows(a) : 0;
   constexpr int XS = X == ROW_BF16 ? 2 : 4, TYPE = FORMAT == MOE_CKPT_INT8 ? ROW_INT8 : ROW_E4M3;
-  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N; i0 < items;
-       i0 += step) {
-    int64_t row = div.row(i0);
-    int k = static_cast<int>(i0 - row * div.per);
+  uint8_t* x = static_cast<uint8_t*>(a.out) + w.row * a.ldx * XS;
+  const uint8_t* codes = static_cast<const uint8_t*>(a.codes_in) + w.row * a.ld;
+  const float* scales = a.scales_in + w.row * a.blocks;
+  const int64_t x_step = w.groups * a.ldx * XS, c_step = w.groups * a.ld, s_step = w.groups * a.blocks;
+  for (int64_t row = w.row; row < live; row += N * w.groups) {
     Raw8 raw[N];
     float sc[N][8 / V];
-    uint8_t* out[N];
-    int chunk[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      out[i] = static_cast<uint8_t*>(a.out) + row * a.ldx * XS;
-      chunk[i] = i0 + i < items ? k * CHUNK : a.C;
-      load_raw<V>(raw[i], static_cast<const uint8_t*>(a.codes_in) + row * a.ld, TYPE, chunk[i], a.C,
-                  lane);
-      load_scales<V>(sc[i], a.scales_in + row * a.blocks, 0, chunk[i], a.C, lane);
-      if (++k == div.per) { k = 0; ++row; }
+      if (row + i * w.groups < live) {
+        load_raw<V>(raw[i], codes, TYPE, w.chunk, a.C, lane);
+        load_chunk_scales<V>(sc[i], scales, w.chunk, a.C, lane);
+      }
+      codes += c_step;
+      scales += s_step;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float f[8];
-      unpack_raw<V>(raw[i], TYPE, f);
-      scale_values<V>(f, sc[i]);
-      store_values<V>(out[i], X, chunk[i], a.C, lane, f);
+      if (row + i * w.groups < live) {
+        float f[8];
+        unpack_raw<V>(raw[i], TYPE, f);
+        scale_values<V>(f, sc[i]);
+        store_values<V>(x, X, w.chunk, a.C, lane, f);
+      }
+      x += x_step;
     }
   }
   griddep_launch();
 }
 
-// [a | b] and h, or with BACK [da | db] and h from dh: f = C / 2 columns, a warp takes N chunks of
-// 256 of them.  With s = sigma(a): h = a s b, da = dh b s (1 + a (1 - s)), db = dh a s, from the
-// 32-bit restored values, each rounded once.
+// [a | b] and h, or with BACK [da | db] and h from dh, N rows at a time.  With s = sigma(a):
+// h = a s b, da = dh b s (1 + a (1 - s)), db = dh a s, from the 32-bit restored values, each rounded
+// once.
 template <int V, int N, bool BACK, int TYPE>
-__global__ void __launch_bounds__(THREADS)
-swiglu_kernel(const __grid_constant__ CkptArgs p, RowDiv div) {
+__global__ void __launch_bounds__(WALK_THREADS)
+swiglu_kernel(const __grid_constant__ CkptArgs p, int per, int groups) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
   const int f = p.C / 2;
-  const int64_t items = live_rows(p) * div.per;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * WARPS * N;
-  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * WARPS + (threadIdx.x >> 5)) * N; i0 < items;
-       i0 += step) {
-    int64_t row = div.row(i0);
-    int k = static_cast<int>(i0 - row * div.per);
+  const Walk w = walk_start(per, groups);
+  const int64_t live = w.any ? live_rows(p) : 0;
+  const uint8_t* codes = static_cast<const uint8_t*>(p.codes_in) + w.row * p.ld;
+  const float* scales = p.scales_in + w.row * p.blocks;
+  const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(p.dh) + w.row * f;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row * p.C;
+  __nv_bfloat16* hr = static_cast<__nv_bfloat16*>(p.h) + w.row * f;
+  const int64_t c_step = w.groups * p.ld, s_step = w.groups * p.blocks, h_step = w.groups * f;
+  for (int64_t row = w.row; row < live; row += N * w.groups) {
     Raw8 ra[N], rb[N], rd[N];
     float sa[N][8 / V], sb[N][8 / V];
-    int64_t at[N];
-    int chunk[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      at[i] = row;
-      chunk[i] = k * CHUNK;
-      if (i0 + i < items) {
-        const uint8_t* codes = static_cast<const uint8_t*>(p.codes_in) + row * p.ld;
-        const float* scales = p.scales_in + row * p.blocks;
-        load_raw<V>(ra[i], codes, TYPE, chunk[i], f, lane);
-        load_raw<V>(rb[i], codes + f, TYPE, chunk[i], f, lane);
-        if (BACK)
-          load_raw<V>(rd[i], static_cast<const __nv_bfloat16*>(p.dh) + row * f, ROW_BF16, chunk[i],
-                      f, lane);
-        load_scales<V>(sa[i], scales, 0, chunk[i], f, lane);
-        load_scales<V>(sb[i], scales, f, chunk[i], f, lane);
+      if (row + i * w.groups < live) {
+        load_raw<V>(ra[i], codes, TYPE, w.chunk, f, lane);
+        load_raw<V>(rb[i], codes + f, TYPE, w.chunk, f, lane);
+        if (BACK) load_raw<V>(rd[i], dh, ROW_BF16, w.chunk, f, lane);
+        load_chunk_scales<V>(sa[i], scales, w.chunk, f, lane);
+        load_scales<V>(sb[i], scales, f, w.chunk, f, lane);
       }
-      if (++k == div.per) { k = 0; ++row; }
+      codes += c_step;
+      scales += s_step;
+      dh += h_step;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (i0 + i >= items) break;
-      float a[8], b[8], h[8];
-      unpack_raw<V>(ra[i], TYPE, a);
-      unpack_raw<V>(rb[i], TYPE, b);
-      scale_values<V>(a, sa[i]);
-      scale_values<V>(b, sb[i]);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at[i] * p.C;
-      if (BACK) {
-        float d[8];
-        unpack_raw<V>(rd[i], ROW_BF16, d);
+      if (row + i * w.groups < live) {
+        float a[8], b[8], h[8];
+        unpack_raw<V>(ra[i], TYPE, a);
+        unpack_raw<V>(rb[i], TYPE, b);
+        scale_values<V>(a, sa[i]);
+        scale_values<V>(b, sb[i]);
+        if (BACK) {
+          float d[8];
+          unpack_raw<V>(rd[i], ROW_BF16, d);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float s = sigmoid_fast(a[j]), as = a[j] * s;
-          const float da = d[j] * b[j] * fmaf(as, 1.0f - s, s);
-          h[j] = as * b[j];
-          b[j] = d[j] * as;
-          a[j] = da;
+          for (int j = 0; j < 8; ++j) {
+            const float s = sigmoid_fast(a[j]), as = a[j] * s;
+            const float da = d[j] * b[j] * fmaf(as, 1.0f - s, s);
+            h[j] = as * b[j];
+            b[j] = d[j] * as;
+            a[j] = da;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[j] = a[j] * sigmoid_fast(a[j]) * b[j];
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = a[j] * sigmoid_fast(a[j]) * b[j];
+        if (BACK || p.out) {
+          store_values<V>(out, ROW_BF16, w.chunk, f, lane, a);
+          store_values<V>(out + f, ROW_BF16, w.chunk, f, lane, b);
+        }
+        if (p.h) store_values<V>(hr, ROW_BF16, w.chunk, f, lane, h);
       }
-      if (p.out) {
-        store_values<V>(out, ROW_BF16, chunk[i], f, lane, a);
-        store_values<V>(out + f, ROW_BF16, chunk[i], f, lane, b);
-      }
-      if (p.h)
-        store_values<V>(static_cast<__nv_bfloat16*>(p.h) + at[i] * f, ROW_BF16, chunk[i], f, lane, h);
+      out += 2 * h_step;
+      hr += h_step;
     }
+  }
+  griddep_launch();
+}
+
+// ------------------------------------------------------------------ rows of whole vectors
+// The three above for rows of whole 16-byte vectors: the rows that follow come through shared memory
+// (rows8.cuh) in SLOTS slots.
+template <int N, int X, int FORMAT>
+__global__ void __launch_bounds__(WALK_THREADS, 2)
+save_ring_kernel(const __grid_constant__ CkptArgs a, int per, int groups) {
+  griddep_wait();
+  constexpr int XS = X == ROW_BF16 ? 2 : 4, BYTES = CHUNK * XS;
+  __shared__ __align__(16) uint8_t ring[WALK_WARPS][SLOTS][N][BYTES];
+  const int lane = threadIdx.x & 31;
+  const Walk w = walk_start(per, groups);
+  if (!w.any) return;
+  const int64_t live = live_rows(a);
+  uint8_t(*mine)[N][BYTES] = ring[threadIdx.x >> 5];
+  const bool past = w.chunk + 8 * lane >= a.C;
+  if (past)
+    for (int s = 0; s < SLOTS; ++s)
+#pragma unroll
+      for (int i = 0; i < N; ++i) clear_chunk(mine[s][i], X, lane);
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) + w.row * a.ldx * XS;
+  const int64_t x_step = w.groups * a.ldx * XS;
+  int64_t next = w.row;
+  auto fetch = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (next < live) copy_chunk(mine[slot][i], x, X, w.chunk, a.C, lane);
+      x += x_step;
+      next += w.groups;
+    }
+    copy_commit();
+  };
+  for (int s = 0; s + 1 < SLOTS; ++s) fetch(s);
+  uint8_t* codes = static_cast<uint8_t*>(a.codes) + w.row * a.ld;
+  float* scales = a.scales + w.row * a.blocks;
+  const int64_t c_step = w.groups * a.ld, s_step = w.groups * a.blocks;
+  int slot = 0, ahead = SLOTS - 1;
+  for (int64_t row = w.row; row < live; row += N * w.groups) {
+    fetch(ahead);
+    if (++ahead == SLOTS) ahead = 0;
+    copy_wait(SLOTS - 1);
+    void* to[N];
+    float* ts[N];
+    int chunk[N];
+    float2 f[N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      chunk[i] = row + i * w.groups < live ? w.chunk : a.C;   // (a chunk at C has no columns)
+      to[i] = codes;
+      ts[i] = scales;
+      codes += c_step;
+      scales += s_step;
+      slot_values(f[i], mine[slot][i], X, lane);
+    }
+    if (++slot == SLOTS) slot = 0;
+    save_chunks<8, N>(to, ts, FORMAT, chunk, a.C, lane, reinterpret_cast<const float(*)[8]>(f));
+  }
+  griddep_launch();
+}
+
+template <int X, int FORMAT>
+__global__ void __launch_bounds__(WALK_THREADS, 4)
+load_ring_kernel(const __grid_constant__ CkptArgs a, int per, int groups) {
+  griddep_wait();
+  constexpr int XS = X == ROW_BF16 ? 2 : 4, TYPE = FORMAT == MOE_CKPT_INT8 ? ROW_INT8 : ROW_E4M3;
+  constexpr int N = 2;
+  struct Slot { uint8_t codes[CHUNK]; float scale[32]; };
+  __shared__ __align__(16) Slot ring[WALK_WARPS][SLOTS][N];
+  const int lane = threadIdx.x & 31;
+  const Walk w = walk_start(per, groups);
+  if (!w.any) return;
+  const int64_t live = live_rows(a);
+  Slot(*mine)[N] = ring[threadIdx.x >> 5];
+  const int col = w.chunk + 8 * lane;
+  if (col >= a.C) return;   // (nothing below is for the whole warp)
+  const uint8_t* codes = static_cast<const uint8_t*>(a.codes_in) + w.row * a.ld;
+  const float* scales = a.scales_in + w.row * a.blocks + (col >> 7);
+  const int64_t c_step = w.groups * a.ld, s_step = w.groups * a.blocks;
+  int64_t next = w.row;
+  auto fetch = [&](int slot) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (next < live) {
+        copy_chunk(mine[slot][i].codes, codes, TYPE, w.chunk, a.C, lane);
+        copy_async4(smem_u32(&mine[slot][i].scale[lane]), scales);
+      }
+      codes += c_step;
+      scales += s_step;
+      next += w.groups;
+    }
+    copy_commit();
+  };
+  for (int s = 0; s + 1 < SLOTS; ++s) fetch(s);
+  uint8_t* x = static_cast<uint8_t*>(a.out) + w.row * a.ldx * XS;
+  const int64_t x_step = w.groups * a.ldx * XS;
+  int slot = 0, ahead = SLOTS - 1;
+  for (int64_t row = w.row; row < live; row += N * w.groups) {
+    fetch(ahead);
+    if (++ahead == SLOTS) ahead = 0;
+    copy_wait(SLOTS - 1);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (row + i * w.groups < live) {
+        float2 f[4];
+        slot_values(f, mine[slot][i].codes, TYPE, lane);
+        const float2 sc = both(mine[slot][i].scale[lane]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(f[j], sc);
+        store_pairs(x, X, col, f);
+      }
+      x += x_step;
+    }
+    if (++slot == SLOTS) slot = 0;
+  }
+  griddep_launch();
+}
+
+template <bool BACK, int TYPE>
+__global__ void __launch_bounds__(WALK_THREADS, 4)
+swiglu_ring_kernel(const __grid_constant__ CkptArgs p, int per, int groups) {
+  griddep_wait();
+  struct Slot { uint8_t dh[BACK ? 2 * CHUNK : 16]; uint8_t a[CHUNK], b[CHUNK]; float sa[32], sb[32]; };
+  __shared__ __align__(16) Slot ring[WALK_WARPS][SLOTS];
+  const int lane = threadIdx.x & 31;
+  const int f = p.C / 2;
+  const Walk w = walk_start(per, groups);
+  if (!w.any) return;
+  const int64_t live = live_rows(p);
+  Slot* mine = ring[threadIdx.x >> 5];
+  const int col = w.chunk + 8 * lane;
+  if (col >= f) return;   // (nothing below is for the whole warp)
+  const uint8_t* codes = static_cast<const uint8_t*>(p.codes_in) + w.row * p.ld;
+  const float* scales = p.scales_in + w.row * p.blocks;
+  const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(p.dh) + w.row * f;
+  const int64_t c_step = w.groups * p.ld, s_step = w.groups * p.blocks, h_step = w.groups * f;
+  const int block_a = col >> 7, block_b = (f + col) >> 7;
+  int64_t next = w.row;
+  auto fetch = [&](int slot) {
+    if (next < live) {
+      Slot& t = mine[slot];
+      copy_chunk(t.a, codes, TYPE, w.chunk, f, lane);
+      copy_chunk(t.b, codes + f, TYPE, w.chunk, f, lane);
+      if (BACK) copy_chunk(t.dh, dh, ROW_BF16, w.chunk, f, lane);
+      copy_async4(smem_u32(&t.sa[lane]), scales + block_a);
+      copy_async4(smem_u32(&t.sb[lane]), scales + block_b);
+    }
+    codes += c_step;
+    scales += s_step;
+    dh += h_step;
+    next += w.groups;
+    copy_commit();
+  };
+  for (int s = 0; s + 1 < SLOTS; ++s) fetch(s);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row * p.C;
+  __nv_bfloat16* hr = static_cast<__nv_bfloat16*>(p.h) + w.row * f;
+  int slot = 0, ahead = SLOTS - 1;
+  for (int64_t row = w.row; row < live; row += w.groups) {
+    fetch(ahead);
+    if (++ahead == SLOTS) ahead = 0;
+    copy_wait(SLOTS - 1);
+    const Slot& t = mine[slot];
+    if (++slot == SLOTS) slot = 0;
+    float2 a[4], b[4], h[4], d[4];
+    slot_values(a, t.a, TYPE, lane);
+    slot_values(b, t.b, TYPE, lane);
+    if (BACK) slot_values(d, t.dh, ROW_BF16, lane);
+    const float2 sa = both(t.sa[lane]), sb = both(t.sb[lane]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = __fmul2_rn(a[j], sa);
+      b[j] = __fmul2_rn(b[j], sb);
+      const float2 s = make_float2(sigmoid_fast(a[j].x), sigmoid_fast(a[j].y));
+      const float2 as = __fmul2_rn(a[j], s);
+      h[j] = __fmul2_rn(as, b[j]);
+      if (BACK) {
+        const float2 one = __ffma2_rn(s, both(-1.0f), both(1.0f));   // 1 - s
+        a[j] = __fmul2_rn(__fmul2_rn(d[j], b[j]), __ffma2_rn(as, one, s));
+        b[j] = __fmul2_rn(d[j], as);
+      }
+    }
+    if (BACK || p.out) {
+      store_pairs(out, ROW_BF16, col, a);
+      store_pairs(out + f, ROW_BF16, col, b);
+    }
+    if (p.h) store_pairs(hr, ROW_BF16, col, h);
+    out += 2 * h_step;
+    hr += h_step;
   }
   griddep_launch();
 }
@@ -237,13 +431,6 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint8_t* __restrict__ cod
   griddep_launch();
 }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 // f(the rows' type, the format) as constants
 template <typename F>
 cudaError_t by_types(const CkptArgs& a, F f) {
@@ -255,57 +442,43 @@ cudaError_t by_types(const CkptArgs& a, F f) {
   return a.format == MOE_CKPT_INT8 ? f(Fp32(), Int8()) : f(Fp32(), E4m3());
 }
 
-dim3 item_grid(int64_t rows, int per, int n) {
-  const int64_t need = (rows * per + WARPS * n - 1) / (WARPS * n);
-  const int64_t most = static_cast<int64_t>(1) << 30;
-  return dim3(static_cast<unsigned>(need < most ? need : most));
+template <typename K>
+cudaError_t launch_walk(K kern, const CkptArgs& a, int C, cudaStream_t st, int warps = 64) {
+  const WalkGrid g = walk_grid(a.rows, C, warps);
+  return launch_pdl(kern, g.grid, dim3(WALK_THREADS), 0, st, 1, a, g.per, g.groups);
 }
 
 }  // namespace
 
 cudaError_t launch_ckpt_save(const CkptArgs& a, cudaStream_t st) {
-  const RowDiv div((a.C + CHUNK - 1) / CHUNK);
   const int xs = row_size(a.x_type);
-  auto go = [&](auto kern, int n) {
-    return launch_pdl(kern, item_grid(a.rows, div.per, n), dim3(THREADS), 0, st, 1, a, div);
-  };
-  auto pick = [&](auto x, auto format) {
+  return by_types(a, [&](auto x, auto format) {
     constexpr int X = decltype(x)::value, F = decltype(format)::value;
-    if (a.C % 8 == 0 && rows_fit(a.x, a.ldx, xs, 8)) return go(save_kernel<8, 4, X, F>, 4);
-    if (a.C % 2 == 0 && rows_fit(a.x, a.ldx, xs, 2)) return go(save_kernel<2, 2, X, F>, 2);
-    return go(save_kernel<1, 2, X, F>, 2);
-  };
-  return by_types(a, pick);
+    if (a.C % 8 == 0 && rows_fit(a.x, a.ldx, xs, 8)) return launch_walk(save_ring_kernel<X == ROW_BF16 ? 4 : 2, X, F>, a, a.C, st, 128);
+    if (a.C % 2 == 0 && rows_fit(a.x, a.ldx, xs, 2)) return launch_walk(save_kernel<2, 2, X, F>, a, a.C, st);
+    return launch_walk(save_kernel<1, 2, X, F>, a, a.C, st);
+  });
 }
 
 cudaError_t launch_ckpt_load(const CkptArgs& a, cudaStream_t st) {
-  const RowDiv div((a.C + CHUNK - 1) / CHUNK);
   const int xs = row_size(a.x_type);
-  auto go = [&](auto kern, int n) {
-    return launch_pdl(kern, item_grid(a.rows, div.per, n), dim3(THREADS), 0, st, 1, a, div);
-  };
-  auto pick = [&](auto x, auto format) {
+  return by_types(a, [&](auto x, auto format) {
     constexpr int X = decltype(x)::value, F = decltype(format)::value;
-    if (a.C % 8 == 0 && rows_fit(a.out, a.ldx, xs, 8)) return go(load_kernel<8, 4, X, F>, 4);
-    if (a.C % 2 == 0 && rows_fit(a.out, a.ldx, xs, 2)) return go(load_kernel<2, 2, X, F>, 2);
-    return go(load_kernel<1, 2, X, F>, 2);
-  };
-  return by_types(a, pick);
+    if (a.C % 8 == 0 && rows_fit(a.out, a.ldx, xs, 8)) return launch_walk(load_ring_kernel<X, F>, a, a.C, st, 256);
+    if (a.C % 2 == 0 && rows_fit(a.out, a.ldx, xs, 2)) return launch_walk(load_kernel<2, 2, X, F>, a, a.C, st);
+    return launch_walk(load_kernel<1, 2, X, F>, a, a.C, st);
+  });
 }
 
 cudaError_t launch_ckpt_swiglu(const CkptArgs& a, cudaStream_t st) {
   const int f = a.C / 2;
-  const RowDiv div((f + CHUNK - 1) / CHUNK);
-  auto go = [&](auto kern, int n) {
-    return launch_pdl(kern, item_grid(a.rows, div.per, n), dim3(THREADS), 0, st, 1, a, div);
-  };
   auto pick = [&](auto back, auto format) {
     constexpr bool B = decltype(back)::value;
     constexpr int T = decltype(format)::value == MOE_CKPT_INT8 ? ROW_INT8 : ROW_E4M3;
     // (dh, [a | b] and h are dense from 16-byte addresses: the width alone decides)
-    if (f % 8 == 0) return go(swiglu_kernel<8, 2, B, T>, 2);
-    if (f % 2 == 0) return go(swiglu_kernel<2, 1, B, T>, 1);
-    return go(swiglu_kernel<1, 1, B, T>, 1);
+    if (f % 8 == 0) return launch_walk(swiglu_ring_kernel<B, T>, a, f, st, 256);
+    if (f % 2 == 0) return launch_walk(swiglu_kernel<2, 1, B, T>, a, f, st);
+    return launch_walk(swiglu_kernel<1, 1, B, T>, a, f, st);
   };
   using Int8 = std::integral_constant<int, MOE_CKPT_INT8>;
   using E4m3 = std::integral_constant<int, MOE_CKPT_E4M3>;
@@ -319,7 +492,7 @@ cudaError_t launch_ckpt_combine_bwd(const void* dy, const void* codes, int64_t l
                                     const int32_t* dest_row, int64_t T, int k, int d,
                                     int64_t rows_cap, void* dyp, float* dw, int* err,
                                     cudaStream_t st) {
-  const int64_t need = (T + WARPS - 1) / WARPS, cap = static_cast<int64_t>(sm_count()) * 8;
+  const int64_t need = (T + WARPS - 1) / WARPS, cap = static_cast<int64_t>(row_sms()) * 8;
   const dim3 grid(static_cast<unsigned>(need < cap ? need : cap));
 #define MOE_COMBINE_T(KM, TY)                                                                   \
   launch_pdl(combine_bwd_kernel<KM, TY>, grid, dim3(THREADS), 0, st, 1,                         \

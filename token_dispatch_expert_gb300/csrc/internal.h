@@ -292,21 +292,6 @@ bool fp8_codes_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld,
                    uint32_t box_rows);
 
 // ----------------------------------------------------------------- rows: norm.cu, norm_bwd.cu, ckpt.cu
-// n / per for the items of rows of `per` items each, by a multiplication: with m = floor(2^64 /
-// per) + 1 the high half of n m is exact while n * per < 2^64 (here both are far below).
-struct RowDiv {
-  uint64_t m;
-  int per;
-  explicit RowDiv(int per_row)
-      : m(per_row == 1 ? 0 : ~static_cast<uint64_t>(0) / static_cast<uint64_t>(per_row) + 1),
-        per(per_row) {}
-#ifdef __CUDACC__
-  __device__ __forceinline__ int64_t row(int64_t n) const {
-    return per == 1 ? n : static_cast<int64_t>(__umul64hi(static_cast<uint64_t>(n), m));
-  }
-#endif
-};
-
 // Rows and what is done with them; types are RowType (rows8.cuh), distances in elements.
 struct NormArgs {
   const void* x;          // the rows, or their codes

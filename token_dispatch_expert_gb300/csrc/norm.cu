@@ -148,8 +148,8 @@ norm_kernel(const __grid_constant__ NormArgs a, int nw) {
 }
 
 // The same for rows of whole 16-byte vectors, through shared memory: the rows that follow are
-// fetched while one is worked on.  nw warps share a row, N chunks to a warp; slots: 1 (the widest
-// rows: no fetching ahead) to 3.
+// fetched while one is worked on.  nw warps share a row, N chunks to a warp; slots: 2, or 1 for the
+// widest rows, which are not fetched ahead.
 template <int N, int X, bool ADD>
 __global__ void __launch_bounds__(32 * MAX_WARPS)
 norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
@@ -259,23 +259,29 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
       save_row_chunks<8, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
                             chunk, a.C, lane, reinterpret_cast<const float(*)[8]>(f));
     void* yr = row_at(a.y, row, a.ld_y, row_size(a.y_type));
+    const float2 low = both(-shift * rstd);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = chunk[i] + 8 * lane;
       if (c >= a.C) continue;
-      float2 p[4];
+      float2 p[4], b[4];
+      // xhat = (v - mean) rstd - shift rstd: the shift is the mean's rounding, far below a step of it
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        f[i][j] = __fmul2_rn(__fadd2_rn(__fadd2_rn(f[i][j], both(-mean)), both(-shift)), both(rstd));
-      if (a.gamma) {
+        f[i][j] = __ffma2_rn(__fadd2_rn(f[i][j], both(-mean)), both(rstd), low);
+      if (a.gamma && a.beta) {
+        vector_values(p, a.gamma, a.p_type, c);
+        vector_values(b, a.beta, a.p_type, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[i][j] = __ffma2_rn(f[i][j], p[j], b[j]);
+      } else if (a.gamma) {
         vector_values(p, a.gamma, a.p_type, c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i][j] = __fmul2_rn(f[i][j], p[j]);
-      }
-      if (a.beta) {
-        vector_values(p, a.beta, a.p_type, c);
+      } else if (a.beta) {
+        vector_values(b, a.beta, a.p_type, c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f[i][j] = __fadd2_rn(f[i][j], p[j]);
+        for (int j = 0; j < 4; ++j) f[i][j] = __fadd2_rn(f[i][j], b[j]);
       }
       store_pairs(yr, a.y_type, c, f[i]);
     }
@@ -347,49 +353,66 @@ norm_wide_kernel(const __grid_constant__ NormArgs a) {
   griddep_launch();
 }
 
-// Normalised rows from a checkpoint and the statistics: element by element, a warp takes N
-// chunks of 256 columns, going on over the rows' ends.
-template <int V, int N>
-__global__ void __launch_bounds__(256)
-ckpt_norm_kernel(const __grid_constant__ NormArgs a, RowDiv div) {
+// Normalised rows from a checkpoint and the statistics, N rows at a time; the columns' gamma and
+// beta stay in registers.
+template <int V, int N, int TYPE>
+__global__ void __launch_bounds__(WALK_THREADS, V == 8 ? 3 : 1)
+ckpt_norm_kernel(const __grid_constant__ NormArgs a, int per, int groups) {
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t items = a.rows * div.per;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 8 * N;
-  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * N; i0 < items;
-       i0 += step) {
-    int64_t row = div.row(i0);
-    int k = static_cast<int>(i0 - row * div.per);
+  const Walk w = walk_start(per, groups);
+  if (!w.any) return;
+  const bool layer = a.kind == MOE_NORM_LAYER;
+  const int ys = row_size(a.y_type);
+  float g[8], b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    g[j] = 1.0f;
+    b[j] = 0.0f;
+  }
+  if (a.gamma) load_values<V>(g, a.gamma, a.p_type, w.chunk, a.C, lane);
+  if (a.beta) load_values<V>(b, a.beta, a.p_type, w.chunk, a.C, lane);
+  const uint8_t* codes = static_cast<const uint8_t*>(a.x) + w.row * a.ldx;
+  const float* scales = a.x_scales + w.row * a.blocks;
+  uint8_t* y = static_cast<uint8_t*>(a.y) + w.row * a.ld_y * ys;
+  const int64_t c_step = w.groups * a.ldx, s_step = w.groups * a.blocks, y_step = w.groups * a.ld_y * ys;
+  for (int64_t row = w.row; row < a.rows; row += N * w.groups) {
     Raw8 raw[N];
     float sc[N][8 / V], mean[N], rstd[N];
-    int64_t at[N];
-    int chunk[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      at[i] = row;
-      chunk[i] = k * CHUNK;
-      if (i0 + i < items) {
-        load_raw<V>(raw[i], row_at(a.x, row, a.ldx, 1), a.src_type, chunk[i], a.C, lane);
-        load_scales<V>(sc[i], a.x_scales + row * a.blocks, 0, chunk[i], a.C, lane);
-        mean[i] = a.kind == MOE_NORM_LAYER ? a.mean[row] : 0.0f;
-        rstd[i] = a.rstd[row];
+      const int64_t r = row + i * w.groups;
+      mean[i] = 0.0f;
+      if (r < a.rows) {
+        load_raw<V>(raw[i], codes, TYPE, w.chunk, a.C, lane);
+        load_chunk_scales<V>(sc[i], scales, w.chunk, a.C, lane);
+        if (layer) mean[i] = a.mean[r];
+        rstd[i] = a.rstd[r];
       }
-      if (++k == div.per) { k = 0; ++row; }
+      codes += c_step;
+      scales += s_step;
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (i0 + i >= items) break;
-      float f[8];
-      unpack_raw<V>(raw[i], a.src_type, f);
-      scale_values<V>(f, sc[i]);
+      if (row + i * w.groups < a.rows) {
+        float f[8];
+        unpack_raw<V>(raw[i], TYPE, f);
+        scale_values<V>(f, sc[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = (f[j] - mean[i]) * rstd[i];
-      affine_store<V>(f, a, row_at(a.y, at[i], a.ld_y, row_size(a.y_type)), chunk[i], lane);
+        for (int j = 0; j < 8; j += 2) {
+          float2 v = __fadd2_rn(make_float2(f[j], f[j + 1]), both(-mean[i]));
+          v = __ffma2_rn(__fmul2_rn(v, both(rstd[i])), make_float2(g[j], g[j + 1]),
+                         make_float2(b[j], b[j + 1]));
+          f[j] = v.x;
+          f[j + 1] = v.y;
+        }
+        store_values<V>(y, a.y_type, w.chunk, a.C, lane, f);
+      }
+      y += y_step;
     }
   }
   griddep_launch();
 }
-
 
 }  // namespace
 
@@ -411,10 +434,9 @@ cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
   const int warps = nw == 1 ? 4 : nw;
   const int slot = warps * N * CHUNK * row_size(X) * (ADD ? 2 : 1);
   // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
-  int per = (N == 4 ? 640 : 1024) / (32 * warps);
-  if (per < 1) per = 1;
+  int per = ctas_by_registers<norm_ring_kernel<N, X, ADD>>(32 * warps);
   while (per > 1 && per * 2 * slot > ROW_SMEM) --per;
-  const int slots = per * 3 * slot <= ROW_SMEM ? 3 : per * 2 * slot <= ROW_SMEM ? 2 : 1;
+  const int slots = per * 2 * slot <= ROW_SMEM ? 2 : 1;
   const int64_t ctas = nw == 1 ? (a.rows + warps - 1) / warps : a.rows;
   const int64_t most = static_cast<int64_t>(row_sms()) * per;
   const int smem = slots * slot;
@@ -467,13 +489,15 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
 
 cudaError_t launch_ckpt_norm(const NormArgs& a, cudaStream_t st) {
   const int v = norm_vector(a);
-  const RowDiv div((a.C + CHUNK - 1) / CHUNK);
-  const int64_t items = a.rows * div.per, need = (items + 8 * 2 - 1) / (8 * 2);
-  const int64_t most = static_cast<int64_t>(1) << 30;
-  const dim3 grid(static_cast<unsigned>(need < most ? need : most)), block(256);
-  if (v == 8) return launch_pdl(ckpt_norm_kernel<8, 2>, grid, block, 0, st, 1, a, div);
-  if (v == 2) return launch_pdl(ckpt_norm_kernel<2, 2>, grid, block, 0, st, 1, a, div);
-  return launch_pdl(ckpt_norm_kernel<1, 2>, grid, block, 0, st, 1, a, div);
+  const WalkGrid g = walk_grid(a.rows, a.C, 64);
+  auto go = [&](auto kern) {
+    return launch_pdl(kern, g.grid, dim3(WALK_THREADS), 0, st, 1, a, g.per, g.groups);
+  };
+  if (a.src_type == ROW_INT8)
+    return v == 8 ? go(ckpt_norm_kernel<8, 4, ROW_INT8>) : v == 2 ? go(ckpt_norm_kernel<2, 2, ROW_INT8>)
+                                                                  : go(ckpt_norm_kernel<1, 2, ROW_INT8>);
+  return v == 8 ? go(ckpt_norm_kernel<8, 4, ROW_E4M3>) : v == 2 ? go(ckpt_norm_kernel<2, 2, ROW_E4M3>)
+                                                                : go(ckpt_norm_kernel<1, 2, ROW_E4M3>);
 }
 
 }  // namespace moe

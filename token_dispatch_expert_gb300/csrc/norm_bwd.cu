@@ -434,8 +434,7 @@ cudaError_t launch_ring(const NormArgs& a, int nw, cudaStream_t st, int* parts) 
                     (a.x_scales ? 128 : 0);
   const int slot = warps * (N * chunk + 256), gam = N < 4 ? warps * N * CHUNK * 4 : 0;
   // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
-  int per = (N == 1 ? 768 : 512) / (32 * warps);
-  if (per < 1) per = 1;
+  int per = ctas_by_registers<norm_bwd_ring_kernel<N, S, X, Y>>(32 * warps);
   if (per > NORM_PARTS / 152) per = NORM_PARTS / 152;
   while (per > 1 && per * (2 * slot + gam) > ROW_SMEM) --per;
   int slots = 4;

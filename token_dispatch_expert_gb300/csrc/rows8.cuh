@@ -35,52 +35,65 @@ __device__ __forceinline__ int elem_col(int chunk, int lane, int j) {
   return chunk + (j / V) * 32 * V + lane * V + j % V;
 }
 
-// The bytes of a lane's eight elements of the row at `row`; columns from C on are zeros.
+// The bytes of a lane's eight elements of the row at `row`; columns from C on are zeros.  Whole
+// chunks, which most are, are read without a condition on every vector.
+template <int V, bool ALL>
+__device__ __forceinline__ void load_vectors(Raw8& r, const uint8_t* p, int type, int chunk, int C,
+                                             int lane) {
+#pragma unroll
+  for (int i = 0; i < 8 / V; ++i) {
+    const int c = elem_col<V>(chunk, lane, i * V);
+    if (V == 2) {
+      if (type == ROW_FP32) {
+        uint2 v = make_uint2(0, 0);
+        if (ALL || c < C) v = *reinterpret_cast<const uint2*>(p + 4 * static_cast<int64_t>(c));
+        r.w[2 * i] = v.x;
+        r.w[2 * i + 1] = v.y;
+      } else {
+        r.w[i] = 0;
+        if (ALL || c < C)
+          r.w[i] = type == ROW_BF16
+                       ? *reinterpret_cast<const uint32_t*>(p + 2 * static_cast<int64_t>(c))
+                       : static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + c));
+      }
+    } else {
+      r.w[i] = 0;
+      if (ALL || c < C)
+        r.w[i] = type == ROW_BF16 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p + 2 * static_cast<int64_t>(c)))
+                 : type == ROW_FP32 ? *reinterpret_cast<const uint32_t*>(p + 4 * static_cast<int64_t>(c))
+                                    : static_cast<uint32_t>(p[c]);
+    }
+  }
+}
 template <int V>
 __device__ __forceinline__ void load_raw(Raw8& r, const void* row, int type, int chunk, int C,
                                          int lane) {
   const uint8_t* p = static_cast<const uint8_t*>(row);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) r.w[j] = 0;
-  if (V == 8) {
-    const int c = chunk + 8 * lane;
-    if (c >= C) return;
-    if (type == ROW_BF16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p + 2 * static_cast<int64_t>(c));
-      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-    } else if (type == ROW_FP32) {
+  if (V < 8) {
+    if (chunk + CHUNK <= C) load_vectors<V, true>(r, p, type, chunk, C, lane);
+    else load_vectors<V, false>(r, p, type, chunk, C, lane);
+    return;
+  }
+  const int c = chunk + 8 * lane;
+  uint4 v = make_uint4(0, 0, 0, 0), u = v;
+  if (type == ROW_BF16) {
+    if (c < C) v = *reinterpret_cast<const uint4*>(p + 2 * static_cast<int64_t>(c));
+  } else if (type == ROW_FP32) {
+    if (c < C) {
       const uint4* q = reinterpret_cast<const uint4*>(p + 4 * static_cast<int64_t>(c));
-      const uint4 v = q[0], u = q[1];
-      r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-      r.w[4] = u.x; r.w[5] = u.y; r.w[6] = u.z; r.w[7] = u.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(p + c);
-      r.w[0] = v.x; r.w[1] = v.y;
+      v = q[0];
+      u = q[1];
     }
-  } else if (V == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = elem_col<V>(chunk, lane, 2 * i);
-      if (c >= C) continue;
-      if (type == ROW_BF16) {
-        r.w[i] = *reinterpret_cast<const uint32_t*>(p + 2 * static_cast<int64_t>(c));
-      } else if (type == ROW_FP32) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * static_cast<int64_t>(c));
-        r.w[2 * i] = v.x; r.w[2 * i + 1] = v.y;
-      } else {
-        r.w[i] = *reinterpret_cast<const uint16_t*>(p + c);
-      }
-    }
+    r.w[4] = u.x; r.w[5] = u.y; r.w[6] = u.z; r.w[7] = u.w;
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = elem_col<V>(chunk, lane, j);
-      if (c >= C) continue;
-      if (type == ROW_BF16) r.w[j] = *reinterpret_cast<const uint16_t*>(p + 2 * static_cast<int64_t>(c));
-      else if (type == ROW_FP32) r.w[j] = *reinterpret_cast<const uint32_t*>(p + 4 * static_cast<int64_t>(c));
-      else r.w[j] = p[c];
+    if (c < C) {
+      const uint2 t = *reinterpret_cast<const uint2*>(p + c);
+      v.x = t.x;
+      v.y = t.y;
     }
   }
+  r.w[0] = v.x; r.w[1] = v.y;
+  if (type == ROW_BF16 || type == ROW_FP32) { r.w[2] = v.z; r.w[3] = v.w; }
 }
 
 // Byte i of w as a number: with the sign bit flipped it is a whole number from 0 to 255 above
@@ -131,40 +144,43 @@ __device__ __forceinline__ void load_values(float* f, const void* row, int type,
 }
 
 // Store a lane's eight values, rounded to nearest where the type is bf16.
-template <int V>
-__device__ __forceinline__ void store_values(void* row, int type, int chunk, int C, int lane,
-                                             const float* f) {
-  uint8_t* p = static_cast<uint8_t*>(row);
-  if (V == 8) {
-    const int c = chunk + 8 * lane;
-    if (c >= C) return;
-    if (type == ROW_BF16) {
-      *reinterpret_cast<uint4*>(p + 2 * static_cast<int64_t>(c)) = pack8(f);
-    } else {
-      float4* q = reinterpret_cast<float4*>(p + 4 * static_cast<int64_t>(c));
-      q[0] = make_float4(f[0], f[1], f[2], f[3]);
-      q[1] = make_float4(f[4], f[5], f[6], f[7]);
-    }
-  } else if (V == 2) {
+template <int V, bool ALL>
+__device__ __forceinline__ void store_vectors(uint8_t* p, int type, int chunk, int C, int lane,
+                                              const float* f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = elem_col<V>(chunk, lane, 2 * i);
-      if (c >= C) continue;
+  for (int i = 0; i < 8 / V; ++i) {
+    const int c = elem_col<V>(chunk, lane, i * V);
+    if (!ALL && c >= C) continue;
+    if (V == 2) {
       if (type == ROW_BF16)
         *reinterpret_cast<uint32_t*>(p + 2 * static_cast<int64_t>(c)) = pack_bf16x2(f[2 * i], f[2 * i + 1]);
       else
         *reinterpret_cast<float2*>(p + 4 * static_cast<int64_t>(c)) = make_float2(f[2 * i], f[2 * i + 1]);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = elem_col<V>(chunk, lane, j);
-      if (c >= C) continue;
+    } else {
       if (type == ROW_BF16)
-        *reinterpret_cast<__nv_bfloat16*>(p + 2 * static_cast<int64_t>(c)) = __float2bfloat16_rn(f[j]);
+        *reinterpret_cast<__nv_bfloat16*>(p + 2 * static_cast<int64_t>(c)) = __float2bfloat16_rn(f[i]);
       else
-        *reinterpret_cast<float*>(p + 4 * static_cast<int64_t>(c)) = f[j];
+        *reinterpret_cast<float*>(p + 4 * static_cast<int64_t>(c)) = f[i];
     }
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_values(void* row, int type, int chunk, int C, int lane,
+                                             const float* f) {
+  uint8_t* p = static_cast<uint8_t*>(row);
+  if (V < 8) {
+    if (chunk + CHUNK <= C) store_vectors<V, true>(p, type, chunk, C, lane, f);
+    else store_vectors<V, false>(p, type, chunk, C, lane, f);
+    return;
+  }
+  const int c = chunk + 8 * lane;
+  if (c >= C) return;
+  if (type == ROW_BF16) {
+    *reinterpret_cast<uint4*>(p + 2 * static_cast<int64_t>(c)) = pack8(f);
+  } else {
+    float4* q = reinterpret_cast<float4*>(p + 4 * static_cast<int64_t>(c));
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
   }
 }
 
@@ -181,10 +197,26 @@ __device__ __forceinline__ void load_scales(float* s, const float* row_scales, i
     s[i] = c < C ? row_scales[(first + c) >> 7] : 0.0f;
   }
 }
+// the same where the chunk starts at a block's border: two blocks at most to a lane
+template <int V>
+__device__ __forceinline__ void load_chunk_scales(float* s, const float* row_scales, int chunk, int C,
+                                                  int lane) {
+  if (V == 8) {
+    load_scales<V>(s, row_scales, 0, chunk, C, lane);
+    return;
+  }
+  const float lo = row_scales[chunk >> 7], hi = chunk + 128 < C ? row_scales[(chunk >> 7) + 1] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8 / V; ++i) s[i] = i < 4 / V ? lo : hi;
+}
 template <int V>
 __device__ __forceinline__ void scale_values(float* f, const float* s) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] *= s[j / V];
+  for (int j = 0; j < 8; j += 2) {
+    const float2 p = __fmul2_rn(make_float2(f[j], f[j + 1]), make_float2(s[j / V], s[(j + 1) / V]));
+    f[j] = p.x;
+    f[j + 1] = p.y;
+  }
 }
 
 // ------------------------------------------------------------------ rows through shared memory
@@ -300,25 +332,30 @@ constexpr float CKPT_AMAX_FLOOR = 0x1p-110f;
 __device__ __forceinline__ float ckpt_top(int format) {
   return format == MOE_CKPT_INT8 ? 127.0f : 448.0f;
 }
-// of two magnitudes the larger; a NaN wins
+// of two magnitudes the larger, of three numbers the largest magnitude; a NaN wins
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+__device__ __forceinline__ float max_mag3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // The largest magnitudes of a lane's block(s): m[0] for V = 8 (the lane's half), m[0] and m[1]
-// for V = 2 and 1; complete after block_max over the warp.
+// for V = 2 and 1; complete after the exchange over the warp.
 template <int V>
 __device__ __forceinline__ void lane_max(const float* f, float* m) {
+  if (V == 8) {
+    m[0] = max_mag3(max_mag3(f[0], f[1], f[2]), f[3], f[4]);
+    m[0] = m[1] = max_mag3(max_mag3(m[0], f[5], f[6]), f[7], 0.0f);
+  } else {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float a = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) a = max_nan(a, fabsf(f[4 * h + j]));
-    m[h] = a;
+    for (int h = 0; h < 2; ++h)
+      m[h] = max_mag3(max_mag3(f[4 * h], f[4 * h + 1], f[4 * h + 2]), f[4 * h + 3], 0.0f);
   }
-  if (V == 8) m[0] = m[1] = max_nan(m[0], m[1]);
 }
 
 // scale and factor of a block
@@ -512,6 +549,60 @@ __device__ __forceinline__ void* row_at(void* p, int64_t row, int64_t ld, int si
   return static_cast<uint8_t*>(p) + row * ld * size;
 }
 
+// ------------------------------------------------------------------ columns that stay
+// What has no sums over a row goes down the columns: a warp keeps one chunk of 256 columns and takes
+// every `groups`-th row, so that the columns' conditions and parameters are found once and a row's
+// address is the last one's plus a constant.
+constexpr int WALK_THREADS = 256, WALK_WARPS = WALK_THREADS / 32;
+struct Walk {
+  int chunk;
+  int64_t row, groups;
+  bool any;
+};
+__device__ __forceinline__ Walk walk_start(int per, int groups) {
+  const unsigned gw = blockIdx.x * WALK_WARPS + (threadIdx.x >> 5);
+  Walk w;
+  w.row = gw / static_cast<unsigned>(per);
+  w.chunk = static_cast<int>(gw - static_cast<unsigned>(w.row) * per) * CHUNK;
+  w.groups = groups;
+  w.any = w.row < groups;
+  return w;
+}
+// how many groups of warps: enough for `warps` to an SM, no more than rows
+struct WalkGrid {
+  int per, groups;
+  dim3 grid;
+};
+inline int row_sms() {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+// CTAs of a kernel that an SM holds by its registers
+template <auto KERNEL>
+inline int ctas_by_registers(int threads) {
+  static const int regs = [] {   // (of this kernel, whatever the device: one architecture)
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, KERNEL) == cudaSuccess ? (f.numRegs + 7) / 8 * 8 : 128;
+  }();
+  int n = 65536 / (regs * threads);
+  if (n > 2048 / threads) n = 2048 / threads;
+  return n < 1 ? 1 : n;
+}
+inline WalkGrid walk_grid(int64_t rows, int C, int warps) {
+  WalkGrid g;
+  g.per = (C + CHUNK - 1) / CHUNK;
+  // (not so many that a warp has fewer than 16 rows, down to what runs at once)
+  const int64_t most = rows * g.per / (16 * static_cast<int64_t>(row_sms()));
+  if (warps > most) warps = static_cast<int>(most < 32 ? 32 : most);
+  int64_t n = (static_cast<int64_t>(row_sms()) * warps + g.per - 1) / g.per;
+  if (n > rows) n = rows;
+  g.groups = static_cast<int>(n < 1 ? 1 : n);
+  g.grid = dim3(static_cast<unsigned>((static_cast<int64_t>(g.groups) * g.per + WALK_WARPS - 1) / WALK_WARPS));
+  return g;
+}
+
 // ------------------------------------------------------------------ host: which V
 // Rows at p, `ld` elements of `size` bytes apart.
 inline bool rows_fit(const void* p, int64_t ld, int size, int v) {
@@ -521,11 +612,5 @@ inline bool rows_fit(const void* p, int64_t ld, int size, int v) {
 __host__ __device__ inline int row_size(int type) { return type == ROW_BF16 ? 2 : type == ROW_FP32 ? 4 : 1; }
 
 constexpr int ROW_SMEM = 216 * 1024;   // of an SM's shared memory, for the rows in flight
-inline int row_sms() {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
 
 }  // namespace moe
