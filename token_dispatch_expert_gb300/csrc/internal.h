@@ -308,6 +308,7 @@ struct NormArgs {
   void* dgamma;           // may be null
   void* dbeta;            // may be null
   float* part;            // the rows' sums of the CTAs
+  int* err;               // error word; may be null
   int64_t rows, ldx, ld_add, ld_y, ld_out, ld_codes;
   int C, blocks;          // blocks: ceil(C / 128)
   int kind, format;

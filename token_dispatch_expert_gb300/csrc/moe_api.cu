@@ -1236,6 +1236,7 @@ moe_status_t moe_norm_bwd(const moe_norm_t* p, const void* dy, const void* x, co
   a.dgamma = dgamma;
   a.dbeta = dbeta;
   a.part = ws ? at<float>(ws, WS_HEADER_BYTES) : nullptr;
+  a.err = static_cast<int*>(ws);
   return cuda_status(launch_norm_bwd(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -133,128 +133,133 @@ norm_bwd_kernel(const __grid_constant__ NormArgs a, int nw) {
   }
 }
 
-// The same for rows of whole 16-byte vectors, through shared memory: dy, v (with its scales), add
-// and the statistics of the rows that follow are fetched while one is worked on; gamma stays
-// there too, but for the widest rows, whose slots leave it no room.  With up to two chunks to a
-// warp a row's G and xhat stay in registers between the two passes over it, with four they are
-// computed again, from the slot.  S: the type of v or its codes, X: of add and dx, Y: of dy.
+// The same for rows of whole 16-byte vectors.  dy, v and add of the rows that follow come into
+// shared memory by bulk copies while one is worked on; the statistics and a chunk's scale are loaded
+// a row ahead.  With nw > 1 thread 0 copies for the CTA: when all have passed the barrier in a row's
+// sums, all are done with the row before, whose slot is filled again.  With nw = 1 lane 0 copies for
+// its warp.  gamma lies in shared memory too (but for the widest rows, which leave it no room): from
+// L1, which the slots leave little of, it came from L2 for every row, and 16384 x 4096 took 107 us
+// instead of 90.  With up to two chunks to a warp a row's G and xhat stay in registers between the two
+// passes over it, with four they are computed again, from the slot.  S: the type of v or its codes,
+// X: of add and dx, Y: of dy.
+constexpr int MAX_SLOTS = 4;
+constexpr long long BULK_BUDGET = 4000000000LL;   // clock cycles (about 2 s)
+
 template <int N, int S, int X, int Y>
 __global__ void __launch_bounds__(N == 1 ? 256 : 32 * MAX_WARPS, N == 1 ? 3 : 1)
 norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
-  griddep_wait();
   __shared__ RowSums sh;
+  __shared__ __align__(8) uint64_t full[MAX_WARPS][MAX_SLOTS];
+  __shared__ int gave_up;
   extern __shared__ __align__(16) uint8_t ring[];
-  row_sum_init(sh);
-  constexpr bool GAMMA = N < 4, KEEP = N < 4, CODES = S == ROW_INT8 || S == ROW_E4M3;
+  constexpr bool KEEP = N < 4, GAMMA = N < 4, CODES = S == ROW_INT8 || S == ROW_E4M3;
   constexpr int XS = X == ROW_BF16 ? 2 : 4, YS = Y == ROW_BF16 ? 2 : 4;
   constexpr int SS = CODES ? 1 : S == ROW_BF16 ? 2 : 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int w = nw == 1 ? 0 : warp;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (nw == 1 ? warps : 1);
-  const int64_t first = nw == 1 ? static_cast<int64_t>(blockIdx.x) * warps + warp : blockIdx.x;
+  const int w = nw == 1 ? 0 : warp, own = nw == 1 ? warp : 0;
+  const bool copies = nw == 1 ? lane == 0 : threadIdx.x == 0;
+  if (copies)
+    for (int s = 0; s < slots; ++s) mbar_init(smem_u32(&full[own][s]), 1);
+  if (threadIdx.x == 0) gave_up = 0;
+  fence_mbar_init();
+  row_sum_init(sh);
+  griddep_wait();   // see common.cuh: dependent launches
+  // (32 bits hold every row and the few steps past the last one)
+  const uint32_t rows = static_cast<uint32_t>(a.rows), step = gridDim.x * (nw == 1 ? warps : 1);
+  const uint32_t first = nw == 1 ? blockIdx.x * warps + warp : blockIdx.x;
   const float over = 1.0f / static_cast<float>(a.C);
   const bool layer = a.kind == MOE_NORM_LAYER, add = a.add != nullptr;
-  // a warp's part of a slot: per chunk dy, v, its scales and add, then the statistics
-  constexpr int AT_X = CHUNK * YS, AT_SC = AT_X + CHUNK * SS, AT_ADD = AT_SC + (CODES ? 128 : 0);
-  const int chunk_bytes = AT_ADD + (add ? CHUNK * XS : 0), warp_bytes = N * chunk_bytes + 256;
-  const int slot_bytes = warps * warp_bytes;
-  uint8_t* const mine = ring + warp * warp_bytes;
-  uint8_t* const gam = ring + slots * slot_bytes + warp * N * CHUNK * 4;   // fp32
+  // a slot: dy, v, add, each a whole row and up to 16 bytes
+  const int y_bytes = a.C * YS, x_bytes = (a.C * SS + 15) / 16 * 16, a_bytes = add ? a.C * XS : 0;
+  const int slot_bytes = y_bytes + x_bytes + a_bytes;
+  uint8_t* const gam = ring + warp * N * 1024;   // each thread's gamma in fp32, then the slots
+  uint8_t* const mine = ring + (GAMMA ? warps * N * 1024 : 0) + own * slots * slot_bytes;
+  auto at = [](const void* p, uint32_t row, int64_t ld) {
+    return static_cast<const uint8_t*>(p) + static_cast<int64_t>(row) * ld;
+  };
+  uint32_t odd = 0, started = 0;   // of the copying thread: slots filled an odd number of times, ever
+  auto fetch = [&](uint32_t row, int slot) {
+    if (*static_cast<volatile int*>(&gave_up)) return;
+    odd ^= 1u << slot;
+    started |= 1u << slot;
+    const uint32_t bar = smem_u32(&full[own][slot]), to = smem_u32(mine + slot * slot_bytes);
+    mbar_arrive_expect_tx(bar, slot_bytes);
+    bulk_load(to, at(a.y, row, a.ld_y * YS), y_bytes, bar);
+    bulk_load(to + y_bytes, at(a.x, row, a.ldx * SS), x_bytes, bar);
+    if (add) bulk_load(to + y_bytes + x_bytes, at(a.add, row, a.ld_add * XS), a_bytes, bar);
+  };
+  if (copies)
+    for (int s = 0; s < (slots > 1 ? slots - 1 : 1); ++s)
+      if (first + s * step < rows) fetch(first + s * step, s);
   float2 dg[N][4], db[N][4];
-  int chunk[N];
+  int col[N];
+  float sc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    chunk[i] = (i * nw + w) * CHUNK;
+    col[i] = (i * nw + w) * CHUNK + 8 * lane;
+    sc[i] = 0.0f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) dg[i][j] = db[i][j] = both(0.0f);
-    const int c = chunk[i] + 8 * lane;
-    float2 p[4] = {both(1.0f), both(1.0f), both(1.0f), both(1.0f)};
-    if (c < a.C) {
-      if (GAMMA && a.gamma) vector_values(p, a.gamma, a.p_type, c);
-    } else {
-      for (int s = 0; s < slots; ++s) {
-        uint8_t* z = mine + s * slot_bytes + i * chunk_bytes;
-        clear_chunk(z, Y, lane);
-        clear_chunk(z + AT_X, S, lane);
-        if (CODES) *reinterpret_cast<float*>(z + AT_SC + 4 * lane) = 0.0f;
-        if (add) clear_chunk(z + AT_ADD, X, lane);
-      }
-    }
-    if (!GAMMA) continue;
-    *reinterpret_cast<float4*>(gam + i * 1024 + 16 * lane) = make_float4(p[0].x, p[0].y, p[1].x, p[1].y);
-    *reinterpret_cast<float4*>(gam + i * 1024 + 512 + 16 * lane) =
-        make_float4(p[2].x, p[2].y, p[3].x, p[3].y);
   }
-  const uint8_t* yr = static_cast<const uint8_t*>(row_at(static_cast<const void*>(a.y), first, a.ld_y, YS));
-  const uint8_t* xr = static_cast<const uint8_t*>(row_at(a.x, first, a.ldx, SS));
-  const uint8_t* ar = static_cast<const uint8_t*>(row_at(a.add, first, a.ld_add, XS));
-  const int64_t y_step = step * a.ld_y * YS, x_step = step * a.ldx * SS, a_step = step * a.ld_add * XS;
-  int64_t next = first;
-  auto fetch = [&](int slot) {
-    if (next < a.rows) {
-      uint8_t* to = mine + slot * slot_bytes;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        uint8_t* t = to + i * chunk_bytes;
-        copy_chunk(t, yr, Y, chunk[i], a.C, lane);
-        copy_chunk(t + AT_X, xr, S, chunk[i], a.C, lane);
-        const int c = chunk[i] + 8 * lane;
-        if (CODES && c < a.C)
-          copy_async4(smem_u32(t + AT_SC + 4 * lane), a.x_scales + next * a.blocks + (c >> 7));
-        if (add) copy_chunk(t + AT_ADD, ar, X, chunk[i], a.C, lane);
-      }
-      const uint32_t st = smem_u32(to + N * chunk_bytes + 8 * lane);
-      if (layer) copy_async4(st, a.mean + next);
-      copy_async4(st + 4, a.rstd + next);
-      yr += y_step;
-      xr += x_step;
-      ar += a_step;
-      next += step;
-    }
-    copy_commit();
-  };
-  // G and xhat of a chunk in a slot
-  auto values = [&](const uint8_t* t, int i, float2 st, float2* g, float2* xh, bool sums) {
-    float2 p[4];
-    slot_values(g, t, Y, lane);
-    slot_values(xh, t + AT_X, S, lane);
+  float mean = 0.0f, rstd = 0.0f;
+  auto small = [&](uint32_t row) {
+    if (layer) mean = a.mean[row];
+    rstd = a.rstd[row];
     if (CODES) {
-      const float sc = *reinterpret_cast<const float*>(t + AT_SC + 4 * lane);
+      const float* sr = a.x_scales + static_cast<int64_t>(row) * a.blocks;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) xh[j] = __fmul2_rn(xh[j], both(sc));
+      for (int i = 0; i < N; ++i)
+        if (col[i] < a.C) sc[i] = sr[col[i] >> 7];
     }
-    if (GAMMA) {
-      slot_values(p, gam + i * 1024, ROW_FP32, lane);
-    } else {
+  };
+  // G and xhat of a chunk in a slot; past the row's end zeros
+  auto values = [&](const uint8_t* t, int i, float2 st, float scale, float2* g, float2* xh, bool sums) {
+    if (col[i] >= a.C) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = both(1.0f);
-      if (a.gamma && chunk[i] + 8 * lane < a.C) vector_values(p, a.gamma, a.p_type, chunk[i] + 8 * lane);
+      for (int j = 0; j < 4; ++j) g[j] = xh[j] = both(0.0f);
+      return;
     }
+    float2 p[4];
+    smem_row_values<Y>(g, t, col[i]);
+    smem_row_values<S>(xh, t + y_bytes, col[i]);
+    if (GAMMA) slot_values(p, gam + i * 1024, ROW_FP32, lane);
+    else if (a.gamma) vector_values(p, a.gamma, a.p_type, col[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (CODES) xh[j] = __fmul2_rn(xh[j], both(scale));
       xh[j] = __fmul2_rn(__fadd2_rn(xh[j], both(-st.x)), both(st.y));
       if (sums) {
         dg[i][j] = __ffma2_rn(g[j], xh[j], dg[i][j]);
         db[i][j] = __fadd2_rn(db[i][j], g[j]);
       }
-      g[j] = __fmul2_rn(g[j], p[j]);
+      if (GAMMA || a.gamma) g[j] = __fmul2_rn(g[j], p[j]);
     }
   };
-  for (int s = 0; s + 1 < slots; ++s) fetch(s);
-  int slot = 0, ahead = slots - 1, turn = 0;
-  for (int64_t row = first; row < a.rows; row += step) {
-    fetch(ahead);
-    if (++ahead == slots) ahead = 0;
-    copy_wait(slots - 1);
+  if (GAMMA)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float2 p[4] = {both(1.0f), both(1.0f), both(1.0f), both(1.0f)};
+      if (a.gamma && col[i] < a.C) vector_values(p, a.gamma, a.p_type, col[i]);
+      *reinterpret_cast<float4*>(gam + i * 1024 + 16 * lane) = make_float4(p[0].x, p[0].y, p[1].x, p[1].y);
+      *reinterpret_cast<float4*>(gam + i * 1024 + 512 + 16 * lane) = make_float4(p[2].x, p[2].y, p[3].x, p[3].y);
+    }
+  if (first < rows) small(first);
+  int slot = 0, turn = 0;
+  uint32_t phase = 0;
+  for (uint32_t row = first; row < rows; row += step) {
+    const float2 st = make_float2(mean, rstd);
+    float s0[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) s0[i] = sc[i];
+    if (row + step < rows) small(row + step);
+    // (one that gives up goes on, so that the barriers below stay whole: the error word says so)
+    mbar_wait_bounded(smem_u32(&full[own][slot]), phase, &gave_up, a.err, BULK_BUDGET);
     const uint8_t* from = mine + slot * slot_bytes;
-    if (++slot == slots) slot = 0;
-    float2 st = *reinterpret_cast<const float2*>(from + N * chunk_bytes + 8 * lane);
-    if (!layer) st.x = 0.0f;
     float2 g[KEEP ? N : 1][4], xh[KEEP ? N : 1][4], c1 = both(0.0f), c2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int k = KEEP ? i : 0;
-      values(from + i * chunk_bytes, i, st, g[k], xh[k], true);
+      values(from, i, st, s0[i], g[k], xh[k], true);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         c1 = __fadd2_rn(c1, g[k][j]);
@@ -263,33 +268,56 @@ norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
     }
     const float2 c = row_sum2(c1.x + c1.y, c2.x + c2.y, sh, turn, w, nw);
     turn ^= 1;
+    if (nw == 1) __syncwarp();
+    if (copies) {
+      // the slot of the row before is free; with one slot it is this row's, filled below
+      const uint32_t next = row + (slots - 1) * step;
+      if (slots > 1 && next < rows) fetch(next, slot == 0 ? slots - 1 : slot - 1);
+    }
     const float m1 = layer ? -c.x * over : 0.0f, m2 = -c.y * over;
-    void* dr = row_at(a.out, row, a.ld_out, XS);
+    uint8_t* dr = const_cast<uint8_t*>(at(a.out, row, a.ld_out * XS));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int k = KEEP ? i : 0;
-      if (!KEEP) values(from + i * chunk_bytes, i, st, g[k], xh[k], false);
+      if (!KEEP) values(from, i, st, s0[i], g[k], xh[k], false);
+      if (col[i] >= a.C) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         g[k][j] = __fmul2_rn(__ffma2_rn(xh[k][j], both(m2), __fadd2_rn(g[k][j], both(m1))), both(st.y));
       if (add) {
         float2 p[4];
-        slot_values(p, from + i * chunk_bytes + AT_ADD, X, lane);
+        smem_row_values<X>(p, from + y_bytes + x_bytes, col[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) g[k][j] = __fadd2_rn(g[k][j], p[j]);
       }
-      const int col = chunk[i] + 8 * lane;
-      if (col < a.C) store_pairs(dr, X, col, g[k]);
+      store_pairs(dr, X, col[i], g[k]);
     }
+    if (slots == 1) {
+      if (nw == 1) __syncwarp();
+      else __syncthreads();
+      if (copies && row + step < rows) fetch(row + step, 0);
+    }
+    if (++slot == slots) {
+      slot = 0;
+      phase ^= 1;
+    }
+  }
+  if (copies && *static_cast<volatile int*>(&gave_up)) {
+    // a copy may still be under way: this CTA's shared memory is not left to it
+    const long long t0 = clock64();
+    for (int s = 0; s < slots; ++s)
+      if (started >> s & 1)
+        while (!mbar_try_wait(smem_u32(&full[own][s]), (odd >> s & 1) ^ 1) && clock64() - t0 < BULK_BUDGET / 4) {
+        }
   }
   griddep_launch();
   if (!a.part) return;
   const int64_t wide = norm_part_floats(a.C) / 2;
   float* out = a.part + 2 * wide * blockIdx.x;
   if (nw == 1) {
-    // the warps' sums one after another, so that their order is fixed (the copies are done: every
-    // group up to the last row's was waited for, and those behind it are empty)
-    float2* columns = reinterpret_cast<float2*>(ring);
+    // the warps' sums one after another, so that their order is fixed (every copy has been waited
+    // for: none was started for rows past the last one)
+    float2* cols = reinterpret_cast<float2*>(ring);
     __syncthreads();
     for (int k = 0; k < warps; ++k) {
       if (warp == k) {
@@ -297,7 +325,7 @@ norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
         for (int i = 0; i < N; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            float2* p = columns + (i * 4 + j) * 64 + lane;
+            float2* p = cols + (i * 4 + j) * 64 + lane;
             if (k > 0) {
               dg[i][j] = __fadd2_rn(dg[i][j], p[0]);
               db[i][j] = __fadd2_rn(db[i][j], p[32]);
@@ -312,10 +340,9 @@ norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int c = chunk[i] + 8 * lane;
-    if (c >= a.C) continue;
-    store_pairs(out, ROW_FP32, c, dg[i]);
-    store_pairs(out + wide, ROW_FP32, c, db[i]);
+    if (col[i] >= a.C) continue;
+    store_pairs(out, ROW_FP32, col[i], dg[i]);
+    store_pairs(out + wide, ROW_FP32, col[i], db[i]);
   }
 }
 
@@ -428,18 +455,18 @@ norm_sum_kernel(const float* part, int parts, int64_t wide, int C, void* dgamma,
 
 template <int N, int S, int X, int Y>
 cudaError_t launch_ring(const NormArgs& a, int nw, cudaStream_t st, int* parts) {
-  auto kern = norm_bwd_ring_kernel<N, S, X, Y>;
+  constexpr auto kern = norm_bwd_ring_kernel<N, S, X, Y>;
   const int warps = nw == 1 ? 8 : nw;
-  const int chunk = CHUNK * (row_size(Y) + row_size(S) + (a.add ? row_size(X) : 0)) +
-                    (a.x_scales ? 128 : 0);
-  const int slot = warps * (N * chunk + 256), gam = N < 4 ? warps * N * CHUNK * 4 : 0;
-  // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
-  int per = ctas_by_registers<norm_bwd_ring_kernel<N, S, X, Y>>(32 * warps);
+  const int row = a.C * row_size(Y) + (a.C * row_size(S) + 15) / 16 * 16 + (a.add ? a.C * row_size(X) : 0);
+  const int slot = nw == 1 ? warps * row : row, least = nw == 1 ? 2 * N * CHUNK * 4 : 0;
+  const int gam = N < 4 ? warps * N * 1024 : 0;
+  // CTAs to an SM by registers, then as many slots as their shared memory allows
+  int per = ctas_by_registers<kern>(32 * warps);
   if (per > NORM_PARTS / 152) per = NORM_PARTS / 152;
   while (per > 1 && per * (2 * slot + gam) > ROW_SMEM) --per;
-  int slots = 4;
+  int slots = MAX_SLOTS;
   while (slots > 1 && per * (slots * slot + gam) > ROW_SMEM) --slots;
-  const int smem = slots * slot + gam;
+  const int smem = (slots * slot > least ? slots * slot : least) + gam;
   if (smem > 47 * 1024) {   // (the kernel has a little of its own)
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

@@ -502,15 +502,57 @@ __device__ __forceinline__ void save_row_chunks(void* codes, float* scales, int 
   save_chunks<V, N>(c, s, format, chunk, C, lane, f);
 }
 
+// Whole rows through shared memory by bulk copies: a lane's eight values at column `col` of a row.
+template <int TYPE>
+__device__ __forceinline__ void smem_row_values(float2* v, const uint8_t* row, int col) {
+  if constexpr (TYPE == ROW_BF16) {
+    const uint4 r = *reinterpret_cast<const uint4*>(row + 2 * col);
+    v[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
+    v[1] = make_float2(bf16_lo(r.y), bf16_hi(r.y));
+    v[2] = make_float2(bf16_lo(r.z), bf16_hi(r.z));
+    v[3] = make_float2(bf16_lo(r.w), bf16_hi(r.w));
+  } else if constexpr (TYPE == ROW_FP32) {
+    const float4 a = *reinterpret_cast<const float4*>(row + 4 * col);
+    const float4 b = *reinterpret_cast<const float4*>(row + 4 * col + 16);
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+  } else {
+    const uint2 r = *reinterpret_cast<const uint2*>(row + col);
+    if constexpr (TYPE == ROW_INT8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t u = (j < 2 ? r.x : r.y) ^ 0x80808080u;
+        v[j] = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u | (j % 2 * 2))),
+                                      __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u | (j % 2 * 2 + 1)))),
+                          both(-8388736.0f));
+      }
+    } else {
+      v[0] = e4m3_values(r.x);
+      v[1] = e4m3_values(r.x >> 16);
+      v[2] = e4m3_values(r.y);
+      v[3] = e4m3_values(r.y >> 16);
+    }
+  }
+}
+// untiled bulk copy global -> shared of a multiple of 16 bytes between 16-byte addresses
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 // ------------------------------------------------------------------ sums over a row
 constexpr int MAX_WARPS = 16;   // of a row that stays in registers: 16 * 4 chunks of 256 columns
 
 struct RowSums {
-  float part[2][2][MAX_WARPS];   // [buffer][which sum][warp]
+  float part[2][4][MAX_WARPS];   // [buffer][which sum][warp]
 };
 // Before the first sum: the parts that no warp writes are zeros, so that they are read by fours.
 __device__ __forceinline__ void row_sum_init(RowSums& sh) {
-  for (int i = threadIdx.x; i < 4 * MAX_WARPS; i += blockDim.x) (&sh.part[0][0][0])[i] = 0.0f;
+  for (int i = threadIdx.x; i < 8 * MAX_WARPS; i += blockDim.x) (&sh.part[0][0][0])[i] = 0.0f;
   __syncthreads();
 }
 __device__ __forceinline__ float row_total(const float* part, int nw) {
@@ -541,6 +583,23 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, RowSums& sh, int tu
   if ((lane & 15) == 0) sh.part[turn][lane >> 4][warp] = v;
   __syncthreads();
   return make_float2(row_total(sh.part[turn][0], nw), row_total(sh.part[turn][1], nw));
+}
+// of four numbers: after two exchanges a quarter of the warp has one each
+__device__ __forceinline__ float4 row_sum4(float4 a, RowSums& sh, int turn, int warp, int nw) {
+  const int lane = threadIdx.x & 31;
+  const bool up = lane & 16, hi = lane & 8;
+  float p = (up ? a.z : a.x) + __shfl_xor_sync(FULL_MASK, up ? a.x : a.z, 16);
+  const float q = (up ? a.w : a.y) + __shfl_xor_sync(FULL_MASK, up ? a.y : a.w, 16);
+  p = (hi ? q : p) + __shfl_xor_sync(FULL_MASK, hi ? p : q, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) p += __shfl_xor_sync(FULL_MASK, p, o);
+  if (nw == 1)
+    return make_float4(__shfl_sync(FULL_MASK, p, 0), __shfl_sync(FULL_MASK, p, 8),
+                       __shfl_sync(FULL_MASK, p, 16), __shfl_sync(FULL_MASK, p, 24));
+  if ((lane & 7) == 0) sh.part[turn][lane >> 3][warp] = p;
+  __syncthreads();
+  return make_float4(row_total(sh.part[turn][0], nw), row_total(sh.part[turn][1], nw),
+                     row_total(sh.part[turn][2], nw), row_total(sh.part[turn][3], nw));
 }
 __device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t ld, int size) {
   return static_cast<const uint8_t*>(p) + row * ld * size;
