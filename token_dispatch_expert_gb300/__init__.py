@@ -12,6 +12,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from ._build import LIB_PATH, build  # noqa: F401
@@ -715,12 +716,27 @@ def _load_row_types():
     _formats.update({torch.int8: 0, torch.float8_e4m3fn: 1})
 
 
+# A small call's time is the host's.  The structs depend on sizes, types and distances alone and are
+# never changed, so one of each is kept and passed by its address.
+@functools.lru_cache(maxsize=1024)
+def _norm_struct(*fields):
+    p = _NormC(*fields)
+    return p, _addr(p)
+
+
+@functools.lru_cache(maxsize=1024)
+def _ckpt_struct(*fields):
+    p = _CkptC(*fields)
+    return p, _addr(p)
+
+
 def _row_type(t, name):
     """moe_out_t of a tensor."""
-    if not _row_types:
-        _load_row_types()
     k = _row_types.get(t.dtype)
     if k is None:
+        if not _row_types:
+            _load_row_types()
+            return _row_type(t, name)
         raise ValueError(f"{name}: expected bfloat16 or float32, got {t.dtype}")
     return k
 
@@ -728,50 +744,75 @@ def _row_type(t, name):
 def _rows(t, name, shape, kind=None):
     """(pointer, moe_out_t, elements between rows) of a matrix whose rows may be strided; kind: the
     type that it has to be of."""
-    k = _row_type(t, name)
+    k = _row_types.get(t.dtype)
+    if k is None:
+        k = _row_type(t, name)
     if kind is not None and k != kind:
         raise ValueError(f"{name}: expected {'float32' if kind else 'bfloat16'}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    ld, one = t.stride()
-    if one != 1 and shape[1] > 1:
-        raise ValueError(f"{name}: expected a matrix with adjacent columns")
+    ld = shape[1]
+    if not t.is_contiguous():
+        step, one = t.stride()
+        if one != 1 and ld > 1:
+            raise ValueError(f"{name}: expected a matrix with adjacent columns")
+        if shape[0] > 1:
+            ld = step
     if not t.is_cuda:
         raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
-    return t.data_ptr(), k, ld if shape[0] > 1 else shape[1]
+    return t.data_ptr(), k, ld
 
 
-def _vector(t, name, n, dtype="float32"):
-    """_p of n elements of one type."""
-    if t is not None and t.numel() != n:
+def _vector(t, name, n):
+    """The address of n fp32 elements."""
+    if t is None:
+        return None
+    if _row_types.get(t.dtype) != 1:
+        raise ValueError(f"{name}: expected float32, got {t.dtype}")
+    if t.numel() != n:
         raise ValueError(f"{name}: expected {n} elements, got {t.numel()}")
-    return _typed(t, dtype, name)
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _p(t)
 
 
 def _params(C, a, b, names):
     """(type, pointer, pointer) of two vectors of one type, each of which may be missing."""
-    kind = 0
-    for t, name in ((a, names[0]), (b, names[1])):
-        if t is not None:
-            kind = _row_type(t, name)
-            if t.numel() != C:
-                raise ValueError(f"{name}: expected {C} elements, got {t.numel()}")
-    if a is not None and b is not None and a.dtype is not b.dtype:
-        raise ValueError(f"{names[1]}: expected {a.dtype}, got {b.dtype}")
-    return kind, _p(a), _p(b)
+    kind, pa, pb = 0, None, None
+    if a is not None:
+        kind = _row_type(a, names[0])
+        if a.numel() != C:
+            raise ValueError(f"{names[0]}: expected {C} elements, got {a.numel()}")
+        pa = a.data_ptr() if a.is_cuda and a.is_contiguous() else _p(a)
+    if b is not None:
+        kb = _row_type(b, names[1])
+        if b.numel() != C:
+            raise ValueError(f"{names[1]}: expected {C} elements, got {b.numel()}")
+        if a is not None and kb != kind:
+            raise ValueError(f"{names[1]}: expected {a.dtype}, got {b.dtype}")
+        kind = kb
+        pb = b.data_ptr() if b.is_cuda and b.is_contiguous() else _p(b)
+    return kind, pa, pb
 
 
 def _checkpoint(codes, scales, rows, C):
     """(format, bytes between rows, pointer, pointer) of a checkpoint of [rows, C]."""
-    if not _formats:
-        _load_row_types()
     fmt = _formats.get(codes.dtype)
     if fmt is None:
+        if not _formats:
+            _load_row_types()
+            return _checkpoint(codes, scales, rows, C)
         raise ValueError(f"codes: expected int8 or float8_e4m3fn, got {codes.dtype}")
-    ld = codes.shape[-1]
-    _shape("codes", codes, (rows, ld))
-    _shape("scales", scales, (rows, (C + 127) // 128))
-    return fmt, ld, _p(codes), _typed(scales, "float32", "scales")
+    shape = codes.shape
+    ld = shape[-1]
+    if shape != (rows, ld):
+        _shape("codes", codes, (rows, ld))
+    if scales is None or scales.shape != (rows, (C + 127) // 128):
+        raise ValueError(f"scales: expected shape {(rows, (C + 127) // 128)}, got "
+                         f"{None if scales is None else tuple(scales.shape)}")
+    if _row_types.get(scales.dtype) != 1:
+        raise ValueError(f"scales: expected float32, got {scales.dtype}")
+    if codes.is_cuda and scales.is_cuda and codes.is_contiguous() and scales.is_contiguous():
+        return fmt, ld, codes.data_ptr(), scales.data_ptr()
+    return fmt, ld, _p(codes), _p(scales)
 
 
 def _live(offsets):
@@ -811,9 +852,11 @@ def moe_norm(x, y, gamma=None, beta=None, *, residual=None, total=None, mean=Non
     elif scales is not None:
         raise ValueError("scales: given without codes")
     kt, pg, pb = _params(C, gamma, beta, ("gamma", "beta"))
-    p = _NormC(rows, C, _kind(kind), eps, xt, yt, kt, 0, fmt, ldx, ldr, ldy, ldt, ldc)
-    _check(lib().moe_norm(_addr(p), px, pr, pg, pb, py, pt, _vector(mean, "mean", rows),
-                          _vector(rstd, "rstd", rows), pc, ps, _s(stream)), "moe_norm")
+    p, at = _norm_struct(rows, C, _kind(kind), eps, xt, yt, kt, 0, fmt, ldx, ldr, ldy, ldt, ldc)
+    s = (_lib or lib()).moe_norm(at, px, pr, pg, pb, py, pt, _vector(mean, "mean", rows),
+                                 _vector(rstd, "rstd", rows), pc, ps, _s(stream))
+    if s:
+        raise MoEError(s, "moe_norm")
 
 
 def moe_norm_ws_size(rows, C) -> int:
@@ -846,8 +889,8 @@ def moe_norm_bwd(dy, x, mean, rstd, dx, dgamma=None, dbeta=None, *, gamma=None, 
         need = moe_norm_ws_size(rows, C)
         if ws.numel() * ws.element_size() < need:
             raise ValueError(f"ws: expected {need} bytes, got {ws.numel() * ws.element_size()}")
-    p = _NormC(rows, C, _kind(kind), 0.0, xt, yt, kt, gt, fmt, ldx, lda, ldy, ldd, ldc)
-    _check(lib().moe_norm_bwd(_addr(p), py, px, ps, _vector(mean, "mean", rows),
+    p, at = _norm_struct(rows, C, _kind(kind), 0.0, xt, yt, kt, gt, fmt, ldx, lda, ldy, ldd, ldc)
+    _check(lib().moe_norm_bwd(at, py, px, ps, _vector(mean, "mean", rows),
                               _vector(rstd, "rstd", rows), pg, pa, pd, pdg, pdb, _p(ws),
                               _s(stream)), "moe_norm_bwd")
 
@@ -862,8 +905,8 @@ def moe_ckpt_norm(codes, scales, mean, rstd, y, gamma=None, beta=None, *, kind="
     py, yt, ldy = _rows(y, "y", shape)
     fmt, ldc, pc, ps = _checkpoint(codes, scales, rows, C)
     kt, pg, pb = _params(C, gamma, beta, ("gamma", "beta"))
-    p = _NormC(rows, C, _kind(kind), 0.0, yt, yt, kt, 0, fmt, 0, 0, ldy, 0, ldc)
-    _check(lib().moe_ckpt_norm(_addr(p), pc, ps, _vector(mean, "mean", rows),
+    p, at = _norm_struct(rows, C, _kind(kind), 0.0, yt, yt, kt, 0, fmt, 0, 0, ldy, 0, ldc)
+    _check(lib().moe_ckpt_norm(at, pc, ps, _vector(mean, "mean", rows),
                                _vector(rstd, "rstd", rows), pg, pb, py, _s(stream)),
            "moe_ckpt_norm")
 
@@ -877,8 +920,8 @@ def moe_ckpt_save(x, codes, scales, *, offsets=None, ws, stream=None):
     rows, C = x.shape
     px, xt, ldx = _rows(x, "x", x.shape)
     fmt, ld, pc, ps = _checkpoint(codes, scales, rows, C)
-    p = _CkptC(rows, C, fmt, xt, ldx, ld)
-    _check(lib().moe_ckpt_save(_addr(p), px, _live(offsets), pc, ps, _p(ws), _s(stream)),
+    p, at = _ckpt_struct(rows, C, fmt, xt, ldx, ld)
+    _check(lib().moe_ckpt_save(at, px, _live(offsets), pc, ps, _p(ws), _s(stream)),
            "moe_ckpt_save")
 
 
@@ -889,8 +932,8 @@ def moe_ckpt_load(codes, scales, x, *, offsets=None, ws, stream=None):
     rows, C = x.shape
     px, xt, ldx = _rows(x, "x", x.shape)
     fmt, ld, pc, ps = _checkpoint(codes, scales, rows, C)
-    p = _CkptC(rows, C, fmt, xt, ldx, ld)
-    _check(lib().moe_ckpt_load(_addr(p), pc, ps, _live(offsets), px, _p(ws), _s(stream)),
+    p, at = _ckpt_struct(rows, C, fmt, xt, ldx, ld)
+    _check(lib().moe_ckpt_load(at, pc, ps, _live(offsets), px, _p(ws), _s(stream)),
            "moe_ckpt_load")
 
 
@@ -907,8 +950,8 @@ def moe_ckpt_swiglu(codes, scales, ab=None, h=None, *, offsets=None, ws, stream=
     if h is not None:
         _shape("h", h, (rows, C // 2))
     fmt, ld, pc, ps = _checkpoint(codes, scales, rows, C)
-    p = _CkptC(rows, C, fmt, 0, C, ld)
-    _check(lib().moe_ckpt_swiglu(_addr(p), pc, ps, _live(offsets), _typed(ab, "bfloat16", "ab"),
+    p, at = _ckpt_struct(rows, C, fmt, 0, C, ld)
+    _check(lib().moe_ckpt_swiglu(at, pc, ps, _live(offsets), _typed(ab, "bfloat16", "ab"),
                                  _typed(h, "bfloat16", "h"), _p(ws), _s(stream)),
            "moe_ckpt_swiglu")
 
@@ -923,8 +966,8 @@ def moe_ckpt_swiglu_bwd(dh, codes, scales, dab, h=None, *, offsets=None, ws, str
     if h is not None:
         _shape("h", h, (rows, f))
     fmt, ld, pc, ps = _checkpoint(codes, scales, rows, 2 * f)
-    p = _CkptC(rows, 2 * f, fmt, 0, 2 * f, ld)
-    _check(lib().moe_ckpt_swiglu_bwd(_addr(p), _typed(dh, "bfloat16", "dh"), pc, ps,
+    p, at = _ckpt_struct(rows, 2 * f, fmt, 0, 2 * f, ld)
+    _check(lib().moe_ckpt_swiglu_bwd(at, _typed(dh, "bfloat16", "dh"), pc, ps,
                                      _live(offsets), _typed(dab, "bfloat16", "dab"),
                                      _typed(h, "bfloat16", "h"), _p(ws), _s(stream)),
            "moe_ckpt_swiglu_bwd")

@@ -11,7 +11,6 @@
 namespace moe {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
 constexpr int SLOTS = 3;
 
 __device__ __forceinline__ int64_t live_rows(const CkptArgs& a) {
@@ -357,21 +356,26 @@ swiglu_ring_kernel(const __grid_constant__ CkptArgs p, int per, int groups) {
   griddep_launch();
 }
 
-// One warp per token: dyp[p_j] = w_j dy[t], dw_j = <dy[t], codes * scales of row p_j>; 0 for a
-// dropped slot.  The codes of a lane's eight columns are summed before the block's scale
-// multiplies them.
+// One CTA per token, whose warps share its columns: dyp[p_j] = w_j dy[t], dw_j = <dy[t], codes *
+// scales of row p_j>, 0 for a dropped slot.  dy and the slots' codes of the next chunks come through
+// shared memory (rows8.cuh), their scales by one load of the warp a chunk ahead: lane 2 j + h holds
+// the one of slot j's block h.  The codes of a lane's eight columns are summed before their scale
+// multiplies them.  A warp to a token left the card's last round of tokens a third empty (4096 tokens
+// of 7168 columns, 8 slots each: 137 us).
+constexpr int COMBINE_WARPS = 8;
 template <int KMAX, int TYPE>
-__global__ void __launch_bounds__(THREADS)
-combine_bwd_kernel(const uint4* __restrict__ dy, const uint8_t* __restrict__ codes, int64_t ld,
+__global__ void __launch_bounds__(32 * COMBINE_WARPS)
+combine_bwd_kernel(const void* __restrict__ dy, const uint8_t* __restrict__ codes, int64_t ld,
                    const float* __restrict__ scales, int blocks, const float* __restrict__ topk_w,
                    const int32_t* __restrict__ dest_row, int64_t T, int k, int d, int64_t rows_cap,
-                   uint4* __restrict__ dyp, float* __restrict__ dw, int* err) {
+                   __nv_bfloat16* __restrict__ dyp, float* __restrict__ dw, int* err) {
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int nvec = d / 8;
-  const int64_t gw = (static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x) >> 5;
-  const int64_t nw = (static_cast<int64_t>(gridDim.x) * THREADS) >> 5;
-  for (int64_t t = gw; t < T; t += nw) {
+  struct Slot { uint8_t dy[2 * CHUNK]; uint8_t codes[KMAX][CHUNK]; };
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float dots[COMBINE_WARPS][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  Slot* mine = reinterpret_cast<Slot*>(smem) + warp * SLOTS;
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     int my_p = -1;
     float my_w = 0.0f;
     if (lane < k) {
@@ -382,51 +386,82 @@ combine_bwd_kernel(const uint4* __restrict__ dy, const uint8_t* __restrict__ cod
         my_p = -1;
       }
     }
-    int64_t p[KMAX];
-    float wt[KMAX], dot[KMAX];
+    int p[KMAX];
+    float wt[KMAX];
+    float2 dot[KMAX];
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
       p[j] = __shfl_sync(FULL_MASK, my_p, j);
       wt[j] = __shfl_sync(FULL_MASK, my_w, j);
-      if (j >= k) p[j] = -1;
-      dot[j] = 0.0f;
+      dot[j] = both(0.0f);
     }
-    for (int c = lane; c < nvec; c += 32) {
-      const uint4 g = dy[t * nvec + c];
-      uint2 v[KMAX];
-      float sc[KMAX];
+    // the slot and block whose scale this lane fetches
+    const int of = __shfl_sync(FULL_MASK, my_p, lane >> 1);
+    const bool mine_lives = lane < 2 * KMAX && of >= 0;
+    const float* sr = scales + (mine_lives ? static_cast<int64_t>(of) * blocks + (lane & 1) : 0);
+    const uint8_t* row = static_cast<const uint8_t*>(dy) + t * d * 2;
+    auto scale_of = [&](int chunk) {
+      return mine_lives && chunk + 128 * (lane & 1) < d ? sr[chunk >> 7] : 0.0f;
+    };
+    auto fetch = [&](int chunk, int slot) {
+      if (chunk < d) {
+        Slot& s = mine[slot];
+        copy_chunk(s.dy, row, ROW_BF16, chunk, d, lane);
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j)
-        if (p[j] >= 0) {
-          v[j] = *reinterpret_cast<const uint2*>(codes + p[j] * ld + 8 * c);
-          sc[j] = scales[p[j] * blocks + (c >> 4)];
+        for (int j = 0; j < KMAX; ++j)
+          if (p[j] >= 0) copy_chunk(s.codes[j], codes + static_cast<int64_t>(p[j]) * ld, TYPE, chunk, d, lane);
+      }
+      copy_commit();
+    };
+    const int step = warps * CHUNK;
+    for (int s = 0; s + 1 < SLOTS; ++s) fetch(warp * CHUNK + s * step, s);
+    float sc_next = scale_of(warp * CHUNK);
+    int slot = 0, ahead = SLOTS - 1;
+    for (int chunk = warp * CHUNK; chunk < d; chunk += step) {
+      fetch(chunk + (SLOTS - 1) * step, ahead);
+      if (++ahead == SLOTS) ahead = 0;
+      const float sc = sc_next;
+      sc_next = chunk + step < d ? scale_of(chunk + step) : 0.0f;
+      copy_wait(SLOTS - 1);
+      const Slot& s = mine[slot];
+      if (++slot == SLOTS) slot = 0;
+      const int c = chunk + 8 * lane;
+      const bool in = c < d;
+      float2 g[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) g[q] = both(0.0f);
+      if (in) slot_values(g, s.dy, ROW_BF16, lane);
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        const float scale = __shfl_sync(FULL_MASK, sc, 2 * j + (lane >> 4));
+        if (p[j] < 0 || !in) continue;
+        float2 f[4], v = both(0.0f);
+        slot_values(f, s.codes[j], TYPE, lane);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v = __ffma2_rn(g[q], f[q], v);
+          f[q] = __fmul2_rn(g[q], both(wt[j]));
         }
-      float gf[8];
-      unpack8(g, gf);
-#pragma unroll
-      for (int j = 0; j < KMAX; ++j)
-        if (p[j] >= 0) {
-          Raw8 raw;
-          raw.w[0] = v[j].x;
-          raw.w[1] = v[j].y;
-          float f[8], o[8], s = 0.0f;
-          unpack_raw<8>(raw, TYPE, f);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            s = fmaf(gf[q], f[q], s);
-            o[q] = wt[j] * gf[q];
-          }
-          dot[j] = fmaf(s, sc[j], dot[j]);
-          dyp[p[j] * nvec + c] = pack8(o);
-        }
+        dot[j] = __ffma2_rn(v, both(scale), dot[j]);
+        store_pairs(dyp + static_cast<int64_t>(p[j]) * d, ROW_BF16, c, f);
+      }
     }
-    float mine = 0.0f;
+    float all = 0.0f;
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-      dot[j] = warp_sum(dot[j]);
-      if (j == lane) mine = dot[j];
+      const float v = warp_sum(dot[j].x + dot[j].y);
+      if (j == lane) all = v;
     }
-    if (lane < k) dw[t * k + lane] = mine;
+    if (warps > 1) {
+      if (lane < 8) dots[warp][lane] = all;
+      __syncthreads();
+      if (warp == 0 && lane < k) {
+        all = 0.0f;
+        for (int i = 0; i < warps; ++i) all += dots[i][lane];
+      }
+    }
+    if (warp == 0 && lane < k) dw[t * k + lane] = all;
+    if (t + gridDim.x < T) __syncthreads();
   }
   griddep_launch();
 }
@@ -492,21 +527,29 @@ cudaError_t launch_ckpt_combine_bwd(const void* dy, const void* codes, int64_t l
                                     const int32_t* dest_row, int64_t T, int k, int d,
                                     int64_t rows_cap, void* dyp, float* dw, int* err,
                                     cudaStream_t st) {
-  const int64_t need = (T + WARPS - 1) / WARPS, cap = static_cast<int64_t>(row_sms()) * 8;
-  const dim3 grid(static_cast<unsigned>(need < cap ? need : cap));
-#define MOE_COMBINE_T(KM, TY)                                                                   \
-  launch_pdl(combine_bwd_kernel<KM, TY>, grid, dim3(THREADS), 0, st, 1,                         \
-             static_cast<const uint4*>(dy), static_cast<const uint8_t*>(codes), ld, scales,      \
-             (d + 127) / 128, topk_w, dest_row, T, k, d, rows_cap, static_cast<uint4*>(dyp), dw, \
-             err)
+  // warps to a token: a chunk each while there are few tokens, else about four
+  const int chunks = (d + CHUNK - 1) / CHUNK;
+  int warps = T < 4 * row_sms() ? chunks : (chunks + 3) / 4;
+  if (warps > COMBINE_WARPS) warps = COMBINE_WARPS;
+  const int64_t most = int64_t(1) << 30;
+  const dim3 grid(static_cast<unsigned>(T < most ? T : most));
+  auto go = [&](auto kern, int kmax) {
+    const int smem = warps * SLOTS * (2 + kmax) * CHUNK;
+    if (smem > 47 * 1024) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kern, grid, dim3(32 * warps), smem, st, 1, dy, static_cast<const uint8_t*>(codes), ld,
+                      scales, (d + 127) / 128, topk_w, dest_row, T, k, d, rows_cap,
+                      static_cast<__nv_bfloat16*>(dyp), dw, err);
+  };
 #define MOE_COMBINE(KM) \
-  (format == MOE_CKPT_INT8 ? MOE_COMBINE_T(KM, ROW_INT8) : MOE_COMBINE_T(KM, ROW_E4M3))
+  (format == MOE_CKPT_INT8 ? go(combine_bwd_kernel<KM, ROW_INT8>, KM) : go(combine_bwd_kernel<KM, ROW_E4M3>, KM))
   if (k <= 2) return MOE_COMBINE(2);
   if (k <= 4) return MOE_COMBINE(4);
   if (k <= 6) return MOE_COMBINE(6);
   return MOE_COMBINE(8);
 #undef MOE_COMBINE
-#undef MOE_COMBINE_T
 }
 
 }  // namespace moe
