@@ -620,7 +620,8 @@ moe_status_t moe_fp8_wgrad(const moe_fp8_wgrad_t *g, const void *a, const float 
  *   MOE_CKPT_E4M3  scale and code as moe_fp8_quantize's along the row (pow2 = 0), so that the row
  *                  codes of a product's operand are its checkpoint
  * with quotients correctly rounded in fp32.  A value is restored as code * scale in fp32, and
- * rounded once more where it is stored as bf16.  A block that holds a NaN or an infinity restores
+ * rounded once more where it is stored as bf16; where a mean is taken from it, code * scale - mean is
+ * rounded once.  A block that holds a NaN or an infinity restores
  * as NaN throughout.  ld is a multiple of 16 and at least C; what lies past C is neither written
  * nor read.
  *

@@ -161,6 +161,11 @@ def device_checkpoint(x, fmt):
     return codes, g.t, restore(q, s)
 
 
+def unrounded(codes, scales, C):
+    """code * scale of a checkpoint, the products not yet rounded to 32 bits."""
+    return f64(codes)[:, :C] * np.repeat(f64(scales), BLOCK, 1)[:, :C]
+
+
 def new_ws(n=256):
     import token_dispatch_expert_gb300 as tde
     ws = torch.full((n,), PATTERN, dtype=torch.uint8, device="cuda")

@@ -533,18 +533,20 @@ cudaError_t launch_ckpt_combine_bwd(const void* dy, const void* codes, int64_t l
   if (warps > COMBINE_WARPS) warps = COMBINE_WARPS;
   const int64_t most = int64_t(1) << 30;
   const dim3 grid(static_cast<unsigned>(T < most ? T : most));
-  auto go = [&](auto kern, int kmax) {
-    const int smem = warps * SLOTS * (2 + kmax) * CHUNK;
-    if (smem > 47 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-    }
+  auto go = [&](auto slots, auto type) {
+    constexpr int KMAX = decltype(slots)::value;
+    constexpr auto kern = combine_bwd_kernel<KMAX, decltype(type)::value>;
+    const int smem = warps * SLOTS * (2 + KMAX) * CHUNK;
+    const cudaError_t e = allow_smem<kern>(smem);
+    if (e != cudaSuccess) return e;
     return launch_pdl(kern, grid, dim3(32 * warps), smem, st, 1, dy, static_cast<const uint8_t*>(codes), ld,
                       scales, (d + 127) / 128, topk_w, dest_row, T, k, d, rows_cap,
                       static_cast<__nv_bfloat16*>(dyp), dw, err);
   };
 #define MOE_COMBINE(KM) \
-  (format == MOE_CKPT_INT8 ? go(combine_bwd_kernel<KM, ROW_INT8>, KM) : go(combine_bwd_kernel<KM, ROW_E4M3>, KM))
+  (format == MOE_CKPT_INT8                                                                       \
+       ? go(std::integral_constant<int, KM>(), std::integral_constant<int, ROW_INT8>())          \
+       : go(std::integral_constant<int, KM>(), std::integral_constant<int, ROW_E4M3>()))
   if (k <= 2) return MOE_COMBINE(2);
   if (k <= 4) return MOE_COMBINE(4);
   if (k <= 6) return MOE_COMBINE(6);

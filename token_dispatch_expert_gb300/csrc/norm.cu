@@ -397,10 +397,10 @@ ckpt_norm_kernel(const __grid_constant__ NormArgs a, int per, int groups) {
       if (row + i * w.groups < a.rows) {
         float f[8];
         unpack_raw<V>(raw[i], TYPE, f);
-        scale_values<V>(f, sc[i]);
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          float2 v = __fadd2_rn(make_float2(f[j], f[j + 1]), both(-mean[i]));
+          float2 v = __ffma2_rn(make_float2(f[j], f[j + 1]), make_float2(sc[i][j / V], sc[i][(j + 1) / V]),
+                                both(-mean[i]));
           v = __ffma2_rn(__fmul2_rn(v, both(rstd[i])), make_float2(g[j], g[j + 1]),
                          make_float2(b[j], b[j + 1]));
           f[j] = v.x;
@@ -430,7 +430,7 @@ int norm_vector(const NormArgs& a) {
 namespace {
 template <int N, int X, bool ADD>
 cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
-  auto kern = norm_ring_kernel<N, X, ADD>;
+  constexpr auto kern = norm_ring_kernel<N, X, ADD>;
   const int warps = nw == 1 ? 4 : nw;
   const int slot = warps * N * CHUNK * row_size(X) * (ADD ? 2 : 1);
   // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
@@ -440,10 +440,8 @@ cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
   const int64_t ctas = nw == 1 ? (a.rows + warps - 1) / warps : a.rows;
   const int64_t most = static_cast<int64_t>(row_sms()) * per;
   const int smem = slots * slot;
-  if (smem > 47 * 1024) {   // (the kernel has a little of its own)
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem<kern>(smem);
+  if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(32 * warps), smem,
                     st, 1, a, nw, slots);
 }

@@ -13,6 +13,8 @@
 
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -502,9 +504,39 @@ __device__ __forceinline__ void save_row_chunks(void* codes, float* scales, int 
   save_chunks<V, N>(c, s, format, chunk, C, lane, f);
 }
 
-// Whole rows through shared memory by bulk copies: a lane's eight values at column `col` of a row.
-template <int TYPE>
-__device__ __forceinline__ void smem_row_values(float2* v, const uint8_t* row, int col) {
+// Whole rows through shared memory by bulk copies.  Eight adjacent columns of a lane (V = 8: the row
+// starts at 16 bytes), or 32 columns apart (V = 1: rows at any element).
+__device__ __forceinline__ float int8_number(uint32_t byte) {   // (see int8_value)
+  return __uint_as_float((byte ^ 0x80u) | 0x4B000000u) - 8388736.0f;
+}
+template <int TYPE, int V>
+__device__ __forceinline__ void smem_row_values(float2* v, const uint8_t* row, int chunk, int C, int lane) {
+  if constexpr (V == 1) {
+    const bool all = chunk + CHUNK <= C;
+    const int c0 = chunk + lane;
+    uint32_t r[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + 32 * j;
+      r[j] = 0;
+      if (all || c < C) {
+        if constexpr (TYPE == ROW_BF16) r[j] = *reinterpret_cast<const uint16_t*>(row + 2 * c);
+        else if constexpr (TYPE == ROW_FP32) r[j] = *reinterpret_cast<const uint32_t*>(row + 4 * c);
+        else r[j] = row[c];
+      } else if constexpr (TYPE == ROW_INT8) {
+        r[j] = 0;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (TYPE == ROW_BF16) v[j] = make_float2(bf16_lo(r[2 * j]), bf16_lo(r[2 * j + 1]));
+      else if constexpr (TYPE == ROW_FP32) v[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+      else if constexpr (TYPE == ROW_INT8) v[j] = make_float2(int8_number(r[2 * j]), int8_number(r[2 * j + 1]));
+      else v[j] = e4m3_values(__byte_perm(r[2 * j], r[2 * j + 1], 0x0040));
+    }
+    return;
+  }
+  const int col = chunk + 8 * lane;
   if constexpr (TYPE == ROW_BF16) {
     const uint4 r = *reinterpret_cast<const uint4*>(row + 2 * col);
     v[0] = make_float2(bf16_lo(r.x), bf16_hi(r.x));
@@ -536,6 +568,31 @@ __device__ __forceinline__ void smem_row_values(float2* v, const uint8_t* row, i
     }
   }
 }
+// The bytes [p, p + n) of rows that lie in [first, end), into shared memory at `to`, a 16-byte address
+// that stands for p's rounded down: whole 16-byte pieces by a bulk copy counted on `bar`, what the
+// tensor's own ends cut off a piece by plain copies (ordered by the caller's arrival on bar).
+// Returns the bytes that the bulk copy brings.  One thread.
+struct Span {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ Span bulk_span(const void* p, uint32_t n, const void* first, const void* end) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p), f = reinterpret_cast<uint64_t>(first);
+  const uint64_t e = reinterpret_cast<uint64_t>(end);
+  Span s{a & ~15ull, (a + n + 15) & ~15ull};
+  if (s.lo < f) s.lo = (f + 15) & ~15ull;
+  if (s.hi > e) s.hi = e & ~15ull;
+  if (s.hi < s.lo) s.hi = s.lo;
+  return s;
+}
+__device__ __forceinline__ void span_ends(uint8_t* to, const void* p, uint32_t n, const Span& s) {
+  const uint8_t* a = static_cast<const uint8_t*>(p);
+  const uint64_t at = reinterpret_cast<uint64_t>(p), low = at & ~15ull;
+  for (uint64_t i = at; i < at + n; ++i) {
+    if (i >= s.lo && i < s.hi) i = s.hi;
+    if (i < at + n) to[i - low] = a[i - at];
+  }
+}
+
 // untiled bulk copy global -> shared of a multiple of 16 bytes between 16-byte addresses
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
@@ -548,11 +605,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 constexpr int MAX_WARPS = 16;   // of a row that stays in registers: 16 * 4 chunks of 256 columns
 
 struct RowSums {
-  float part[2][4][MAX_WARPS];   // [buffer][which sum][warp]
+  float part[2][2][MAX_WARPS];   // [buffer][which sum][warp]
 };
 // Before the first sum: the parts that no warp writes are zeros, so that they are read by fours.
 __device__ __forceinline__ void row_sum_init(RowSums& sh) {
-  for (int i = threadIdx.x; i < 8 * MAX_WARPS; i += blockDim.x) (&sh.part[0][0][0])[i] = 0.0f;
+  for (int i = threadIdx.x; i < 4 * MAX_WARPS; i += blockDim.x) (&sh.part[0][0][0])[i] = 0.0f;
   __syncthreads();
 }
 __device__ __forceinline__ float row_total(const float* part, int nw) {
@@ -572,8 +629,10 @@ __device__ __forceinline__ float row_sum1(float a, RowSums& sh, int turn, int wa
   __syncthreads();
   return row_total(sh.part[turn][0], nw);
 }
-// of two numbers at once: the halves of the warp take one each after the first exchange
-__device__ __forceinline__ float2 row_sum2(float a, float b, RowSums& sh, int turn, int warp, int nw) {
+// of two numbers at once: the halves of the warp take one each after the first exchange.  `barrier`:
+// the group of nw warps' own one, where a CTA holds several.
+__device__ __forceinline__ float2 row_sum2(float a, float b, RowSums& sh, int turn, int warp, int nw,
+                                           int barrier = 0) {
   const int lane = threadIdx.x & 31;
   const bool up = lane & 16;
   float v = (up ? b : a) + __shfl_xor_sync(FULL_MASK, up ? a : b, 16);
@@ -581,25 +640,9 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, RowSums& sh, int tu
   for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
   if (nw == 1) return make_float2(__shfl_sync(FULL_MASK, v, 0), __shfl_sync(FULL_MASK, v, 16));
   if ((lane & 15) == 0) sh.part[turn][lane >> 4][warp] = v;
-  __syncthreads();
+  if (barrier == 0) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(32 * nw) : "memory");
   return make_float2(row_total(sh.part[turn][0], nw), row_total(sh.part[turn][1], nw));
-}
-// of four numbers: after two exchanges a quarter of the warp has one each
-__device__ __forceinline__ float4 row_sum4(float4 a, RowSums& sh, int turn, int warp, int nw) {
-  const int lane = threadIdx.x & 31;
-  const bool up = lane & 16, hi = lane & 8;
-  float p = (up ? a.z : a.x) + __shfl_xor_sync(FULL_MASK, up ? a.x : a.z, 16);
-  const float q = (up ? a.w : a.y) + __shfl_xor_sync(FULL_MASK, up ? a.y : a.w, 16);
-  p = (hi ? q : p) + __shfl_xor_sync(FULL_MASK, hi ? p : q, 8);
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) p += __shfl_xor_sync(FULL_MASK, p, o);
-  if (nw == 1)
-    return make_float4(__shfl_sync(FULL_MASK, p, 0), __shfl_sync(FULL_MASK, p, 8),
-                       __shfl_sync(FULL_MASK, p, 16), __shfl_sync(FULL_MASK, p, 24));
-  if ((lane & 7) == 0) sh.part[turn][lane >> 3][warp] = p;
-  __syncthreads();
-  return make_float4(row_total(sh.part[turn][0], nw), row_total(sh.part[turn][1], nw),
-                     row_total(sh.part[turn][2], nw), row_total(sh.part[turn][3], nw));
 }
 __device__ __forceinline__ const void* row_at(const void* p, int64_t row, int64_t ld, int size) {
   return static_cast<const uint8_t*>(p) + row * ld * size;
@@ -626,6 +669,24 @@ __device__ __forceinline__ Walk walk_start(int per, int groups) {
   w.groups = groups;
   w.any = w.row < groups;
   return w;
+}
+// How much shared memory a kernel may be launched with: all there is, said once for each device.
+template <auto KERNEL>
+inline cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> said{0};
+  if (bytes <= 40 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (said.load(std::memory_order_relaxed) & bit && dev < 64) return cudaSuccess;
+  cudaFuncAttributes f;
+  e = cudaFuncGetAttributes(&f, KERNEL);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             227 * 1024 - static_cast<int>(f.sharedSizeBytes));
+  if (e == cudaSuccess) said.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 // how many groups of warps: enough for `warps` to an SM, no more than rows
 struct WalkGrid {
