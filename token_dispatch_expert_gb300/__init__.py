@@ -31,6 +31,7 @@ __all__ = [
     "moe_fp8_swiglu", "moe_fp8_swiglu_bwd", "moe_fp8_gemm", "moe_fp8_wgrad", "Fp8MoELayer",
     "moe_norm", "moe_norm_ws_size", "moe_norm_bwd", "moe_ckpt_norm", "moe_ckpt_save",
     "moe_ckpt_load", "moe_ckpt_swiglu", "moe_ckpt_swiglu_bwd", "moe_ckpt_combine_bwd",
+    "MoEScratch", "CheckpointedMoELayer", "MoENorm",
     "moe_status", "moe_status_string", "moe_selftest_wait_timeout", "moe_gemm_clock_trace",
     "moe_gemm_clock_read", "ctx_views", "MoELayer", "CTX_FIELDS",
 ]
@@ -1101,6 +1102,164 @@ class MoELayer:
         return moe_status(self.ws, stream)
 
 
+CKPT_FORMATS = ("int8", "e4m3")
+
+
+def _new_checkpoint(rows, C, fmt, device):
+    """(codes, scales) for rows of C columns."""
+    import torch
+    if fmt not in CKPT_FORMATS:
+        raise ValueError(f"checkpoint: expected one of {CKPT_FORMATS}, got {fmt!r}")
+    codes = torch.empty((rows, (C + 15) // 16 * 16), dtype=torch.int8, device=device)
+    if fmt == "e4m3":
+        codes = codes.view(torch.float8_e4m3fn)
+    return codes, torch.empty((rows, (C + 127) // 128), dtype=torch.float32, device=device)
+
+
+class MoEScratch:
+    """The full-size buffers of a CheckpointedMoELayer: none is read after the call that wrote it, so
+    the layers of one configuration share one (on one stream)."""
+
+    def __init__(self, cfg: MoEConfigC, device="cuda"):
+        import torch
+        R, d, f = cfg.T * cfg.k, cfg.d, cfg.ffn
+        bf = dict(dtype=torch.bfloat16, device=device)
+        self.cfg, self.device = cfg, device
+        self.ws = torch.empty(moe_workspace_size(cfg)[0], dtype=torch.uint8, device=device)
+        moe_ws_init(self.ws)
+        self.ab, self.dab = torch.empty((R, 2 * f), **bf), torch.empty((R, 2 * f), **bf)
+        self.h = torch.empty((R, f), **bf)
+        self.rows, self.dxp = torch.empty((R, d), **bf), torch.empty((R, d), **bf)
+        self.dw = torch.empty((cfg.T, cfg.k), dtype=torch.float32, device=device)
+
+
+class CheckpointedMoELayer:
+    """MoELayer (bf16, no shared expert) that keeps for its backward pass the routing and, in 8 bits,
+    the first product's output and the experts' outputs; everything else is scratch.
+
+        scratch = MoEScratch(cfg)
+        layers = [CheckpointedMoELayer(scratch) for _ in range(n)]
+        y = layer.forward(logits, x, W1, W2)
+        g = layer.backward(logits, x, dy, W1, W2)     # dx, dW1, dW2, dlogits
+    """
+
+    def __init__(self, scratch: MoEScratch, checkpoint="int8"):
+        import torch
+        c, device = scratch.cfg, scratch.device
+        if c.ffn_shared:
+            raise ValueError("CheckpointedMoELayer has no shared expert")
+        if c.mxfp8 or c.recompute:
+            raise ValueError("CheckpointedMoELayer: cfg.mxfp8 and cfg.recompute must be unset")
+        self.cfg, self.scratch = c, scratch
+        T, k, E, R = c.T, c.k, c.E, c.T * c.k
+        new = lambda shape, dt: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
+        i32 = torch.int32
+        self.r = {"topk_idx": new((T, k), i32), "topk_w": new((T, k), torch.float32),
+                  "counts": new((E,), i32), "kept": new((E,), i32), "offsets": new((E + 1,), i32),
+                  "dest_row": new((T, k), i32), "src_tok": new((R,), i32),
+                  "src_slot": new((R,), i32), "drop_mask": new((T, k), torch.uint8)}
+        self.ab = _new_checkpoint(R, 2 * c.ffn, checkpoint, device)
+        self.yp = _new_checkpoint(R, c.d, checkpoint, device)
+        # the gate's gradient: that of weights renormalised over the chosen, whatever chose them
+        softmax = c.gate == GATES["softmax"]
+        self._gate = (make_config(T, c.d, E, k, c.ffn, route_scale=1.0 if softmax else c.route_scale),
+                      make_router("softmax" if softmax else "sigmoid", renorm=True))
+
+    def forward(self, logits, x, W1, W2, y=None, stream=None):
+        import torch
+        c, r, s = self.cfg, self.r, self.scratch
+        if y is None:
+            y = torch.empty_like(x)
+        moe_route(c, logits, *r.values(), s.ws, stream)
+        moe_grouped_ffn_gather(c, x, r["src_tok"], r["offsets"], W1, W2, s.ab, s.h, s.rows, s.ws,
+                               stream)
+        moe_ckpt_save(s.ab, *self.ab, offsets=r["offsets"], ws=s.ws, stream=stream)
+        moe_ckpt_save(s.rows, *self.yp, offsets=r["offsets"], ws=s.ws, stream=stream)
+        moe_combine(c, s.rows, r["dest_row"], r["topk_w"], None, y, s.ws, stream)
+        return y
+
+    def backward(self, logits, x, dy, W1, W2, out=None, stream=None):
+        """After forward() on the same logits, x and weights; other layers may have used the scratch
+        in between."""
+        import torch
+        c, r, s = self.cfg, self.r, self.scratch
+        if out is None:
+            out = {"dx": torch.empty_like(x), "dW1": torch.empty_like(W1),
+                   "dW2": torch.empty_like(W2), "dlogits": torch.empty_like(logits)}
+        moe_ckpt_combine_bwd(c, dy, *self.yp, r["topk_w"], r["dest_row"], s.rows, s.dw, s.ws, stream)
+        moe_route_groups_bwd(*self._gate, logits, r["topk_idx"], s.dw, out["dlogits"], s.ws, stream)
+        moe_ckpt_swiglu(*self.ab, s.ab, s.h, offsets=r["offsets"], ws=s.ws, stream=stream)
+        moe_grouped_ffn_bwd_gather(c, s.rows, x, r["src_tok"], r["offsets"], W1, W2, s.ab, s.h, s.dab,
+                                   s.dxp, out["dW1"], out["dW2"], s.ws, stream)
+        moe_unpermute_reduce(c, s.dxp, r["dest_row"], None, out["dx"], s.ws, stream)
+        return out
+
+    def status(self, stream=None):
+        return moe_status(self.scratch.ws, stream)
+
+
+class MoENorm:
+    """The normalisation in front of a layer, with what its backward pass needs: the statistics and,
+    in 8 bits, the rows that were normalised (checkpoint None: the caller's tensor itself).
+
+        norm = MoENorm(T, d)
+        n, s = norm.forward(x, gamma, beta, residual=r)     # s = x + r, n = norm(s)
+        n = norm.restore(gamma, beta)                       # n again, for the layer's backward pass
+        g = norm.backward(dn, gamma, add=ds)                # dx (of x and of r), dgamma, dbeta
+    """
+
+    def __init__(self, T, d, kind="layer", eps=1e-5, dtype=None, checkpoint="int8", device="cuda"):
+        import torch
+        _kind(kind)
+        self.T, self.d, self.kind, self.eps = int(T), int(d), kind, float(eps)
+        self.dtype = torch.bfloat16 if dtype is None else dtype     # of the stream
+        f32 = dict(dtype=torch.float32, device=device)
+        self.mean = torch.empty(self.T, **f32) if kind == "layer" else None
+        self.rstd = torch.empty(self.T, **f32)
+        self.kept = _new_checkpoint(self.T, self.d, checkpoint, device) if checkpoint else None
+        self.x = None
+        self.ws = torch.empty(moe_norm_ws_size(self.T, self.d), dtype=torch.uint8, device=device)
+        moe_ws_init(self.ws)
+
+    def forward(self, x, gamma=None, beta=None, residual=None, stream=None):
+        """(y in bf16, what was normalised: x itself or the sum)."""
+        import torch
+        _shape("x", x, (self.T, self.d))
+        if x.dtype is not self.dtype:
+            raise ValueError(f"x: expected {self.dtype}, got {x.dtype}")
+        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        total = None if residual is None else torch.empty_like(x)
+        codes, scales = self.kept or (None, None)
+        moe_norm(x, y, gamma, beta, residual=residual, total=total, mean=self.mean, rstd=self.rstd,
+                 codes=codes, scales=scales, eps=self.eps, kind=self.kind, stream=stream)
+        v = x if total is None else total
+        self.x = None if self.kept else v
+        return y, v
+
+    def restore(self, gamma=None, beta=None, stream=None):
+        import torch
+        y = torch.empty((self.T, self.d), dtype=torch.bfloat16, device=self.rstd.device)
+        if self.kept:
+            moe_ckpt_norm(*self.kept, self.mean, self.rstd, y, gamma, beta, kind=self.kind,
+                          stream=stream)
+        else:
+            moe_norm(self.x, y, gamma, beta, eps=self.eps, kind=self.kind, stream=stream)
+        return y
+
+    def backward(self, dy, gamma=None, add=None, beta=False, stream=None):
+        """dx (plus add), dgamma in fp32, and with beta=True dbeta."""
+        import torch
+        f32 = dict(dtype=torch.float32, device=dy.device)
+        out = {"dx": torch.empty((self.T, self.d), dtype=self.dtype, device=dy.device),
+               "dgamma": torch.empty(self.d, **f32)}
+        if beta:
+            out["dbeta"] = torch.empty(self.d, **f32)
+        x, scales = self.kept or (self.x, None)
+        moe_norm_bwd(dy, x, self.mean, self.rstd, out["dx"], out["dgamma"], out.get("dbeta"),
+                     gamma=gamma, scales=scales, add=add, kind=self.kind, ws=self.ws, stream=stream)
+        return out
+
+
 class Fp8MoELayer:
     """A layer whose router limits the choice to groups of experts and whose routed experts run
     on 8-bit operands with a scale per block of 128, forward and backward.  Owns its buffers;
@@ -1110,12 +1269,20 @@ class Fp8MoELayer:
         w = layer.quantize_weights(W1, W2)
         y = layer.forward(logits, x, w)
         g = layer.backward(logits, x, dy, w)      # dx, dW1, dW2, dlogits
+
+    checkpoint ("int8" or "e4m3"): what the backward pass reads of the forward's, the first product's
+    output and the experts' outputs, is kept in 8 bits instead of bf16.  Then everything else but the
+    routing is scratch, and `scratch`, another layer of the same configuration, lends its own: a
+    model's layers keep 8 bits each and share one set of full-size buffers (on one stream).
     """
 
-    def __init__(self, cfg: MoEConfigC, router: MoERouterC, device="cuda", grad_dtype=None):
+    def __init__(self, cfg: MoEConfigC, router: MoERouterC, device="cuda", grad_dtype=None,
+                 checkpoint=None, scratch=None):
         import torch
         if cfg.ffn_shared:
             raise ValueError("Fp8MoELayer has no shared expert")
+        if scratch is not None and (checkpoint is None or scratch.checkpoint is None):
+            raise ValueError("scratch: only between layers with checkpoints")
         self.cfg, self.router, self.device = cfg, router, device
         self.grad_dtype = torch.bfloat16 if grad_dtype is None else grad_dtype
         T, k, E, d, f = cfg.T, cfg.k, cfg.E, cfg.d, cfg.ffn
@@ -1131,6 +1298,18 @@ class Fp8MoELayer:
                   "counts": new((E,), i32), "kept": new((E,), i32), "offsets": new((E + 1,), i32),
                   "dest_row": new((T, k), i32), "src_tok": new((R,), i32),
                   "src_slot": new((R,), i32), "drop_mask": new((T, k), torch.uint8)}
+        self.checkpoint = checkpoint
+        if checkpoint is not None:
+            self.kept = {n: _new_checkpoint(R, c, checkpoint, device)
+                         for n, c in (("ab", 2 * f), ("yp", d))}
+        if scratch is not None:
+            o = scratch.cfg
+            if (o.T, o.k, o.E, o.d, o.ffn) != (T, k, E, d, f):
+                raise ValueError("scratch: expected a layer of the same configuration")
+            for n in ("ws", "ab", "yp", "q", "qt", "dyp", "dh", "dxp", "dw", "h"):
+                setattr(self, n, getattr(scratch, n))
+            return
+        self.h = new((R, f), bf) if checkpoint is not None else None
         self.ab, self.yp = new((R, 2 * f), bf), new((R, d), bf)
         # along the row: the operands of the products; along the tokens: of the weight gradients
         self.q = {n: (new((R, c), e4), new((R, blk(c)), f32))
@@ -1163,8 +1342,12 @@ class Fp8MoELayer:
         seg = dict(offsets=r["offsets"], ws=ws, stream=stream)
         moe_fp8_quantize(x, *self.q["x"], src_tok=r["src_tok"], **seg)
         moe_fp8_gemm(*self.q["x"], *w["W1"], self.ab, c.d, **seg)
+        if self.checkpoint is not None:
+            moe_ckpt_save(self.ab, *self.kept["ab"], **seg)
         moe_fp8_swiglu(self.ab, *self.q["h"], **seg)
         moe_fp8_gemm(*self.q["h"], *w["W2"], self.yp, c.ffn, **seg)
+        if self.checkpoint is not None:
+            moe_ckpt_save(self.yp, *self.kept["yp"], **seg)
         moe_combine(c, self.yp, r["dest_row"], r["topk_w"], None, y, ws, stream)
         return y
 
@@ -1179,13 +1362,24 @@ class Fp8MoELayer:
                                       device=x.device),
                    "dW2": torch.empty((c.E, c.d, c.ffn), dtype=self.grad_dtype, device=x.device)}
         seg = dict(offsets=r["offsets"], ws=ws, stream=stream)
-        moe_combine_bwd_dw(c, dy, self.yp, r["topk_w"], r["dest_row"], self.dyp, self.dw, ws,
-                           stream)
+        if self.checkpoint is not None:
+            moe_ckpt_combine_bwd(c, dy, *self.kept["yp"], r["topk_w"], r["dest_row"], self.dyp,
+                                 self.dw, ws, stream)
+        else:
+            moe_combine_bwd_dw(c, dy, self.yp, r["topk_w"], r["dest_row"], self.dyp, self.dw, ws,
+                               stream)
         moe_route_groups_bwd(c, self.router, logits, r["topk_idx"], self.dw, out["dlogits"], ws,
                              stream)
         moe_fp8_quantize(self.dyp, *self.q["dy"], *self.qt["dy"], **seg)
         moe_fp8_gemm(*self.q["dy"], *w["W2_t"], self.dh, c.d, **seg)
-        moe_fp8_swiglu_bwd(self.dh, self.ab, *self.q["dab"], *self.qt["dab"], *self.qt["h"], **seg)
+        if self.checkpoint is not None:
+            dab = self.ab          # (the forward's is not read any more)
+            moe_ckpt_swiglu_bwd(self.dh, *self.kept["ab"], dab, self.h, **seg)
+            moe_fp8_quantize(dab, *self.q["dab"], *self.qt["dab"], **seg)
+            moe_fp8_quantize(self.h, codes_t=self.qt["h"][0], scales_t=self.qt["h"][1], **seg)
+        else:
+            moe_fp8_swiglu_bwd(self.dh, self.ab, *self.q["dab"], *self.qt["dab"], *self.qt["h"],
+                               **seg)
         moe_fp8_wgrad(*self.qt["dy"], *self.qt["h"], out["dW2"], rows=R, **seg)
         moe_fp8_gemm(*self.q["dab"], *w["W1_t"], self.dxp, 2 * c.ffn, **seg)
         moe_unpermute_reduce(c, self.dxp, r["dest_row"], None, out["dx"], ws, stream)
