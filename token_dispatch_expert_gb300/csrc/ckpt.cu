@@ -97,73 +97,22 @@ load_kernel(const __grid_constant__ CkptArgs a, int per, int groups) {
   griddep_launch();
 }
 
-// [a | b] and h, or with BACK [da | db] and h from dh, N rows at a time.  With s = sigma(a):
-// h = a s b, da = dh b s (1 + a (1 - s)), db = dh a s, from the 32-bit restored values, each rounded
-// once.
-template <int V, int N, bool BACK, int TYPE>
-__global__ void __launch_bounds__(WALK_THREADS)
-swiglu_kernel(const __grid_constant__ CkptArgs p, int per, int groups) {
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int f = p.C / 2;
-  const Walk w = walk_start(per, groups);
-  const int64_t live = w.any ? live_rows(p) : 0;
-  const uint8_t* codes = static_cast<const uint8_t*>(p.codes_in) + w.row * p.ld;
-  const float* scales = p.scales_in + w.row * p.blocks;
-  const __nv_bfloat16* dh = static_cast<const __nv_bfloat16*>(p.dh) + w.row * f;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row * p.C;
-  __nv_bfloat16* hr = static_cast<__nv_bfloat16*>(p.h) + w.row * f;
-  const int64_t c_step = w.groups * p.ld, s_step = w.groups * p.blocks, h_step = w.groups * f;
-  for (int64_t row = w.row; row < live; row += N * w.groups) {
-    Raw8 ra[N], rb[N], rd[N];
-    float sa[N][8 / V], sb[N][8 / V];
+// [a | b] and h, or with BACK [da | db] and h from dh.  With s = sigma(a): h = a s b, da = dh b s (1 + a
+// (1 - s)), db = dh a s, from the 32-bit restored values, each rounded once.  In place: a and b become
+// what is stored for them.
+template <bool BACK>
+__device__ __forceinline__ void swiglu_pairs(float2* a, float2* b, const float2* d, float2* h) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (row + i * w.groups < live) {
-        load_raw<V>(ra[i], codes, TYPE, w.chunk, f, lane);
-        load_raw<V>(rb[i], codes + f, TYPE, w.chunk, f, lane);
-        if (BACK) load_raw<V>(rd[i], dh, ROW_BF16, w.chunk, f, lane);
-        load_chunk_scales<V>(sa[i], scales, w.chunk, f, lane);
-        load_scales<V>(sb[i], scales, f, w.chunk, f, lane);
-      }
-      codes += c_step;
-      scales += s_step;
-      dh += h_step;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (row + i * w.groups < live) {
-        float a[8], b[8], h[8];
-        unpack_raw<V>(ra[i], TYPE, a);
-        unpack_raw<V>(rb[i], TYPE, b);
-        scale_values<V>(a, sa[i]);
-        scale_values<V>(b, sb[i]);
-        if (BACK) {
-          float d[8];
-          unpack_raw<V>(rd[i], ROW_BF16, d);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float s = sigmoid_fast(a[j]), as = a[j] * s;
-            const float da = d[j] * b[j] * fmaf(as, 1.0f - s, s);
-            h[j] = as * b[j];
-            b[j] = d[j] * as;
-            a[j] = da;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[j] = a[j] * sigmoid_fast(a[j]) * b[j];
-        }
-        if (BACK || p.out) {
-          store_values<V>(out, ROW_BF16, w.chunk, f, lane, a);
-          store_values<V>(out + f, ROW_BF16, w.chunk, f, lane, b);
-        }
-        if (p.h) store_values<V>(hr, ROW_BF16, w.chunk, f, lane, h);
-      }
-      out += 2 * h_step;
-      hr += h_step;
+  for (int j = 0; j < 4; ++j) {
+    const float2 s = make_float2(sigmoid_fast(a[j].x), sigmoid_fast(a[j].y));
+    const float2 as = __fmul2_rn(a[j], s);
+    h[j] = __fmul2_rn(as, b[j]);
+    if (BACK) {
+      const float2 one = __ffma2_rn(s, both(-1.0f), both(1.0f));   // 1 - s
+      a[j] = __fmul2_rn(__fmul2_rn(d[j], b[j]), __ffma2_rn(as, one, s));
+      b[j] = __fmul2_rn(d[j], as);
     }
   }
-  griddep_launch();
 }
 
 // ------------------------------------------------------------------ rows of whole vectors
@@ -336,20 +285,108 @@ swiglu_ring_kernel(const __grid_constant__ CkptArgs p, int per, int groups) {
     for (int j = 0; j < 4; ++j) {
       a[j] = __fmul2_rn(a[j], sa);
       b[j] = __fmul2_rn(b[j], sb);
-      const float2 s = make_float2(sigmoid_fast(a[j].x), sigmoid_fast(a[j].y));
-      const float2 as = __fmul2_rn(a[j], s);
-      h[j] = __fmul2_rn(as, b[j]);
-      if (BACK) {
-        const float2 one = __ffma2_rn(s, both(-1.0f), both(1.0f));   // 1 - s
-        a[j] = __fmul2_rn(__fmul2_rn(d[j], b[j]), __ffma2_rn(as, one, s));
-        b[j] = __fmul2_rn(d[j], as);
-      }
     }
+    swiglu_pairs<BACK>(a, b, d, h);
     if (BACK || p.out) {
       store_pairs(out, ROW_BF16, col, a);
       store_pairs(out + f, ROW_BF16, col, b);
     }
     if (p.h) store_pairs(hr, ROW_BF16, col, h);
+    out += 2 * h_step;
+    hr += h_step;
+  }
+  griddep_launch();
+}
+
+// The same for rows of any width: a warp copies the 16-byte pieces that its 256 columns touch (33 of
+// dh, 16 of a's codes, 17 of b's) and the scales of their blocks (two and three), and reads them
+// element by element, 32 columns apart.  Pieces of codes lie within a row's distance; one of dh that
+// would pass the buffer's end is read by bytes.
+template <bool BACK, int TYPE>
+__global__ void __launch_bounds__(WALK_THREADS, 3)
+swiglu_odd_kernel(const __grid_constant__ CkptArgs p, int per, int groups) {
+  griddep_wait();
+  struct Slot { uint8_t dh[BACK ? 33 * 16 : 16]; uint8_t a[16 * 16], b[17 * 16]; float sa[4], sb[4]; };
+  __shared__ __align__(16) Slot ring[WALK_WARPS][SLOTS];
+  const int lane = threadIdx.x & 31;
+  const int f = p.C / 2;
+  const Walk w = walk_start(per, groups);
+  if (!w.any) return;
+  const int64_t live = live_rows(p);
+  Slot* mine = ring[threadIdx.x >> 5];
+  const uint8_t* codes = static_cast<const uint8_t*>(p.codes_in) + w.row * p.ld;
+  const float* scales = p.scales_in + w.row * p.blocks;
+  const int64_t c_step = w.groups * p.ld, s_step = w.groups * p.blocks, h_step = w.groups * f;
+  const int first_b = f + w.chunk, b_low = first_b & ~15, b_skip = first_b & 15, b_block = first_b & 127;
+  const int n = f - w.chunk < CHUNK ? f - w.chunk : CHUNK;    // columns of this chunk
+  const uint64_t dh_end = reinterpret_cast<uint64_t>(p.dh) + static_cast<uint64_t>(p.rows) * f * 2;
+  uint64_t dh = reinterpret_cast<uint64_t>(p.dh) + (static_cast<uint64_t>(w.row) * f + w.chunk) * 2;
+  int64_t next = w.row;
+  // the lane's own piece and, of three lanes, what is left over
+  const int block = lane < 4 ? (w.chunk >> 7) + lane - 2 : (first_b >> 7) + lane - 4;
+  auto piece_of_dh = [&](uint8_t* to, int i) {
+    const uint64_t low = dh & ~15ull, at = low + 16 * i;
+    if (at >= dh + 2 * n) return;
+    if (at + 16 <= dh_end) {
+      copy_async16(smem_u32(to + 16 * i), reinterpret_cast<const void*>(at));
+    } else {
+      for (uint64_t b = at; b < dh_end; ++b) to[b - low] = *reinterpret_cast<const uint8_t*>(b);
+    }
+  };
+  auto fetch = [&](int slot) {
+    if (next < live) {
+      Slot& t = mine[slot];
+      if (BACK) piece_of_dh(t.dh, lane);
+      if (lane < 16) {
+        if (16 * lane < n) copy_async16(smem_u32(t.a + 16 * lane), codes + w.chunk + 16 * lane);
+      } else if (b_low + 16 * (lane - 16) < first_b + n) {
+        copy_async16(smem_u32(t.b + 16 * (lane - 16)), codes + b_low + 16 * (lane - 16));
+      }
+      if (BACK && lane == 0) piece_of_dh(t.dh, 32);
+      if (lane == 1 && b_low + 256 < first_b + n) copy_async16(smem_u32(t.b + 256), codes + b_low + 256);
+      if (lane >= 2 && lane < 7 && block < p.blocks)
+        copy_async4(smem_u32(lane < 4 ? &t.sa[lane - 2] : &t.sb[lane - 4]), scales + block);
+    }
+    codes += c_step;
+    scales += s_step;
+    dh += 2 * h_step;
+    next += w.groups;
+    copy_commit();
+  };
+  for (int s = 0; s + 1 < SLOTS; ++s) fetch(s);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + w.row * p.C;
+  __nv_bfloat16* hr = static_cast<__nv_bfloat16*>(p.h) + w.row * f;
+  // where this row's dh begins in its first piece: 2 * f bytes further with every row
+  uint32_t skip = (static_cast<uint32_t>(reinterpret_cast<uint64_t>(p.dh)) +
+                   (static_cast<uint32_t>(w.row) * static_cast<uint32_t>(f) + w.chunk) * 2u) & 15u;
+  const uint32_t skip_step = static_cast<uint32_t>(h_step) * 2u;
+  int slot = 0, ahead = SLOTS - 1;
+  for (int64_t row = w.row; row < live; row += w.groups) {
+    __syncwarp();   // all are done with the slot that is filled now
+    fetch(ahead);
+    if (++ahead == SLOTS) ahead = 0;
+    copy_wait(SLOTS - 1);
+    __syncwarp();   // ... and see what the others copied
+    const Slot& t = mine[slot];
+    if (++slot == SLOTS) slot = 0;
+    float2 a[4], b[4], h[4], d[4];
+    smem_row_values<TYPE, 1>(a, t.a, 0, n, lane);
+    smem_row_values<TYPE, 1>(b, t.b + b_skip, 0, n, lane);
+    if (BACK) smem_row_values<ROW_BF16, 1>(d, t.dh + skip, 0, n, lane);
+    skip = (skip + skip_step) & 15u;
+    const float2 lo = both(t.sa[0]), hi = both(t.sa[1]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      a[j] = __fmul2_rn(a[j], j < 2 ? lo : hi);
+      b[j] = __fmul2_rn(b[j], make_float2(t.sb[(b_block + 64 * j + lane) >> 7],
+                                          t.sb[(b_block + 64 * j + 32 + lane) >> 7]));
+    }
+    swiglu_pairs<BACK>(a, b, d, h);
+    if (BACK || p.out) {
+      store_values<1>(out + w.chunk, ROW_BF16, 0, n, lane, reinterpret_cast<const float*>(a));
+      store_values<1>(out + f + w.chunk, ROW_BF16, 0, n, lane, reinterpret_cast<const float*>(b));
+    }
+    if (p.h) store_values<1>(hr + w.chunk, ROW_BF16, 0, n, lane, reinterpret_cast<const float*>(h));
     out += 2 * h_step;
     hr += h_step;
   }
@@ -512,8 +549,7 @@ cudaError_t launch_ckpt_swiglu(const CkptArgs& a, cudaStream_t st) {
     constexpr int T = decltype(format)::value == MOE_CKPT_INT8 ? ROW_INT8 : ROW_E4M3;
     // (dh, [a | b] and h are dense from 16-byte addresses: the width alone decides)
     if (f % 8 == 0) return launch_walk(swiglu_ring_kernel<B, T>, a, f, st, 256);
-    if (f % 2 == 0) return launch_walk(swiglu_kernel<2, 1, B, T>, a, f, st);
-    return launch_walk(swiglu_kernel<1, 1, B, T>, a, f, st);
+    return launch_walk(swiglu_odd_kernel<B, T>, a, f, st, 64);
   };
   using Int8 = std::integral_constant<int, MOE_CKPT_INT8>;
   using E4m3 = std::integral_constant<int, MOE_CKPT_E4M3>;

@@ -324,6 +324,10 @@ cudaError_t launch_ckpt_norm(const NormArgs& a, cudaStream_t st);
 constexpr int NORM_PARTS = 608;
 __host__ __device__ inline int64_t norm_part_floats(int64_t C) { return 2 * ((C + 63) / 64 * 64); }
 cudaError_t launch_norm_bwd(const NormArgs& a, cudaStream_t st);
+// its rows that stay in registers, by the stream's type; *parts: the CTAs that leave sums
+cudaError_t launch_norm_bwd_bf16(const NormArgs& a, int v, int chunks, cudaStream_t st, int* parts);
+cudaError_t launch_norm_bwd_fp32(const NormArgs& a, int chunks, cudaStream_t st, int* parts);
+cudaError_t launch_norm_bwd_fp32_odd(const NormArgs& a, int chunks, cudaStream_t st, int* parts);
 
 struct CkptArgs {
   const void* x;          // rows to save
