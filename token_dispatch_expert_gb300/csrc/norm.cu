@@ -11,6 +11,8 @@
 // rounding of the first sum), all in fp32.  By their bytes these kernels belong to memory: 4 bytes
 // an element forward for bf16 rows (9 with a residual and a checkpoint), 6 backward (8 with the
 // stream's gradient).
+#include <type_traits>
+
 #include "rows8.cuh"
 
 namespace moe {
@@ -49,115 +51,19 @@ __device__ __forceinline__ void affine_store(float* f, const NormArgs& a, void* 
   store_values<V>(yr, a.y_type, chunk, a.C, lane, f);
 }
 
-// nw warps share a row, N chunks to a warp; with nw = 1 the CTA's warps have rows of their own.
-template <int V, int N>
-__global__ void __launch_bounds__(32 * MAX_WARPS)
-norm_kernel(const __grid_constant__ NormArgs a, int nw) {
-  griddep_wait();   // see common.cuh: dependent launches
-  __shared__ RowSums sh;
-  row_sum_init(sh);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int w = nw == 1 ? 0 : warp;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * (nw == 1 ? blockDim.x >> 5 : 1);
-  const int xs = row_size(a.x_type);
-  for (int64_t row = nw == 1 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
-       row < a.rows; row += step) {
-    const void* xr = row_at(a.x, row, a.ldx, xs);
-    const void* rr = a.add ? row_at(a.add, row, a.ld_add, xs) : nullptr;
-    float f[N][8];
-    int chunk[N];
-    {
-      Raw8 x[N], r[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        chunk[i] = (i * nw + w) * CHUNK;
-        load_raw<V>(x[i], xr, a.x_type, chunk[i], a.C, lane);
-      }
-      if (rr) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) load_raw<V>(r[i], rr, a.x_type, chunk[i], a.C, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        unpack_raw<V>(x[i], a.x_type, f[i]);
-        if (rr) {
-          float g[8];
-          unpack_raw<V>(r[i], a.x_type, g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            f[i][j] += g[j];
-            if (a.x_type == ROW_BF16) f[i][j] = __bfloat162float(__float2bfloat16_rn(f[i][j]));
-          }
-        }
-      }
-    }
-    if (a.out) {
-      void* tr = row_at(a.out, row, a.ld_out, xs);
-#pragma unroll
-      for (int i = 0; i < N; ++i) store_values<V>(tr, a.x_type, chunk[i], a.C, lane, f[i]);
-    }
-    float mean = 0.0f;
-    if (a.kind == MOE_NORM_LAYER) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float t = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) t += f[i][j];
-        s += t;
-      }
-      mean = row_sum1(s, sh, 0, w, nw) / static_cast<float>(a.C);
-    }
-    float s = 0.0f, q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float t = 0.0f, u = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = elem_col<V>(chunk[i], lane, j) < a.C ? f[i][j] - mean : 0.0f;
-        t += d;
-        u = fmaf(d, d, u);
-      }
-      s += t;
-      q += u;
-    }
-    const float2 sq = row_sum2(s, q, sh, 1, w, nw);
-    const float shift = a.kind == MOE_NORM_LAYER ? sq.x / static_cast<float>(a.C) : 0.0f;
-    const float var = fmaxf(sq.y / static_cast<float>(a.C) - shift * shift, 0.0f);
-    const float rstd = rsqrtf((sq.y != sq.y ? sq.y : var) + a.eps);
-    if (lane == 0 && w == 0) {
-      if (a.mean) a.mean[row] = mean + shift;
-      if (a.rstd) a.rstd[row] = rstd;
-    }
-    if (a.codes)
-      save_row_chunks<V, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
-                        chunk, a.C, lane, f);
-    void* yr = row_at(a.y, row, a.ld_y, row_size(a.y_type));
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = ((f[i][j] - mean) - shift) * rstd;
-      affine_store<V>(f[i], a, yr, chunk[i], lane);
-    }
-    // with several warps to a row: part[0] of the next row is written only after all have read
-    // part[1] of this one at their next barrier, and part[1] after part[0]'s; the RMS norm sums
-    // through part[1] alone
-    if (nw > 1 && a.kind != MOE_NORM_LAYER) __syncthreads();
-  }
-  griddep_launch();
-}
-
-// The same for rows of whole 16-byte vectors, through shared memory: the rows that follow are
-// fetched while one is worked on.  nw warps share a row, N chunks to a warp; slots: 2, or 1 for the
-// widest rows, which are not fetched ahead.
-template <int N, int X, bool ADD>
+// Rows that stay in registers: nw warps share a row, N chunks to a warp; with nw = 1 the CTA's warps have
+// rows of their own.  The rows that follow come through shared memory while one is worked on; slots:
+// 2, or 1 for the widest rows, which are not fetched ahead.  V = 8: rows of whole 16-byte vectors, a
+// thread copies what it reads; V = 1: rows at any element and of any width, a warp copies the pieces
+// that its columns touch and reads them element by element, 32 columns apart.
+template <int N, int X, bool ADD, int V>
 __global__ void __launch_bounds__(32 * MAX_WARPS)
 norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
   griddep_wait();
   __shared__ RowSums sh;
   extern __shared__ __align__(16) uint8_t ring[];
   row_sum_init(sh);
-  constexpr int XS = X == ROW_BF16 ? 2 : 4, BYTES = CHUNK * XS, PARTS = ADD ? 2 : 1;
+  constexpr int XS = X == ROW_BF16 ? 2 : 4, BYTES = CHUNK * XS + (V == 1 ? 16 : 0), PARTS = ADD ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int w = nw == 1 ? 0 : warp;
   const bool layer = a.kind == MOE_NORM_LAYER;
@@ -169,7 +75,7 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     chunk[i] = (i * nw + w) * CHUNK;
-    if (chunk[i] + 8 * lane >= a.C)
+    if (V == 8 && chunk[i] + 8 * lane >= a.C)
       for (int s = 0; s < slots; ++s)
 #pragma unroll
         for (int t = 0; t < PARTS; ++t) clear_chunk(mine + s * slot_bytes + (i * PARTS + t) * BYTES, X, lane);
@@ -177,12 +83,28 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
   const uint8_t* xr = static_cast<const uint8_t*>(row_at(a.x, first, a.ldx, XS));
   const uint8_t* rr = ADD ? static_cast<const uint8_t*>(row_at(a.add, first, a.ld_add, XS)) : nullptr;
   const int64_t x_step = step * a.ldx * XS, r_step = step * a.ld_add * XS;
+  const uint8_t* const x_end = static_cast<const uint8_t*>(row_at(a.x, a.rows - 1, a.ldx, XS)) + a.C * XS;
+  const uint8_t* const r_end =
+      ADD ? static_cast<const uint8_t*>(row_at(a.add, a.rows - 1, a.ld_add, XS)) + a.C * XS : nullptr;
+  // columns of a chunk; where they begin in the first 16 bytes of their pieces
+  auto width = [&](int i) { return a.C - chunk[i] < CHUNK ? a.C - chunk[i] : CHUNK; };
+  auto skip = [&](const void* p, int64_t row, int64_t ld) {
+    return (static_cast<uint32_t>(reinterpret_cast<uint64_t>(p)) +
+            static_cast<uint32_t>(row) * static_cast<uint32_t>(ld * XS)) & 15u;
+  };
   int64_t next = first;
   auto fetch = [&](int slot) {
     if (next < a.rows) {
       uint8_t* to = mine + slot * slot_bytes;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
+        if (chunk[i] >= a.C) break;
+        if (V == 1) {
+          const int at = chunk[i] * XS, n = width(i) * XS;
+          copy_pieces<XS / 2>(to + i * PARTS * BYTES, xr + at, n, a.x, x_end, lane);
+          if (ADD) copy_pieces<XS / 2>(to + (i * PARTS + 1) * BYTES, rr + at, n, a.add, r_end, lane);
+          continue;
+        }
         copy_chunk(to + i * PARTS * BYTES, xr, X, chunk[i], a.C, lane);
         if (ADD) copy_chunk(to + (i * PARTS + 1) * BYTES, rr, X, chunk[i], a.C, lane);
       }
@@ -192,22 +114,40 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
     }
     copy_commit();
   };
+  auto some = [&](int i) { return V == 8 ? chunk[i] + 8 * lane < a.C : chunk[i] + lane < a.C; };
+  auto put = [&](void* row, int type, int i, const float2* v) {
+    if (V == 1) store_values<1>(row, type, chunk[i], a.C, lane, reinterpret_cast<const float*>(v));
+    else if (some(i)) store_pairs(row, type, chunk[i] + 8 * lane, v);
+  };
+  auto get = [&](float2* v, const void* p, int i) {
+    if (V == 1) load_values<1>(reinterpret_cast<float*>(v), p, a.p_type, chunk[i], a.C, lane);
+    else vector_values(v, p, a.p_type, chunk[i] + 8 * lane);
+  };
   for (int s = 0; s + 1 < slots; ++s) fetch(s);
   int slot = 0, ahead = slots - 1;
   const float over = 1.0f / static_cast<float>(a.C);
   for (int64_t row = first; row < a.rows; row += step) {
+    if (V == 1) __syncwarp();   // all are done with the slot that is filled now
     fetch(ahead);
     if (++ahead == slots) ahead = 0;
     copy_wait(slots - 1);
+    if (V == 1) __syncwarp();   // ... and see what the others copied
     const uint8_t* from = mine + slot * slot_bytes;
     if (++slot == slots) slot = 0;
     float2 f[N][4];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      slot_values(f[i], from + i * PARTS * BYTES, X, lane);
+      // (a chunk begins 512 or 1024 bytes after the one before: the same place in its first piece)
+      if (V == 1)
+        smem_row_values<X, 1>(f[i], from + i * PARTS * BYTES + skip(a.x, row, a.ldx), 0, width(i), lane);
+      else
+        slot_values(f[i], from + i * PARTS * BYTES, X, lane);
       if (ADD) {
         float2 r[4];
-        slot_values(r, from + (i * PARTS + 1) * BYTES, X, lane);
+        if (V == 1)
+          smem_row_values<X, 1>(r, from + (i * PARTS + 1) * BYTES + skip(a.add, row, a.ld_add), 0, width(i), lane);
+        else
+          slot_values(r, from + (i * PARTS + 1) * BYTES, X, lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           f[i][j] = __fadd2_rn(f[i][j], r[j]);
@@ -221,10 +161,7 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
     if (ADD && a.out) {
       void* tr = row_at(a.out, row, a.ld_out, XS);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int c = chunk[i] + 8 * lane;
-        if (c < a.C) store_pairs(tr, X, c, f[i]);
-      }
+      for (int i = 0; i < N; ++i) put(tr, X, i, f[i]);
     }
     float mean = 0.0f;
     if (layer) {
@@ -239,10 +176,15 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
     float2 s = both(0.0f), q = both(0.0f);
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (chunk[i] + 8 * lane < a.C) {
+      if (V == 1 ? chunk[i] + lane < a.C : chunk[i] + 8 * lane < a.C) {
+        const bool all = V == 8 || chunk[i] + CHUNK <= a.C;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 d = __fadd2_rn(f[i][j], both(-mean));
+          float2 d = __fadd2_rn(f[i][j], both(-mean));
+          if (!all) {
+            if (chunk[i] + 64 * j + lane >= a.C) d.x = 0.0f;
+            if (chunk[i] + 64 * j + 32 + lane >= a.C) d.y = 0.0f;
+          }
           s = __fadd2_rn(s, d);
           q = __ffma2_rn(d, d, q);
         }
@@ -256,36 +198,38 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
       if (a.rstd) a.rstd[row] = rstd;
     }
     if (a.codes)
-      save_row_chunks<8, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
+      save_row_chunks<V, N>(row_at(a.codes, row, a.ld_codes, 1), a.scales + row * a.blocks, a.format,
                             chunk, a.C, lane, reinterpret_cast<const float(*)[8]>(f));
     void* yr = row_at(a.y, row, a.ld_y, row_size(a.y_type));
     const float2 low = both(-shift * rstd);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int c = chunk[i] + 8 * lane;
-      if (c >= a.C) continue;
+      if (!some(i)) continue;
       float2 p[4], b[4];
       // xhat = (v - mean) rstd - shift rstd: the shift is the mean's rounding, far below a step of it
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         f[i][j] = __ffma2_rn(__fadd2_rn(f[i][j], both(-mean)), both(rstd), low);
       if (a.gamma && a.beta) {
-        vector_values(p, a.gamma, a.p_type, c);
-        vector_values(b, a.beta, a.p_type, c);
+        get(p, a.gamma, i);
+        get(b, a.beta, i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i][j] = __ffma2_rn(f[i][j], p[j], b[j]);
       } else if (a.gamma) {
-        vector_values(p, a.gamma, a.p_type, c);
+        get(p, a.gamma, i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i][j] = __fmul2_rn(f[i][j], p[j]);
       } else if (a.beta) {
-        vector_values(b, a.beta, a.p_type, c);
+        get(b, a.beta, i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i][j] = __fadd2_rn(f[i][j], b[j]);
       }
-      store_pairs(yr, a.y_type, c, f[i]);
+      put(yr, a.y_type, i, f[i]);
     }
-    if (nw > 1 && !layer) __syncthreads();   // (as in norm_kernel)
+    // with several warps to a row: the first sum's parts of the next row are written only after all
+    // have read the second's of this one at their next barrier, and the second's after the first's;
+    // the RMS norm has the second alone
+    if (nw > 1 && !layer) __syncthreads();
   }
   griddep_launch();
 }
@@ -428,14 +372,15 @@ int norm_vector(const NormArgs& a) {
 }
 
 namespace {
-template <int N, int X, bool ADD>
+template <int N, int X, bool ADD, int V>
 cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
-  constexpr auto kern = norm_ring_kernel<N, X, ADD>;
+  constexpr auto kern = norm_ring_kernel<N, X, ADD, V>;
   const int warps = nw == 1 ? 4 : nw;
-  const int slot = warps * N * CHUNK * row_size(X) * (ADD ? 2 : 1);
+  const int slot = warps * N * (CHUNK * row_size(X) + (V == 1 ? 16 : 0)) * (ADD ? 2 : 1);
   // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
-  int per = ctas_by_registers<norm_ring_kernel<N, X, ADD>>(32 * warps);
+  int per = ctas_by_registers<kern>(32 * warps);
   while (per > 1 && per * 2 * slot > ROW_SMEM) --per;
+  // (more than two took L1 from the parameters and gained nothing, for short rows either)
   const int slots = per * 2 * slot <= ROW_SMEM ? 2 : 1;
   const int64_t ctas = nw == 1 ? (a.rows + warps - 1) / warps : a.rows;
   const int64_t most = static_cast<int64_t>(row_sms()) * per;
@@ -445,14 +390,17 @@ cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(32 * warps), smem,
                     st, 1, a, nw, slots);
 }
-// Chunks to a warp: four where that leaves few of them empty, else two.
-template <int X, bool ADD>
+// Chunks to a warp: four to all of a row of up to four, since then no barrier is needed (1024 columns
+// with sum and checkpoint 65 us, with two to a warp 70); two up to eight chunks (2048 columns 71 us, with
+// four 99) and where four leave an eighth of them empty; else four (4096 columns 69 us, with two 74).
+// Element by element always four (1413 columns without a sum 127 us, with two 215).
+template <int X, bool ADD, int V>
 cudaError_t launch_norm_rows(const NormArgs& a, int chunks, cudaStream_t st) {
-  if (chunks == 1) return launch_norm_ring<1, X, ADD>(a, 1, st);
+  if (chunks == 1) return launch_norm_ring<1, X, ADD, V>(a, 1, st);
   const int fours = (chunks + 3) / 4, twos = (chunks + 1) / 2;
-  if (chunks == 2 || (twos <= MAX_WARPS && 8 * (4 * fours - chunks) > chunks))
-    return launch_norm_ring<2, X, ADD>(a, twos, st);
-  return launch_norm_ring<4, X, ADD>(a, fours, st);
+  const bool two = chunks == 2 || (V == 8 && chunks > 4 && twos <= MAX_WARPS &&
+                                   (chunks <= 8 || 8 * (4 * fours - chunks) > chunks));
+  return two ? launch_norm_ring<2, X, ADD, V>(a, twos, st) : launch_norm_ring<4, X, ADD, V>(a, fours, st);
 }
 }  // namespace
 
@@ -466,23 +414,15 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
     if (v == 2) return launch_pdl(norm_wide_kernel<2>, grid, dim3(512), 0, st, 1, a);
     return launch_pdl(norm_wide_kernel<1>, grid, dim3(512), 0, st, 1, a);
   }
-  if (v == 8) {
+  auto go = [&](auto vector) {
+    constexpr int V = decltype(vector)::value;
     if (a.x_type == ROW_BF16)
-      return a.add ? launch_norm_rows<ROW_BF16, true>(a, chunks, st)
-                   : launch_norm_rows<ROW_BF16, false>(a, chunks, st);
-    return a.add ? launch_norm_rows<ROW_FP32, true>(a, chunks, st)
-                 : launch_norm_rows<ROW_FP32, false>(a, chunks, st);
-  }
-  const int n = chunks == 1 ? 1 : chunks == 2 ? 2 : 4;
-  const int nw = (chunks + n - 1) / n;
-  const int warps = nw == 1 ? 4 : nw;
-  const int64_t ctas = nw == 1 ? (a.rows + 3) / 4 : a.rows;
-  const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most)), block(32 * warps);
-#define MOE_NORM(V, N) launch_pdl(norm_kernel<V, N>, grid, block, 0, st, 1, a, nw)
-#define MOE_NORM_N(V) (n == 1 ? MOE_NORM(V, 1) : n == 2 ? MOE_NORM(V, 2) : MOE_NORM(V, 4))
-  return v == 2 ? MOE_NORM_N(2) : MOE_NORM_N(1);
-#undef MOE_NORM_N
-#undef MOE_NORM
+      return a.add ? launch_norm_rows<ROW_BF16, true, V>(a, chunks, st)
+                   : launch_norm_rows<ROW_BF16, false, V>(a, chunks, st);
+    return a.add ? launch_norm_rows<ROW_FP32, true, V>(a, chunks, st)
+                 : launch_norm_rows<ROW_FP32, false, V>(a, chunks, st);
+  };
+  return v == 8 ? go(std::integral_constant<int, 8>()) : go(std::integral_constant<int, 1>());
 }
 
 cudaError_t launch_ckpt_norm(const NormArgs& a, cudaStream_t st) {

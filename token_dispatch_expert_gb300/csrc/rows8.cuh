@@ -593,6 +593,26 @@ __device__ __forceinline__ void span_ends(uint8_t* to, const void* p, uint32_t n
   }
 }
 
+// The 16-byte pieces that the bytes [p, p + n) touch, copied by a warp to `to`, which stands for p rounded
+// down; at most 32 * ROUNDS + 1 of them.  A piece that passes an end of its tensor, [first, end), is
+// read by bytes.
+template <int ROUNDS>
+__device__ __forceinline__ void copy_pieces(uint8_t* to, const void* p, int n, const void* first,
+                                            const void* end, int lane) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p), low = a & ~15ull;
+  const uint64_t f = reinterpret_cast<uint64_t>(first), e = reinterpret_cast<uint64_t>(end);
+#pragma unroll
+  for (int r = 0; r <= ROUNDS; ++r) {
+    if (r == ROUNDS && lane != 0) break;
+    const uint64_t at = low + 16 * (32 * r + lane);
+    if (at >= a + n) break;
+    if (at >= f && at + 16 <= e) {
+      copy_async16(smem_u32(to + (at - low)), reinterpret_cast<const void*>(at));
+    } else {
+      for (uint64_t b = at < f ? f : at; b < at + 16 && b < e; ++b) to[b - low] = *reinterpret_cast<const uint8_t*>(b);
+    }
+  }
+}
 // untiled bulk copy global -> shared of a multiple of 16 bytes between 16-byte addresses
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile(
