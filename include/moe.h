@@ -616,7 +616,8 @@ moe_status_t moe_fp8_wgrad(const moe_fp8_wgrad_t *g, const void *a, const float 
  * block of 128 along the row (the last one may be shorter).  With amax the block's largest
  * magnitude, held at or above 2^-110:
  *   MOE_CKPT_INT8  scale amax / 127, code = the whole number nearest to v * (127 / amax), ties to
- *                  even, the product rounded once: a value is off by at most half a scale
+ *                  even, the product rounded once: a value is off by at most half a scale (and the
+ *                  largest fp32 number itself may be restored as infinity)
  *   MOE_CKPT_E4M3  scale and code as moe_fp8_quantize's along the row (pow2 = 0), so that the row
  *                  codes of a product's operand are its checkpoint
  * with quotients correctly rounded in fp32.  A value is restored as code * scale in fp32, and
@@ -659,7 +660,8 @@ typedef struct {
  * Statistics are fp32: squares of magnitudes above 2^63 overflow.  A constant row with eps = 0 is
  * NaN.  Rows of x, residual, y and total may be strided and need only their elements' alignment
  * (off 16 bytes, or with a width off 8, accesses are narrower); gamma, beta, mean, rstd, codes and
- * scales are dense.  total may be x or residual itself, and y may be x or residual.
+ * scales are dense.  total may be x or residual itself, and so may y if it is of their type and has
+ * their distance.
  */
 moe_status_t moe_norm(const moe_norm_t *p, const void *x, const void *residual_or_null,
                       const void *gamma_or_null, const void *beta_or_null, void *y,
@@ -678,8 +680,8 @@ int64_t moe_norm_ws_size(int64_t rows, int32_t C);
  * and rstd are moe_norm's, of v itself; mean is NULL with MOE_NORM_RMS.  dx is the gradient of x
  * and of residual alike; add (NULL: none) is the gradient that reaches v by another way, the
  * stream's own.  dgamma and dbeta may be NULL; with rows = 0 they are zeros.  Sums over the rows
- * are fp32, in an order that rows, C and the device alone decide: the same bits every time.  dx may
- * be add or dy itself.  ws: moe_norm_ws_size bytes; its contents need not be kept.
+ * are fp32, in an order that rows, C, the types, the alignment and the device decide: the same bits
+ * every time.  dx may be add itself, or dy if that is of its type and has its distance.  ws: moe_norm_ws_size bytes; its contents need not be kept.
  */
 moe_status_t moe_norm_bwd(const moe_norm_t *p, const void *dy, const void *x,
                           const float *x_scales_or_null, const float *mean, const float *rstd,

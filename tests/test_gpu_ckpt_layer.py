@@ -243,6 +243,53 @@ def test_example_runs():
                                     checkpoint=fmt, log=lambda s: None)).all()
 
 
+FIRST_CALLS_IN_A_CAPTURE = """
+import torch
+import token_dispatch_expert_gb300 as tde
+T, C = 40, {C}
+x, dy = (torch.randn((T, C), device="cuda").bfloat16() for _ in range(2))
+gamma = torch.rand(C, device="cuda")
+new = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")
+ws = torch.zeros(tde.moe_norm_ws_size(T, C), dtype=torch.uint8, device="cuda")
+ld = (C + 15) // 16 * 16
+def step(o):
+    c = o["codes"], o["scales"]
+    tde.moe_norm(x, o["y"], gamma, residual=dy, total=o["s"], mean=o["mean"], rstd=o["rstd"], codes=c[0], scales=c[1])
+    tde.moe_norm_bwd(dy, c[0], o["mean"], o["rstd"], o["dx"], o["dg"], o["db"], gamma=gamma, scales=c[1], ws=ws)
+    tde.moe_ckpt_norm(*c, o["mean"], o["rstd"], o["n"], gamma)
+    tde.moe_ckpt_save(x, *c, ws=ws)
+    tde.moe_ckpt_load(*c, o["x"], ws=ws)
+    if C % 2 == 0:
+        tde.moe_ckpt_swiglu(*c, o["ab"], o["h"], ws=ws)
+        tde.moe_ckpt_swiglu_bwd(o["h"], *c, o["dab"], ws=ws)
+def buffers():
+    bf = torch.bfloat16
+    return dict({{n: new(T, C, dt=bf) for n in ("y", "s", "dx", "n", "x", "ab", "dab")}}, h=new(T, C // 2, dt=bf),
+                mean=new(T), rstd=new(T), dg=new(C), db=new(C), codes=new(T, ld, dt=torch.int8),
+                scales=new(T, (C + 127) // 128))
+a, b = buffers(), buffers()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step(a)
+g.replay()
+step(b)
+assert all(torch.equal(a[n], b[n]) for n in a), [n for n in a if not torch.equal(a[n], b[n])]
+assert tde.moe_status(ws) == (0, 0) and bool(a["y"].any()) and bool(a["dg"].any())
+print("same")
+"""
+
+
+@pytest.mark.parametrize("C", [4096, 1410, 7169])
+def test_first_calls_of_a_process_in_a_capture(C):
+    """Whatever the library looks up once (registers, shared memory) it can look up in a capture."""
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_IN_A_CAPTURE.format(C=C)], cwd=root, capture_output=True,
+                       text=True, timeout=120)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_refusals():
     cfg = tde.make_config(64, 128, 8, 2, 64)
     with pytest.raises(ValueError, match="^checkpoint: expected"):

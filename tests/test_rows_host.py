@@ -231,6 +231,7 @@ def test_ckpt_binding():
             (lambda: tde.moe_ckpt_save(d(4, 16, dt=torch.float16), c, s, ws=ws), "x: expected bfloat16 or"),
             (lambda: tde.moe_ckpt_load(c, s, d(5, 16), ws=ws), "codes: expected shape"),
             (lambda: tde.moe_ckpt_save(d(4, 16), c, s, offsets=d(3, dt=torch.int64), ws=ws), "offsets: expected int32"),
+            (lambda: tde.moe_ckpt_save(d(4, 16), c, s, offsets=d(0, dt=torch.int32), ws=ws), "offsets: expected at least"),
             (lambda: tde.moe_ckpt_swiglu(c, s, ws=ws), "ab, h: expected"),
             (lambda: tde.moe_ckpt_swiglu(c, s, d(4, 15), ws=ws), "ab: expected an even"),
             (lambda: tde.moe_ckpt_swiglu(c, s, d(4, 16), d(4, 16), ws=ws), "h: expected shape"),

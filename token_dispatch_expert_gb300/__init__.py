@@ -775,6 +775,15 @@ def _vector(t, name, n):
     return t.data_ptr() if t.is_cuda and t.is_contiguous() else _p(t)
 
 
+def _bf16(t, name):
+    """The address of a dense bf16 buffer."""
+    if t is None:
+        return None
+    if _row_types.get(t.dtype) != 0:
+        raise ValueError(f"{name}: expected bfloat16, got {t.dtype}")
+    return t.data_ptr() if t.is_cuda and t.is_contiguous() else _p(t)
+
+
 def _params(C, a, b, names):
     """(type, pointer, pointer) of two vectors of one type, each of which may be missing."""
     kind, pa, pb = 0, None, None
@@ -820,6 +829,8 @@ def _live(offsets):
     """Address of the last of the segments' offsets: the number of live rows."""
     if offsets is None:
         return None
+    if offsets.numel() < 1:
+        raise ValueError("offsets: expected at least one element, got 0")
     return _typed(offsets, "int32", "offsets") + 4 * (offsets.numel() - 1)
 
 
@@ -952,8 +963,8 @@ def moe_ckpt_swiglu(codes, scales, ab=None, h=None, *, offsets=None, ws, stream=
         _shape("h", h, (rows, C // 2))
     fmt, ld, pc, ps = _checkpoint(codes, scales, rows, C)
     p, at = _ckpt_struct(rows, C, fmt, 0, C, ld)
-    _check(lib().moe_ckpt_swiglu(at, pc, ps, _live(offsets), _typed(ab, "bfloat16", "ab"),
-                                 _typed(h, "bfloat16", "h"), _p(ws), _s(stream)),
+    _check(lib().moe_ckpt_swiglu(at, pc, ps, _live(offsets), _bf16(ab, "ab"),
+                                 _bf16(h, "h"), _p(ws), _s(stream)),
            "moe_ckpt_swiglu")
 
 
@@ -968,9 +979,9 @@ def moe_ckpt_swiglu_bwd(dh, codes, scales, dab, h=None, *, offsets=None, ws, str
         _shape("h", h, (rows, f))
     fmt, ld, pc, ps = _checkpoint(codes, scales, rows, 2 * f)
     p, at = _ckpt_struct(rows, 2 * f, fmt, 0, 2 * f, ld)
-    _check(lib().moe_ckpt_swiglu_bwd(at, _typed(dh, "bfloat16", "dh"), pc, ps,
-                                     _live(offsets), _typed(dab, "bfloat16", "dab"),
-                                     _typed(h, "bfloat16", "h"), _p(ws), _s(stream)),
+    _check(lib().moe_ckpt_swiglu_bwd(at, _bf16(dh, "dh"), pc, ps,
+                                     _live(offsets), _bf16(dab, "dab"),
+                                     _bf16(h, "h"), _p(ws), _s(stream)),
            "moe_ckpt_swiglu_bwd")
 
 
