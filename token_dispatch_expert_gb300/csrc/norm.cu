@@ -74,7 +74,9 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
   const bool layer = a.kind == MOE_NORM_LAYER;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (nw == 1 ? warps : 1);
   const int64_t first = nw == 1 ? static_cast<int64_t>(blockIdx.x) * warps + warp : blockIdx.x;
-  uint8_t* const mine = ring + warp * (N * PARTS * BYTES);
+  // V = 1: first the columns' gamma and beta in fp32, as each thread reads them
+  uint8_t* const par = ring + w * N * 2048;
+  uint8_t* const mine = ring + (V == 1 ? nw * N * 2048 : 0) + warp * (N * PARTS * BYTES);
   const int slot_bytes = warps * (N * PARTS * BYTES);
   int chunk[N];
 #pragma unroll
@@ -124,10 +126,24 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
     if (V == 1) store_values<1>(row, type, chunk[i], a.C, lane, reinterpret_cast<const float*>(v));
     else if (some(i)) store_pairs(row, type, chunk[i] + 8 * lane, v);
   };
-  auto get = [&](float2* v, const void* p, int i) {
-    if (V == 1) load_values<1>(reinterpret_cast<float*>(v), p, a.p_type, chunk[i], a.C, lane);
+  auto get = [&](float2* v, const void* p, int i, int which) {
+    if (V == 1) slot_values(v, par + (which * N + i) * 1024, ROW_FP32, lane);
     else vector_values(v, p, a.p_type, chunk[i] + 8 * lane);
   };
+  if (V == 1)
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {
+      const void* p = t ? a.beta : a.gamma;
+      if (!p) continue;
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {   // (with nw = 1 every warp writes the same; a thread reads its own)
+        float v[8];
+        load_values<1>(v, p, a.p_type, (i * nw + w) * CHUNK, a.C, lane);
+        uint8_t* to = par + (t * N + i) * 1024 + 16 * lane;
+        *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(to + 512) = make_float4(v[4], v[5], v[6], v[7]);
+      }
+    }
   for (int s = 0; s + 1 < slots; ++s) fetch(s);
   int slot = 0, ahead = slots - 1;
   const float over = 1.0f / static_cast<float>(a.C);
@@ -216,16 +232,16 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
       for (int j = 0; j < 4; ++j)
         f[i][j] = __ffma2_rn(__fadd2_rn(f[i][j], both(-mean)), both(rstd), low);
       if (a.gamma && a.beta) {
-        get(p, a.gamma, i);
-        get(b, a.beta, i);
+        get(p, a.gamma, i, 0);
+        get(b, a.beta, i, 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i][j] = __ffma2_rn(f[i][j], p[j], b[j]);
       } else if (a.gamma) {
-        get(p, a.gamma, i);
+        get(p, a.gamma, i, 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i][j] = __fmul2_rn(f[i][j], p[j]);
       } else if (a.beta) {
-        get(b, a.beta, i);
+        get(b, a.beta, i, 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) f[i][j] = __fadd2_rn(f[i][j], b[j]);
       }
@@ -383,13 +399,14 @@ cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
   const int warps = nw == 1 ? 4 : nw;
   const int slot = warps * N * (CHUNK * row_size(X) + (V == 1 ? 16 : 0)) * (ADD ? 2 : 1);
   // CTAs to an SM by threads (registers), then as many slots as their shared memory allows
+  const int par = V == 1 ? nw * N * 2048 : 0;
   int per = ctas_by_registers<kern>(32 * warps);
-  while (per > 1 && per * 2 * slot > ROW_SMEM) --per;
+  while (per > 1 && per * (2 * slot + par) > ROW_SMEM) --per;
   // (more than two took L1 from the parameters and gained nothing, for short rows either)
-  const int slots = per * 2 * slot <= ROW_SMEM ? 2 : 1;
+  const int slots = per * (2 * slot + par) <= ROW_SMEM ? 2 : 1;
   const int64_t ctas = nw == 1 ? (a.rows + warps - 1) / warps : a.rows;
   const int64_t most = static_cast<int64_t>(row_sms()) * per;
-  const int smem = slots * slot;
+  const int smem = slots * slot + par;
   const cudaError_t e = allow_smem<kern>(smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas < most ? ctas : most)), dim3(32 * warps), smem,

@@ -593,24 +593,26 @@ __device__ __forceinline__ void span_ends(uint8_t* to, const void* p, uint32_t n
 }
 
 // The 16-byte pieces that the bytes [p, p + n) touch, copied by a warp to `to`, which stands for p rounded
-// down; at most 32 * ROUNDS + 1 of them.  A piece that passes an end of its tensor, [first, end), is
-// read by bytes.
+// down; at most 32 * ROUNDS + 1 of them.  Where they pass an end of their tensor, [first, end), the bytes
+// themselves are read.
 template <int ROUNDS>
 __device__ __forceinline__ void copy_pieces(uint8_t* to, const void* p, int n, const void* first,
                                             const void* end, int lane) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p), low = a & ~15ull;
-  const uint64_t f = reinterpret_cast<uint64_t>(first), e = reinterpret_cast<uint64_t>(end);
+  const uint64_t low = reinterpret_cast<uint64_t>(p) & ~15ull;
+  const int skip = static_cast<int>(reinterpret_cast<uint64_t>(p)) & 15, want = skip + n;   // bytes from low
+  if (low >= reinterpret_cast<uint64_t>(first) &&
+      low + ((want + 15) & ~15) <= reinterpret_cast<uint64_t>(end)) {
+    const uint32_t dst = smem_u32(to);
 #pragma unroll
-  for (int r = 0; r <= ROUNDS; ++r) {
-    if (r == ROUNDS && lane != 0) break;
-    const uint64_t at = low + 16 * (32 * r + lane);
-    if (at >= a + n) break;
-    if (at >= f && at + 16 <= e) {
-      copy_async16(smem_u32(to + (at - low)), reinterpret_cast<const void*>(at));
-    } else {
-      for (uint64_t b = at < f ? f : at; b < at + 16 && b < e; ++b) to[b - low] = *reinterpret_cast<const uint8_t*>(b);
-    }
+    for (int r = 0; r < ROUNDS; ++r)
+      if (512 * r + 16 * lane < want)
+        copy_async16(dst + 512 * r + 16 * lane, reinterpret_cast<const uint8_t*>(low) + 512 * r + 16 * lane);
+    if (lane == 0 && 512 * ROUNDS < want)
+      copy_async16(dst + 512 * ROUNDS, reinterpret_cast<const uint8_t*>(low) + 512 * ROUNDS);
+    return;
   }
+  // (a tensor's first and last rows)
+  for (int i = skip + lane; i < want; i += 32) to[i] = reinterpret_cast<const uint8_t*>(low)[i];
 }
 // untiled bulk copy global -> shared of a multiple of 16 bytes between 16-byte addresses
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
