@@ -55,7 +55,7 @@ def check_stats(mean, rstd, v, kind, eps):
 
 
 WIDTHS = [1, 2, 7, 64, 100, 127, 128, 129, 256, 257, 512, 513, 1000, 1024, 1413, 2056, 4096, 7168,
-          9001, 16384, 16392, 20010, 33001]
+          9001, 11999, 13579, 16002, 16384, 16392, 20010, 33001]
 
 
 def run_norm(rng, R, C, kind, x, y, p, add, fmt, eps=1e-5, offset=0.0, first=0, pad=0):

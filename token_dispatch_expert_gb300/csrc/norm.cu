@@ -13,7 +13,7 @@
 // stream's gradient).  What is reached, where a copy reaches 6.79 TB/s:
 //   16,384 x 4096 bf16 with sum, statistics and int8 codes   5.6 TB/s, 108 us: two barriers a row, and
 //                                                gamma and beta from L1 for every row
-//   28,308 x 1413, the same                      1.4 TB/s, 200 us: instructions, an element at a time
+//   28,308 x 1413, the same                      2.3 TB/s, 156 us: instructions, an element at a time
 //   from codes, 4096 x 7168                      4.9 TB/s, 18 us: 3 of it the launch's ramp
 // (the gradient: norm_bwd.cu)
 #include <type_traits>
@@ -415,7 +415,8 @@ cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
 // Chunks to a warp: four to all of a row of up to four, since then no barrier is needed (1024 columns
 // with sum and checkpoint 65 us, with two to a warp 70); two up to eight chunks (2048 columns 71 us, with
 // four 99) and where four leave an eighth of them empty; else four (4096 columns 69 us, with two 74).
-// Element by element always four (1413 columns without a sum 127 us, with two 215).
+// Element by element always four (1413 columns without a sum 127 us, with two 215; since the parameters
+// lie in shared memory there, 71).
 template <int X, bool ADD, int V>
 cudaError_t launch_norm_rows(const NormArgs& a, int chunks, cudaStream_t st) {
   if (chunks == 1) return launch_norm_ring<1, X, ADD, V>(a, 1, st);
@@ -430,7 +431,10 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t st) {
   const int chunks = (a.C + CHUNK - 1) / CHUNK;
   const int v = norm_vector(a);
   const int64_t most = static_cast<int64_t>(1) << 30;
-  if (chunks > 4 * MAX_WARPS) {
+  // (element by element the parameters take shared memory too: the widest fp32 rows with a residual
+  // leave them no room)
+  const int row = (chunks + 3) / 4 * 4 * ((CHUNK * row_size(a.x_type) + 16) * (a.add ? 2 : 1) + 2048);
+  if (chunks > 4 * MAX_WARPS || (v != 8 && row > ROW_SMEM)) {
     const dim3 grid(static_cast<unsigned>(a.rows < most ? a.rows : most));
     if (v == 8) return launch_pdl(norm_wide_kernel<8>, grid, dim3(512), 0, st, 1, a);
     if (v == 2) return launch_pdl(norm_wide_kernel<2>, grid, dim3(512), 0, st, 1, a);
