@@ -55,7 +55,7 @@ class Block:
         return o["dx"], grads
 
 
-def train(tokens=2048, width=1024, ffn=512, experts=16, k=2, blocks=4, steps=6, lr=0.5, kind="layer",
+def train(tokens=2048, width=1024, ffn=512, experts=16, k=2, blocks=4, steps=6, lr=0.1, kind="layer",
           checkpoint="int8", seed=0, log=print):
     """Runs the steps; returns the losses."""
     g = torch.Generator(device="cuda").manual_seed(seed)
