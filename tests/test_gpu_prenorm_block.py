@@ -1,0 +1,111 @@
+"""A pre-norm block (norm, gate, layer that keeps checkpoints) as the README runs it, against 64-bit
+numpy that rounds and quantises where the block does.
+
+Each block is compared on the arguments that it was given, so a tolerance is that of the layers that
+it is built from: within 2e-2 of rms + |o| and rel-L2 1e-2 (gpu_util); from E4M3 checkpoints within 0.1,
+since a value that lies next to a border between two codes may be kept as either, a step of 2^-3
+(test_gpu_fp8_layer).
+"""
+
+import os
+
+import numpy as np
+import pytest
+import torch
+
+import block_ref
+import rows_ref as ref
+import token_dispatch_expert_gb300 as tde
+from gpu_util import assert_close
+from rows_ref import f64
+from test_gpu_ckpt_layer import bf, kept
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def block(p, stream, branch, dstream, dbranch, logits, r, kind, fmt):
+    """Forward and backward of one block.  p: gamma, beta, gate, W1, W2; logits: the gate's, in 32 bits;
+    r: the routing that the layer chose from them (checked by other tests)."""
+    T, d = stream.shape
+    E, f = p["W1"].shape[0], p["W1"].shape[1] // 2
+    W1, W2 = (ref.typed(p[n], "bf16") for n in ("W1", "W2"))
+    s = ref.typed(ref.f32(stream + branch), "bf16")
+    beta = p["beta"] if kind == "layer" else 0.0
+    n = ref.typed(ref.norm(s, p["gamma"], beta, kind, 1e-5), "bf16")
+    m, rstd = ref.stats(s, kind, 1e-5)
+    sk = kept(s, fmt)
+    again = ref.typed((sk - m[:, None]) * rstd[:, None] * p["gamma"] + beta, "bf16")
+    seg = [slice(r["offsets"][e], r["offsets"][e + 1]) for e in range(E)]
+    rows = r["offsets"][-1]
+    src = r["src_tok"][:rows]
+    ab, yp = np.zeros((rows, 2 * f)), np.zeros((rows, d))
+    for e in range(E):
+        ab[seg[e]] = ref.typed(n[src[seg[e]]] @ W1[e].T, "bf16")
+    h = ref.typed(ref.swiglu(ab[:, :f], ab[:, f:]), "bf16")
+    for e in range(E):
+        yp[seg[e]] = ref.typed(h[seg[e]] @ W2[e].T, "bf16")
+    abk, ypk = kept(ab, fmt), kept(yp, fmt)
+    hk, abk = ref.typed(ref.swiglu(abk[:, :f], abk[:, f:]), "bf16"), ref.typed(abk, "bf16")
+    w = r["topk_w"].astype(np.float64)
+    y, dw, dyp = np.zeros((T, d)), np.zeros(w.shape), np.zeros((rows, d))
+    slots = [(t, j, r["dest_row"][t, j]) for t, j in np.ndindex(w.shape) if r["dest_row"][t, j] >= 0]
+    for t, j, at in slots:
+        y[t] += w[t, j] * yp[at]
+        dw[t, j] = dbranch[t] @ ypk[at]
+        dyp[at] = ref.typed(w[t, j] * dbranch[t], "bf16")
+    dab, dxp, dx = np.zeros((rows, 2 * f)), np.zeros((rows, d)), np.zeros((T, d))
+    dW1, dW2 = np.zeros(W1.shape), np.zeros(W2.shape)
+    for e in range(E):
+        g = seg[e]
+        dab[g] = ref.typed(np.concatenate(ref.swiglu_bwd(dyp[g] @ W2[e], abk[g, :f], abk[g, f:]), 1), "bf16")
+        dxp[g] = ref.typed(dab[g] @ W1[e], "bf16")
+        dW1[e], dW2[e] = dab[g].T @ again[src[g]], dyp[g].T @ hk[g]
+    for t, j, at in slots:
+        dx[t] += dxp[at]
+    dl = block_ref.route_grad(logits, r["topk_idx"], dw, score="softmax", renorm=True, scale=1.0)
+    by_gate = dl @ p["gate"]
+    dn = ref.typed(ref.f32(ref.typed(dx, "bf16") + by_gate), "bf16")
+    dv, dgamma, dbeta = ref.norm_bwd(dn, sk, m, rstd, p["gamma"], dstream, kind)
+    grads = {"gamma": dgamma, "gate": dl.T @ again, "W1": dW1, "W2": dW2}
+    if kind == "layer":
+        grads["beta"] = dbeta
+    # what the gradient loses without the gate's share: far more than any tolerance here
+    assert np.linalg.norm(by_gate) > 0.1 * np.linalg.norm(dn)
+    return {"n": n, "stream": s, "branch": y, "dx": dv, "grads": grads}
+
+
+def routing(layer):
+    return {n: v.cpu().numpy() for n, v in layer.r.items()}
+
+
+def inputs(rng, T, d, E, f):
+    p = {"gamma": 1 + 0.3 * rng.normal(size=d), "beta": 0.2 * rng.normal(size=d),
+         "gate": 0.3 * rng.normal(size=(E, d)), "W1": 0.2 * rng.normal(size=(E, 2 * f, d)),
+         "W2": 0.2 * rng.normal(size=(E, d, f))}
+    return {n: ref.f32(v) for n, v in p.items()}, [ref.typed(rng.normal(size=(T, d)), "bf16") for _ in range(4)]
+
+
+def test_readme_block():
+    """The README's lines for a pre-norm block, as they stand there."""
+    text = open(os.path.join(ROOT, "README.md")).read()
+    lines = text[text.index("# a pre-norm block"):]
+    lines = lines[:lines.index("```")]
+    T, d, E, k, f = 150, 128, 8, 2, 64
+    p, (stream, branch, dstream, dbranch) = inputs(np.random.default_rng(4), T, d, E, f)
+    put = lambda v: torch.from_numpy(v.astype(np.float32)).cuda()  # noqa: E731
+    n = ref.typed(ref.norm(ref.typed(ref.f32(stream + branch), "bf16"), p["gamma"], p["beta"], "layer", 1e-5), "bf16")
+    names = dict(tde=tde, torch=torch, cfg=tde.make_config(T, d, E, k, f), T=T, d=d, E=E, k=k, ffn=f,
+                 stream=bf(stream), branch=bf(branch), dstream=bf(dstream), dbranch=bf(dbranch),
+                 gamma=put(p["gamma"]), beta=put(p["beta"]), gate=put(p["gate"]), W1=bf(p["W1"]), W2=bf(p["W2"]),
+                 logits=put(n) @ put(p["gate"]).t())
+    exec(lines, names)
+    o = block(p, stream, branch, dstream, dbranch, f64(names["logits"]), routing(names["moe"]), "layer", "int8")
+    assert_close("logits", f64(names["logits"]), o["n"] @ p["gate"].T)
+    assert_close("stream", f64(names["stream"]), o["stream"])
+    assert_close("branch", f64(names["branch"]), o["branch"])
+    assert_close("dx", f64(names["g2"]["dx"]), o["dx"])
+    assert_close("dgamma", f64(names["g2"]["dgamma"]), o["grads"]["gamma"])
+    assert_close("dbeta", f64(names["g2"]["dbeta"]), o["grads"]["beta"])
+    for name in ("W1", "W2"):
+        assert_close("d" + name, f64(names["g"]["d" + name]), o["grads"][name])
