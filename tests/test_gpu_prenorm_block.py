@@ -1,5 +1,5 @@
-"""A pre-norm block (norm, gate, layer that keeps checkpoints) as the README runs it, against 64-bit
-numpy that rounds and quantises where the block does.
+"""A pre-norm block (norm, gate, layer that keeps checkpoints) and a stack of them, as the README and
+the example program run them, against 64-bit numpy that rounds and quantises where the block does.
 
 Each block is compared on the arguments that it was given, so a tolerance is that of the layers that
 it is built from: within 2e-2 of rms + |o| and rel-L2 1e-2 (gpu_util); from E4M3 checkpoints within 0.1,
@@ -8,6 +8,7 @@ since a value that lies next to a border between two codes may be kept as either
 """
 
 import os
+import sys
 
 import numpy as np
 import pytest
@@ -109,3 +110,52 @@ def test_readme_block():
     assert_close("dbeta", f64(names["g2"]["dbeta"]), o["grads"]["beta"])
     for name in ("W1", "W2"):
         assert_close("d" + name, f64(names["g"]["d" + name]), o["grads"][name])
+
+
+@pytest.mark.parametrize("kind,fmt", [("layer", "int8"), ("rms", "int8"), ("layer", "e4m3")])
+def test_example_stack(kind, fmt, monkeypatch):
+    """One step of the example's stack: what each block gives for what it was given, what it was given
+    by the block before it or behind it, and the parameters after the step."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import prenorm_moe_training_step as ex
+    blocks, T, d, E, k, f, lr = [], 130, 128, 8, 2, 64, 0.1
+
+    class Recorded(ex.Block):
+        def __init__(self, *a):
+            super().__init__(*a)
+            rng = np.random.default_rng(len(blocks))
+            self.start, _ = inputs(rng, T, d, E, f)
+            self.p = {n: torch.from_numpy(v.astype(np.float32)).cuda() for n, v in self.start.items()}
+            blocks.append(self)
+
+        def forward(self, *a):
+            self.args, self.out = a, super().forward(*a)
+            return self.out
+
+        def backward(self, *a):
+            self.dargs, self.dout = a, super().backward(*a)
+            return self.dout
+
+    monkeypatch.setattr(ex, "Block", Recorded)
+    losses = ex.train(tokens=T, width=d, ffn=f, experts=E, k=k, blocks=3, steps=1, lr=lr, kind=kind,
+                      checkpoint=fmt, log=lambda s: None)
+    assert len(blocks) == 3 and np.isfinite(losses).all()
+    tol = 0.1 if fmt == "e4m3" else 2e-2
+    for i, b in enumerate(blocks):
+        o = block(b.start, *(f64(t) for t in b.args + b.dargs), f64(b.logits), routing(b.moe), kind, fmt)
+        assert_close("logits", f64(b.logits), o["n"] @ b.start["gate"].T)
+        assert_close("stream", f64(b.out[0]), o["stream"])
+        assert_close("branch", f64(b.out[1]), o["branch"])
+        assert_close("dx", f64(b.dout[0]), o["dx"], max_tol=tol)
+        assert set(b.dout[1]) == set(o["grads"])
+        for n, want in o["grads"].items():
+            assert_close("d" + n, f64(b.dout[1][n]), want, max_tol=tol)
+            assert torch.equal(b.p[n], torch.from_numpy(b.start[n].astype(np.float32)).cuda() - lr / T * b.dout[1][n])
+        if i:   # a block's arguments are what the one before it gave; both have one gradient
+            assert all(a is g for a, g in zip(b.args, blocks[i - 1].out))
+            assert all(a is b.dout[0] for a in blocks[i - 1].dargs)
+    # the last block's results are added up: half the summed square's gradient is the difference
+    last = blocks[-1]
+    assert last.dargs[0] is last.dargs[1]
+    want = float((f64(last.dargs[0]) ** 2).mean())     # (rounded to bf16: 2^-8 of each difference)
+    assert abs(losses[0] - want) <= 1e-2 * want
