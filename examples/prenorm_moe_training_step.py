@@ -22,7 +22,7 @@ import token_dispatch_expert_gb300 as tde  # noqa: E402
 class Block:
     def __init__(self, scratch, rand, kind, checkpoint):
         c = scratch.cfg
-        self.norm = tde.MoENorm(c.T, c.d, kind=kind, checkpoint=checkpoint)
+        self.norm = tde.MoENorm(c.T, c.d, kind=kind, checkpoint=checkpoint, ws=scratch.ws)
         self.moe = tde.CheckpointedMoELayer(scratch, checkpoint)
         self.p = {"gamma": torch.ones(c.d, device="cuda"), "beta": torch.zeros(c.d, device="cuda"),
                   "gate": 0.02 * rand(c.E, c.d), "W1": 0.03 * rand(c.E, 2 * c.ffn, c.d),

@@ -1,0 +1,57 @@
+"""What the norms and the layers that keep 8-bit checkpoints hold, counted from their tensors.  CPU only:
+the buffers are made on the meta device."""
+
+import pytest
+import torch
+
+import token_dispatch_expert_gb300 as tde
+
+
+@pytest.fixture(autouse=True)
+def no_device(monkeypatch):
+    tde.build()
+    monkeypatch.setattr(tde, "moe_ws_init", lambda ws, stream=None: None)
+
+
+def tensors(o):
+    if isinstance(o, torch.Tensor):
+        return [o]
+    if isinstance(o, dict):
+        o = o.values()
+    elif not isinstance(o, (tuple, list)):
+        return []
+    return [t for v in o for t in tensors(v)]
+
+
+def held(o, *shared):
+    """Bytes of an object's own tensors: those that `shared` objects have too are theirs."""
+    theirs = {id(t) for s in shared for t in tensors(vars(s))}
+    own = {id(t): t for t in tensors(vars(o)) if id(t) not in theirs}
+    return sum(t.numel() * t.element_size() for t in own.values())
+
+
+def cfg(T=4096, d=4096, E=8, k=2, f=1408):
+    return tde.make_config(T, d, E, k, f)
+
+
+@pytest.mark.parametrize("T,d", [(1, 64), (256, 1024), (2048, 1024), (4096, 4096), (4096, 7168)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_norm_in_8_bits_holds_less_than_its_rows(T, d, fmt):
+    """Codes, a scale for 128 of them and the statistics: no workspace of its own beside a shared one."""
+    scratch = tde.MoEScratch(cfg(T, d, 8, 2, 64), device="meta")
+    norms = [tde.MoENorm(T, d, checkpoint=fmt, device="meta", ws=scratch.ws) for _ in range(2)]
+    for n in norms:
+        assert n.ws is scratch.ws
+        assert held(n, scratch) == T * d + T * -(-d // 128) * 4 + T * 8 < 2 * T * d
+
+
+def test_workspaces_serve_the_norms():
+    for T, d, k, f in ((1, 64, 1, 64), (3, 8192, 1, 64), (4096, 512, 2, 128)):
+        c = cfg(T, d, 8, k, f)
+        for ws in (tde.MoEScratch(c, device="meta").ws, tde.Fp8MoELayer(c, tde.make_router(), device="meta").ws):
+            assert tde.MoENorm(T, d, device="meta", ws=ws).ws is ws
+    with pytest.raises(ValueError, match="^ws: expected"):
+        tde.MoENorm(4, 64, device="meta", ws=torch.empty(256, dtype=torch.uint8, device="meta"))
+    # without one it has its own, as large as its gradient needs
+    n = tde.MoENorm(4, 64, device="meta")
+    assert n.ws.numel() == tde.moe_norm_ws_size(4, 64)

@@ -1129,14 +1129,16 @@ def _new_checkpoint(rows, C, fmt, device):
 
 class MoEScratch:
     """The full-size buffers of a CheckpointedMoELayer: none is read after the call that wrote it, so
-    the layers of one configuration share one (on one stream)."""
+    the layers of one configuration share one (on one stream).  Its ws serves the norms of the same
+    rows too: MoENorm(T, d, ws=scratch.ws)."""
 
     def __init__(self, cfg: MoEConfigC, device="cuda"):
         import torch
         R, d, f = cfg.T * cfg.k, cfg.d, cfg.ffn
         bf = dict(dtype=torch.bfloat16, device=device)
         self.cfg, self.device = cfg, device
-        self.ws = torch.empty(moe_workspace_size(cfg)[0], dtype=torch.uint8, device=device)
+        self.ws = torch.empty(max(moe_workspace_size(cfg)[0], moe_norm_ws_size(cfg.T, d)),
+                              dtype=torch.uint8, device=device)
         moe_ws_init(self.ws)
         self.ab, self.dab = torch.empty((R, 2 * f), **bf), torch.empty((R, 2 * f), **bf)
         self.h = torch.empty((R, f), **bf)
@@ -1217,9 +1219,15 @@ class MoENorm:
         n, s = norm.forward(x, gamma, beta, residual=r)     # s = x + r, n = norm(s)
         n = norm.restore(gamma, beta)                       # n again, for the layer's backward pass
         g = norm.backward(dn, gamma, add=ds)                # dx (of x and of r), dgamma, dbeta
+
+    ws: the workspace of another call on the same stream (a layer's or a MoEScratch's, or any of
+    moe_norm_ws_size(T, d) bytes after moe_ws_init), written only while backward runs.  Up to 608 d
+    pairs of fp32 sums: below some 5000 rows more than the checkpoint saves, so the norms of a model
+    share one.  None: one of its own.
     """
 
-    def __init__(self, T, d, kind="layer", eps=1e-5, dtype=None, checkpoint="int8", device="cuda"):
+    def __init__(self, T, d, kind="layer", eps=1e-5, dtype=None, checkpoint="int8", device="cuda",
+                 ws=None):
         import torch
         _kind(kind)
         self.T, self.d, self.kind, self.eps = int(T), int(d), kind, float(eps)
@@ -1229,8 +1237,13 @@ class MoENorm:
         self.rstd = torch.empty(self.T, **f32)
         self.kept = _new_checkpoint(self.T, self.d, checkpoint, device) if checkpoint else None
         self.x = None
-        self.ws = torch.empty(moe_norm_ws_size(self.T, self.d), dtype=torch.uint8, device=device)
-        moe_ws_init(self.ws)
+        need = moe_norm_ws_size(self.T, self.d)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=device)
+            moe_ws_init(ws)
+        elif ws.numel() * ws.element_size() < need:
+            raise ValueError(f"ws: expected {need} bytes, got {ws.numel() * ws.element_size()}")
+        self.ws = ws
 
     def forward(self, x, gamma=None, beta=None, residual=None, stream=None):
         """(y in bf16, what was normalised: x itself or the sum)."""
@@ -1299,7 +1312,8 @@ class Fp8MoELayer:
         T, k, E, d, f = cfg.T, cfg.k, cfg.E, cfg.d, cfg.ffn
         R = T * k
         B = moe_fp8_token_blocks(R, E)
-        self.ws = torch.empty(moe_workspace_size(cfg)[0], dtype=torch.uint8, device=device)
+        self.ws = torch.empty(max(moe_workspace_size(cfg)[0], moe_norm_ws_size(T, d)),
+                              dtype=torch.uint8, device=device)
         moe_ws_init(self.ws)
         new = lambda shape, dt: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
         i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
