@@ -153,6 +153,12 @@ int32_t moe_capacity_from_factor(int64_t T, int32_t k, int32_t E, double c);
  * both out-pointers may be NULL. */
 moe_status_t moe_workspace_size(const moe_config_t *cfg, size_t *ws_bytes, size_t *ctx_bytes);
 
+/* Bytes of a workspace for the calls of single stages alone (route, permute, grouped FFN, combine
+ * and their gradients, the norms' and checkpoints' error word): the part of moe_workspace_size's that
+ * holds no whole intermediates.  Not for moe_layer_fwd, moe_layer_bwd, their MXFP8 forms and
+ * moe_grouped_ffn_bwd_mx.  Host-only. */
+moe_status_t moe_stage_workspace_size(const moe_config_t *cfg, size_t *ws_bytes);
+
 /* Byte offset of every saved tensor inside `ctx`; offsets[MOE_CTX_NFIELDS]. Host-only. */
 moe_status_t moe_ctx_offsets(const moe_config_t *cfg, size_t *offsets);
 

@@ -1,5 +1,5 @@
 """Layers that lend and borrow their full-size buffers: forward and backward of both in the order of a
-training step give bit by bit what layers with buffers of their own give."""
+training step give bit by bit what layers with buffers of their own give; and what they write of their workspace."""
 
 import pytest
 import torch
@@ -46,3 +46,28 @@ def test_layers_that_share_scratch(kind, fmt):
         assert set(gs[i]) == {"dx", "dW1", "dW2", "dlogits"}
         for n in gs[i]:
             assert torch.equal(gs[i][n], go[i][n]) and bool(gs[i][n].any()), (i, n)
+
+
+@pytest.mark.parametrize("T,E,k,kw", [(300, 8, 2, {}), (1, 4, 1, {}), (257, 64, 6, dict(capacity=20, drop_by_score=True)),
+                                      (513, 256, 8, dict(gate="sigmoid", drop_negative=True))])
+def test_stages_stay_in_their_workspace(T, E, k, kw):
+    """Nothing is written behind moe_stage_workspace_size, and the layer is right whatever it holds."""
+    d, f = 128, 64
+    c = tde.make_config(T, d, E, k, f, **kw)
+    n, room = tde.moe_stage_workspace_size(c), 1 << 20
+    rand = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    lg, x, dy = rand(T, E), rand(T, d).bfloat16(), rand(T, d).bfloat16()
+    W1, W2 = (0.2 * rand(E, 2 * f, d)).bfloat16(), (0.2 * rand(E, d, f)).bfloat16()
+    out = []
+    for fill in (0xa5, 0x3c):
+        scratch = tde.MoEScratch(c)
+        buf = torch.full((n + room,), fill, dtype=torch.uint8, device="cuda")
+        scratch.ws = buf[:n]
+        tde.moe_ws_init(scratch.ws)
+        m = tde.CheckpointedMoELayer(scratch)
+        y = m.forward(lg, x, W1, W2)
+        g = m.backward(lg, x, dy, W1, W2)
+        assert m.status() == (0, 0)
+        assert (buf[n:] == fill).all()
+        out.append([y, *g.values()])
+    assert all(torch.equal(a, b) for a, b in zip(*out))

@@ -1,6 +1,8 @@
 """What the norms and the layers that keep 8-bit checkpoints hold, counted from their tensors.  CPU only:
 the buffers are made on the meta device."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -55,3 +57,33 @@ def test_workspaces_serve_the_norms():
     # without one it has its own, as large as its gradient needs
     n = tde.MoENorm(4, 64, device="meta")
     assert n.ws.numel() == tde.moe_norm_ws_size(4, 64)
+
+
+def up(n):
+    return (n + 255) // 256 * 256
+
+
+def test_stage_workspace_size():
+    """The word of errors, the routing's scratch and the segments' maps; the rest of the whole layer's
+    workspace is its intermediates."""
+    for kw in ({}, dict(capacity=900, drop_by_score=True), dict(gate="sigmoid", drop_negative=True)):
+        for T, d, E, k, f in ((1, 64, 1, 1, 64), (4096, 4096, 8, 2, 1408), (8192, 2048, 128, 8, 768)):
+            c, R = tde.make_config(T, d, E, k, f, **kw), T * k
+            stage, whole = tde.moe_stage_workspace_size(c), tde.moe_workspace_size(c)[0]
+            assert stage + 2 * up(2 * R * d) + up(4 * R * f) == whole
+            assert stage >= 256 + up(4 * E) + 256 * E + (4 * R if kw.get("drop_by_score") else 0)
+    L, n = tde.lib(), ctypes.c_size_t(7)
+    bad = tde.make_config(4, 100, 8, 2, 64)
+    assert L.moe_stage_workspace_size(ctypes.byref(bad), ctypes.byref(n)) == 2 and n.value == 7
+    assert L.moe_stage_workspace_size(None, ctypes.byref(n)) == 1
+    assert L.moe_stage_workspace_size(ctypes.byref(cfg()), None) == 1
+
+
+def test_scratch_holds_each_buffer_once():
+    """[a | b] and its gradient, h, rows of the experts' outputs (then of their gradient) and of the
+    inputs' gradient, dw, and a workspace without room for a second copy of any of them."""
+    for T, d, E, k, f in ((256, 128, 8, 2, 256), (4096, 4096, 8, 2, 14336), (8192, 2048, 128, 8, 768)):
+        c, R = tde.make_config(T, d, E, k, f), T * k
+        s = tde.MoEScratch(c, device="meta")
+        ws = max(tde.moe_stage_workspace_size(c), tde.moe_norm_ws_size(T, d))
+        assert held(s) == R * (2 * 4 * f + 2 * f + 2 * 2 * d) + 4 * R + ws

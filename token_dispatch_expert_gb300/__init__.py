@@ -19,7 +19,8 @@ from ._build import LIB_PATH, build  # noqa: F401
 
 __all__ = [
     "MoEConfigC", "MoEError", "make_config", "lib",
-    "moe_capacity_from_factor", "moe_workspace_size", "moe_ctx_offsets", "moe_ws_init",
+    "moe_capacity_from_factor", "moe_workspace_size", "moe_stage_workspace_size", "moe_ctx_offsets",
+    "moe_ws_init",
     "moe_route", "moe_route_noalloc", "moe_permute", "moe_grouped_ffn", "moe_combine", "moe_combine_bwd",
     "moe_grouped_ffn_bwd", "moe_unpermute_reduce", "moe_layer_fwd", "moe_layer_bwd",
     "moe_grouped_ffn_gather", "moe_grouped_ffn_bwd_gather", "moe_grouped_ffn_bwd_dispatch",
@@ -117,6 +118,7 @@ def lib() -> ctypes.CDLL:
             "moe_capacity_from_factor": ([I64, I32, I32, ctypes.c_double], I32),
             "moe_workspace_size": ([cfgp, ctypes.POINTER(ctypes.c_size_t),
                                     ctypes.POINTER(ctypes.c_size_t)], I32),
+            "moe_stage_workspace_size": ([cfgp, ctypes.POINTER(ctypes.c_size_t)], I32),
             "moe_ctx_offsets": ([cfgp, ctypes.POINTER(ctypes.c_size_t)], I32),
             "moe_ws_init": ([P, P], I32),
             "moe_route": ([cfgp] + [P] * 12, I32),
@@ -249,6 +251,13 @@ def moe_workspace_size(cfg):
     _check(lib().moe_workspace_size(_cfg(cfg), ctypes.byref(ws), ctypes.byref(ctx)),
            "moe_workspace_size")
     return ws.value, ctx.value
+
+
+def moe_stage_workspace_size(cfg):
+    """Bytes of a workspace for the calls of single stages alone (see include/moe.h)."""
+    ws = ctypes.c_size_t(0)
+    _check(lib().moe_stage_workspace_size(_cfg(cfg), ctypes.byref(ws)), "moe_stage_workspace_size")
+    return ws.value
 
 
 def moe_ctx_offsets(cfg):
@@ -1137,7 +1146,7 @@ class MoEScratch:
         R, d, f = cfg.T * cfg.k, cfg.d, cfg.ffn
         bf = dict(dtype=torch.bfloat16, device=device)
         self.cfg, self.device = cfg, device
-        self.ws = torch.empty(max(moe_workspace_size(cfg)[0], moe_norm_ws_size(cfg.T, d)),
+        self.ws = torch.empty(max(moe_stage_workspace_size(cfg), moe_norm_ws_size(cfg.T, d)),
                               dtype=torch.uint8, device=device)
         moe_ws_init(self.ws)
         self.ab, self.dab = torch.empty((R, 2 * f), **bf), torch.empty((R, 2 * f), **bf)

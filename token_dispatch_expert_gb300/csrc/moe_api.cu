@@ -104,6 +104,7 @@ WsLayout ws_layout(const moe_config_t* c) {
   size_t o = WS_HEADER_BYTES;
   L.route = o; o += align_up(route_scratch_bytes(c));
   L.maps = o;  o += align_up(2 * static_cast<size_t>(c->E) * SEG_MAP_BYTES);
+  // (moe_stage_workspace_size ends here: what follows is the whole layer's alone)
   L.dyp = o;   o += align_up(R * d * 2);
   L.dab = o;   o += align_up(R * 2 * f * 2);
   L.dxp = o;   o += align_up(R * d * 2);
@@ -332,6 +333,14 @@ moe_status_t moe_workspace_size(const moe_config_t* cfg, size_t* ws_bytes, size_
   if (s != MOE_OK) return s;
   if (ws_bytes) *ws_bytes = ws_layout(cfg).total;
   if (ctx_bytes) *ctx_bytes = ctx_layout(cfg).total;
+  return MOE_OK;
+}
+
+moe_status_t moe_stage_workspace_size(const moe_config_t* cfg, size_t* ws_bytes) {
+  const moe_status_t s = validate(cfg);
+  if (s != MOE_OK) return s;
+  if (!ws_bytes) return MOE_ERR_INVALID_ARG;
+  *ws_bytes = ws_layout(cfg).dyp;
   return MOE_OK;
 }
 
