@@ -87,3 +87,32 @@ def test_scratch_holds_each_buffer_once():
         s = tde.MoEScratch(c, device="meta")
         ws = max(tde.moe_stage_workspace_size(c), tde.moe_norm_ws_size(T, d))
         assert held(s) == R * (2 * 4 * f + 2 * f + 2 * 2 * d) + 4 * R + ws
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_borrowing_layer_allocates_what_it_keeps(monkeypatch, fmt):
+    """The routing and two checkpoints, also while it is made; the lender the full-size buffers once."""
+    T, d, E, k, f = 4096, 4096, 8, 2, 1408
+    c, r, R, made = cfg(T, d, E, k, f), tde.make_router(), T * k, []
+    empty = torch.empty
+
+    def counted(*a, **kw):
+        t = empty(*a, **kw)
+        made.append(t.numel() * t.element_size())
+        return t
+    monkeypatch.setattr(torch, "empty", counted)
+    lender = tde.Fp8MoELayer(c, r, device="meta", checkpoint=fmt)
+    total = sum(made)
+    assert total == held(lender)
+    made.clear()
+    borrower = tde.Fp8MoELayer(c, r, device="meta", checkpoint=fmt, scratch=lender)
+    routing = 4 * (5 * R + 3 * E + 1) + R
+    checkpoints = R * (2 * f + d) + R * 4 * (-(-2 * f // 128) + d // 128)
+    assert sum(made) == held(borrower, lender) == routing + checkpoints
+    # full-size: bf16 [a | b], h, dh, rows of d three times; codes of x, h, dy, dab both ways
+    B = tde.moe_fp8_token_blocks(R, E)
+    bf16 = 2 * R * (2 * f + f + f + 3 * d) + 4 * R
+    codes = R * (2 * d + 3 * f) + 4 * R * (2 * (d // 128) + f // 128 + 2 * f // 128)
+    codes_t = 128 * B * (2 * d + 3 * f) + 4 * B * (2 * d + 3 * f)
+    ws = max(tde.moe_stage_workspace_size(c), tde.moe_norm_ws_size(T, d))
+    assert total == routing + checkpoints + bf16 + codes + codes_t + ws

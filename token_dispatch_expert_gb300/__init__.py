@@ -1321,9 +1321,6 @@ class Fp8MoELayer:
         T, k, E, d, f = cfg.T, cfg.k, cfg.E, cfg.d, cfg.ffn
         R = T * k
         B = moe_fp8_token_blocks(R, E)
-        self.ws = torch.empty(max(moe_workspace_size(cfg)[0], moe_norm_ws_size(T, d)),
-                              dtype=torch.uint8, device=device)
-        moe_ws_init(self.ws)
         new = lambda shape, dt: torch.empty(shape, dtype=dt, device=device)  # noqa: E731
         i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
         e4 = torch.float8_e4m3fn
@@ -1343,6 +1340,9 @@ class Fp8MoELayer:
             for n in ("ws", "ab", "yp", "q", "qt", "dyp", "dh", "dxp", "dw", "h"):
                 setattr(self, n, getattr(scratch, n))
             return
+        stages = moe_workspace_size(cfg)[0] if checkpoint is None else moe_stage_workspace_size(cfg)
+        self.ws = new((max(stages, moe_norm_ws_size(T, d)),), torch.uint8)
+        moe_ws_init(self.ws)
         self.h = new((R, f), bf) if checkpoint is not None else None
         self.ab, self.yp = new((R, 2 * f), bf), new((R, d), bf)
         # along the row: the operands of the products; along the tokens: of the weight gradients
