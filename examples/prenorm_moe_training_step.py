@@ -1,7 +1,7 @@
 """A few training steps of a stack of pre-norm mixture-of-experts blocks that keep their activations in
 8 bits: each block adds its input to the stream, normalises it, routes and runs its experts.  Between
-the passes a block holds the routing, the statistics and 8-bit checkpoints; the full-size buffers are
-shared by all blocks.
+the passes a block holds the gate's logits, the routing, the statistics, 8-bit checkpoints and its
+weights in bf16; the full-size buffers and the workspace are shared by all blocks.
 
     python examples/prenorm_moe_training_step.py [--tokens 2048 --width 1024 --blocks 4 ...]
 
@@ -29,8 +29,11 @@ class Block:
                   "W2": 0.03 * rand(c.E, c.d, c.ffn)}           # fp32 masters
 
     def kept_bytes(self):
-        kept = [*self.norm.kept, *self.moe.ab, *self.moe.yp, *self.moe.r.values(), self.norm.rstd]
-        return sum(t.numel() * t.element_size() for t in kept)
+        """(of activations, of weights in bf16): all that it holds from forward to backward but the
+        masters."""
+        n, m = self.norm, self.moe
+        kept = [*n.kept, n.rstd, *([] if n.mean is None else [n.mean]), *m.ab, *m.yp, *m.r.values(), self.logits]
+        return tuple(sum(t.numel() * t.element_size() for t in part) for part in (kept, self.w))
 
     def _beta(self):
         return self.p["beta"] if self.norm.kind == "layer" else None
@@ -64,12 +67,14 @@ def train(tokens=2048, width=1024, ffn=512, experts=16, k=2, blocks=4, steps=6, 
     scratch = tde.MoEScratch(cfg)
     stack = [Block(scratch, rand, kind, checkpoint) for _ in range(blocks)]
     x, target = rand(tokens, width).bfloat16(), rand(tokens, width).bfloat16()
-    log(f"kept by a block: {stack[0].kept_bytes() / 2**20:.1f} MiB")
     losses = []
     for step in range(steps):
         stream, branch = x, torch.zeros_like(x)
         for b in stack:
             stream, branch = b.forward(stream, branch)
+        if step == 0:
+            kept = [n / 2**20 for n in stack[0].kept_bytes()]
+            log(f"kept by a block: {kept[0]:.1f} MiB of activations, {kept[1]:.1f} MiB of weights")
         diff = stream.float() + branch.float() - target.float()
         losses.append(float(diff.square().mean()))
         d = diff.bfloat16()                     # of half the summed square

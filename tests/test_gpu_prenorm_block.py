@@ -159,3 +159,27 @@ def test_example_stack(kind, fmt, monkeypatch):
     assert last.dargs[0] is last.dargs[1]
     want = float((f64(last.dargs[0]) ** 2).mean())     # (rounded to bf16: 2^-8 of each difference)
     assert abs(losses[0] - want) <= 1e-2 * want
+
+
+@pytest.mark.parametrize("kind,fmt", [("layer", "int8"), ("rms", "e4m3")])
+def test_kept_bytes(kind, fmt):
+    """What the example says that a block keeps is every tensor that it, its norm and its layer hold
+    between the passes, but the masters and what the blocks share."""
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    import prenorm_moe_training_step as ex
+
+    def tensors(o):
+        if isinstance(o, torch.Tensor):
+            return [o]
+        o = list(o.values()) if isinstance(o, dict) else o if isinstance(o, (tuple, list)) else []
+        return [t for v in o for t in tensors(v)]
+    cfg = tde.make_config(100, 256, 8, 2, 64)
+    scratch = tde.MoEScratch(cfg)
+    b = ex.Block(scratch, lambda *s: torch.randn(*s, device="cuda"), kind, fmt)
+    x = torch.randn((100, 256), device="cuda").bfloat16()
+    b.forward(x, torch.zeros_like(x))
+    own = {id(t): t for o in (b, b.norm, b.moe) for t in tensors(vars(o))}
+    for t in tensors(vars(scratch)) + tensors(b.p):
+        own.pop(id(t), None)
+    assert sum(b.kept_bytes()) == sum(t.numel() * t.element_size() for t in own.values())
+    assert b.kept_bytes()[1] == 2 * 8 * 3 * 64 * 256
