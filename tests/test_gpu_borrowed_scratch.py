@@ -71,3 +71,14 @@ def test_stages_stay_in_their_workspace(T, E, k, kw):
         assert (buf[n:] == fill).all()
         out.append([y, *g.values()])
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_status_of_a_norm():
+    """The word of errors of its workspace, read and cleared, whose ever the workspace is."""
+    scratch = tde.MoEScratch(tde.make_config(16, 64, 4, 1, 64))
+    for n in (tde.MoENorm(16, 64), tde.MoENorm(16, 64, ws=scratch.ws)):
+        assert n.status() == (0, 0)
+        n.ws[:4].view(torch.int32).fill_(tde.DEVERR["TIMEOUT"])
+        status, flags = n.status()
+        assert tde.moe_status_string(status) == "MOE_ERR_TIMEOUT" and flags == tde.DEVERR["TIMEOUT"]
+        assert n.status() == (0, 0)

@@ -1292,6 +1292,10 @@ class MoENorm:
                      gamma=gamma, scales=scales, add=add, kind=self.kind, ws=self.ws, stream=stream)
         return out
 
+    def status(self, stream=None):
+        """Of backward, whose copies are waited for with a limit (and of all that share the workspace)."""
+        return moe_status(self.ws, stream)
+
 
 class Fp8MoELayer:
     """A layer whose router limits the choice to groups of experts and whose routed experts run
