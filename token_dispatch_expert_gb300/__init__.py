@@ -1311,6 +1311,9 @@ class Fp8MoELayer:
     output and the experts' outputs, is kept in 8 bits instead of bf16.  Then everything else but the
     routing is scratch, and `scratch`, another layer of the same configuration, lends its own: a
     model's layers keep 8 bits each and share one set of full-size buffers (on one stream).
+    The gradient then differs in two ways: it is taken at the restored values, and [da | db] and h are
+    rounded to bf16 before they become 8-bit operands, where the layer without checkpoints quantises
+    them from fp32.
     """
 
     def __init__(self, cfg: MoEConfigC, router: MoERouterC, device="cuda", grad_dtype=None,
@@ -1412,6 +1415,10 @@ class Fp8MoELayer:
         moe_fp8_gemm(*self.q["dy"], *w["W2_t"], self.dh, c.d, **seg)
         if self.checkpoint is not None:
             dab = self.ab          # (the forward's is not read any more)
+            # The checkpoint's gradient leaves [da | db] and h in bf16, which the quantiser reads: a
+            # rounding of at most 2^-8 of a value before E4M3's own of up to 2^-4, and 21 bytes a column
+            # of f moved where one pass from fp32 would move 9.  8192 tokens, top-8 of 128 experts of
+            # 2048 x 768: the backward takes 1.53 ms, without checkpoints 1.54.
             moe_ckpt_swiglu_bwd(self.dh, *self.kept["ab"], dab, self.h, **seg)
             moe_fp8_quantize(dab, *self.q["dab"], *self.qt["dab"], **seg)
             moe_fp8_quantize(self.h, codes_t=self.qt["h"][0], scales_t=self.qt["h"][1], **seg)
