@@ -12,7 +12,7 @@ import torch
 import rows_ref as ref
 import token_dispatch_expert_gb300 as tde
 from rows_ref import DT, Guarded, U, f32, f64
-from test_gpu_norm import E18, check_stats, check_y, rows_of
+from test_gpu_norm import E18, check_stats, check_y, rows_of, run_bwd
 
 pytestmark = pytest.mark.gpu
 WIDTHS = [1, 64, 129, 300, 513, 1413, 4096, 4097, 12001, 17000, 17001]
@@ -175,3 +175,11 @@ def test_gradient_in_place(C, x, pad):
     ref.check("dx", out[0][0], want, E18 * r[:, None] * (np.abs(dy) + mean(dy) + xh * mean(dy * xh)) +
               2 * U * np.abs(ad) + 1.01 * ref.HALF[x] * np.abs(want) + 1e-38)
     assert tde.moe_status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("C,R", [(3, 20001), (77, 20001), (1413, 5001), (4099, 2003)])
+@pytest.mark.parametrize("first", [1, 5])
+def test_gradient_of_dense_rows_off_16_bytes(C, R, first):
+    """The first and last rows' ends are cut off a piece of 16 bytes and written by plain stores; the
+    rows that take their places later come whole."""
+    run_bwd(np.random.default_rng(C), R, C, "layer", "bf16", "bf16", "fp32", True, "", first=first, offset=1.0)

@@ -84,6 +84,7 @@ norm_bwd_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
       sa = bulk_span(ar, a.C * XS, a.add, end(a.add, a.ld_add, XS));
       span_ends(to + y_bytes + x_bytes, ar, a.C * XS, sa);
     }
+    fence_proxy_async_smem();   // (a later row's bulk copy takes the same bytes of the slot)
     mbar_arrive_expect_tx(bar, static_cast<uint32_t>((sy.hi - sy.lo) + (sx.hi - sx.lo) + (sa.hi - sa.lo)));
     auto go = [&](uint8_t* t, const uint8_t* p, const Span& s) {
       if (s.hi > s.lo)

@@ -568,9 +568,9 @@ __device__ __forceinline__ void smem_row_values(float2* v, const uint8_t* row, i
   }
 }
 // The bytes [p, p + n) of rows that lie in [first, end), into shared memory at `to`, a 16-byte address
-// that stands for p's rounded down: whole 16-byte pieces by a bulk copy counted on `bar`, what the
-// tensor's own ends cut off a piece by plain copies (ordered by the caller's arrival on bar).
-// Returns the bytes that the bulk copy brings.  One thread.
+// that stands for p's rounded down: whole 16-byte pieces by the caller's bulk copy, bulk_span says
+// which; what the tensor's own ends cut off a piece by plain copies, span_ends (ordered by the caller's
+// arrival on the copy's barrier).  One thread.
 struct Span {
   uint64_t lo, hi;
 };
