@@ -629,8 +629,8 @@ moe_status_t moe_fp8_wgrad(const moe_fp8_wgrad_t *g, const void *a, const float 
  * with quotients correctly rounded in fp32.  A value is restored as code * scale in fp32, and
  * rounded once more where it is stored as bf16; where a mean is taken from it, code * scale - mean is
  * rounded once.  A block that holds a NaN or an infinity restores
- * as NaN throughout.  ld is a multiple of 16 and at least C; what lies past C is neither written
- * nor read.
+ * as NaN throughout.  ld is a multiple of 16 and at least C; nothing is written past C, and
+ * what lies there does not count.
  *
  * `live` (device, one int32, 4-byte aligned; NULL: all rows): the number of rows that hold
  * something, &offsets[E] for the rows of the expert segments.  Rows behind it are neither read nor
@@ -663,11 +663,12 @@ typedef struct {
  *   y = (v - m) * rstd * gamma + beta        (gamma or beta NULL: 1 or 0; fp32, rounded once)
  *   total = v (only with residual), mean = m [rows] (not with MOE_NORM_RMS), rstd [rows], and the
  *   checkpoint of v (codes, scales); each of these may be NULL.
- * Statistics are fp32: squares of magnitudes above 2^63 overflow.  A constant row with eps = 0 is
- * NaN.  Rows of x, residual, y and total may be strided and need only their elements' alignment
- * (off 16 bytes, or with a width off 8, accesses are narrower); gamma, beta, mean, rstd, codes and
- * scales are dense.  total may be x or residual itself, and so may y if it is of their type and has
- * their distance.
+ * Statistics are fp32: squares of magnitudes above 2^63 overflow.  A constant row has no answer with
+ * eps = 0: NaN where the sum of its values is exact, else what the sum's rounding leaves.  Rows of x,
+ * residual, y and total may be strided and need only their elements' alignment (off 16 bytes, or with
+ * a width off 8, accesses are narrower); gamma, beta, mean, rstd, codes and scales are dense and start
+ * at 16 bytes, as pointers do elsewhere.  total may be x or residual itself, and so may y if it is of
+ * their type and has their distance.
  */
 moe_status_t moe_norm(const moe_norm_t *p, const void *x, const void *residual_or_null,
                       const void *gamma_or_null, const void *beta_or_null, void *y,
@@ -687,7 +688,8 @@ int64_t moe_norm_ws_size(int64_t rows, int32_t C);
  * and of residual alike; add (NULL: none) is the gradient that reaches v by another way, the
  * stream's own.  dgamma and dbeta may be NULL; with rows = 0 they are zeros.  Sums over the rows
  * are fp32, in an order that rows, C, the types, the alignment and the device decide: the same bits
- * every time.  dx may be add itself, or dy if that is of its type and has its distance.  ws: moe_norm_ws_size bytes; its contents need not be kept.
+ * every time.  dx may be add itself, or dy if that is of its type and has its distance.  ws:
+ * moe_norm_ws_size bytes, whose contents need not be kept: the calls of a stream may share it.
  */
 moe_status_t moe_norm_bwd(const moe_norm_t *p, const void *dy, const void *x,
                           const float *x_scales_or_null, const float *mean, const float *rstd,

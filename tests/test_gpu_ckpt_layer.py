@@ -1,6 +1,6 @@
-"""The norm, the layers that keep 8-bit checkpoints, and a stack of blocks of both, run together as a
-training step uses them, against the same path in 64-bit numpy (quantised and rounded where the layers
-quantise and round).
+"""The layers that keep 8-bit checkpoints, as a training step uses them, against the same path in 64-bit
+numpy (quantised and rounded where the layers quantise and round); the norm's module; blocks of both that
+share their scratch (their numbers: test_gpu_prenorm_block.py).
 
 Tolerances as in the tests of the layers that they are built from: bf16 products within 2e-2 of rms +
 |o| (gpu_util), products of 8-bit operands within 0.1 (test_gpu_fp8_layer).

@@ -1182,7 +1182,9 @@ class CheckpointedMoELayer:
                   "src_slot": new((R,), i32), "drop_mask": new((T, k), torch.uint8)}
         self.ab = _new_checkpoint(R, 2 * c.ffn, checkpoint, device)
         self.yp = _new_checkpoint(R, c.d, checkpoint, device)
-        # the gate's gradient: that of weights renormalised over the chosen, whatever chose them
+        # the gate's gradient: that of weights renormalised over the chosen, whatever chose them (for
+        # logits whose weights are no numbers, such as infinities, the limit's, where moe_combine_bwd's
+        # are NaN too)
         softmax = c.gate == GATES["softmax"]
         self._gate = (make_config(T, c.d, E, k, c.ffn, route_scale=1.0 if softmax else c.route_scale),
                       make_router("softmax" if softmax else "sigmoid", renorm=True))

@@ -9,7 +9,9 @@
 //   [a | b] and h, 44,236 rows of 2816           6.3 TB/s, 79 us
 //   SwiGLU's gradient, 65,536 x 768, with h      6.5 TB/s, 78 us
 //   the same, 15,563 x 1409 of E4M3 codes        4.1 TB/s, 53 us: instructions, an element at a time
-//   combine's gradient, 4096 tokens of 7168, 8 slots   6.4 TB/s, 120 us
+//   restore 65,536 x 1536 from int8 to bf16      5.9 TB/s, 52 us
+//   [a | b] and h of f = 1001 or 1409, 40 M codes   3.9 TB/s, 41 us: instructions, an element at a time
+//   combine's gradient, 4096 tokens of 7168, 8 slots   6.4 TB/s, 120 us (six slots spill a register)
 //   save 39,960 x 1001                           3.3 TB/s, 37 us: latency, loads of two bytes
 // Rows fetched ahead through shared memory took the first three from 58, 88 and 94 us: with loads to
 // registers a warp has nothing under way while it computes, and more registers for more rows leave

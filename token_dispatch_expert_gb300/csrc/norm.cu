@@ -13,8 +13,13 @@
 // stream's gradient).  What is reached, where a copy reaches 6.79 TB/s:
 //   16,384 x 4096 bf16 with sum, statistics and int8 codes   5.6 TB/s, 108 us: two barriers a row, and
 //                                                gamma and beta from L1 for every row
-//   28,308 x 1413, the same                      2.3 TB/s, 156 us: instructions, an element at a time
+//   40 M elements of 4096 or 7168 columns, alone 3.2, 2.8 TB/s, 49, 56 us: the same, and sixteen warps
+//                                                to an SM (110 registers); a barrier less, by merging the
+//                                                warps' own means and squares, is open
+//   28,308 x 1413 with sum and codes             2.3 TB/s, 156 us: instructions, an element at a time
 //   from codes, 4096 x 7168                      4.9 TB/s, 18 us: 3 of it the launch's ramp
+//   from codes, 40 M elements of 1001 to 7169    1.7-2.0 TB/s, 61-70 us: loads of one or two bytes, not
+//                                                fetched ahead
 // (the gradient: norm_bwd.cu)
 #include <type_traits>
 
@@ -190,7 +195,7 @@ norm_ring_kernel(const __grid_constant__ NormArgs a, int nw, int slots) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
         s = __fadd2_rn(s, __fadd2_rn(__fadd2_rn(f[i][0], f[i][1]), __fadd2_rn(f[i][2], f[i][3])));
-      // (a quotient, not a product: exact for a constant row)
+      // (a quotient, not a product: a constant row's mean is exact wherever its sum is)
       mean = row_sum1(s.x + s.y, sh, 0, w, nw) / static_cast<float>(a.C);
     }
     // (columns past the row's end must not count as differences from the mean)
@@ -415,8 +420,8 @@ cudaError_t launch_norm_ring(const NormArgs& a, int nw, cudaStream_t st) {
 // Chunks to a warp: four to all of a row of up to four, since then no barrier is needed (1024 columns
 // with sum and checkpoint 65 us, with two to a warp 70); two up to eight chunks (2048 columns 71 us, with
 // four 99) and where four leave an eighth of them empty; else four (4096 columns 69 us, with two 74).
-// Element by element always four (1413 columns without a sum 127 us, with two 215; since the parameters
-// lie in shared memory there, 71).
+// Element by element four from three chunks on (1413 columns without a sum 127 us, with two 215; since the
+// parameters lie in shared memory there, 71).  Two chunks to a warp with a sum in bf16 spill two registers.
 template <int X, bool ADD, int V>
 cudaError_t launch_norm_rows(const NormArgs& a, int chunks, cudaStream_t st) {
   if (chunks == 1) return launch_norm_ring<1, X, ADD, V>(a, 1, st);

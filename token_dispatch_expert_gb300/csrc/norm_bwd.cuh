@@ -8,16 +8,18 @@ namespace moe {
 namespace {
 
 // nw warps share a row, N chunks to a warp; a CTA holds several such groups where nw is small.  dy, v
-// and add of the rows that follow come into
-// shared memory by bulk copies while one is worked on; the statistics and a chunk's scale are loaded
-// a row ahead.  The first thread of a group of nw warps copies for it: when all have passed
-// the barrier in a row's sums, all are done with the row before, whose slot is filled again.  gamma lies in shared memory too (but for the widest rows, which leave it no room): from
-// L1, which the slots leave little of, it came from L2 for every row, and 16384 x 4096 took 107 us
+// and add of the rows that follow come into shared memory by bulk copies while one is worked on; the
+// statistics and a chunk's scale are loaded a row ahead.  The first thread of a group of nw warps copies
+// for it: when all have passed the barrier in a row's sums, all are done with the row before, whose slot
+// is filled again.  gamma lies in shared memory too (but for the widest rows, which leave it no room):
+// from L1, which the slots leave little of, it came from L2 for every row, and 16384 x 4096 took 107 us
 // instead of 90.  With up to two chunks to a warp a row's G and xhat stay in registers between the two
-// passes over it, with four they are computed again, from the slot.  S: the type of v or its codes,
-// X: of add and dx, Y: of dy.  V = 8: rows of whole 16-byte vectors; V = 1: rows at any element and of
-// any width, whose copies bring the whole 16-byte pieces that a row touches, and which are read and
-// written element by element from there.
+// passes over it, with four they are computed again, from the slot.  Even so four chunks, whose sums
+// alone are 64 registers, spill: up to 132 bytes a thread from codes, 64 from fp32 rows and 328 element
+// by element (40 M elements of 16384 columns from int8 codes 119 us, of 256 to 7168 columns 60-67).
+// S: the type of v or its codes, X: of add and dx, Y: of dy.  V = 8: rows of whole 16-byte vectors;
+// V = 1: rows at any element and of any width, whose copies bring the whole 16-byte pieces that a row
+// touches, and which are read and written element by element from there.
 constexpr int MAX_SLOTS = 4, MAX_GROUPS = 8;
 constexpr long long BULK_BUDGET = 4000000000LL;   // clock cycles (about 2 s)
 
